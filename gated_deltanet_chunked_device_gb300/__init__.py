@@ -136,6 +136,7 @@ def lib():
                 L.gdn_prefill_plan_destroy.restype = None
                 L.gdn_status_string.argtypes = [ctypes.c_int]
                 L.gdn_status_string.restype = ctypes.c_char_p
+                linear._register(L)
                 _lib = L
     return _lib
 
@@ -521,3 +522,9 @@ def read_chunk_map(plan: _Plan, ws: torch.Tensor, num_seqs: int):
     cmap = i32(lay.chunk_map, 2 * max(n_chunks, 0)).view(-1, 2)
     order = i32(lay.seq_order, num_seqs)
     return offsets, cmap, n_chunks, order
+
+
+from . import linear  # noqa: E402 - needs the names above
+from .linear import *  # noqa: E402,F401,F403
+
+__all__ += linear.__all__

@@ -1,0 +1,71 @@
+// gdn_linear.cuh -- parameters shared by the host code and the kernels of the
+// gated linear recurrence (include/gdn_linear.h).  Not part of the public C ABI.
+#pragma once
+
+#include "../../include/gdn_linear.h"
+#include "gdn_internal.cuh"
+
+namespace gdn {
+
+struct LinearParams {
+    const void* x;
+    const void* a;
+    const void* b;                 // nullptr = ones
+    int64_t x_stride, a_stride, b_stride;
+    int32_t D;
+    int32_t C;                     // H * D channels
+    int32_t H;
+    int32_t gate_div;              // channels a gate serves: 1, or D with gates per head
+    int32_t x_dt, gate_dt, state_dt;
+    const void* cu_seqlens;        // nullptr: one sequence [0, T)
+    int cu_i64;
+    int32_t N;
+    int64_t T;
+    const void* initial_state;     // nullptr = zeros
+    void* output_state;            // nullptr = not written
+    int64_t state_stride;
+    const void* state_indices;     // nullptr: row = sequence
+    int idx_i64;
+    int32_t n_pool;
+    int32_t* status;               // nullptr: nothing is reported
+    void* y;
+    int64_t y_stride;
+    float* tile_states;            // [ceil(T / 64)][C]
+    const void* dy;
+    int64_t dy_stride;
+    const float* d_final;
+    float* d_initial;
+    void* dx;
+    void* da;
+    void* db;
+    int64_t dx_stride, da_stride, db_stride;
+    int32_t m;                     // decode: tokens per sequence
+    float* scratch;                // backward with gates per head: [T][H][2] fp32 sums
+};
+
+// One element of any of the types, at element offset `off`.
+__device__ __forceinline__ float load1(const void* p, int64_t off, int32_t dt) {
+    if (dt == GDN_DTYPE_F32) return static_cast<const float*>(p)[off];
+    if (dt == GDN_DTYPE_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[off]);
+    if (dt == GDN_DTYPE_F16) return __half2float(static_cast<const __half*>(p)[off]);
+    float lo, hi;
+    fp8x2_to_f32(static_cast<const uint8_t*>(p)[off], dt, lo, hi);
+    return lo;
+}
+
+__device__ __forceinline__ void store1(void* p, int64_t off, int32_t dt, float v) {
+    if (dt == GDN_DTYPE_F32)
+        static_cast<float*>(p)[off] = v;
+    else if (dt == GDN_DTYPE_BF16)
+        static_cast<__nv_bfloat16*>(p)[off] = __float2bfloat16_rn(v);
+    else if (dt == GDN_DTYPE_F16)
+        static_cast<__half*>(p)[off] = __float2half_rn(v);
+    else
+        static_cast<uint8_t*>(p)[off] = static_cast<uint8_t>(f32_to_fp8x2(v, 0.f, dt));
+}
+
+cudaError_t launch_linear_forward(const LinearParams& p, cudaStream_t stream);
+cudaError_t launch_linear_backward(const LinearParams& p, cudaStream_t stream);
+cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream);
+
+}  // namespace gdn
