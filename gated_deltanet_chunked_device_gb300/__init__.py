@@ -137,6 +137,7 @@ def lib():
                 L.gdn_status_string.argtypes = [ctypes.c_int]
                 L.gdn_status_string.restype = ctypes.c_char_p
                 linear._register(L)
+                pages._register(L)
                 _lib = L
     return _lib
 
@@ -524,7 +525,8 @@ def read_chunk_map(plan: _Plan, ws: torch.Tensor, num_seqs: int):
     return offsets, cmap, n_chunks, order
 
 
-from . import linear  # noqa: E402 - needs the names above
+from . import linear, pages  # noqa: E402 - they need the names above
 from .linear import *  # noqa: E402,F401,F403
+from .pages import *  # noqa: E402,F401,F403
 
-__all__ += linear.__all__
+__all__ += linear.__all__ + pages.__all__
