@@ -5,9 +5,17 @@
 // One block of 128 threads per (sequence, head); a thread owns every 128th
 // channel of the head and walks the sequence's tokens.  Right for every case,
 // and as slow as the longest sequence.
-#include "gdn_linear.cuh"
+#include "gdn_linear_scan.cuh"
 
 namespace gdn {
+
+cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+
 namespace {
 
 constexpr int kThreads = 128;
@@ -44,7 +52,7 @@ __device__ __forceinline__ bool seq_row(const LinearParams& p, int64_t i, int64_
     return false;
 }
 
-__global__ void __launch_bounds__(kThreads) gdn_linear_forward_kernel(LinearParams p) {
+__global__ void __launch_bounds__(kThreads) gdn_linear_decode_kernel(LinearParams p) {
     const int64_t i = blockIdx.x / p.H;
     const int32_t h = static_cast<int32_t>(blockIdx.x % p.H);
     int64_t s, e, row;
@@ -64,84 +72,61 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_forward_kernel(LinearPara
     }
 }
 
-__global__ void __launch_bounds__(kThreads) gdn_linear_backward_kernel(LinearParams p) {
-    __shared__ float sums[2][kThreads / 32];
-    const int64_t i = blockIdx.x / p.H;
-    const int32_t h = static_cast<int32_t>(blockIdx.x % p.H);
-    int64_t s, e;
-    if (!seq_range(p, i, s, e)) return;
-    for (int32_t d0 = 0; d0 < p.D; d0 += kThreads) {
-        const int32_t d = d0 + threadIdx.x;
-        const bool on = d < p.D;
-        const int64_t c = static_cast<int64_t>(h) * p.D + (on ? d : 0);
-        float carry = on && p.d_final ? p.d_final[i * p.C + c] : 0.f;
-        float before[GDN_LINEAR_TILE];  // the state before each token of a tile
-        for (int64_t end = e; end > s;) {
-            const int64_t f = (end - 1) / GDN_LINEAR_TILE;
-            const int64_t from = f * GDN_LINEAR_TILE > s ? f * GDN_LINEAR_TILE : s;
-            float st = 0.f;
-            if (from > s)
-                st = p.tile_states[(f - 1) * p.C + c];
-            else if (p.initial_state)
-                st = load1(p.initial_state, i * p.state_stride + c, p.state_dt);
-            for (int64_t t = from; t < end; ++t) {
-                before[t - from] = st;
-                float u = load1(p.x, t * p.x_stride + c, p.x_dt);
-                if (p.b) u *= load1(p.b, t * p.b_stride + c / p.gate_div, p.gate_dt);
-                st = fmaf(load1(p.a, t * p.a_stride + c / p.gate_div, p.gate_dt), st, u);
-            }
-            for (int64_t t = end - 1; t >= from; --t) {
-                const float g = load1(p.dy, t * p.dy_stride + c, p.x_dt) + carry;
-                const float x = load1(p.x, t * p.x_stride + c, p.x_dt);
-                const float b = p.b ? load1(p.b, t * p.b_stride + c / p.gate_div, p.gate_dt) : 1.f;
-                carry = load1(p.a, t * p.a_stride + c / p.gate_div, p.gate_dt) * g;
-                float da = on ? g * before[t - from] : 0.f, db = on ? g * x : 0.f;
-                if (on) store1(p.dx, t * p.dx_stride + c, p.x_dt, b * g);
-                if (p.gate_div == 1) {
-                    if (on) store1(p.da, t * p.da_stride + c, p.gate_dt, da);
-                    if (on && p.db) store1(p.db, t * p.db_stride + c, p.gate_dt, db);
-                    continue;
-                }
-                for (int o = 16; o > 0; o >>= 1) {
-                    da += __shfl_xor_sync(0xffffffffu, da, o);
-                    db += __shfl_xor_sync(0xffffffffu, db, o);
-                }
-                if (threadIdx.x % 32 == 0) {
-                    sums[0][threadIdx.x / 32] = da;
-                    sums[1][threadIdx.x / 32] = db;
-                }
-                __syncthreads();
-                if (threadIdx.x < 2) {
-                    float v = 0.f;
-                    for (int w = 0; w < kThreads / 32; ++w) v += sums[threadIdx.x][w];
-                    float* acc = p.scratch + (t * p.H + h) * 2 + threadIdx.x;
-                    if (d0 > 0) v += *acc;
-                    if (d0 + kThreads < p.D)
-                        *acc = v;
-                    else if (threadIdx.x == 0)
-                        store1(p.da, t * p.da_stride + h, p.gate_dt, v);
-                    else if (p.db)
-                        store1(p.db, t * p.db_stride + h, p.gate_dt, v);
-                }
-                __syncthreads();
-            }
-            end = from;
-        }
-        if (on && p.d_initial) p.d_initial[i * p.C + c] = carry;
-    }
+// Whether rows of this tensor can be read 4 elements at a time.
+bool vector_of_4(const void* p, int64_t stride, int32_t dt) {
+    return reinterpret_cast<uintptr_t>(p) % (4 * dtype_bytes(dt)) == 0 && stride % 4 == 0;
+}
+
+// Loads of 4 channels: x, gates per channel and states allow them, and a head's channels do not share 4 with another's.
+bool rows_vector(const LinearParams& p) {
+    bool ok = p.C % 4 == 0 && vector_of_4(p.x, p.x_stride, p.x_dt) && vector_of_4(p.initial_state, p.state_stride, p.state_dt) &&
+              vector_of_4(p.output_state, p.state_stride, p.state_dt);
+    if (p.gate_div != 1) return ok && p.D % 4 == 0;
+    return ok && vector_of_4(p.a, p.a_stride, p.gate_dt) && vector_of_4(p.b, p.b_stride, p.gate_dt);
+}
+
+// The workspace as the kernels take it; what has to start from zero is zeroed, where there is more than one tile.
+cudaError_t scan_space(const LinearParams& p, void* workspace, int64_t blocks, cudaStream_t stream, linear::ScanSpace* s) {
+    const ScanLayout l = scan_layout(p.T, p.C, p.gate_div != 1 ? p.D : 0);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    s->nt = l.nt;
+    s->blocks = static_cast<uint32_t>(blocks);
+    s->ticket = reinterpret_cast<uint32_t*>(ws);
+    s->flags = reinterpret_cast<uint32_t*>(ws + 256);
+    s->pairs = reinterpret_cast<float2*>(ws + l.pairs);
+    s->known = reinterpret_cast<float*>(ws + l.known);
+    return l.nt > 1 ? cudaMemsetAsync(ws, 0, l.zeroed, stream) : cudaSuccess;
 }
 
 }  // namespace
 
-cudaError_t launch_linear_forward(const LinearParams& p, cudaStream_t stream) {
-    gdn_linear_forward_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.H), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream) {
+    linear::ScanSpace s{};
+    const cudaError_t e = scan_space(p, workspace, (p.C + linear::kCols - 1) / linear::kCols, stream, &s);
+    if (e != cudaSuccess) return e;
+    if (p.tile_states) s.known = p.tile_states;
+    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt);
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, vec, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, vec, stream);
+    return launch_linear_forward_f32(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream) { return launch_linear_forward(p, stream); }
+cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream) {
+    linear::ScanSpace s{};
+    const cudaError_t e = scan_space(p, workspace, backward_blocks(p.C, p.gate_div != 1 ? p.D : 0), stream, &s);
+    if (e != cudaSuccess) return e;
+    LinearParams q = p;
+    q.scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + scan_layout(p.T, p.C, p.gate_div != 1 ? p.D : 0).sums);
+    bool vec = rows_vector(p) && vector_of_4(p.dy, p.dy_stride, p.x_dt) && vector_of_4(p.dx, p.dx_stride, p.x_dt) &&
+               vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
+    if (p.gate_div == 1) vec = vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_backward_bf16(q, s, vec, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_backward_f16(q, s, vec, stream);
+    return launch_linear_backward_f32(q, s, vec, stream);
+}
 
-cudaError_t launch_linear_backward(const LinearParams& p, cudaStream_t stream) {
-    gdn_linear_backward_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.H), kThreads, 0, stream>>>(p);
+cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream) {
+    gdn_linear_decode_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.H), kThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

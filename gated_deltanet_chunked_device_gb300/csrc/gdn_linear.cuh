@@ -40,7 +40,7 @@ struct LinearParams {
     void* db;
     int64_t dx_stride, da_stride, db_stride;
     int32_t m;                     // decode: tokens per sequence
-    float* scratch;                // backward with gates per head: [T][H][2] fp32 sums
+    float* scratch;                // backward, heads wider than a block: [T][H][pieces][2] sums
 };
 
 // One element of any of the types, at element offset `off`.
@@ -64,8 +64,39 @@ __device__ __forceinline__ void store1(void* p, int64_t off, int32_t dt, float v
         static_cast<uint8_t*>(p)[off] = static_cast<uint8_t>(f32_to_fp8x2(v, 0.f, dt));
 }
 
-cudaError_t launch_linear_forward(const LinearParams& p, cudaStream_t stream);
-cudaError_t launch_linear_backward(const LinearParams& p, cudaStream_t stream);
+// Blocks of channels of the backward pass: 128 wide, or with gates per head of head_dim channels (0: per channel) as
+// many whole heads as fit into 128, or 128 of one head.
+inline int64_t backward_blocks(int64_t C, int64_t head_dim) {
+    if (head_dim == 0) return (C + 127) / 128;
+    if (head_dim > 128) return C / head_dim * ((head_dim + 127) / 128);
+    const int64_t width = 128 / head_dim * head_dim;
+    return (C + width - 1) / width;
+}
+
+// Workspace of the scans over T tokens and C channels: the ticket and the flags (zeroed before each run), what tiles
+// hand on, and the sums of heads wider than a block.
+struct ScanLayout {
+    size_t zeroed, pairs, known, sums, total;
+    int64_t nt, blocks;
+};
+
+inline ScanLayout scan_layout(int64_t T, int64_t C, int64_t head_dim) {
+    ScanLayout l{};
+    l.nt = T > 0 ? (T + GDN_LINEAR_TILE - 1) / GDN_LINEAR_TILE : 1;
+    l.blocks = backward_blocks(C, head_dim);  // the forward pass has no more
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    l.zeroed = 256 + up(sizeof(uint32_t) * 4 * static_cast<size_t>(l.nt) * l.blocks);
+    l.pairs = l.zeroed;
+    l.known = l.pairs + up(sizeof(float2) * static_cast<size_t>(l.nt) * C);
+    l.sums = l.known + up(sizeof(float) * static_cast<size_t>(l.nt) * C);
+    l.total = l.sums;
+    if (head_dim > 128) l.total += up(sizeof(float2) * static_cast<size_t>(T) * (C / head_dim) * ((head_dim + 127) / 128));
+    return l;
+}
+
+// workspace: scan_layout's total bytes
+cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream);
+cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream);
 
 }  // namespace gdn

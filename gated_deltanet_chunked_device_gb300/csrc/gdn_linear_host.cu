@@ -131,12 +131,13 @@ gdn_status gdn_linear_plan(const gdn_linear_desc* desc, gdn_linear_plan_t* plan,
     if (d.max_total_tokens > 0x7fffffffLL - GDN_LINEAR_TILE) return GDN_ERR_UNSUPPORTED;
     if (!io_dtype(d.x_dtype) || !storage_dtype(d.state_dtype)) return GDN_ERR_UNSUPPORTED;
     if (d.gate_dtype != d.x_dtype && d.gate_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
+    const gdn::ScanLayout scan = gdn::scan_layout(d.max_total_tokens, static_cast<int64_t>(d.num_heads) * d.head_dim,
+                                                  (d.flags & GDN_LINEAR_GATES_PER_HEAD) ? d.head_dim : 0);
+    if (scan.nt * scan.blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;  // tiles of one launch
     gdn_linear_plan_s* p = new (std::nothrow) gdn_linear_plan_s;
     if (!p) return GDN_ERR_INVALID_ARG;
     p->desc = d;
-    p->workspace = 16;
-    if (d.flags & GDN_LINEAR_GATES_PER_HEAD)
-        p->workspace += sizeof(float) * 2 * static_cast<size_t>(d.max_total_tokens) * d.num_heads;
+    p->workspace = scan.total;
     *plan = p;
     *workspace_bytes = p->workspace;
     return GDN_OK;
@@ -151,7 +152,7 @@ gdn_status gdn_linear_forward_run(gdn_linear_plan_t plan, const gdn_linear_args*
     if (st != GDN_OK) return st;
     if (!workspace || workspace_bytes < plan->workspace || !aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
     if (p.N == 0) return GDN_OK;
-    return gdn::launch_linear_forward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::launch_linear_forward(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_linear_backward_run(gdn_linear_plan_t plan, const gdn_linear_args* args, void* workspace,
@@ -161,8 +162,7 @@ gdn_status gdn_linear_backward_run(gdn_linear_plan_t plan, const gdn_linear_args
     if (st != GDN_OK) return st;
     if (!workspace || workspace_bytes < plan->workspace || !aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
     if (p.N == 0) return GDN_OK;
-    p.scratch = static_cast<float*>(workspace);
-    return gdn::launch_linear_backward(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+    return gdn::launch_linear_backward(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
 gdn_status gdn_linear_decode_run(gdn_linear_plan_t plan, const gdn_linear_args* args, int32_t tokens_per_seq,
