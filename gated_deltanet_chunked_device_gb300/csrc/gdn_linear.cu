@@ -5,13 +5,16 @@
 // One block of 128 threads per (sequence, head); a thread owns every 128th
 // channel of the head and walks the sequence's tokens.  Right for every case,
 // and as slow as the longest sequence.
-#include "gdn_linear_scan.cuh"
+#include "gdn_linear_column.cuh"
 
 namespace gdn {
 
-cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
-cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
-cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
+cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
+cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
 cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
@@ -85,6 +88,34 @@ bool rows_vector(const LinearParams& p) {
     return ok && vector_of_4(p.a, p.a_stride, p.gate_dt) && vector_of_4(p.b, p.b_stride, p.gate_dt);
 }
 
+// Whether rows can be copied 16 bytes at a time.
+bool vector_of_16_bytes(const void* p, int64_t stride, int32_t dt, int64_t row) {
+    const int64_t e = dtype_bytes(dt);
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * e % 16 == 0 && row * e % 16 == 0;
+}
+
+bool inputs_wide(const LinearParams& p) {
+    const bool x = vector_of_16_bytes(p.x, p.x_stride, p.x_dt, p.C);
+    if (p.gate_div != 1) return x;
+    return x && vector_of_16_bytes(p.a, p.a_stride, p.gate_dt, p.C) && vector_of_16_bytes(p.b, p.b_stride, p.gate_dt, p.C);
+}
+
+// Segments of the columns: one when the columns alone have enough blocks for the SMs, else as many as the SMs hold.
+linear::Segments segments(const LinearParams& p, int64_t tokens) {
+    linear::Segments s{};
+    const int64_t blocks = (p.C + linear::kColWidth - 1) / linear::kColWidth, n = (p.T + tokens - 1) / tokens;
+    int64_t segs = multiprocessors() / blocks;
+    if (segs > n / 2 - 1) segs = n / 2 - 1;  // two stages or more each
+    s.space.blocks = static_cast<uint32_t>(blocks);
+    s.space.nt = 1;
+    s.stages = static_cast<int32_t>(n > 0 ? n : 1);
+    if (segs > 1) {
+        s.stages = static_cast<int32_t>((n + segs) / (segs + 1));
+        s.space.nt = n <= 2 * s.stages ? 1 : 1 + (n - 2 * s.stages + s.stages - 1) / s.stages;
+    }
+    return s;
+}
+
 // The workspace as the kernels take it; what has to start from zero is zeroed, where there is more than one tile.
 cudaError_t scan_space(const LinearParams& p, void* workspace, int64_t blocks, cudaStream_t stream, linear::ScanSpace* s) {
     const ScanLayout l = scan_layout(p.T, p.C, p.gate_div != 1 ? p.D : 0);
@@ -100,15 +131,40 @@ cudaError_t scan_space(const LinearParams& p, void* workspace, int64_t blocks, c
 
 }  // namespace
 
+int multiprocessors() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
+    return n > 0 ? n : 1;
+}
+
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream) {
+    if (rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt)) {
+        const int e = static_cast<int>(dtype_bytes(p.x_dt)), ge = static_cast<int>(dtype_bytes(p.gate_dt));
+        linear::Segments seg = segments(p, linear::kColWarps * linear::kRuns * linear::forward_run(e, ge, p.gate_div != 1, p.b != nullptr));
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        const size_t zeroed = 256 + sizeof(uint32_t) * seg.space.nt * seg.space.blocks;
+        const size_t pairs = (zeroed + 255) / 256 * 256;
+        seg.space.ticket = reinterpret_cast<uint32_t*>(ws);
+        seg.space.flags = reinterpret_cast<uint32_t*>(ws + 256);
+        seg.space.pairs = reinterpret_cast<float2*>(ws + pairs);
+        seg.space.known = reinterpret_cast<float*>(ws + pairs + sizeof(float2) * seg.space.nt * p.C);
+        if (seg.space.nt > 1) {
+            const cudaError_t err = cudaMemsetAsync(ws, 0, zeroed, stream);
+            if (err != cudaSuccess) return err;
+        }
+        const bool wide = inputs_wide(p);
+        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, wide, stream);
+        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, wide, stream);
+        return launch_linear_column_forward_f32(p, seg, wide, stream);
+    }
     linear::ScanSpace s{};
     const cudaError_t e = scan_space(p, workspace, (p.C + linear::kCols - 1) / linear::kCols, stream, &s);
     if (e != cudaSuccess) return e;
     if (p.tile_states) s.known = p.tile_states;
-    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt);
-    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, vec, stream);
-    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, vec, stream);
-    return launch_linear_forward_f32(p, s, vec, stream);
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, stream);
+    return launch_linear_forward_f32(p, s, stream);
 }
 
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream) {

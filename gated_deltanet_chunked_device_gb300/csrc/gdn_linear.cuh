@@ -94,6 +94,8 @@ inline ScanLayout scan_layout(int64_t T, int64_t C, int64_t head_dim) {
     return l;
 }
 
+int multiprocessors();  // of the current device
+
 // workspace: scan_layout's total bytes
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream);

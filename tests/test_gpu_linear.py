@@ -101,6 +101,25 @@ def test_pool(state, index):
     assert torch.equal(whole[:, H].float(), before[:, H].float())
 
 
+@pytest.mark.parametrize("lens", [[5000], [1500, 3, 0, 4000, 64], [1] * 40 + [2000, 700]])
+def test_pool_in_place_over_long_sequences(lens):
+    """In place, where blocks far apart read and write one row: the same bits as into another pool, every time."""
+    i = make(lens, 1, 32, "f32", seed=24)
+    rows = torch.randperm(len(lens) + 5, generator=torch.Generator().manual_seed(2))[: len(lens)].to(torch.int32).cuda()
+    pool = torch.randn(len(lens) + 5, 1, 32, device="cuda")
+    call = lambda out: gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=start, output_state=out,  # noqa: E731
+                                                   state_indices=rows, output_final_state=True, cu_seqlens=i["cu"])[0]
+    start = pool
+    other = pool.clone()
+    y = call(other)
+    want = ref.forward(f64(i["x"]), f64(i["a"]), f64(i["b"]), i["cul"], f64(pool[rows.long()]))
+    within("y", y, want[0], want[3])
+    within("pool", other[rows.long()], want[1], want[4])
+    for _ in range(30):
+        start = pool.clone()
+        assert torch.equal(call(start), y) and torch.equal(start, other)
+
+
 def test_pool_rows_out_of_range_are_not_followed():
     i = make([10, 80, 3], 2, 16, "f32", seed=7)
     pool = torch.randn(4, 2, 16, device="cuda")
