@@ -33,6 +33,74 @@ __host__ __device__ constexpr int forward_run(int x_bytes, int gate_bytes, bool 
     return x_bytes + (head ? 0 : has_b ? 2 * gate_bytes : gate_bytes) > 6 ? 4 : 8;
 }
 
+// Two fp32 at a time.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t x, y, z, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    memcpy(&z, &c, 8);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+
+// Four channels.
+struct Quad {
+    float2 lo, hi;
+};
+__device__ __forceinline__ Quad mul(Quad a, Quad b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Quad fma(Quad a, Quad b, Quad c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
+__device__ __forceinline__ Quad all4(float v) { return {{v, v}, {v, v}}; }
+__device__ __forceinline__ Quad quad(float4 v) { return {{v.x, v.y}, {v.z, v.w}}; }
+__device__ __forceinline__ float4 flat(Quad v) { return make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y); }
+__device__ __forceinline__ Quad pick(bool c, Quad a, Quad b) {
+    return {{c ? a.lo.x : b.lo.x, c ? a.lo.y : b.lo.y}, {c ? a.hi.x : b.hi.x, c ? a.hi.y : b.hi.y}};
+}
+__device__ __forceinline__ Quad shift_up(Quad v, int lanes) {
+    return {{__shfl_up_sync(0xffffffffu, v.lo.x, lanes), __shfl_up_sync(0xffffffffu, v.lo.y, lanes)},
+            {__shfl_up_sync(0xffffffffu, v.hi.x, lanes), __shfl_up_sync(0xffffffffu, v.hi.y, lanes)}};
+}
+template <class T>
+__device__ __forceinline__ Quad widen(const Pack<T>& p) {
+    return {{to_f32(p.v[0]), to_f32(p.v[1])}, {to_f32(p.v[2]), to_f32(p.v[3])}};
+}
+__device__ __forceinline__ Quad widen(const Pack<__nv_bfloat16>& p) {
+    uint2 w;
+    memcpy(&w, &p, 8);
+    return {{__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u)},
+            {__uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u)}};
+}
+__device__ __forceinline__ Pack<float> narrow(Quad q, float) { return {q.lo.x, q.lo.y, q.hi.x, q.hi.y}; }
+__device__ __forceinline__ Pack<__nv_bfloat16> narrow(Quad q, __nv_bfloat16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(q.lo.x, q.lo.y), b = __floats2bfloat162_rn(q.hi.x, q.hi.y);
+    return {a.x, a.y, b.x, b.y};
+}
+__device__ __forceinline__ Pack<__half> narrow(Quad q, __half) {
+    const __half2 a = __floats2half2_rn(q.lo.x, q.lo.y), b = __floats2half2_rn(q.hi.x, q.hi.y);
+    return {a.x, a.y, b.x, b.y};
+}
+
+// States are read and written where sequences start and end: out of line, to keep them out of the instruction cache.
+static __device__ __noinline__ float4 state_quad_load(const void* base, int64_t off, int32_t dt) {
+    float v[4];
+    state_load4(base, off, dt, v);
+    return make_float4(v[0], v[1], v[2], v[3]);
+}
+static __device__ __noinline__ void state_quad_store(void* base, int64_t off, int32_t dt, float4 q) {
+    const float v[4] = {q.x, q.y, q.z, q.w};
+    state_store4(base, off, dt, v);
+}
+
 template <int kBytes>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
     if constexpr (kBytes == 16)
@@ -58,14 +126,23 @@ struct StageArray {
         constexpr int kStep = 32 * kColWarps / kPerRow;  // tokens between a thread's chunks
         const int part = tid % kPerRow;
         if (part * kElems >= cols) return;
-        int tok = tid / kPerRow;
+        const int tok = tid / kPerRow, n = static_cast<int>(t1 - t0);
         const T* src = base + (t0 + tok) * stride + part * kElems;
-        const int n = static_cast<int>(t1 - t0);
+        uint8_t* dst = stage + tok / S * kRunBytes + tok % S * kRow + part * kChunk;
+        static_assert(kStep % S == 0, "a thread's chunks lie whole runs apart");
+        constexpr int kTimes = kColWarps * kRuns * S / kStep;
+        if (n == kColWarps * kRuns * S) {
 #pragma unroll
-        for (int i = 0; i < kColWarps * kRuns * S / kStep; ++i) {
-            if (tok < n) cp_async<kChunk>(stage + tok / S * kRunBytes + tok % S * kRow + part * kChunk, src);
-            tok += kStep;
-            src += kStep * stride;
+            for (int i = 0; i < kTimes; ++i) {
+                cp_async<kChunk>(dst + i * (kStep / S) * kRunBytes, src);
+                src += kStep * stride;
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kTimes; ++i) {
+                if (tok + i * kStep < n) cp_async<kChunk>(dst + i * (kStep / S) * kRunBytes, src);
+                src += kStep * stride;
+            }
         }
     }
 
@@ -78,6 +155,8 @@ struct StageArray {
 template <int kTokens>
 struct StageBounds {
     uint32_t starts[kTokens / 32], ends[kTokens / 32];
+    uint32_t warps;                // which warps' tokens hold a start
+    uint32_t plain;                // which warps' tokens are all there, with neither a start nor an end
     int32_t start_seq[kTokens], end_seq[kTokens];
 };
 
@@ -109,6 +188,20 @@ __device__ __forceinline__ int64_t stage_bounds(const LinearParams& p, int64_t l
         next_lo += __popc(__ballot_sync(0xffffffffu, i <= p.N && c < t1));
         for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(lo + __ffs(m) - 1);
         if (__any_sync(0xffffffffu, c > t1)) break;
+    }
+    __syncwarp();
+    constexpr int kWarpTokens = kTokens / kColWarps;
+    uint32_t s = 0, e = 0;
+    if (lane < kColWarps) {
+        constexpr uint32_t kMask = kWarpTokens == 32 ? 0xffffffffu : (1u << (kWarpTokens % 32)) - 1u;
+        s = (b.starts[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
+        e = (b.ends[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
+    }
+    const uint32_t warps = __ballot_sync(0xffffffffu, s != 0);
+    const uint32_t plain = __ballot_sync(0xffffffffu, (s | e) == 0 && t0 + (lane + 1) * kWarpTokens <= t1);
+    if (lane == 0) {
+        b.warps = warps;
+        b.plain = plain;
     }
     return next_lo;
 }
@@ -267,10 +360,10 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
         __syncthreads();
         const StageBounds<kTokens>& bd = sm.bounds[q & 1];
         const bool learn = twice && q < stages;
-        const int64_t t0 = stage_start(q);
-        const int n = static_cast<int>(min(static_cast<int64_t>(S), max(static_cast<int64_t>(0), end - t0 - run * S)));
-        float a[S][4], u[S][4], A[4] = {1.f, 1.f, 1.f, 1.f}, B[4] = {0.f, 0.f, 0.f, 0.f};
-        float exA[4], exB[4];
+        const int64_t t0 = stage_start(q), t = t0 + run * S;
+        const int n = static_cast<int>(min(static_cast<int64_t>(S), max(static_cast<int64_t>(0), end - t)));
+        const bool plain = (bd.plain >> (warp % kColWarps)) & 1;
+        Quad a[S], u[S], A = all4(1.f), B = all4(0.f), exA, exB;
         uint32_t starts = 0;
         bool before = false;  // whether a sequence starts in the warp's runs before this one
         if (warp == kColWarps) {
@@ -278,90 +371,79 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
         } else {
             fetch(q + kDepth - 1);
             const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
-            starts = run_bits<S>(bd.starts, run);
 #pragma unroll
             for (int k = 0; k < S; ++k) {
-                const Pack<X> px = AX::get(stage, run, k, l);
-                Pack<G> pa, pb;
-                if constexpr (!kHead) {
-                    pa = AG::get(stage + AX::kBytes, run, k, l);
-                    if constexpr (kHasB) pb = AG::get(stage + AX::kBytes + AG::kBytes, run, k, l);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float g, s = 1.f;
-                    if constexpr (kHead) {
-                        g = to_f32(ha[k]);
-                        if constexpr (kHasB) s = to_f32(hb[k]);
-                    } else {
-                        g = to_f32(pa.v[j]);
-                        if constexpr (kHasB) s = to_f32(pb.v[j]);
-                    }
-                    a[k][j] = k < n ? g : 1.f;
-                    u[k][j] = k < n ? (kHasB ? to_f32(px.v[j]) * s : to_f32(px.v[j])) : 0.f;
+                u[k] = widen(AX::get(stage, run, k, l));
+                if constexpr (kHead) {
+                    a[k] = all4(to_f32(ha[k]));
+                    if constexpr (kHasB) u[k] = mul(u[k], all4(to_f32(hb[k])));
+                } else {
+                    a[k] = widen(AG::get(stage + AX::kBytes, run, k, l));
+                    if constexpr (kHasB) u[k] = mul(u[k], widen(AG::get(stage + AX::kBytes + AG::kBytes, run, k, l)));
                 }
             }
             fetch_gates(q + 1);
+            if (plain) {
+                A = a[0];
+                B = u[0];
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
-                if ((starts >> k) & 1) {
-                    if (p.initial_state && on) {
-                        const int64_t row = state_row(p, bd.start_seq[run * S + k]);
-                        if (row >= 0) {
-                            float h0[4];
+                for (int k = 1; k < S; ++k) {
+                    A = mul(A, a[k]);
+                    B = fma(a[k], B, u[k]);
+                }
+            } else {
+                starts = run_bits<S>(bd.starts, run);
+#pragma unroll
+                for (int k = 0; k < S; ++k) {
+                    if (k >= n) {
+                        a[k] = all4(1.f);
+                        u[k] = all4(0.f);
+                    }
+                    if ((starts >> k) & 1) {
+                        if (p.initial_state && on) {
+                            const int64_t row = state_row(p, bd.start_seq[run * S + k]);
                             // With states in place, a later segment may have written the row of a sequence that starts
                             // here by the time of the second pass: the last one to start, if any.  Its state is kept.
-                            const int64_t t = t0 + run * S + k;
-                            if (twice && !learn && t == sm.kept_at)
-                                get4<true>(sm.kept, l, h0);
-                            else
-                                state_load<true>(p.initial_state, row * p.state_stride + c0, p.state_dt, l, cols, h0);
+                            float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (twice && !learn && t + k == sm.kept_at)
+                                h0 = *reinterpret_cast<const float4*>(&sm.kept[l * 4]);
+                            else if (row >= 0)
+                                h0 = state_quad_load(p.initial_state, row * p.state_stride + c0 + l * 4, p.state_dt);
                             if (learn && is_last_bit<kTokens>(bd.starts, run * S + k)) {
-                                put4<true>(sm.kept, l, h0);
-                                sm.kept_at = t;
+                                *reinterpret_cast<float4*>(&sm.kept[l * 4]) = h0;
+                                sm.kept_at = t + k;
                             }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) u[k][j] = fmaf(a[k][j], h0[j], u[k][j]);
+                            if (row >= 0) u[k] = fma(a[k], quad(h0), u[k]);
                         }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) B[j] = u[k][j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        A[j] *= a[k][j];
-                        B[j] = fmaf(a[k][j], B[j], u[k][j]);
+                        B = u[k];
+                    } else {
+                        A = mul(A, a[k]);
+                        B = fma(a[k], B, u[k]);
                     }
                 }
             }
             // over the warp's runs
-            const uint32_t rs = runs_with<S>(bd.starts, warp);
+            const uint32_t rs = (bd.warps >> warp) & 1 ? runs_with<S>(bd.starts, warp) : 0;
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
                 const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float oa = __shfl_up_sync(0xffffffffu, A[j], o * kLanesRow), ob = __shfl_up_sync(0xffffffffu, B[j], o * kLanesRow);
-                    if (sub >= o) {
-                        B[j] = mine ? B[j] : fmaf(A[j], ob, B[j]);
-                        A[j] *= oa;
-                    }
+                const Quad oa = shift_up(A, o * kLanesRow), ob = shift_up(B, o * kLanesRow);
+                if (sub >= o) {
+                    B = pick(mine, B, fma(A, ob, B));
+                    A = mul(A, oa);
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                exA[j] = __shfl_up_sync(0xffffffffu, A[j], kLanesRow);
-                exB[j] = __shfl_up_sync(0xffffffffu, B[j], kLanesRow);
-                if (sub == 0) {
-                    exA[j] = 1.f;
-                    exB[j] = 0.f;
-                }
+            exA = shift_up(A, kLanesRow);
+            exB = shift_up(B, kLanesRow);
+            if (sub == 0) {
+                exA = all4(1.f);
+                exB = all4(0.f);
             }
             before = (rs & ((1u << sub) - 1u)) != 0;
             if (sub == kRuns - 1) {
                 float4* o = reinterpret_cast<float4*>(&sm.pairs[warp][l * 4]);
-                o[0] = make_float4(A[0], B[0], A[1], B[1]);
-                o[1] = make_float4(A[2], B[2], A[3], B[3]);
+                o[0] = make_float4(A.lo.x, B.lo.x, A.lo.y, B.lo.y);
+                o[1] = make_float4(A.hi.x, B.hi.x, A.hi.y, B.hi.y);
             }
         }
         __syncthreads();
@@ -371,14 +453,10 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
             for (int w = 0; w < kColWarps; ++w) {
                 const float2 ab = sm.pairs[w][lane];
                 if (w == warp) enter = carry;
-                if (runs_with<S>(bd.starts, w)) {
-                    carry = ab.y;
-                    reset = true;
-                } else {
-                    carry = fmaf(ab.x, carry, ab.y);
-                }
-                through *= ab.x;
+                carry = (bd.warps >> w) & 1 ? ab.y : fmaf(ab.x, carry, ab.y);
+                if (learn) through *= ab.x;
             }
+            reset |= bd.warps != 0;
         }
         if (learn) {
             if (q < stages - 1) continue;
@@ -407,29 +485,34 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
             continue;
         }
         if (warp < kColWarps) {
-            float h[4];
+            const Quad e = {{__shfl_sync(0xffffffffu, enter, l * 4), __shfl_sync(0xffffffffu, enter, l * 4 + 1)},
+                            {__shfl_sync(0xffffffffu, enter, l * 4 + 2), __shfl_sync(0xffffffffu, enter, l * 4 + 3)}};
+            Quad h = pick(before, exB, fma(exA, e, exB));
+            if (!on) continue;
+            X* out = y + t * p.y_stride;
+            if (plain) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float e = __shfl_sync(0xffffffffu, enter, l * 4 + j);
-                h[j] = before ? exB[j] : fmaf(exA[j], e, exB[j]);
-            }
-            if (on) {
-                const int64_t t = t0 + run * S;
+                for (int k = 0; k < S; ++k) {
+                    h = fma(a[k], h, u[k]);
+                    store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
+                    out += p.y_stride;
+                }
+                if (p.tile_states && (t + S) % kTile == 0)
+                    *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
+            } else {
                 const uint32_t ends = run_bits<S>(bd.ends, run);
-                X* out = y + t * p.y_stride;
 #pragma unroll
                 for (int k = 0; k < S; ++k) {
                     if (k >= n) break;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[j] = (starts >> k) & 1 ? u[k][j] : fmaf(a[k][j], h[j], u[k][j]);
-                    store4<true>(out, 0, 4, h);
+                    h = pick((starts >> k) & 1, u[k], fma(a[k], h, u[k]));
+                    store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
                     out += p.y_stride;
                     if (((ends >> k) & 1) && p.output_state) {
                         const int64_t row = state_row(p, bd.end_seq[run * S + k]);
-                        if (row >= 0) state_store<true>(p.output_state, row * p.state_stride + c0, p.state_dt, l, cols, h);
+                        if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
                     }
                     if (p.tile_states && ((t + k) % kTile == kTile - 1 || t + k == p.T - 1))
-                        *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = make_float4(h[0], h[1], h[2], h[3]);
+                        *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = flat(h);
                 }
             }
         }
