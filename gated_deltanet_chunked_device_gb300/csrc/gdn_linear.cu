@@ -5,21 +5,35 @@
 // One block of 128 threads per (sequence, head); a thread owns every 128th
 // channel of the head and walks the sequence's tokens.  Right for every case,
 // and as slow as the longest sequence.
+#include <cstdlib>
+#include <cudaTypedefs.h>
+
 #include "gdn_linear_column.cuh"
 
 namespace gdn {
 
-cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
-cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
-cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream);
+cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
+cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
+cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
 cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 
 namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? f : nullptr);
+    }();
+    return fn;
+}
 
 constexpr int kThreads = 128;
 
@@ -100,18 +114,26 @@ bool inputs_wide(const LinearParams& p) {
     return x && vector_of_16_bytes(p.a, p.a_stride, p.gate_dt, p.C) && vector_of_16_bytes(p.b, p.b_stride, p.gate_dt, p.C);
 }
 
-// Segments of the columns: one when the columns alone have enough blocks for the SMs, else as many as the SMs hold.
-linear::Segments segments(const LinearParams& p, int64_t tokens) {
+// Shape and time segments of the columns.
+linear::Segments segments(const LinearParams& p, int* width, int* warps) {
     linear::Segments s{};
-    const int64_t blocks = (p.C + linear::kColWidth - 1) / linear::kColWidth, n = (p.T + tokens - 1) / tokens;
-    int64_t segs = multiprocessors() / blocks;
-    if (segs > n / 2 - 1) segs = n / 2 - 1;  // two stages or more each
+    const char* ew = getenv("LC");
+    const char* ev = getenv("LW");
+    const char* es = getenv("LS");
+    *width = ew ? atoi(ew) : 32;
+    *warps = ev ? atoi(ev) : 8;
+    const int64_t blocks = (p.C + *width - 1) / *width, sms = multiprocessors();
+    int64_t segs = (*warps == 4 ? 2 : 1) * sms / blocks;
+    if (es) segs = atoi(es);
+    const int64_t tokens = *warps * 1024 / *width, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
+    if (segs > n / 2) segs = n / 2;
     s.space.blocks = static_cast<uint32_t>(blocks);
     s.space.nt = 1;
-    s.stages = static_cast<int32_t>(n > 0 ? n : 1);
-    if (segs > 1) {
-        s.stages = static_cast<int32_t>((n + segs) / (segs + 1));
-        s.space.nt = n <= 2 * s.stages ? 1 : 1 + (n - 2 * s.stages + s.stages - 1) / s.stages;
+    s.first = s.stages = static_cast<int32_t>(n);
+    if (segs >= 3) {
+        s.stages = static_cast<int32_t>((n * 10 + 10 * segs - 5) / (10 * segs - 4));
+        s.first = static_cast<int32_t>((s.stages * 6 + 9) / 10);
+        s.space.nt = n <= s.first ? 1 : 1 + (n - s.first + s.stages - 1) / s.stages;
     }
     return s;
 }
@@ -131,6 +153,19 @@ cudaError_t scan_space(const LinearParams& p, void* workspace, int64_t blocks, c
 
 }  // namespace
 
+bool encode_rows(CUtensorMap* map, const void* base, int32_t dt, int64_t stride, int64_t C, int64_t T, int width, int tokens) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const CUtensorMapDataType type = dt == GDN_DTYPE_F32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : dt == GDN_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                           : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(C), static_cast<cuuint64_t>(T)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride * dtype_bytes(dt))};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(width), static_cast<cuuint32_t>(tokens)}, es[2] = {1, 1};
+    return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int multiprocessors() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
@@ -139,9 +174,10 @@ int multiprocessors() {
 }
 
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream) {
-    if (rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt)) {
-        const int e = static_cast<int>(dtype_bytes(p.x_dt)), ge = static_cast<int>(dtype_bytes(p.gate_dt));
-        linear::Segments seg = segments(p, linear::kColWarps * linear::kRuns * linear::forward_run(e, ge, p.gate_div != 1, p.b != nullptr));
+    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt);
+    if (vec && inputs_wide(p)) {
+        int width, warps;
+        linear::Segments seg = segments(p, &width, &warps);
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         const size_t zeroed = 256 + sizeof(uint32_t) * seg.space.nt * seg.space.blocks;
         const size_t pairs = (zeroed + 255) / 256 * 256;
@@ -153,18 +189,17 @@ cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaSt
             const cudaError_t err = cudaMemsetAsync(ws, 0, zeroed, stream);
             if (err != cudaSuccess) return err;
         }
-        const bool wide = inputs_wide(p);
-        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, wide, stream);
-        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, wide, stream);
-        return launch_linear_column_forward_f32(p, seg, wide, stream);
+        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, width, warps, stream);
+        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, width, warps, stream);
+        return launch_linear_column_forward_f32(p, seg, width, warps, stream);
     }
     linear::ScanSpace s{};
     const cudaError_t e = scan_space(p, workspace, (p.C + linear::kCols - 1) / linear::kCols, stream, &s);
     if (e != cudaSuccess) return e;
     if (p.tile_states) s.known = p.tile_states;
-    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, stream);
-    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, stream);
-    return launch_linear_forward_f32(p, s, stream);
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, vec, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, vec, stream);
+    return launch_linear_forward_f32(p, s, vec, stream);
 }
 
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream) {

@@ -96,6 +96,10 @@ inline ScanLayout scan_layout(int64_t T, int64_t C, int64_t head_dim) {
 
 int multiprocessors();  // of the current device
 
+// A map of T rows of C elements, `stride` elements apart, for boxes of `width` elements of `tokens` rows; what lies
+// outside reads as zeros.
+bool encode_rows(CUtensorMap* map, const void* base, int32_t dt, int64_t stride, int64_t C, int64_t T, int width, int tokens);
+
 // workspace: scan_layout's total bytes
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream);

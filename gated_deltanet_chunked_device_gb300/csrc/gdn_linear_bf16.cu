@@ -3,9 +3,9 @@
 
 namespace gdn {
 
-cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream) {
-    return p.gate_dt == GDN_DTYPE_F32 ? linear::forward_typed<__nv_bfloat16, float>(p, s, stream)
-                                      : linear::forward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, stream);
+cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
+    return p.gate_dt == GDN_DTYPE_F32 ? linear::forward_typed<__nv_bfloat16, float>(p, s, vec, stream)
+                                      : linear::forward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, vec, stream);
 }
 
 cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
@@ -13,12 +13,9 @@ cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::Sca
                                       : linear::backward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream) {
-    if (p.gate_dt == GDN_DTYPE_F32)
-        return wide ? linear::column_forward_typed<__nv_bfloat16, float, true>(p, s, stream)
-                    : linear::column_forward_typed<__nv_bfloat16, float, false>(p, s, stream);
-    return wide ? linear::column_forward_typed<__nv_bfloat16, __nv_bfloat16, true>(p, s, stream)
-                : linear::column_forward_typed<__nv_bfloat16, __nv_bfloat16, false>(p, s, stream);
+cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream) {
+    return p.gate_dt == GDN_DTYPE_F32 ? linear::column_forward_typed<__nv_bfloat16, float>(p, s, width, warps, stream)
+                                      : linear::column_forward_typed<__nv_bfloat16, __nv_bfloat16>(p, s, width, warps, stream);
 }
 
 }  // namespace gdn

@@ -2,15 +2,15 @@
 // channels streamed along the tokens (include/gdn_linear.h), for rows that can
 // be copied 4 elements at a time.  Included by one .cu file for each type of x.
 //
-// A block owns 32 channels and walks the packed tokens, a stage of some 100
+// A block owns 16 channels and walks the packed tokens, a stage of some 100
 // tokens after the other, with the next stages on their way into a ring in
 // shared memory.  The state (forward) or the carry (backward) stays in the
 // block from stage to stage, so nothing is handed from block to block, and the
 // loads never wait for the recurrence.
 //
-// In a stage a thread composes S successive tokens of 4 channels (h_out = A
-// h_in + B, see gdn_linear_scan.cuh), 4 such runs are composed over a warp's
-// lanes, the 8 warps through shared memory; then every thread goes over its
+// In a stage a thread composes 8 successive tokens of 4 channels (h_out = A
+// h_in + B, see gdn_linear_scan.cuh), 8 such runs are composed over a warp's
+// lanes, the warps through shared memory; then every thread goes over its
 // tokens once more from their true state.
 #pragma once
 
@@ -20,18 +20,20 @@
 namespace gdn {
 namespace linear {
 
-constexpr int kColWidth = 32;                    // channels of a block
-constexpr int kLanesRow = kColWidth / 4;         // lanes that hold one token's channels
-constexpr int kRuns = 32 / kLanesRow;            // runs of tokens of a warp
-constexpr int kColWarps = 8;                     // and one more, which finds the sequences' bounds
-constexpr int kColThreads = 32 * (kColWarps + 1);
-constexpr int kRingBytes = 220 * 1024;           // shared memory of the ring, at most
+constexpr int kRun = 8;                          // tokens of a run
 
-// Tokens of a thread's run: 8, or 4 where an element of a token takes more than 6 bytes of the inputs, so that the
-// ring holds four stages or more of either.
-__host__ __device__ constexpr int forward_run(int x_bytes, int gate_bytes, bool head, bool has_b) {
-    return x_bytes + (head ? 0 : has_b ? 2 * gate_bytes : gate_bytes) > 6 ? 4 : 8;
-}
+// A block's shape: W channels, NW warps at work (and one more, which finds the sequences' bounds).
+template <int W, int NW>
+struct Column {
+    static constexpr int kLanesRow = W / 4;      // lanes that hold one token's channels
+    static constexpr int kRuns = 32 / kLanesRow; // runs of tokens of a warp
+    static constexpr int kWarpTokens = kRuns * kRun;
+    static constexpr int kTokens = NW * kWarpTokens;
+    static constexpr int kWarps = NW;
+    static constexpr int kThreads = 32 * (NW + 1);
+    static constexpr int kBlocksSm = NW == 4 ? 2 : 1;
+    static constexpr int kRing = NW == 4 ? 108 * 1024 : 216 * 1024;  // shared memory of the ring, at most
+};
 
 // Two fp32 at a time.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -101,53 +103,28 @@ static __device__ __noinline__ void state_quad_store(void* base, int64_t off, in
     state_store4(base, off, dt, v);
 }
 
-template <int kBytes>
-__device__ __forceinline__ void cp_async(void* dst, const void* src) {
-    if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+// A tiled 2-D copy of a box (channels c, tokens t) to shared memory; completes on `bar` as transaction bytes.
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t c, int32_t t) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+                     smem_u32(dst)),
+                 "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c), "r"(t)
+                 : "memory");
 }
 
-// A stage of one array in shared memory: rows of 32 channels, S rows a run; runs are padded so that the runs of a warp
-// lie in different banks.
-template <class T, int S>
+// A stage of one array in shared memory: rows of W channels.
+template <class T, int W, int kTokens>
 struct StageArray {
-    static constexpr int kRow = kColWidth * static_cast<int>(sizeof(T));
-    static constexpr int kRunBytes = S * kRow + (kRow < 128 ? kRow : 0);
-    static constexpr int kBytes = kColWarps * kRuns * kRunBytes;
+    static constexpr int kRow = W * static_cast<int>(sizeof(T));
+    static constexpr int kBytes = kTokens * kRow;
+    static constexpr int kBox = kTokens < 256 ? kTokens : 256;  // tokens of a box
 
-    // This thread's share of the copy of tokens [t0, t1) (at most a stage); kWide: 16 bytes at a time, else 4 elements.
-    template <bool kWide>
-    static __device__ __forceinline__ void fetch(uint8_t* stage, const T* base, int64_t stride, int64_t t0, int64_t t1, int cols,
-                                                 int tid) {
-        constexpr int kChunk = kWide ? 16 : 4 * static_cast<int>(sizeof(T));
-        constexpr int kPerRow = kRow / kChunk, kElems = kChunk / static_cast<int>(sizeof(T));
-        constexpr int kStep = 32 * kColWarps / kPerRow;  // tokens between a thread's chunks
-        const int part = tid % kPerRow;
-        if (part * kElems >= cols) return;
-        const int tok = tid / kPerRow, n = static_cast<int>(t1 - t0);
-        const T* src = base + (t0 + tok) * stride + part * kElems;
-        uint8_t* dst = stage + tok / S * kRunBytes + tok % S * kRow + part * kChunk;
-        static_assert(kStep % S == 0, "a thread's chunks lie whole runs apart");
-        constexpr int kTimes = kColWarps * kRuns * S / kStep;
-        if (n == kColWarps * kRuns * S) {
+    static __device__ __forceinline__ void fetch(uint8_t* stage, const CUtensorMap* map, uint64_t* bar, int c0, int64_t t0) {
 #pragma unroll
-            for (int i = 0; i < kTimes; ++i) {
-                cp_async<kChunk>(dst + i * (kStep / S) * kRunBytes, src);
-                src += kStep * stride;
-            }
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < kTimes; ++i) {
-                if (tok + i * kStep < n) cp_async<kChunk>(dst + i * (kStep / S) * kRunBytes, src);
-                src += kStep * stride;
-            }
-        }
+        for (int i = 0; i < kTokens / kBox; ++i)
+            tma_load_2d(stage + i * kBox * kRow, map, bar, c0, static_cast<int32_t>(t0) + i * kBox);
     }
-
     static __device__ __forceinline__ Pack<T> get(const uint8_t* stage, int run, int k, int l) {
-        return *reinterpret_cast<const Pack<T>*>(stage + run * kRunBytes + k * kRow + l * 4 * static_cast<int>(sizeof(T)));
+        return *reinterpret_cast<const Pack<T>*>(stage + (run * kRun + k) * kRow + l * 4 * static_cast<int>(sizeof(T)));
     }
 };
 
@@ -160,17 +137,28 @@ struct StageBounds {
     int32_t start_seq[kTokens], end_seq[kTokens];
 };
 
-// Fills the bounds of tokens [t0, t1) (one warp); `lo`: an entry of cu_seqlens such that none before it is at or past
-// t0.  Returns such an entry for tokens from t1 on.  empty(i) is called by the whole warp for every empty sequence.
-template <int kTokens, class Empty>
-__device__ __forceinline__ int64_t stage_bounds(const LinearParams& p, int64_t lo, int64_t t0, int64_t t1, bool last, int lane,
-                                                StageBounds<kTokens>& b, Empty empty) {
-#pragma unroll
-    for (int w = 0; w < kTokens / 32; ++w)
-        if (lane == 0) b.starts[w] = b.ends[w] = 0;
+// Where a walk over cu_seqlens has got to: no entry before `lo` is at or past the tokens to come; entry `lo` is `next`.
+struct Cursor {
+    int64_t lo, next;
+};
+
+// Fills the bounds of tokens [t0, t1) (one warp) and moves the cursor on to t1.  empty(i) is called by the whole warp for
+// every empty sequence.  Entries are taken as they are: a malformed cu_seqlens gives wrong bounds, none outside.
+template <int kTokens, int kWarpTokens, class Empty>
+__device__ __forceinline__ void stage_bounds(const LinearParams& p, Cursor& cur, int64_t t0, int64_t t1, bool last, int lane,
+                                             StageBounds<kTokens>& b, Empty empty) {
+    constexpr uint32_t kAll = (1u << (kTokens / kWarpTokens)) - 1u;
+    if (cur.next > t1 && t1 == t0 + kTokens) {  // most stages
+        if (lane == 0) {
+            b.warps = 0;
+            b.plain = kAll;
+        }
+        return;
+    }
+    if (lane < kTokens / 32) b.starts[lane] = b.ends[lane] = 0;
     __syncwarp();
-    int64_t next_lo = lo;
-    for (;; lo += 32) {
+    int64_t moved = cur.lo;
+    for (int64_t lo = cur.lo;; lo += 32) {
         const int64_t i = lo + lane;
         const int64_t c = i <= p.N ? cu_at(p, i) : t1 + 1;
         const int64_t next = i < p.N ? cu_at(p, i + 1) : c, prev = i > 0 && i <= p.N ? cu_at(p, i - 1) : c;
@@ -185,25 +173,25 @@ __device__ __forceinline__ int64_t stage_bounds(const LinearParams& p, int64_t l
             b.end_seq[c - 1 - t0] = static_cast<int32_t>(i - 1);
             atomicOr(&b.ends[(c - 1 - t0) / 32], 1u << ((c - 1 - t0) % 32));
         }
-        next_lo += __popc(__ballot_sync(0xffffffffu, i <= p.N && c < t1));
+        moved += __popc(__ballot_sync(0xffffffffu, i <= p.N && c < t1));
         for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(lo + __ffs(m) - 1);
         if (__any_sync(0xffffffffu, c > t1)) break;
     }
+    cur.lo = moved;
+    cur.next = moved <= p.N ? cu_at(p, moved) : INT64_MAX;
     __syncwarp();
-    constexpr int kWarpTokens = kTokens / kColWarps;
     uint32_t s = 0, e = 0;
-    if (lane < kColWarps) {
-        constexpr uint32_t kMask = kWarpTokens == 32 ? 0xffffffffu : (1u << (kWarpTokens % 32)) - 1u;
-        s = (b.starts[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
-        e = (b.ends[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
+    if (lane < kTokens / kWarpTokens) {
+        static_assert(kWarpTokens == 32 || kWarpTokens == 64, "one word of bounds a warp, or two");
+        s = kWarpTokens == 32 ? b.starts[lane] : b.starts[2 * lane] | b.starts[2 * lane + 1];
+        e = kWarpTokens == 32 ? b.ends[lane] : b.ends[2 * lane] | b.ends[2 * lane + 1];
     }
     const uint32_t warps = __ballot_sync(0xffffffffu, s != 0);
     const uint32_t plain = __ballot_sync(0xffffffffu, (s | e) == 0 && t0 + (lane + 1) * kWarpTokens <= t1);
     if (lane == 0) {
         b.warps = warps;
-        b.plain = plain;
+        b.plain = plain & kAll;
     }
-    return next_lo;
 }
 
 // First entry of cu_seqlens[0 .. n) that is not below t0 (n: none), by 32 probes at a time (one warp).
@@ -220,18 +208,15 @@ __device__ __forceinline__ int64_t first_entry(const LinearParams& p, int64_t n,
     return lo;
 }
 
-// Whether a run (8 bits or fewer of a word) holds one of the bounds.
-template <int S>
-__device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
-    return (words[run * S / 32] >> (run * S % 32)) & ((S == 32 ? 0u : (1u << S)) - 1u);
-}
+// A run's bounds, a bit a token.
+__device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) { return (words[run / 4] >> (run % 4 * 8)) & 0xffu; }
 
-// Of a warp's runs, which hold a bound: one bit each.
-template <int S>
+// Which of a warp's runs hold a bound, a bit a run.
+template <int kRuns>
 __device__ __forceinline__ uint32_t runs_with(const uint32_t* words, int warp) {
     uint32_t r = 0;
 #pragma unroll
-    for (int i = 0; i < kRuns; ++i) r |= (run_bits<S>(words, warp * kRuns + i) ? 1u : 0u) << i;
+    for (int i = 0; i < kRuns; ++i) r |= (run_bits(words, warp * kRuns + i) ? 1u : 0u) << i;
     return r;
 }
 
@@ -243,138 +228,174 @@ __device__ __forceinline__ bool is_last_bit(const uint32_t* words, int at) {
     return after == 0;
 }
 
-// Time segments of a column, where there are too few columns for the GPU's SMs.  The first one is twice as long as the
-// others, which go over their tokens twice: once to learn what they do to a state, and, when the state that enters is
-// known, once more (from L2, mostly).
+// Time segments of a column, where there are too few columns for the GPU's SMs.  Segments after the first go over their
+// tokens twice: once to learn what they do to a state, and, when the state that enters is known, once more (from L2,
+// mostly).
 struct Segments {
     ScanSpace space;               // nt = segments; flags [blocks][nt]
-    int32_t stages;                // stages of a segment but the first
+    int32_t first, stages;         // stages of the first segment, and of the others
 };
 
-template <class X, class G, bool kHead, bool kHasB>
+// Maps of the inputs for tiled copies; a's and b's with gates per channel only.
+struct ColumnMaps {
+    CUtensorMap x, a, b;
+};
+
+// How gates are found: per channel, one head for the block's channels (the head's channels are a multiple of its), or
+// any heads (4 channels of a lane share one).
+enum Gates { kPerChannel, kOneHead, kAnyHead };
+
+template <class X, class G, int kGates, bool kHasB, class Col>
 struct ForwardShape {
-    static constexpr int kArrays = kHead ? 0 : (kHasB ? 2 : 1);
-    static constexpr int S = forward_run(sizeof(X), sizeof(G), kHead, kHasB);
-    static constexpr int kTokens = kColWarps * kRuns * S;
-    static constexpr int kStageBytes = StageArray<X, S>::kBytes + kArrays * StageArray<G, S>::kBytes;
-    static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
+    static constexpr int W = Col::kLanesRow * 4, kTokens = Col::kTokens;
+    using AX = StageArray<X, W, kTokens>;
+    using AG = StageArray<G, W, kTokens>;
+    static constexpr int kStageBytes = AX::kBytes + (kGates != kPerChannel ? 0 : kHasB ? 2 : 1) * AG::kBytes;
+    static constexpr int kDepth = Col::kRing / kStageBytes < 4 ? Col::kRing / kStageBytes : 4;
     struct Tables {
         StageBounds<kTokens> bounds[2];
-        float2 pairs[kColWarps][kColWidth];
-        float enter[kColWidth];
-        alignas(16) float kept[kColWidth];  // initial state of the last sequence that starts in the segment
-        int64_t kept_at;                    // its first token
+        float2 pairs[Col::kWarps][W];
+        alignas(16) float2 gates[kGates == kOneHead ? kTokens : 1];
+        float enter[W];
+        alignas(16) float kept[W];  // initial state of the last sequence that starts in the segment
+        int64_t kept_at;            // its first token
+        uint64_t full[kDepth];      // a stage's inputs have come
         uint32_t ticket;
     };
     static constexpr int kSmem = kDepth * kStageBytes + static_cast<int>(sizeof(Tables));
+    static_assert(kDepth >= 2, "the next stage comes while one is worked on");
 };
 
-template <class X, class G, bool kWide, bool kHead, bool kHasB>
-__global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kernel(const LinearParams p, const Segments seg) {
-    using Shape = ForwardShape<X, G, kHead, kHasB>;
-    using AX = StageArray<X, Shape::S>;
-    using AG = StageArray<G, Shape::S>;
-    constexpr int S = Shape::S, kTokens = Shape::kTokens, kDepth = Shape::kDepth;
-    extern __shared__ __align__(128) uint8_t ring[];
+template <class X, class G, int kGates, bool kHasB, class Col>
+__global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
+    gdn_linear_column_forward_kernel(const LinearParams p, const Segments seg, const __grid_constant__ ColumnMaps maps) {
+    using Shape = ForwardShape<X, G, kGates, kHasB, Col>;
+    using AX = typename Shape::AX;
+    using AG = typename Shape::AG;
+    constexpr int W = Shape::W, kTokens = Shape::kTokens, kDepth = Shape::kDepth, kRuns = Col::kRuns, kLanesRow = Col::kLanesRow;
+    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens;
+    // With two stages the next fetch waits until the oldest stage's inputs are in registers; with more, a stage is free at
+    // the step's start already.
+    constexpr bool kLate = kDepth == 2;
+    extern __shared__ __align__(1024) uint8_t ring[];
     typename Shape::Tables& sm = *reinterpret_cast<typename Shape::Tables*>(ring + kDepth * Shape::kStageBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int sub = lane / kLanesRow, l = lane % kLanesRow, run = warp * kRuns + sub;
+    const int sub = lane / kLanesRow, l = lane % kLanesRow, run = warp * kRuns + sub, ch = lane % W;
     const ScanSpace& sp = seg.space;
-    uint32_t ticket = blockIdx.x;
-    if (sp.nt > 1) {
-        if (threadIdx.x == 0) sm.ticket = atomicAdd(sp.ticket, 1u);
-        __syncthreads();
-        ticket = sm.ticket;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kDepth; ++i) mbar_init(&sm.full[i], 1);
+        fence_mbar_init();
+        sm.kept_at = -1;
+        if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
+    __syncthreads();
+    const uint32_t ticket = sp.nt > 1 ? sm.ticket : blockIdx.x;
     const int64_t part = ticket / sp.blocks;
     const uint32_t blk = ticket % sp.blocks;
-    const int c0 = static_cast<int>(blk) * kColWidth, cols = min(kColWidth, p.C - c0);
-    const int64_t each = seg.stages * static_cast<int64_t>(kTokens);
-    const int64_t from = part == 0 ? 0 : (part + 1) * each, end = part == sp.nt - 1 ? p.T : (part + 2) * each;
+    const int c0 = static_cast<int>(blk) * W, cols = min(W, p.C - c0);
+    const int64_t from = part == 0 ? 0 : (seg.first + (part - 1) * seg.stages) * static_cast<int64_t>(kTokens);
+    const int64_t end = part == sp.nt - 1 ? p.T : (seg.first + part * seg.stages) * static_cast<int64_t>(kTokens);
     const int stages = static_cast<int>(max(static_cast<int64_t>(1), (end - from + kTokens - 1) / kTokens));
     // A later segment learns what it does to a state in steps 0 .. stages - 1.
     const bool twice = part > 0;
-    const int steps = twice ? 2 * stages : stages;
+    const int steps = p.T == 0 ? 0 : twice ? 2 * stages : stages;
     const bool on = l * 4 < cols;
 
-    const X* x = static_cast<const X*>(p.x) + c0;
-    const G* ga = static_cast<const G*>(p.a) + (kHead ? (c0 + (on ? l * 4 : 0)) / p.D : c0);
-    const G* gb = kHasB ? static_cast<const G*>(p.b) + (kHead ? (c0 + (on ? l * 4 : 0)) / p.D : c0) : nullptr;
+    const int head = kGates == kPerChannel ? c0 : (c0 + (kGates == kAnyHead && on ? l * 4 : 0)) / p.D;
+    const G* ga = static_cast<const G*>(p.a) + head;
+    const G* gb = kHasB ? static_cast<const G*>(p.b) + head : nullptr;
     auto stage_start = [&](int q) { return from + static_cast<int64_t>(q < stages ? q : q - stages) * kTokens; };
-    auto fetch = [&](int q) {
-        if (q < steps) {
-            uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
-            const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, end);
-            AX::template fetch<kWide>(stage, x, p.x_stride, t0, t1, cols, threadIdx.x);
-            if constexpr (!kHead) {
-                AG::template fetch<kWide>(stage + AX::kBytes, ga, p.a_stride, t0, t1, cols, threadIdx.x);
-                if constexpr (kHasB) AG::template fetch<kWide>(stage + AX::kBytes + AG::kBytes, gb, p.b_stride, t0, t1, cols, threadIdx.x);
-            }
-        }
-        cp_async_commit();
-    };
-    // gates per head: a thread's own, one stage ahead in registers
-    G ha[kHead ? S : 1], hb[kHead ? S : 1];
-    auto fetch_gates = [&](int q) {
-        if constexpr (kHead) {
-            if (q >= steps) return;
-            const int64_t t = stage_start(q) + run * S;
-#pragma unroll
-            for (int k = 0; k < S; ++k) {
-                if (t + k >= end) continue;
-                ha[k] = ga[(t + k) * p.a_stride];
-                if constexpr (kHasB) hb[k] = gb[(t + k) * p.b_stride];
-            }
-        }
-    };
-    int64_t lo = 0;
-    auto bounds = [&](int q) {
+    auto fetch = [&](int q) {  // one thread
         if (q >= steps) return;
+        uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        uint64_t* bar = &sm.full[q % kDepth];
+        const int64_t t0 = stage_start(q);
+        mbar_arrive_expect_tx(bar, Shape::kStageBytes);
+        AX::fetch(stage, &maps.x, bar, c0, t0);
+        if constexpr (kGates == kPerChannel) {
+            AG::fetch(stage + AX::kBytes, &maps.a, bar, c0, t0);
+            if constexpr (kHasB) AG::fetch(stage + AX::kBytes + AG::kBytes, &maps.b, bar, c0, t0);
+        }
+    };
+    // Gates per head are on their way one step ahead in registers: of two tokens a lane (one head for the block: the
+    // warp shares them through shared memory), or of the lane's own run.
+    constexpr int kHeld = kGates == kPerChannel ? 1 : kGates == kOneHead ? 2 : kRun;
+    G ha[kHeld], hb[kHeld];
+    auto fetch_gates = [&](int q) {
+        if constexpr (kGates != kPerChannel) {
+            if (q >= steps) return;
+            const int64_t t = stage_start(q) + (kGates == kOneHead ? warp * kWarpTokens + lane : run * kRun);
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                const int64_t tk = t + (kGates == kOneHead ? 32 * k : k);
+                if (tk >= end) continue;
+                ha[k] = ga[tk * p.a_stride];
+                if constexpr (kHasB) hb[k] = gb[tk * p.b_stride];
+            }
+        }
+    };
+    Cursor cur{0, 0};
+    auto bounds = [&](int q) {
+        if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, end);
-        if (q == 0 || q == stages) lo = from == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
+        if (q == 0 || q == stages) cur = {from == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane), 0};
         const bool write = q >= steps - stages;
-        lo = stage_bounds<kTokens>(p, lo, t0, t1, t1 == p.T, lane, sm.bounds[q & 1], [&](int64_t i) {
+        stage_bounds<kTokens, kWarpTokens>(p, cur, t0, t1, t1 == p.T, lane, sm.bounds[q & 1], [&](int64_t i) {
             // an empty sequence's final state is its initial one
             if (!write || !p.output_state || p.output_state == p.initial_state) return;
             const int64_t row = state_row(p, i);
             if (row < 0 || lane * 4 >= cols) return;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
-            if (p.initial_state) state_load<true>(p.initial_state, row * p.state_stride + c0, p.state_dt, lane, cols, v);
-            state_store<true>(p.output_state, row * p.state_stride + c0, p.state_dt, lane, cols, v);
+            const int64_t off = row * p.state_stride + c0 + lane * 4;
+            state_quad_store(p.output_state, off, p.state_dt,
+                             p.initial_state ? state_quad_load(p.initial_state, off, p.state_dt) : make_float4(0.f, 0.f, 0.f, 0.f));
         });
     };
 
     if (warp < kColWarps) {
-        for (int q = 0; q < kDepth - 1; ++q) fetch(q);
+        if (threadIdx.x == 0)
+            for (int q = 0; q < (kLate ? kDepth : kDepth - 1); ++q) fetch(q);
         fetch_gates(0);
     } else {
         bounds(0);
         if (blk == 0) check_bounds(p, part, sp.nt, lane);
     }
-    if (threadIdx.x == 0) sm.kept_at = -1;
-    float carry = 0.f, through = 1.f;  // of channel `lane`: the state (in steps that learn, from zero), the gates' product
+    bool ok = true;                    // until a wait runs out
+    float carry = 0.f, through = 1.f;  // of channel `ch`: the state (in steps that learn, from zero), the gates' product
     bool reset = false;                // whether a sequence has started
     X* y = static_cast<X*>(p.y) + c0 + l * 4;
     for (int q = 0; q < steps; ++q) {
-        cp_async_wait<kDepth - 2>();
         __syncthreads();
         const StageBounds<kTokens>& bd = sm.bounds[q & 1];
         const bool learn = twice && q < stages;
-        const int64_t t0 = stage_start(q), t = t0 + run * S;
-        const int n = static_cast<int>(min(static_cast<int64_t>(S), max(static_cast<int64_t>(0), end - t)));
+        const int64_t t = stage_start(q) + run * kRun;
         const bool plain = (bd.plain >> (warp % kColWarps)) & 1;
-        Quad a[S], u[S], A = all4(1.f), B = all4(0.f), exA, exB;
+        Quad a[kRun], u[kRun], A, B, exA, exB;
         uint32_t starts = 0;
+        int n = kRun;
         bool before = false;  // whether a sequence starts in the warp's runs before this one
         if (warp == kColWarps) {
-            bounds(q + 1);
+            bounds(q + 1);  // beside the others, up to the next step
         } else {
-            fetch(q + kDepth - 1);
+            if (!kLate && threadIdx.x == 0) fetch(q + kDepth - 1);
+            if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
+                ok = false;
+                report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+            }
             const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+            if constexpr (kGates == kOneHead) {
 #pragma unroll
-            for (int k = 0; k < S; ++k) {
+                for (int k = 0; k < 2; ++k)
+                    sm.gates[warp * kWarpTokens + 32 * k + lane] = make_float2(to_f32(ha[k]), kHasB ? to_f32(hb[k]) : 1.f);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
                 u[k] = widen(AX::get(stage, run, k, l));
-                if constexpr (kHead) {
+                if constexpr (kGates == kOneHead) {
+                    const float2 g = sm.gates[run * kRun + k];
+                    a[k] = all4(g.x);
+                    if constexpr (kHasB) u[k] = mul(u[k], all4(g.y));
+                } else if constexpr (kGates == kAnyHead) {
                     a[k] = all4(to_f32(ha[k]));
                     if constexpr (kHasB) u[k] = mul(u[k], all4(to_f32(hb[k])));
                 } else {
@@ -387,21 +408,24 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
                 A = a[0];
                 B = u[0];
 #pragma unroll
-                for (int k = 1; k < S; ++k) {
+                for (int k = 1; k < kRun; ++k) {
                     A = mul(A, a[k]);
                     B = fma(a[k], B, u[k]);
                 }
             } else {
-                starts = run_bits<S>(bd.starts, run);
+                n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
+                starts = run_bits(bd.starts, run);
+                A = all4(1.f);
+                B = all4(0.f);
 #pragma unroll
-                for (int k = 0; k < S; ++k) {
+                for (int k = 0; k < kRun; ++k) {
                     if (k >= n) {
                         a[k] = all4(1.f);
                         u[k] = all4(0.f);
                     }
                     if ((starts >> k) & 1) {
                         if (p.initial_state && on) {
-                            const int64_t row = state_row(p, bd.start_seq[run * S + k]);
+                            const int64_t row = state_row(p, bd.start_seq[run * kRun + k]);
                             // With states in place, a later segment may have written the row of a sequence that starts
                             // here by the time of the second pass: the last one to start, if any.  Its state is kept.
                             float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -409,7 +433,7 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
                                 h0 = *reinterpret_cast<const float4*>(&sm.kept[l * 4]);
                             else if (row >= 0)
                                 h0 = state_quad_load(p.initial_state, row * p.state_stride + c0 + l * 4, p.state_dt);
-                            if (learn && is_last_bit<kTokens>(bd.starts, run * S + k)) {
+                            if (learn && is_last_bit<kTokens>(bd.starts, run * kRun + k)) {
                                 *reinterpret_cast<float4*>(&sm.kept[l * 4]) = h0;
                                 sm.kept_at = t + k;
                             }
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
                 }
             }
             // over the warp's runs
-            const uint32_t rs = (bd.warps >> warp) & 1 ? runs_with<S>(bd.starts, warp) : 0;
+            const uint32_t rs = (bd.warps >> warp) & 1 ? runs_with<kRuns>(bd.starts, warp) : 0;
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
                 const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
@@ -446,12 +470,13 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
                 o[1] = make_float4(A.hi.x, B.hi.x, A.hi.y, B.hi.y);
             }
         }
-        __syncthreads();
         float enter = carry;
         if (warp < kColWarps) {
+            named_bar_sync(1, 32 * kColWarps);
+            if (kLate && threadIdx.x == 0) fetch(q + kDepth);
 #pragma unroll
             for (int w = 0; w < kColWarps; ++w) {
-                const float2 ab = sm.pairs[w][lane];
+                const float2 ab = sm.pairs[w][ch];
                 if (w == warp) enter = carry;
                 carry = (bd.warps >> w) & 1 ? ab.y : fmaf(ab.x, carry, ab.y);
                 if (learn) through *= ab.x;
@@ -478,10 +503,10 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
                     if (lane < cols) sp.known[part * p.C + c] = fmaf(through, h, carry);
                     publish(flags + part, kKnown, lane);
                 }
-                sm.enter[lane] = h;
+                if (lane < W) sm.enter[lane] = h;
             }
             __syncthreads();
-            carry = sm.enter[lane];
+            carry = sm.enter[ch];
             continue;
         }
         if (warp < kColWarps) {
@@ -492,23 +517,23 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
             X* out = y + t * p.y_stride;
             if (plain) {
 #pragma unroll
-                for (int k = 0; k < S; ++k) {
+                for (int k = 0; k < kRun; ++k) {
                     h = fma(a[k], h, u[k]);
                     store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
                     out += p.y_stride;
                 }
-                if (p.tile_states && (t + S) % kTile == 0)
+                if (p.tile_states && (t + kRun) % kTile == 0)
                     *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
             } else {
-                const uint32_t ends = run_bits<S>(bd.ends, run);
+                const uint32_t ends = run_bits(bd.ends, run);
 #pragma unroll
-                for (int k = 0; k < S; ++k) {
+                for (int k = 0; k < kRun; ++k) {
                     if (k >= n) break;
                     h = pick((starts >> k) & 1, u[k], fma(a[k], h, u[k]));
                     store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
                     out += p.y_stride;
                     if (((ends >> k) & 1) && p.output_state) {
-                        const int64_t row = state_row(p, bd.end_seq[run * S + k]);
+                        const int64_t row = state_row(p, bd.end_seq[run * kRun + k]);
                         if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
                     }
                     if (p.tile_states && ((t + k) % kTile == kTile - 1 || t + k == p.T - 1))
@@ -523,23 +548,40 @@ __global__ void __launch_bounds__(kColThreads, 1) gdn_linear_column_forward_kern
     }
 }
 
-template <class X, class G, bool kWide, bool kHead, bool kHasB>
+template <class X, class G, int kGates, bool kHasB, class Col>
 cudaError_t launch_column_forward(const LinearParams& p, const Segments& seg, cudaStream_t stream) {
-    constexpr int kSmem = ForwardShape<X, G, kHead, kHasB>::kSmem;
-    auto kernel = gdn_linear_column_forward_kernel<X, G, kWide, kHead, kHasB>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    using Shape = ForwardShape<X, G, kGates, kHasB, Col>;
+    ColumnMaps maps{};
+    bool ok = p.T == 0 || encode_rows(&maps.x, p.x, p.x_dt, p.x_stride, p.C, p.T, Shape::W, Shape::AX::kBox);
+    if (kGates == kPerChannel && p.T > 0) {
+        ok = ok && encode_rows(&maps.a, p.a, p.gate_dt, p.a_stride, p.C, p.T, Shape::W, Shape::AG::kBox);
+        if (kHasB) ok = ok && encode_rows(&maps.b, p.b, p.gate_dt, p.b_stride, p.C, p.T, Shape::W, Shape::AG::kBox);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    auto kernel = gdn_linear_column_forward_kernel<X, G, kGates, kHasB, Col>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
     if (e != cudaSuccess) return e;
-    kernel<<<static_cast<unsigned>(seg.space.nt * seg.space.blocks), kColThreads, kSmem, stream>>>(p, seg);
+    kernel<<<static_cast<unsigned>(seg.space.nt * seg.space.blocks), Col::kThreads, Shape::kSmem, stream>>>(p, seg, maps);
     return cudaGetLastError();
 }
 
-template <class X, class G, bool kWide>
-cudaError_t column_forward_typed(const LinearParams& p, const Segments& seg, cudaStream_t stream) {
-    if (p.gate_div != 1)
-        return p.b ? launch_column_forward<X, G, kWide, true, true>(p, seg, stream)
-                   : launch_column_forward<X, G, kWide, true, false>(p, seg, stream);
-    return p.b ? launch_column_forward<X, G, kWide, false, true>(p, seg, stream)
-               : launch_column_forward<X, G, kWide, false, false>(p, seg, stream);
+template <class X, class G, int kGates>
+cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int W, int warps, cudaStream_t stream) {
+    if (W == 32)
+        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, 8>>(p, seg, stream)
+                   : launch_column_forward<X, G, kGates, false, Column<32, 8>>(p, seg, stream);
+    if (warps == 4)
+        return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 4>>(p, seg, stream)
+                   : launch_column_forward<X, G, kGates, false, Column<16, 4>>(p, seg, stream);
+    return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 8>>(p, seg, stream)
+               : launch_column_forward<X, G, kGates, false, Column<16, 8>>(p, seg, stream);
+}
+
+template <class X, class G>
+cudaError_t column_forward_typed(const LinearParams& p, const Segments& seg, int W, int warps, cudaStream_t stream) {
+    if (p.gate_div == 1) return column_forward_gates<X, G, kPerChannel>(p, seg, W, warps, stream);
+    if (p.D % W == 0) return column_forward_gates<X, G, kOneHead>(p, seg, W, warps, stream);
+    return column_forward_gates<X, G, kAnyHead>(p, seg, W, warps, stream);
 }
 
 }  // namespace linear

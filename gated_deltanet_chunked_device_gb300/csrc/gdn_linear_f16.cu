@@ -3,9 +3,9 @@
 
 namespace gdn {
 
-cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream) {
-    return p.gate_dt == GDN_DTYPE_F32 ? linear::forward_typed<__half, float>(p, s, stream)
-                                      : linear::forward_typed<__half, __half>(p, s, stream);
+cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
+    return p.gate_dt == GDN_DTYPE_F32 ? linear::forward_typed<__half, float>(p, s, vec, stream)
+                                      : linear::forward_typed<__half, __half>(p, s, vec, stream);
 }
 
 cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
@@ -13,12 +13,9 @@ cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::Scan
                                       : linear::backward_typed<__half, __half>(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, bool wide, cudaStream_t stream) {
-    if (p.gate_dt == GDN_DTYPE_F32)
-        return wide ? linear::column_forward_typed<__half, float, true>(p, s, stream)
-                    : linear::column_forward_typed<__half, float, false>(p, s, stream);
-    return wide ? linear::column_forward_typed<__half, __half, true>(p, s, stream)
-                : linear::column_forward_typed<__half, __half, false>(p, s, stream);
+cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream) {
+    return p.gate_dt == GDN_DTYPE_F32 ? linear::column_forward_typed<__half, float>(p, s, width, warps, stream)
+                                      : linear::column_forward_typed<__half, __half>(p, s, width, warps, stream);
 }
 
 }  // namespace gdn

@@ -3,16 +3,16 @@
 
 namespace gdn {
 
-cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, cudaStream_t stream) {
-    return linear::forward_typed<float, float>(p, s, stream);
+cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
+    return linear::forward_typed<float, float>(p, s, vec, stream);
 }
 
 cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
     return linear::backward_typed<float, float>(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, bool, cudaStream_t stream) {
-    return linear::column_forward_typed<float, float, true>(p, s, stream);  // 4 elements are 16 bytes
+cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream) {
+    return linear::column_forward_typed<float, float>(p, s, width, warps, stream);
 }
 
 }  // namespace gdn

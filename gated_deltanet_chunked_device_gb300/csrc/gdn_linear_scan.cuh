@@ -810,10 +810,11 @@ cudaError_t forward_gates(const LinearParams& p, const ScanSpace& s, cudaStream_
     return cudaGetLastError();
 }
 
-// Rows that allow no loads of 4 elements (gdn_linear_column.cuh has the others).
 template <class X, class G>
-cudaError_t forward_typed(const LinearParams& p, const ScanSpace& s, cudaStream_t stream) {
-    return p.gate_div != 1 ? forward_gates<X, G, false, true>(p, s, stream) : forward_gates<X, G, false, false>(p, s, stream);
+cudaError_t forward_typed(const LinearParams& p, const ScanSpace& s, bool vec, cudaStream_t stream) {
+    const bool head = p.gate_div != 1;
+    if (vec) return head ? forward_gates<X, G, true, true>(p, s, stream) : forward_gates<X, G, true, false>(p, s, stream);
+    return head ? forward_gates<X, G, false, true>(p, s, stream) : forward_gates<X, G, false, false>(p, s, stream);
 }
 
 }  // namespace linear
