@@ -5,7 +5,6 @@
 // One block of 128 threads per (sequence, head); a thread owns every 128th
 // channel of the head and walks the sequence's tokens.  Right for every case,
 // and as slow as the longest sequence.
-#include <cstdlib>
 #include <cudaTypedefs.h>
 
 #include "gdn_linear_column.cuh"
@@ -13,11 +12,11 @@
 namespace gdn {
 
 cudaError_t launch_linear_forward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_bf16(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_forward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
-cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream);
+cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
@@ -114,25 +113,21 @@ bool inputs_wide(const LinearParams& p) {
     return x && vector_of_16_bytes(p.a, p.a_stride, p.gate_dt, p.C) && vector_of_16_bytes(p.b, p.b_stride, p.gate_dt, p.C);
 }
 
-// Shape and time segments of the columns.
-linear::Segments segments(const LinearParams& p, int* width, int* warps) {
+// Width and time segments of the columns.
+linear::Segments segments(const LinearParams& p, int* width) {
+    const int64_t sms = multiprocessors(), blocks32 = (p.C + 31) / 32;
+    int64_t segs = sms / blocks32;
+    *width = 5 * blocks32 < 3 * sms && segs < 3 ? 16 : 32;
     linear::Segments s{};
-    const char* ew = getenv("LC");
-    const char* ev = getenv("LW");
-    const char* es = getenv("LS");
-    *width = ew ? atoi(ew) : 32;
-    *warps = ev ? atoi(ev) : 8;
-    const int64_t blocks = (p.C + *width - 1) / *width, sms = multiprocessors();
-    int64_t segs = (*warps == 4 ? 2 : 1) * sms / blocks;
-    if (es) segs = atoi(es);
-    const int64_t tokens = *warps * 1024 / *width, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
+    const int64_t tokens = 8 * 1024 / *width, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
     if (segs > n / 2) segs = n / 2;
-    s.space.blocks = static_cast<uint32_t>(blocks);
+    s.space.blocks = static_cast<uint32_t>((p.C + *width - 1) / *width);
     s.space.nt = 1;
     s.first = s.stages = static_cast<int32_t>(n);
-    if (segs >= 3) {
-        s.stages = static_cast<int32_t>((n * 10 + 10 * segs - 5) / (10 * segs - 4));
-        s.first = static_cast<int32_t>((s.stages * 6 + 9) / 10);
+    if (segs >= 3 && *width == 32) {
+        // first + (segs - 1) stages = n, the first one six tenths of another
+        s.stages = static_cast<int32_t>((10 * n + 10 * segs - 5) / (10 * segs - 4));
+        s.first = static_cast<int32_t>((6 * s.stages + 9) / 10);
         s.space.nt = n <= s.first ? 1 : 1 + (n - s.first + s.stages - 1) / s.stages;
     }
     return s;
@@ -174,10 +169,10 @@ int multiprocessors() {
 }
 
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream) {
-    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt);
+    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
     if (vec && inputs_wide(p)) {
-        int width, warps;
-        linear::Segments seg = segments(p, &width, &warps);
+        int width;
+        linear::Segments seg = segments(p, &width);
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         const size_t zeroed = 256 + sizeof(uint32_t) * seg.space.nt * seg.space.blocks;
         const size_t pairs = (zeroed + 255) / 256 * 256;
@@ -189,9 +184,9 @@ cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaSt
             const cudaError_t err = cudaMemsetAsync(ws, 0, zeroed, stream);
             if (err != cudaSuccess) return err;
         }
-        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, width, warps, stream);
-        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, width, warps, stream);
-        return launch_linear_column_forward_f32(p, seg, width, warps, stream);
+        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, width, stream);
+        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, width, stream);
+        return launch_linear_column_forward_f32(p, seg, width, stream);
     }
     linear::ScanSpace s{};
     const cudaError_t e = scan_space(p, workspace, (p.C + linear::kCols - 1) / linear::kCols, stream, &s);

@@ -14,26 +14,27 @@
 // tokens once more from their true state.
 #pragma once
 
+#include <type_traits>
+
 #include "gdn_linear_scan.cuh"
 #include "sm103_ptx.cuh"
 
 namespace gdn {
 namespace linear {
 
-constexpr int kRun = 8;                          // tokens of a run
-
-// A block's shape: W channels, NW warps at work (and one more, which finds the sequences' bounds).
-template <int W, int NW>
+// A block's shape: W channels, NW warps at work (and one more, which finds the sequences' bounds), runs of R tokens.
+template <int W, int NW, int R>
 struct Column {
+    static constexpr int kWidth = W, kRun = R;
     static constexpr int kLanesRow = W / 4;      // lanes that hold one token's channels
     static constexpr int kRuns = 32 / kLanesRow; // runs of tokens of a warp
     static constexpr int kWarpTokens = kRuns * kRun;
     static constexpr int kTokens = NW * kWarpTokens;
     static constexpr int kWarps = NW;
     static constexpr int kThreads = 32 * (NW + 1);
-    static constexpr int kBlocksSm = NW == 4 ? 2 : 1;
-    static constexpr int kRing = NW == 4 ? 108 * 1024 : 216 * 1024;  // shared memory of the ring, at most
 };
+
+constexpr int kRingBytes = 216 * 1024;           // shared memory of the ring, at most
 
 // Two fp32 at a time.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -67,6 +68,13 @@ __device__ __forceinline__ Quad quad(float4 v) { return {{v.x, v.y}, {v.z, v.w}}
 __device__ __forceinline__ float4 flat(Quad v) { return make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y); }
 __device__ __forceinline__ Quad pick(bool c, Quad a, Quad b) {
     return {{c ? a.lo.x : b.lo.x, c ? a.lo.y : b.lo.y}, {c ? a.hi.x : b.hi.x, c ? a.hi.y : b.hi.y}};
+}
+__device__ __forceinline__ Quad add(Quad a, Quad b) {
+    return {{a.lo.x + b.lo.x, a.lo.y + b.lo.y}, {a.hi.x + b.hi.x, a.hi.y + b.hi.y}};
+}
+__device__ __forceinline__ Quad shift_down(Quad v, int lanes) {
+    return {{__shfl_down_sync(0xffffffffu, v.lo.x, lanes), __shfl_down_sync(0xffffffffu, v.lo.y, lanes)},
+            {__shfl_down_sync(0xffffffffu, v.hi.x, lanes), __shfl_down_sync(0xffffffffu, v.hi.y, lanes)}};
 }
 __device__ __forceinline__ Quad shift_up(Quad v, int lanes) {
     return {{__shfl_up_sync(0xffffffffu, v.lo.x, lanes), __shfl_up_sync(0xffffffffu, v.lo.y, lanes)},
@@ -112,8 +120,9 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
 }
 
 // A stage of one array in shared memory: rows of W channels.
-template <class T, int W, int kTokens>
+template <class T, class Col>
 struct StageArray {
+    static constexpr int W = Col::kWidth, kTokens = Col::kTokens, kRun = Col::kRun;
     static constexpr int kRow = W * static_cast<int>(sizeof(T));
     static constexpr int kBytes = kTokens * kRow;
     static constexpr int kBox = kTokens < 256 ? kTokens : 256;  // tokens of a box
@@ -128,37 +137,43 @@ struct StageArray {
     }
 };
 
+// A stage of gates per head: the 16 bytes of each token's gates that hold the block's head.
+template <class T, class Col>
+struct StageGates {
+    static constexpr int kTokens = Col::kTokens;
+    static constexpr int kHeads = 16 / static_cast<int>(sizeof(T));
+    static constexpr int kBytes = kTokens * 16;
+    static constexpr int kBox = kTokens < 256 ? kTokens : 256;
+
+    static __device__ __forceinline__ void fetch(uint8_t* stage, const CUtensorMap* map, uint64_t* bar, int head, int64_t t0) {
+#pragma unroll
+        for (int i = 0; i < kTokens / kBox; ++i)
+            tma_load_2d(stage + i * kBox * 16, map, bar, head / kHeads * kHeads, static_cast<int32_t>(t0) + i * kBox);
+    }
+    static __device__ __forceinline__ float get(const uint8_t* stage, int token, int head) {
+        return to_f32(reinterpret_cast<const T*>(stage)[token * kHeads + head % kHeads]);
+    }
+};
+
 // The bounds of a stage's tokens.
 template <int kTokens>
 struct StageBounds {
     uint32_t starts[kTokens / 32], ends[kTokens / 32];
-    uint32_t warps;                // which warps' tokens hold a start
-    uint32_t plain;                // which warps' tokens are all there, with neither a start nor an end
+    uint32_t warps_start, warps_end;  // which warps' tokens hold a start, an end
+    uint32_t plain;                   // which warps' tokens are all there, with neither
     int32_t start_seq[kTokens], end_seq[kTokens];
 };
 
-// Where a walk over cu_seqlens has got to: no entry before `lo` is at or past the tokens to come; entry `lo` is `next`.
-struct Cursor {
-    int64_t lo, next;
-};
-
-// Fills the bounds of tokens [t0, t1) (one warp) and moves the cursor on to t1.  empty(i) is called by the whole warp for
-// every empty sequence.  Entries are taken as they are: a malformed cu_seqlens gives wrong bounds, none outside.
+// Fills the bounds of tokens [t0, t1) (one warp); no entry of cu_seqlens before `lo` is at or past t0.  empty(i) is called
+// by the whole warp for every empty sequence.  Entries are taken as they are: a malformed cu_seqlens gives wrong bounds,
+// none outside.  Returns how many entries from `lo` on are before t1.
 template <int kTokens, int kWarpTokens, class Empty>
-__device__ __forceinline__ void stage_bounds(const LinearParams& p, Cursor& cur, int64_t t0, int64_t t1, bool last, int lane,
-                                             StageBounds<kTokens>& b, Empty empty) {
-    constexpr uint32_t kAll = (1u << (kTokens / kWarpTokens)) - 1u;
-    if (cur.next > t1 && t1 == t0 + kTokens) {  // most stages
-        if (lane == 0) {
-            b.warps = 0;
-            b.plain = kAll;
-        }
-        return;
-    }
+__device__ __forceinline__ int64_t fill_bounds(const LinearParams& p, int64_t lo, int64_t t0, int64_t t1, bool last, int lane,
+                                               StageBounds<kTokens>& b, Empty empty) {
     if (lane < kTokens / 32) b.starts[lane] = b.ends[lane] = 0;
     __syncwarp();
-    int64_t moved = cur.lo;
-    for (int64_t lo = cur.lo;; lo += 32) {
+    int64_t moved = 0;
+    for (;; lo += 32) {
         const int64_t i = lo + lane;
         const int64_t c = i <= p.N ? cu_at(p, i) : t1 + 1;
         const int64_t next = i < p.N ? cu_at(p, i + 1) : c, prev = i > 0 && i <= p.N ? cu_at(p, i - 1) : c;
@@ -177,20 +192,35 @@ __device__ __forceinline__ void stage_bounds(const LinearParams& p, Cursor& cur,
         for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(lo + __ffs(m) - 1);
         if (__any_sync(0xffffffffu, c > t1)) break;
     }
-    cur.lo = moved;
-    cur.next = moved <= p.N ? cu_at(p, moved) : INT64_MAX;
     __syncwarp();
     uint32_t s = 0, e = 0;
-    if (lane < kTokens / kWarpTokens) {
-        static_assert(kWarpTokens == 32 || kWarpTokens == 64, "one word of bounds a warp, or two");
-        s = kWarpTokens == 32 ? b.starts[lane] : b.starts[2 * lane] | b.starts[2 * lane + 1];
-        e = kWarpTokens == 32 ? b.ends[lane] : b.ends[2 * lane] | b.ends[2 * lane + 1];
+    constexpr int kWords = kTokens / kWarpTokens;
+    if (lane < kWords) {
+        static_assert(kWarpTokens == 16 || kWarpTokens == 32 || kWarpTokens == 64, "half a word of bounds a warp, one or two");
+        if constexpr (kWarpTokens == 64) {
+            s = b.starts[2 * lane] | b.starts[2 * lane + 1];
+            e = b.ends[2 * lane] | b.ends[2 * lane + 1];
+        } else {
+            constexpr uint32_t kMask = kWarpTokens == 32 ? 0xffffffffu : 0xffffu;
+            s = (b.starts[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
+            e = (b.ends[lane * kWarpTokens / 32] >> (lane * kWarpTokens % 32)) & kMask;
+        }
     }
-    const uint32_t warps = __ballot_sync(0xffffffffu, s != 0);
-    const uint32_t plain = __ballot_sync(0xffffffffu, (s | e) == 0 && t0 + (lane + 1) * kWarpTokens <= t1);
+    const uint32_t ws = __ballot_sync(0xffffffffu, s != 0), we = __ballot_sync(0xffffffffu, e != 0);
+    const uint32_t plain = __ballot_sync(0xffffffffu, lane < kWords && (s | e) == 0 && t0 + (lane + 1) * kWarpTokens <= t1);
     if (lane == 0) {
-        b.warps = warps;
-        b.plain = plain & kAll;
+        b.warps_start = ws;
+        b.warps_end = we;
+        b.plain = plain;
+    }
+    return moved;
+}
+
+template <int kTokens>
+__device__ __forceinline__ void no_bounds(StageBounds<kTokens>& b, int lane) {
+    if (lane == 0) {
+        b.warps_start = b.warps_end = 0;
+        b.plain = 0xffffffffu;
     }
 }
 
@@ -209,14 +239,17 @@ __device__ __forceinline__ int64_t first_entry(const LinearParams& p, int64_t n,
 }
 
 // A run's bounds, a bit a token.
-__device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) { return (words[run / 4] >> (run % 4 * 8)) & 0xffu; }
+template <int kRun>
+__device__ __forceinline__ uint32_t run_bits(const uint32_t* words, int run) {
+    return (words[run * kRun / 32] >> (run * kRun % 32)) & ((1u << kRun) - 1u);
+}
 
 // Which of a warp's runs hold a bound, a bit a run.
-template <int kRuns>
+template <int kRun, int kRuns>
 __device__ __forceinline__ uint32_t runs_with(const uint32_t* words, int warp) {
     uint32_t r = 0;
 #pragma unroll
-    for (int i = 0; i < kRuns; ++i) r |= (run_bits(words, warp * kRuns + i) ? 1u : 0u) << i;
+    for (int i = 0; i < kRuns; ++i) r |= (run_bits<kRun>(words, warp * kRuns + i) ? 1u : 0u) << i;
     return r;
 }
 
@@ -236,26 +269,25 @@ struct Segments {
     int32_t first, stages;         // stages of the first segment, and of the others
 };
 
-// Maps of the inputs for tiled copies; a's and b's with gates per channel only.
+// Maps of the inputs for tiled copies (not of gates of any heads).
 struct ColumnMaps {
     CUtensorMap x, a, b;
 };
 
-// How gates are found: per channel, one head for the block's channels (the head's channels are a multiple of its), or
-// any heads (4 channels of a lane share one).
+// How gates are found: per channel; of one head for the block's channels (the head's channels are a multiple of them, and
+// rows of gates can be copied); or of any heads (4 channels of a lane share one), by plain loads.
 enum Gates { kPerChannel, kOneHead, kAnyHead };
 
 template <class X, class G, int kGates, bool kHasB, class Col>
 struct ForwardShape {
-    static constexpr int W = Col::kLanesRow * 4, kTokens = Col::kTokens;
-    using AX = StageArray<X, W, kTokens>;
-    using AG = StageArray<G, W, kTokens>;
-    static constexpr int kStageBytes = AX::kBytes + (kGates != kPerChannel ? 0 : kHasB ? 2 : 1) * AG::kBytes;
-    static constexpr int kDepth = Col::kRing / kStageBytes < 4 ? Col::kRing / kStageBytes : 4;
+    static constexpr int W = Col::kWidth, kTokens = Col::kTokens;
+    using AX = StageArray<X, Col>;
+    using AG = std::conditional_t<kGates == kOneHead, StageGates<G, Col>, StageArray<G, Col>>;
+    static constexpr int kStageBytes = AX::kBytes + (kGates == kAnyHead ? 0 : kHasB ? 2 : 1) * AG::kBytes;
+    static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
     struct Tables {
-        StageBounds<kTokens> bounds[2];
-        float2 pairs[Col::kWarps][W];
-        alignas(16) float2 gates[kGates == kOneHead ? kTokens : 1];
+        StageBounds<kTokens> bounds[3];
+        alignas(16) float2 pairs[2][Col::kWarps][W];
         float enter[W];
         alignas(16) float kept[W];  // initial state of the last sequence that starts in the segment
         int64_t kept_at;            // its first token
@@ -263,20 +295,18 @@ struct ForwardShape {
         uint32_t ticket;
     };
     static constexpr int kSmem = kDepth * kStageBytes + static_cast<int>(sizeof(Tables));
+    static_assert(kStageBytes % 128 == 0 && alignof(Tables) == 16, "boxes and tables lie aligned");
     static_assert(kDepth >= 2, "the next stage comes while one is worked on");
 };
 
 template <class X, class G, int kGates, bool kHasB, class Col>
-__global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
+__global__ void __launch_bounds__(Col::kThreads, 1)
     gdn_linear_column_forward_kernel(const LinearParams p, const Segments seg, const __grid_constant__ ColumnMaps maps) {
     using Shape = ForwardShape<X, G, kGates, kHasB, Col>;
     using AX = typename Shape::AX;
     using AG = typename Shape::AG;
     constexpr int W = Shape::W, kTokens = Shape::kTokens, kDepth = Shape::kDepth, kRuns = Col::kRuns, kLanesRow = Col::kLanesRow;
-    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens;
-    // With two stages the next fetch waits until the oldest stage's inputs are in registers; with more, a stage is free at
-    // the step's start already.
-    constexpr bool kLate = kDepth == 2;
+    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun;
     extern __shared__ __align__(1024) uint8_t ring[];
     typename Shape::Tables& sm = *reinterpret_cast<typename Shape::Tables*>(ring + kDepth * Shape::kStageBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -312,35 +342,67 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
         const int64_t t0 = stage_start(q);
         mbar_arrive_expect_tx(bar, Shape::kStageBytes);
         AX::fetch(stage, &maps.x, bar, c0, t0);
-        if constexpr (kGates == kPerChannel) {
-            AG::fetch(stage + AX::kBytes, &maps.a, bar, c0, t0);
-            if constexpr (kHasB) AG::fetch(stage + AX::kBytes + AG::kBytes, &maps.b, bar, c0, t0);
+        if constexpr (kGates != kAnyHead) {
+            const int at = kGates == kOneHead ? head : c0;
+            AG::fetch(stage + AX::kBytes, &maps.a, bar, at, t0);
+            if constexpr (kHasB) AG::fetch(stage + AX::kBytes + AG::kBytes, &maps.b, bar, at, t0);
         }
     };
-    // Gates per head are on their way one step ahead in registers: of two tokens a lane (one head for the block: the
-    // warp shares them through shared memory), or of the lane's own run.
-    constexpr int kHeld = kGates == kPerChannel ? 1 : kGates == kOneHead ? 2 : kRun;
-    G ha[kHeld], hb[kHeld];
-    auto fetch_gates = [&](int q) {
-        if constexpr (kGates != kPerChannel) {
-            if (q >= steps) return;
-            const int64_t t = stage_start(q) + (kGates == kOneHead ? warp * kWarpTokens + lane : run * kRun);
+    // A thread's inputs of a stage: x and gates per channel of its run; of gates of one head the token that is its lane's
+    // in the run; of gates of any heads its run's.
+    constexpr int kHeld = kGates == kOneHead ? kRun / kLanesRow : kRun;
+    Pack<X> px[kRun];
+    Pack<G> pa[kGates == kPerChannel ? kRun : 1], pb[kGates == kPerChannel ? kRun : 1];
+    float ha[kHeld], hb[kHeld];
+    bool ok = true;  // until a wait runs out
+    auto take = [&](int q) {
+        if (kGates == kAnyHead) {
+            const int64_t t = stage_start(q) + run * kRun;
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                const int64_t tk = t + (kGates == kOneHead ? 32 * k : k);
-                if (tk >= end) continue;
-                ha[k] = ga[tk * p.a_stride];
-                if constexpr (kHasB) hb[k] = gb[tk * p.b_stride];
+            for (int k = 0; k < kRun; ++k) {
+                ha[k] = hb[k] = 1.f;
+                if (t + k >= end) continue;
+                ha[k] = to_f32(ga[(t + k) * p.a_stride]);
+                if constexpr (kHasB) hb[k] = to_f32(gb[(t + k) * p.b_stride]);
+            }
+        }
+        if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
+            ok = false;
+            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+        }
+        const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        const uint8_t *sa = stage + AX::kBytes, *sb = sa + AG::kBytes;
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            px[k] = AX::get(stage, run, k, l);
+            if constexpr (kGates == kPerChannel) {
+                pa[k] = AG::get(sa, run, k, l);
+                if constexpr (kHasB) pb[k] = AG::get(sb, run, k, l);
+            }
+        }
+        if constexpr (kGates == kOneHead) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int tok = run * kRun + i * kLanesRow + l;
+                ha[i] = AG::get(sa, tok, head);
+                if constexpr (kHasB) hb[i] = AG::get(sb, tok, head);
             }
         }
     };
-    Cursor cur{0, 0};
+    int64_t lo = 0, next = 0;  // the walk over cu_seqlens: entries before `lo` are before the tokens to come, entry `lo` is `next`
     auto bounds = [&](int q) {
         if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, end);
-        if (q == 0 || q == stages) cur = {from == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane), 0};
+        if (q == 0 || q == stages) {
+            lo = from == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
+            next = 0;
+        }
+        if (next > t1 && t1 == t0 + kTokens) {  // most stages
+            no_bounds(sm.bounds[q % 3], lane);
+            return;
+        }
         const bool write = q >= steps - stages;
-        stage_bounds<kTokens, kWarpTokens>(p, cur, t0, t1, t1 == p.T, lane, sm.bounds[q & 1], [&](int64_t i) {
+        lo += fill_bounds<kTokens, kWarpTokens>(p, lo, t0, t1, t1 == p.T, lane, sm.bounds[q % 3], [&](int64_t i) {
             // an empty sequence's final state is its initial one
             if (!write || !p.output_state || p.output_state == p.initial_state) return;
             const int64_t row = state_row(p, i);
@@ -349,61 +411,47 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
             state_quad_store(p.output_state, off, p.state_dt,
                              p.initial_state ? state_quad_load(p.initial_state, off, p.state_dt) : make_float4(0.f, 0.f, 0.f, 0.f));
         });
+        next = lo <= p.N ? cu_at(p, lo) : INT64_MAX;
     };
 
-    if (warp < kColWarps) {
-        if (threadIdx.x == 0)
-            for (int q = 0; q < (kLate ? kDepth : kDepth - 1); ++q) fetch(q);
-        fetch_gates(0);
-    } else {
+    if (threadIdx.x == 0)
+        for (int q = 0; q < kDepth; ++q) fetch(q);
+    if (warp == kColWarps) {
         bounds(0);
         if (blk == 0) check_bounds(p, part, sp.nt, lane);
     }
-    bool ok = true;                    // until a wait runs out
+    __syncthreads();
     float carry = 0.f, through = 1.f;  // of channel `ch`: the state (in steps that learn, from zero), the gates' product
     bool reset = false;                // whether a sequence has started
     X* y = static_cast<X*>(p.y) + c0 + l * 4;
     for (int q = 0; q < steps; ++q) {
-        __syncthreads();
-        const StageBounds<kTokens>& bd = sm.bounds[q & 1];
+        const StageBounds<kTokens>& bd = sm.bounds[q % 3];
         const bool learn = twice && q < stages;
         const int64_t t = stage_start(q) + run * kRun;
-        const bool plain = (bd.plain >> (warp % kColWarps)) & 1;
         Quad a[kRun], u[kRun], A, B, exA, exB;
         uint32_t starts = 0;
         int n = kRun;
-        bool before = false;  // whether a sequence starts in the warp's runs before this one
+        bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
         if (warp == kColWarps) {
-            bounds(q + 1);  // beside the others, up to the next step
+            bounds(q + 1);
         } else {
-            if (!kLate && threadIdx.x == 0) fetch(q + kDepth - 1);
-            if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
-                ok = false;
-                report(p.status, GDN_DEVICE_ERR_TIMEOUT);
-            }
-            const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
-            if constexpr (kGates == kOneHead) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    sm.gates[warp * kWarpTokens + 32 * k + lane] = make_float2(to_f32(ha[k]), kHasB ? to_f32(hb[k]) : 1.f);
-                __syncwarp();
-            }
+            plain = (bd.plain >> warp) & 1;
+            take(q);
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                u[k] = widen(AX::get(stage, run, k, l));
+                u[k] = widen(px[k]);
                 if constexpr (kGates == kOneHead) {
-                    const float2 g = sm.gates[run * kRun + k];
-                    a[k] = all4(g.x);
-                    if constexpr (kHasB) u[k] = mul(u[k], all4(g.y));
+                    const int from_lane = sub * kLanesRow + k % kLanesRow;
+                    a[k] = all4(__shfl_sync(0xffffffffu, ha[k / kLanesRow], from_lane));
+                    if constexpr (kHasB) u[k] = mul(u[k], all4(__shfl_sync(0xffffffffu, hb[k / kLanesRow], from_lane)));
                 } else if constexpr (kGates == kAnyHead) {
-                    a[k] = all4(to_f32(ha[k]));
-                    if constexpr (kHasB) u[k] = mul(u[k], all4(to_f32(hb[k])));
+                    a[k] = all4(ha[k]);
+                    if constexpr (kHasB) u[k] = mul(u[k], all4(hb[k]));
                 } else {
-                    a[k] = widen(AG::get(stage + AX::kBytes, run, k, l));
-                    if constexpr (kHasB) u[k] = mul(u[k], widen(AG::get(stage + AX::kBytes + AG::kBytes, run, k, l)));
+                    a[k] = widen(pa[k]);
+                    if constexpr (kHasB) u[k] = mul(u[k], widen(pb[k]));
                 }
             }
-            fetch_gates(q + 1);
             if (plain) {
                 A = a[0];
                 B = u[0];
@@ -414,7 +462,7 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
                 }
             } else {
                 n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
-                starts = run_bits(bd.starts, run);
+                starts = run_bits<kRun>(bd.starts, run);
                 A = all4(1.f);
                 B = all4(0.f);
 #pragma unroll
@@ -447,7 +495,7 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
                 }
             }
             // over the warp's runs
-            const uint32_t rs = (bd.warps >> warp) & 1 ? runs_with<kRuns>(bd.starts, warp) : 0;
+            const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
                 const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
@@ -465,23 +513,25 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
             }
             before = (rs & ((1u << sub) - 1u)) != 0;
             if (sub == kRuns - 1) {
-                float4* o = reinterpret_cast<float4*>(&sm.pairs[warp][l * 4]);
+                float4* o = reinterpret_cast<float4*>(&sm.pairs[q & 1][warp][l * 4]);
                 o[0] = make_float4(A.lo.x, B.lo.x, A.lo.y, B.lo.y);
                 o[1] = make_float4(A.hi.x, B.hi.x, A.hi.y, B.hi.y);
             }
         }
+        // The step's one barrier.  Past it: every warp's pair is there and every thread has its inputs of this stage, so its
+        // place in the ring is free; the bounds of the next stage are known.
+        __syncthreads();
         float enter = carry;
         if (warp < kColWarps) {
-            named_bar_sync(1, 32 * kColWarps);
-            if (kLate && threadIdx.x == 0) fetch(q + kDepth);
+            if (threadIdx.x == 0) fetch(q + kDepth);
 #pragma unroll
             for (int w = 0; w < kColWarps; ++w) {
-                const float2 ab = sm.pairs[w][ch];
+                const float2 ab = sm.pairs[q & 1][w][ch];
                 if (w == warp) enter = carry;
-                carry = (bd.warps >> w) & 1 ? ab.y : fmaf(ab.x, carry, ab.y);
+                carry = (bd.warps_start >> w) & 1 ? ab.y : fmaf(ab.x, carry, ab.y);
                 if (learn) through *= ab.x;
             }
-            reset |= bd.warps != 0;
+            reset |= bd.warps_start != 0;
         }
         if (learn) {
             if (q < stages - 1) continue;
@@ -525,7 +575,7 @@ __global__ void __launch_bounds__(Col::kThreads, Col::kBlocksSm)
                 if (p.tile_states && (t + kRun) % kTile == 0)
                     *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
             } else {
-                const uint32_t ends = run_bits(bd.ends, run);
+                const uint32_t ends = run_bits<kRun>(bd.ends, run);
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
                     if (k >= n) break;
@@ -553,9 +603,11 @@ cudaError_t launch_column_forward(const LinearParams& p, const Segments& seg, cu
     using Shape = ForwardShape<X, G, kGates, kHasB, Col>;
     ColumnMaps maps{};
     bool ok = p.T == 0 || encode_rows(&maps.x, p.x, p.x_dt, p.x_stride, p.C, p.T, Shape::W, Shape::AX::kBox);
-    if (kGates == kPerChannel && p.T > 0) {
-        ok = ok && encode_rows(&maps.a, p.a, p.gate_dt, p.a_stride, p.C, p.T, Shape::W, Shape::AG::kBox);
-        if (kHasB) ok = ok && encode_rows(&maps.b, p.b, p.gate_dt, p.b_stride, p.C, p.T, Shape::W, Shape::AG::kBox);
+    if (kGates != kAnyHead && p.T > 0) {
+        const int64_t row = kGates == kOneHead ? p.H : p.C;
+        const int width = kGates == kOneHead ? 16 / static_cast<int>(sizeof(G)) : Shape::W;
+        ok = ok && encode_rows(&maps.a, p.a, p.gate_dt, p.a_stride, row, p.T, width, Shape::AG::kBox);
+        if (kHasB) ok = ok && encode_rows(&maps.b, p.b, p.gate_dt, p.b_stride, row, p.T, width, Shape::AG::kBox);
     }
     if (!ok) return cudaErrorInvalidValue;
     auto kernel = gdn_linear_column_forward_kernel<X, G, kGates, kHasB, Col>;
@@ -566,22 +618,28 @@ cudaError_t launch_column_forward(const LinearParams& p, const Segments& seg, cu
 }
 
 template <class X, class G, int kGates>
-cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int W, int warps, cudaStream_t stream) {
-    if (W == 32)
-        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, 8>>(p, seg, stream)
-                   : launch_column_forward<X, G, kGates, false, Column<32, 8>>(p, seg, stream);
-    if (warps == 4)
-        return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 4>>(p, seg, stream)
-                   : launch_column_forward<X, G, kGates, false, Column<16, 4>>(p, seg, stream);
-    return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 8>>(p, seg, stream)
-               : launch_column_forward<X, G, kGates, false, Column<16, 8>>(p, seg, stream);
+cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
+    if (width == 32)
+        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, 8, 8>>(p, seg, stream)
+                   : launch_column_forward<X, G, kGates, false, Column<32, 8, 8>>(p, seg, stream);
+    return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 8, 8>>(p, seg, stream)
+               : launch_column_forward<X, G, kGates, false, Column<16, 8, 8>>(p, seg, stream);
+}
+
+// Whether a block of `width` channels has one head, and its gates can be copied.
+template <class G>
+bool one_head(const LinearParams& p, int width) {
+    const auto rows = [](const void* g, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(g) % 16 == 0 && stride * static_cast<int64_t>(sizeof(G)) % 16 == 0;
+    };
+    return p.D % width == 0 && rows(p.a, p.a_stride) && rows(p.b, p.b_stride);
 }
 
 template <class X, class G>
-cudaError_t column_forward_typed(const LinearParams& p, const Segments& seg, int W, int warps, cudaStream_t stream) {
-    if (p.gate_div == 1) return column_forward_gates<X, G, kPerChannel>(p, seg, W, warps, stream);
-    if (p.D % W == 0) return column_forward_gates<X, G, kOneHead>(p, seg, W, warps, stream);
-    return column_forward_gates<X, G, kAnyHead>(p, seg, W, warps, stream);
+cudaError_t column_forward_typed(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
+    if (p.gate_div == 1) return column_forward_gates<X, G, kPerChannel>(p, seg, width, stream);
+    if (one_head<G>(p, width)) return column_forward_gates<X, G, kOneHead>(p, seg, width, stream);
+    return column_forward_gates<X, G, kAnyHead>(p, seg, width, stream);
 }
 
 }  // namespace linear

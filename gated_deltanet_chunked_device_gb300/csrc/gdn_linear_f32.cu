@@ -11,8 +11,8 @@ cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::Scan
     return linear::backward_typed<float, float>(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, int warps, cudaStream_t stream) {
-    return linear::column_forward_typed<float, float>(p, s, width, warps, stream);
+cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream) {
+    return linear::column_forward_typed<float, float>(p, s, width, stream);
 }
 
 }  // namespace gdn

@@ -69,6 +69,21 @@ def test_misaligned_bases():
     check_backward(i, tiles)
 
 
+def test_misaligned_saved_states():
+    """tile_states, and the gradients of states, that start at any float."""
+    i = make([90, 30], 2, 64, "bf16", "f32", seed=25)
+    want = ref.forward(f64(i["x"]), f64(i["a"]), f64(i["b"]), i["cul"], f64(i["h0"]))
+    odd = lambda *shape: torch.empty(torch.Size(shape).numel() + 1, device="cuda")[1:].view(shape)  # noqa: E731
+    tiles = odd(2, 2, 64)
+    y, final = gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=i["h0"], output_final_state=True,
+                                           cu_seqlens=i["cu"], tile_states=tiles)
+    within("tile_states", tiles, want[0][[63, 119]], want[3][[63, 119]])
+    df = odd(2, 2, 64)
+    df.copy_(i["df"])
+    i["df"] = df
+    check_backward(i, tiles)
+
+
 def test_in_place():
     i = make([77, 500], 2, 128, "bf16", seed=5)
     y = gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], cu_seqlens=i["cu"])
