@@ -18,8 +18,11 @@ cudaError_t launch_linear_column_forward_f16(const LinearParams& p, const linear
 cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
 cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_backward_bf16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_backward_bf16(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_backward_f16(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_backward_f16(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream);
+cudaError_t launch_linear_column_backward_f32(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream);
 
 namespace {
 
@@ -113,13 +116,13 @@ bool inputs_wide(const LinearParams& p) {
     return x && vector_of_16_bytes(p.a, p.a_stride, p.gate_dt, p.C) && vector_of_16_bytes(p.b, p.b_stride, p.gate_dt, p.C);
 }
 
-// Width and time segments of the columns.
-linear::Segments segments(const LinearParams& p, int* width) {
+// Width and time segments of the columns, with runs of `run` tokens.
+linear::Segments segments(const LinearParams& p, int run, int* width) {
     const int64_t sms = multiprocessors(), blocks32 = (p.C + 31) / 32;
     int64_t segs = sms / blocks32;
     *width = 5 * blocks32 < 3 * sms && segs < 3 ? 16 : 32;
     linear::Segments s{};
-    const int64_t tokens = 8 * 1024 / *width, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
+    const int64_t tokens = 8 * (128 / *width) * run, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
     if (segs > n / 2) segs = n / 2;
     s.space.blocks = static_cast<uint32_t>((p.C + *width - 1) / *width);
     s.space.nt = 1;
@@ -131,6 +134,18 @@ linear::Segments segments(const LinearParams& p, int* width) {
         s.space.nt = n <= s.first ? 1 : 1 + (n - s.first + s.stages - 1) / s.stages;
     }
     return s;
+}
+
+// The workspace as the kernels of columns take it.
+cudaError_t segment_space(const LinearParams& p, void* workspace, cudaStream_t stream, linear::Segments* seg) {
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    linear::ScanSpace& s = seg->space;
+    const size_t zeroed = 256 + sizeof(uint32_t) * s.nt * s.blocks, pairs = (zeroed + 255) / 256 * 256;
+    s.ticket = reinterpret_cast<uint32_t*>(ws);
+    s.flags = reinterpret_cast<uint32_t*>(ws + 256);
+    s.pairs = reinterpret_cast<float2*>(ws + pairs);
+    s.known = reinterpret_cast<float*>(ws + pairs + sizeof(float2) * s.nt * p.C);
+    return s.nt > 1 ? cudaMemsetAsync(ws, 0, zeroed, stream) : cudaSuccess;
 }
 
 // The workspace as the kernels take it; what has to start from zero is zeroed, where there is more than one tile.
@@ -172,18 +187,9 @@ cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaSt
     const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
     if (vec && inputs_wide(p)) {
         int width;
-        linear::Segments seg = segments(p, &width);
-        uint8_t* ws = static_cast<uint8_t*>(workspace);
-        const size_t zeroed = 256 + sizeof(uint32_t) * seg.space.nt * seg.space.blocks;
-        const size_t pairs = (zeroed + 255) / 256 * 256;
-        seg.space.ticket = reinterpret_cast<uint32_t*>(ws);
-        seg.space.flags = reinterpret_cast<uint32_t*>(ws + 256);
-        seg.space.pairs = reinterpret_cast<float2*>(ws + pairs);
-        seg.space.known = reinterpret_cast<float*>(ws + pairs + sizeof(float2) * seg.space.nt * p.C);
-        if (seg.space.nt > 1) {
-            const cudaError_t err = cudaMemsetAsync(ws, 0, zeroed, stream);
-            if (err != cudaSuccess) return err;
-        }
+        linear::Segments seg = segments(p, 8, &width);
+        const cudaError_t e = segment_space(p, workspace, stream, &seg);
+        if (e != cudaSuccess) return e;
         if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, width, stream);
         if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, width, stream);
         return launch_linear_column_forward_f32(p, seg, width, stream);
@@ -198,14 +204,26 @@ cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaSt
 }
 
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream) {
-    linear::ScanSpace s{};
-    const cudaError_t e = scan_space(p, workspace, backward_blocks(p.C, p.gate_div != 1 ? p.D : 0), stream, &s);
-    if (e != cudaSuccess) return e;
     LinearParams q = p;
-    q.scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + scan_layout(p.T, p.C, p.gate_div != 1 ? p.D : 0).sums);
+    const int64_t head_dim = p.gate_div != 1 ? p.D : 0;
+    q.scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + scan_layout(p.T, p.C, head_dim).sums);
     bool vec = rows_vector(p) && vector_of_4(p.dy, p.dy_stride, p.x_dt) && vector_of_4(p.dx, p.dx_stride, p.x_dt) &&
                vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
     if (p.gate_div == 1) vec = vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
+    if (vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
+        int width;
+        linear::Segments seg = segments(p, p.gate_div == 1 && p.x_dt == GDN_DTYPE_F32 ? 4 : 8, &width);
+        if (p.gate_div == 1 || linear::one_head(p, width)) {
+            const cudaError_t e = segment_space(p, workspace, stream, &seg);
+            if (e != cudaSuccess) return e;
+            if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_backward_bf16(q, seg, width, stream);
+            if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_backward_f16(q, seg, width, stream);
+            return launch_linear_column_backward_f32(q, seg, width, stream);
+        }
+    }
+    linear::ScanSpace s{};
+    const cudaError_t e = scan_space(p, workspace, backward_blocks(p.C, head_dim), stream, &s);
+    if (e != cudaSuccess) return e;
     if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_backward_bf16(q, s, vec, stream);
     if (p.x_dt == GDN_DTYPE_F16) return launch_linear_backward_f16(q, s, vec, stream);
     return launch_linear_backward_f32(q, s, vec, stream);

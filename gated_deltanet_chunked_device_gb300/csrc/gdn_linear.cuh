@@ -90,7 +90,8 @@ inline ScanLayout scan_layout(int64_t T, int64_t C, int64_t head_dim) {
     l.known = l.pairs + up(sizeof(float2) * static_cast<size_t>(l.nt) * C);
     l.sums = l.known + up(sizeof(float) * static_cast<size_t>(l.nt) * C);
     l.total = l.sums;
-    if (head_dim > 128) l.total += up(sizeof(float2) * static_cast<size_t>(T) * (C / head_dim) * ((head_dim + 127) / 128));
+    if (head_dim > 16)  // a block has 16 channels or more
+        l.total += up(sizeof(float2) * static_cast<size_t>(T) * (C / head_dim) * ((head_dim + 15) / 16));
     return l;
 }
 

@@ -34,7 +34,7 @@ struct Column {
     static constexpr int kThreads = 32 * (NW + 1);
 };
 
-constexpr int kRingBytes = 216 * 1024;           // shared memory of the ring, at most
+constexpr int kRingBytes = 192 * 1024;           // shared memory of the ring, at most
 
 // Two fp32 at a time.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -271,7 +271,7 @@ struct Segments {
 
 // Maps of the inputs for tiled copies (not of gates of any heads).
 struct ColumnMaps {
-    CUtensorMap x, a, b;
+    CUtensorMap x, a, b, dy;
 };
 
 // How gates are found: per channel; of one head for the block's channels (the head's channels are a multiple of them, and
@@ -627,10 +627,9 @@ cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int
 }
 
 // Whether a block of `width` channels has one head, and its gates can be copied.
-template <class G>
-bool one_head(const LinearParams& p, int width) {
-    const auto rows = [](const void* g, int64_t stride) {
-        return reinterpret_cast<uintptr_t>(g) % 16 == 0 && stride * static_cast<int64_t>(sizeof(G)) % 16 == 0;
+inline bool one_head(const LinearParams& p, int width) {
+    const auto rows = [&](const void* g, int64_t stride) {
+        return reinterpret_cast<uintptr_t>(g) % 16 == 0 && stride * dtype_bytes(p.gate_dt) % 16 == 0;
     };
     return p.D % width == 0 && rows(p.a, p.a_stride) && rows(p.b, p.b_stride);
 }
@@ -638,7 +637,7 @@ bool one_head(const LinearParams& p, int width) {
 template <class X, class G>
 cudaError_t column_forward_typed(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
     if (p.gate_div == 1) return column_forward_gates<X, G, kPerChannel>(p, seg, width, stream);
-    if (one_head<G>(p, width)) return column_forward_gates<X, G, kOneHead>(p, seg, width, stream);
+    if (one_head(p, width)) return column_forward_gates<X, G, kOneHead>(p, seg, width, stream);
     return column_forward_gates<X, G, kAnyHead>(p, seg, width, stream);
 }
 

@@ -1,0 +1,463 @@
+// gdn_linear_column_backward.cuh -- the backward pass of the gated linear
+// recurrence with columns of channels streamed along the tokens, from the last
+// token to the first (gdn_linear_column.cuh has the forward pass and the
+// layout).
+//
+//     c_t = a_t g_t,  g_t = dy_t + c_{t+1}:   dx = b g, db = x g, da = h_{t-1} g
+//
+// The carry c is composed from the right as the forward pass composes the
+// state from the left.  The states h are composed from the left again, inside
+// a tile of 64 tokens only: the forward pass has saved the state at each
+// tile's end.
+#pragma once
+
+#include "gdn_linear_column.cuh"
+
+namespace gdn {
+namespace linear {
+
+template <class X, class G, int kGates, bool kHasB, class Col>
+struct BackwardShape {
+    static constexpr int W = Col::kWidth, kTokens = Col::kTokens;
+    using AX = StageArray<X, Col>;
+    using AG = std::conditional_t<kGates == kOneHead, StageGates<G, Col>, StageArray<G, Col>>;
+    // dy, a, x, b: the first two are what a pass that learns needs
+    static constexpr int kLearnBytes = AX::kBytes + AG::kBytes;
+    static constexpr int kStageBytes = 2 * AX::kBytes + (kHasB ? 2 : 1) * AG::kBytes;
+    static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
+    struct Tables {
+        StageBounds<kTokens> bounds[3];
+        alignas(16) float4 pairs[2][Col::kWarps][W];  // a warp's tokens: product of the gates, state and carry from zero
+        float enter[W];
+        uint64_t full[kDepth];
+        uint32_t ticket;
+    };
+    static constexpr int kSmem = kDepth * kStageBytes + static_cast<int>(sizeof(Tables));
+    static_assert(kDepth >= 2, "the next stage comes while one is worked on");
+    static_assert(kStageBytes % 128 == 0 && alignof(Tables) == 16, "boxes and tables lie aligned");
+};
+
+template <class X, class G, int kGates, bool kHasB, class Col>
+__global__ void __launch_bounds__(Col::kThreads, 1)
+    gdn_linear_column_backward_kernel(const LinearParams p, const Segments seg, const __grid_constant__ ColumnMaps maps) {
+    using Shape = BackwardShape<X, G, kGates, kHasB, Col>;
+    using AX = typename Shape::AX;
+    using AG = typename Shape::AG;
+    constexpr int W = Shape::W, kTokens = Shape::kTokens, kDepth = Shape::kDepth, kRuns = Col::kRuns, kLanesRow = Col::kLanesRow;
+    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun;
+    constexpr int kTileWarps = kTile / kWarpTokens;  // warps whose tokens are a tile
+    extern __shared__ __align__(1024) uint8_t ring[];
+    typename Shape::Tables& sm = *reinterpret_cast<typename Shape::Tables*>(ring + kDepth * Shape::kStageBytes);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int sub = lane / kLanesRow, l = lane % kLanesRow, run = warp * kRuns + sub, ch = lane % W;
+    const ScanSpace& sp = seg.space;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kDepth; ++i) mbar_init(&sm.full[i], 1);
+        fence_mbar_init();
+        if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
+    }
+    __syncthreads();
+    const uint32_t ticket = sp.nt > 1 ? sm.ticket : blockIdx.x;
+    const int64_t part = ticket / sp.blocks;  // segments are counted from the right
+    const uint32_t blk = ticket % sp.blocks;
+    const int c0 = static_cast<int>(blk) * W, cols = min(W, p.C - c0);
+    // stages of the whole axis are counted from the left; this segment has [left, right)
+    const int64_t all = max(static_cast<int64_t>(1), (p.T + kTokens - 1) / kTokens);
+    const int64_t right = part == 0 ? all : all - seg.first - (part - 1) * seg.stages;
+    const int64_t left = part == sp.nt - 1 ? 0 : all - seg.first - part * seg.stages;
+    const int stages = static_cast<int>(right - left);
+    const bool twice = part > 0;
+    const int steps = p.T == 0 ? 0 : twice ? 2 * stages : stages;
+    const bool on = l * 4 < cols;
+    const int head = c0 / p.D;
+
+    auto stage_start = [&](int q) { return (right - 1 - (q < stages ? q : q - stages)) * kTokens; };
+    auto fetch = [&](int q) {  // one thread
+        if (q >= steps) return;
+        uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        uint64_t* bar = &sm.full[q % kDepth];
+        const int64_t t0 = stage_start(q);
+        const int at = kGates == kOneHead ? head : c0;
+        const bool learn = twice && q < stages;
+        mbar_arrive_expect_tx(bar, learn ? Shape::kLearnBytes : Shape::kStageBytes);
+        AX::fetch(stage, &maps.dy, bar, c0, t0);
+        AG::fetch(stage + AX::kBytes, &maps.a, bar, at, t0);
+        if (learn) return;
+        AX::fetch(stage + Shape::kLearnBytes, &maps.x, bar, c0, t0);
+        if constexpr (kHasB) AG::fetch(stage + Shape::kLearnBytes + AX::kBytes, &maps.b, bar, at, t0);
+    };
+    // The walk over cu_seqlens, from the right: entry `lo` is the first that is not before the tokens done, `at` its value,
+    // `before` the value of the one before it.
+    int64_t lo = 0, at = 0, before = 0;
+    auto bounds = [&](int q) {
+        if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
+        const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, p.T);
+        if (q == 0 || q == stages) {
+            lo = first_entry(p, static_cast<int64_t>(p.N) + 1, t1, lane);
+            at = before = t1;
+        }
+        StageBounds<kTokens>& b = sm.bounds[q % 3];
+        if (before < t0 && at > t1 && t1 == t0 + kTokens) {  // most stages
+            no_bounds(b, lane);
+            return;
+        }
+        const bool write = q >= steps - stages;
+        const int64_t from = first_entry(p, lo, t0, lane);
+        fill_bounds<kTokens, kWarpTokens>(p, from, t0, t1, t1 == p.T, lane, b, [&](int64_t i) {
+            // an empty sequence hands the gradient of its final state on
+            if (!write || !p.d_initial || lane * 4 >= cols) return;
+            const int64_t off = i * p.C + c0 + lane * 4;
+            *reinterpret_cast<float4*>(p.d_initial + off) =
+                p.d_final ? *reinterpret_cast<const float4*>(p.d_final + off) : make_float4(0.f, 0.f, 0.f, 0.f);
+        });
+        lo = from;
+        at = lo <= p.N ? cu_at(p, lo) : INT64_MAX;
+        before = lo > 0 ? cu_at(p, lo - 1) : -1;
+    };
+    // The state that enters this warp's tile (of channel `ch`), from the forward pass: one step ahead.
+    float saved = 0.f;
+    auto fetch_saved = [&](int q) {
+        saved = 0.f;
+        if (q >= steps || q < steps - stages || ch >= cols) return;
+        const int64_t tile = stage_start(q) / kTile + warp / kTileWarps;
+        if (tile > 0 && tile * kTile < p.T) saved = p.tile_states[(tile - 1) * p.C + c0 + ch];
+    };
+
+    if (threadIdx.x == 0)
+        for (int q = 0; q < kDepth - 1; ++q) fetch(q);
+    if (warp == kColWarps) {
+        bounds(0);
+        if (blk == 0) check_bounds(p, part, sp.nt, lane);
+    } else {
+        fetch_saved(0);
+    }
+    __syncthreads();
+    float carry = 0.f, through = 1.f;  // of channel `ch`: the carry (in steps that learn, from zero), the gates' product
+    bool reset = false, ok = true;     // whether a sequence has ended; until a wait runs out
+    const int pieces = kGates == kOneHead ? p.D / W : 1, piece = kGates == kOneHead ? c0 % p.D / W : 0;
+    for (int q = 0; q < steps; ++q) {
+        const StageBounds<kTokens>& bd = sm.bounds[q % 3];
+        const bool learn = twice && q < stages;
+        const int64_t t = stage_start(q) + run * kRun;
+        const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        const uint8_t *sa = stage + AX::kBytes, *sx = stage + Shape::kLearnBytes, *sb = sx + AX::kBytes;
+        Quad a[kRun], u[kRun], A, B = all4(0.f), E, exA, exB, rxA, rxE;
+        constexpr int kHeld = kGates == kOneHead ? (kRun + kLanesRow - 1) / kLanesRow : 1;
+        float ha[kHeld], hb[kHeld];
+        uint32_t starts = 0, ends = 0;
+        int n = kRun;
+        bool plain = true, started = false, ended = false;  // whether a sequence starts in the runs before, ends in those after
+        // gates of one head: lane l of a run holds the run's token l
+        auto shared_gate = [&](const float(&held)[kHeld], int k) {
+            return all4(__shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow));
+        };
+        if (warp == kColWarps) {
+            bounds(q + 1);
+        } else {
+            plain = (bd.plain >> warp) & 1;
+            if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
+                ok = false;
+                report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+            }
+            if constexpr (kGates == kOneHead) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    const int tok = run * kRun + min(i * kLanesRow + l, kRun - 1);
+                    ha[i] = AG::get(sa, tok, head);
+                    if (kHasB && !learn) hb[i] = AG::get(sb, tok, head);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kRun; ++k) {
+                if constexpr (kGates == kOneHead)
+                    a[k] = shared_gate(ha, k);
+                else
+                    a[k] = widen(AG::get(sa, run, k, l));
+            }
+            if (!learn) {
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) {
+                    u[k] = widen(AX::get(sx, run, k, l));
+                    if constexpr (kHasB) {
+                        if constexpr (kGates == kOneHead)
+                            u[k] = mul(u[k], shared_gate(hb, k));
+                        else
+                            u[k] = mul(u[k], widen(AG::get(sb, run, k, l)));
+                    }
+                }
+            }
+            A = all4(1.f);
+            E = all4(0.f);
+            if (plain) {
+#pragma unroll
+                for (int k = kRun - 1; k >= 0; --k) {
+                    E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
+                    A = mul(A, a[k]);
+                }
+                if (!learn) {
+                    B = u[0];
+#pragma unroll
+                    for (int k = 1; k < kRun; ++k) B = fma(a[k], B, u[k]);
+                }
+            } else {
+                n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), p.T - t)));
+                starts = run_bits<kRun>(bd.starts, run);
+                ends = run_bits<kRun>(bd.ends, run);
+#pragma unroll
+                for (int k = kRun - 1; k >= 0; --k) {
+                    if (k >= n) continue;
+                    if ((ends >> k) & 1)
+                        E = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
+                                                                   GDN_DTYPE_F32))
+                                            : all4(0.f);
+                    E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
+                    A = mul(A, a[k]);
+                }
+                if (!learn) {
+#pragma unroll
+                    for (int k = 0; k < kRun; ++k) {
+                        if (k >= n) continue;
+                        if ((starts >> k) & 1)
+                            B = p.initial_state && on
+                                    ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
+                                    : all4(0.f);
+                        B = fma(a[k], B, u[k]);
+                    }
+                }
+            }
+            // over the warp's runs: the carry from the right, the state from the left
+            const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
+            const uint32_t re = (bd.warps_end >> warp) & 1 ? runs_with<kRun, kRuns>(bd.ends, warp) : 0;
+            Quad RA = A;
+#pragma unroll
+            for (int o = 1; o < kRuns; o <<= 1) {
+                const bool mine = (re >> sub) & ((1u << o) - 1u);
+                const Quad oa = shift_down(RA, o * kLanesRow), oe = shift_down(E, o * kLanesRow);
+                if (sub + o < kRuns) {
+                    E = pick(mine, E, fma(RA, oe, E));
+                    RA = mul(RA, oa);
+                }
+            }
+            rxA = shift_down(RA, kLanesRow);
+            rxE = shift_down(E, kLanesRow);
+            if (sub == kRuns - 1) {
+                rxA = all4(1.f);
+                rxE = all4(0.f);
+            }
+            ended = (re >> (sub + 1)) != 0;
+            if (!learn) {
+#pragma unroll
+                for (int o = 1; o < kRuns; o <<= 1) {
+                    const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
+                    const Quad oa = shift_up(A, o * kLanesRow), ob = shift_up(B, o * kLanesRow);
+                    if (sub >= o) {
+                        B = pick(mine, B, fma(A, ob, B));
+                        A = mul(A, oa);
+                    }
+                }
+                exA = shift_up(A, kLanesRow);
+                exB = shift_up(B, kLanesRow);
+                if (sub == 0) {
+                    exA = all4(1.f);
+                    exB = all4(0.f);
+                }
+                started = (rs & ((1u << sub) - 1u)) != 0;
+            }
+            // the warp's: the product and the carry are the first run's, the state is the last one's
+            const Quad lastB = {{__shfl_sync(0xffffffffu, B.lo.x, 32 - kLanesRow + l), __shfl_sync(0xffffffffu, B.lo.y, 32 - kLanesRow + l)},
+                                {__shfl_sync(0xffffffffu, B.hi.x, 32 - kLanesRow + l), __shfl_sync(0xffffffffu, B.hi.y, 32 - kLanesRow + l)}};
+            if (sub == 0) {
+                float4* o = &sm.pairs[q & 1][warp][l * 4];
+                o[0] = make_float4(RA.lo.x, lastB.lo.x, E.lo.x, 0.f);
+                o[1] = make_float4(RA.lo.y, lastB.lo.y, E.lo.y, 0.f);
+                o[2] = make_float4(RA.hi.x, lastB.hi.x, E.hi.x, 0.f);
+                o[3] = make_float4(RA.hi.y, lastB.hi.y, E.hi.y, 0.f);
+            }
+        }
+        // The step's one barrier.  Past it: every warp's pair is there, nobody reads the stage before any more (its place in
+        // the ring is free), and the bounds of the next stage are known.
+        __syncthreads();
+        float enter_c = carry, enter_h = saved;
+        if (warp < kColWarps) {
+            if (threadIdx.x == 0) fetch(q + kDepth - 1);
+#pragma unroll
+            for (int w = kColWarps - 1; w >= 0; --w) {
+                const float4 v = sm.pairs[q & 1][w][ch];
+                if (w == warp) enter_c = carry;
+                carry = (bd.warps_end >> w) & 1 ? v.z : fmaf(v.x, carry, v.z);
+                if (learn) through *= v.x;
+            }
+            reset |= bd.warps_end != 0;
+            // the state at the tile's start, through the tile's warps before this one
+#pragma unroll
+            for (int w = 0; w < kTileWarps - 1; ++w) {
+                const int v = warp / kTileWarps * kTileWarps + w;
+                if (v >= warp) break;
+                const float4 ab = sm.pairs[q & 1][v][ch];
+                enter_h = (bd.warps_start >> v) & 1 ? ab.y : fmaf(ab.x, enter_h, ab.y);
+            }
+            fetch_saved(q + 1);
+        }
+        if (learn) {
+            if (q < stages - 1) continue;
+            if (warp == 0) {  // hand the pair on, get the carry that enters
+                const int c = c0 + lane;
+                uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
+                const bool lastpart = part == sp.nt - 1;
+                if (!lastpart) {
+                    if (lane < cols) {
+                        if (reset)
+                            sp.known[part * p.C + c] = carry;
+                        else
+                            sp.pairs[part * p.C + c] = make_float2(through, carry);
+                    }
+                    publish(flags + part, reset ? kKnown : kPair, lane);
+                }
+                const float v = look_back(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
+                if (!lastpart && !reset) {
+                    if (lane < cols) sp.known[part * p.C + c] = fmaf(through, v, carry);
+                    publish(flags + part, kKnown, lane);
+                }
+                if (lane < W) sm.enter[lane] = v;
+            }
+            __syncthreads();
+            carry = sm.enter[ch];
+            continue;
+        }
+        if (warp == kColWarps) continue;
+        auto spread = [&](float v) {
+            return Quad{{__shfl_sync(0xffffffffu, v, l * 4), __shfl_sync(0xffffffffu, v, l * 4 + 1)},
+                        {__shfl_sync(0xffffffffu, v, l * 4 + 2), __shfl_sync(0xffffffffu, v, l * 4 + 3)}};
+        };
+        Quad h = pick(started, exB, fma(exA, spread(enter_h), exB));
+        Quad c = pick(ended, rxE, fma(rxA, spread(enter_c), rxE));
+        // states before each token, from the left; they take u's place
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            if (!plain && ((starts >> k) & 1))
+                h = p.initial_state && on
+                        ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
+                        : all4(0.f);
+            const Quad next = fma(a[k], h, u[k]);
+            u[k] = h;
+            h = next;
+        }
+        // gradients, from the right
+        X* dx = static_cast<X*>(p.dx) + t * p.dx_stride + c0 + l * 4;
+        G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : t * p.da_stride + c0 + l * 4);
+        G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : t * p.db_stride + c0 + l * 4) : nullptr;
+        float sums[kGates == kOneHead ? kRun : 1][2];
+#pragma unroll
+        for (int k = kRun - 1; k >= 0; --k) {
+            const bool in = plain || k < n;
+            if (!plain && in && ((ends >> k) & 1))
+                c = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
+                                                           GDN_DTYPE_F32))
+                                    : all4(0.f);
+            const Quad g = add(widen(AX::get(stage, run, k, l)), c);
+            const Quad x = widen(AX::get(sx, run, k, l));
+            const Quad va = mul(g, u[k]), vb = mul(g, x);
+            Quad vx = g;
+            if constexpr (kHasB) {
+                if constexpr (kGates == kOneHead)
+                    vx = mul(g, shared_gate(hb, k));
+                else
+                    vx = mul(g, widen(AG::get(sb, run, k, l)));
+            }
+            if (in) c = mul(a[k], g);
+            if (in && on) {
+                store_stream(reinterpret_cast<Pack<X>*>(dx + k * p.dx_stride), narrow(vx, X{}));
+                if constexpr (kGates == kPerChannel) {
+                    store_stream(reinterpret_cast<Pack<G>*>(da + k * p.da_stride), narrow(va, G{}));
+                    if constexpr (kHasB) store_stream(reinterpret_cast<Pack<G>*>(db + k * p.db_stride), narrow(vb, G{}));
+                }
+                if (!plain && ((starts >> k) & 1) && p.d_initial)
+                    *reinterpret_cast<float4*>(p.d_initial + static_cast<int64_t>(bd.start_seq[run * kRun + k]) * p.C + c0 + l * 4) = flat(c);
+            }
+            if constexpr (kGates == kOneHead) {
+                sums[k][0] = (va.lo.x + va.lo.y) + (va.hi.x + va.hi.y);
+                sums[k][1] = (vb.lo.x + vb.lo.y) + (vb.hi.x + vb.hi.y);
+            }
+        }
+        if constexpr (kGates == kOneHead) {
+            // Over the run's lanes: each exchange halves the tokens that a lane has sums of, until it has one (kRun / lanes).
+            static_assert(kRun % kLanesRow == 0, "every lane ends with tokens of its own");
+#pragma unroll
+            for (int o = kLanesRow / 2, m = kRun; o > 0; o >>= 1) {
+                m /= 2;
+                const bool up = (l & o) != 0;
+#pragma unroll
+                for (int i = 0; i < m; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float keep = up ? sums[i + m][j] : sums[i][j], give = up ? sums[i][j] : sums[i + m][j];
+                        sums[i][j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+                    }
+            }
+            constexpr int kMine = kRun / kLanesRow;
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const int k = l * kMine + i;
+                if (!plain && k >= n) continue;
+                const int64_t tk = t + k;
+                if (pieces == 1) {
+                    from_f32(sums[i][0], static_cast<G*>(p.da)[tk * p.da_stride + head]);
+                    if constexpr (kHasB) from_f32(sums[i][1], static_cast<G*>(p.db)[tk * p.db_stride + head]);
+                } else {
+                    reinterpret_cast<float2*>(p.scratch)[(tk * p.H + head) * pieces + piece] = make_float2(sums[i][0], sums[i][1]);
+                }
+            }
+        }
+    }
+    if (part == 0 && sp.nt > 1 && warp == 0) {  // the first segment's carry
+        if (lane < cols) sp.known[c0 + lane] = carry;
+        publish(sp.flags + static_cast<int64_t>(blk) * sp.nt, kKnown, lane);
+    }
+}
+
+template <class X, class G, int kGates, bool kHasB, class Col>
+cudaError_t launch_column_backward(const LinearParams& p, const Segments& seg, cudaStream_t stream) {
+    using Shape = BackwardShape<X, G, kGates, kHasB, Col>;
+    ColumnMaps maps{};
+    if (p.T > 0) {
+        const int64_t row = kGates == kOneHead ? p.H : p.C;
+        const int width = kGates == kOneHead ? 16 / static_cast<int>(sizeof(G)) : Shape::W;
+        bool ok = encode_rows(&maps.x, p.x, p.x_dt, p.x_stride, p.C, p.T, Shape::W, Shape::AX::kBox) &&
+                  encode_rows(&maps.dy, p.dy, p.x_dt, p.dy_stride, p.C, p.T, Shape::W, Shape::AX::kBox) &&
+                  encode_rows(&maps.a, p.a, p.gate_dt, p.a_stride, row, p.T, width, Shape::AG::kBox);
+        if (kHasB) ok = ok && encode_rows(&maps.b, p.b, p.gate_dt, p.b_stride, row, p.T, width, Shape::AG::kBox);
+        if (!ok) return cudaErrorInvalidValue;
+    }
+    auto kernel = gdn_linear_column_backward_kernel<X, G, kGates, kHasB, Col>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+    if (e != cudaSuccess) return e;
+    kernel<<<static_cast<unsigned>(seg.space.nt * seg.space.blocks), Col::kThreads, Shape::kSmem, stream>>>(p, seg, maps);
+    if (kGates == kOneHead && p.D > Shape::W && p.T > 0)
+        gdn_linear_join_kernel<G><<<static_cast<unsigned>((p.T * p.H + 255) / 256), 256, 0, stream>>>(p, p.D / Shape::W);
+    return cudaGetLastError();
+}
+
+// Tokens of a run: 8, or 4 where the inputs of an element take 16 bytes and a stage would fill the ring.
+template <class X, class G>
+constexpr int backward_run() {
+    return sizeof(X) == 4 ? 4 : 8;
+}
+
+template <class X, class G, int kGates>
+cudaError_t column_backward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
+    constexpr int R = kGates == kOneHead ? 8 : backward_run<X, G>();
+    if (width == 32)
+        return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R>>(p, seg, stream)
+                   : launch_column_backward<X, G, kGates, false, Column<32, 8, R>>(p, seg, stream);
+    return p.b ? launch_column_backward<X, G, kGates, true, Column<16, 8, R>>(p, seg, stream)
+               : launch_column_backward<X, G, kGates, false, Column<16, 8, R>>(p, seg, stream);
+}
+
+template <class X, class G>
+cudaError_t column_backward_typed(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
+    if (p.gate_div == 1) return column_backward_gates<X, G, kPerChannel>(p, seg, width, stream);
+    return column_backward_gates<X, G, kOneHead>(p, seg, width, stream);
+}
+
+}  // namespace linear
+}  // namespace gdn

@@ -7,10 +7,6 @@ cudaError_t launch_linear_forward_f32(const LinearParams& p, const linear::ScanS
     return linear::forward_typed<float, float>(p, s, vec, stream);
 }
 
-cudaError_t launch_linear_backward_f32(const LinearParams& p, const linear::ScanSpace& s, bool vec, cudaStream_t stream) {
-    return linear::backward_typed<float, float>(p, s, vec, stream);
-}
-
 cudaError_t launch_linear_column_forward_f32(const LinearParams& p, const linear::Segments& s, int width, cudaStream_t stream) {
     return linear::column_forward_typed<float, float>(p, s, width, stream);
 }

@@ -766,10 +766,9 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_backward_kernel(const Lin
 
 // Joins the pieces' sums of heads wider than a block.
 template <class G>
-__global__ void gdn_linear_join_kernel(const LinearParams p) {
+__global__ void gdn_linear_join_kernel(const LinearParams p, int pieces) {
     const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     if (i >= p.T * p.H) return;
-    const int pieces = (p.D + kCols - 1) / kCols;
     float sa = 0.f, sb = 0.f;
     for (int k = 0; k < pieces; ++k) {
         const float2 v = reinterpret_cast<const float2*>(p.scratch)[i * pieces + k];
@@ -789,7 +788,7 @@ cudaError_t backward_gates(const LinearParams& p, const ScanSpace& s, cudaStream
     else
         gdn_linear_backward_kernel<X, G, kVec, kHead, false><<<grid, kThreads, 0, stream>>>(p, s);
     if (kHead && p.D > kCols && p.T > 0)
-        gdn_linear_join_kernel<G><<<static_cast<unsigned>((p.T * p.H + 255) / 256), 256, 0, stream>>>(p);
+        gdn_linear_join_kernel<G><<<static_cast<unsigned>((p.T * p.H + 255) / 256), 256, 0, stream>>>(p, (p.D + kCols - 1) / kCols);
     return cudaGetLastError();
 }
 
