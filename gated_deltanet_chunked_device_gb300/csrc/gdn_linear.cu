@@ -212,7 +212,7 @@ cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaS
     if (p.gate_div == 1) vec = vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
     if (vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
         int width;
-        linear::Segments seg = segments(p, p.gate_div == 1 && p.x_dt == GDN_DTYPE_F32 ? 4 : 8, &width);
+        linear::Segments seg = segments(p, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &width);
         if (p.gate_div == 1 || linear::one_head(p, width)) {
             const cudaError_t e = segment_space(p, workspace, stream, &seg);
             if (e != cudaSuccess) return e;

@@ -22,7 +22,7 @@
 namespace gdn {
 namespace linear {
 
-// A block's shape: W channels, NW warps at work (and one more, which finds the sequences' bounds), runs of R tokens.
+// A block's shape: W channels, NW warps, runs of R tokens.
 template <int W, int NW, int R>
 struct Column {
     static constexpr int kWidth = W, kRun = R;
@@ -31,7 +31,7 @@ struct Column {
     static constexpr int kWarpTokens = kRuns * kRun;
     static constexpr int kTokens = NW * kWarpTokens;
     static constexpr int kWarps = NW;
-    static constexpr int kThreads = 32 * (NW + 1);
+    static constexpr int kThreads = 32 * NW;
 };
 
 constexpr int kRingBytes = 192 * 1024;           // shared memory of the ring, at most
@@ -42,6 +42,15 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     memcpy(&x, &a, 8);
     memcpy(&y, &b, 8);
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    float2 r;
+    memcpy(&r, &d, 8);
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t x, y, d;
+    memcpy(&x, &a, 8);
+    memcpy(&y, &b, 8);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
     float2 r;
     memcpy(&r, &d, 8);
     return r;
@@ -69,9 +78,7 @@ __device__ __forceinline__ float4 flat(Quad v) { return make_float4(v.lo.x, v.lo
 __device__ __forceinline__ Quad pick(bool c, Quad a, Quad b) {
     return {{c ? a.lo.x : b.lo.x, c ? a.lo.y : b.lo.y}, {c ? a.hi.x : b.hi.x, c ? a.hi.y : b.hi.y}};
 }
-__device__ __forceinline__ Quad add(Quad a, Quad b) {
-    return {{a.lo.x + b.lo.x, a.lo.y + b.lo.y}, {a.hi.x + b.hi.x, a.hi.y + b.hi.y}};
-}
+__device__ __forceinline__ Quad add(Quad a, Quad b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
 __device__ __forceinline__ Quad shift_down(Quad v, int lanes) {
     return {{__shfl_down_sync(0xffffffffu, v.lo.x, lanes), __shfl_down_sync(0xffffffffu, v.lo.y, lanes)},
             {__shfl_down_sync(0xffffffffu, v.hi.x, lanes), __shfl_down_sync(0xffffffffu, v.hi.y, lanes)}};
@@ -416,10 +423,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 
     if (threadIdx.x == 0)
         for (int q = 0; q < kDepth; ++q) fetch(q);
-    if (warp == kColWarps) {
-        bounds(0);
-        if (blk == 0) check_bounds(p, part, sp.nt, lane);
-    }
+    if (warp == kColWarps - 1) bounds(0);
+    if (warp == kColWarps - 2 && blk == 0) check_bounds(p, part, sp.nt, lane);
     __syncthreads();
     float carry = 0.f, through = 1.f;  // of channel `ch`: the state (in steps that learn, from zero), the gates' product
     bool reset = false;                // whether a sequence has started
@@ -432,9 +437,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         uint32_t starts = 0;
         int n = kRun;
         bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
-        if (warp == kColWarps) {
-            bounds(q + 1);
-        } else {
+        if (warp == kColWarps - 1) bounds(q + 1);
+        {
             plain = (bd.plain >> warp) & 1;
             take(q);
 #pragma unroll
@@ -522,16 +526,22 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         // place in the ring is free; the bounds of the next stage are known.
         __syncthreads();
         float enter = carry;
-        if (warp < kColWarps) {
+        {
             if (threadIdx.x == 0) fetch(q + kDepth);
+            float2 ab[kColWarps];
+#pragma unroll
+            for (int w = 0; w < kColWarps; ++w) ab[w] = sm.pairs[q & 1][w][ch];
+            const uint32_t resets = bd.warps_start;
 #pragma unroll
             for (int w = 0; w < kColWarps; ++w) {
-                const float2 ab = sm.pairs[q & 1][w][ch];
                 if (w == warp) enter = carry;
-                carry = (bd.warps_start >> w) & 1 ? ab.y : fmaf(ab.x, carry, ab.y);
-                if (learn) through *= ab.x;
+                carry = fmaf(ab[w].x, carry, ab[w].y);
+                if (resets != 0 && ((resets >> w) & 1)) carry = ab[w].y;
             }
-            reset |= bd.warps_start != 0;
+            if (learn)
+#pragma unroll
+                for (int w = 0; w < kColWarps; ++w) through *= ab[w].x;
+            reset |= resets != 0;
         }
         if (learn) {
             if (q < stages - 1) continue;
@@ -559,7 +569,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             carry = sm.enter[ch];
             continue;
         }
-        if (warp < kColWarps) {
+        {
             const Quad e = {{__shfl_sync(0xffffffffu, enter, l * 4), __shfl_sync(0xffffffffu, enter, l * 4 + 1)},
                             {__shfl_sync(0xffffffffu, enter, l * 4 + 2), __shfl_sync(0xffffffffu, enter, l * 4 + 3)}};
             Quad h = pick(before, exB, fma(exA, e, exB));

@@ -27,7 +27,8 @@ struct BackwardShape {
     static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
     struct Tables {
         StageBounds<kTokens> bounds[3];
-        alignas(16) float4 pairs[2][Col::kWarps][W];  // a warp's tokens: product of the gates, state and carry from zero
+        alignas(16) float2 pairs[2][Col::kWarps][W];  // a warp's tokens: product of the gates, carry from zero
+        alignas(16) float states[2][Col::kWarps][W];  // and the state from zero
         float enter[W];
         uint64_t full[kDepth];
         uint32_t ticket;
@@ -125,12 +126,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 
     if (threadIdx.x == 0)
         for (int q = 0; q < kDepth - 1; ++q) fetch(q);
-    if (warp == kColWarps) {
-        bounds(0);
-        if (blk == 0) check_bounds(p, part, sp.nt, lane);
-    } else {
-        fetch_saved(0);
-    }
+    if (warp == kColWarps - 1) bounds(0);
+    if (warp == kColWarps - 2 && blk == 0) check_bounds(p, part, sp.nt, lane);
+    fetch_saved(0);
     __syncthreads();
     float carry = 0.f, through = 1.f;  // of channel `ch`: the carry (in steps that learn, from zero), the gates' product
     bool reset = false, ok = true;     // whether a sequence has ended; until a wait runs out
@@ -151,9 +149,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         auto shared_gate = [&](const float(&held)[kHeld], int k) {
             return all4(__shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow));
         };
-        if (warp == kColWarps) {
-            bounds(q + 1);
-        } else {
+        if (warp == kColWarps - 1) bounds(q + 1);
+        {
             plain = (bd.plain >> warp) & 1;
             if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
                 ok = false;
@@ -263,39 +260,43 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 }
                 started = (rs & ((1u << sub) - 1u)) != 0;
             }
-            // the warp's: the product and the carry are the first run's, the state is the last one's
-            const Quad lastB = {{__shfl_sync(0xffffffffu, B.lo.x, 32 - kLanesRow + l), __shfl_sync(0xffffffffu, B.lo.y, 32 - kLanesRow + l)},
-                                {__shfl_sync(0xffffffffu, B.hi.x, 32 - kLanesRow + l), __shfl_sync(0xffffffffu, B.hi.y, 32 - kLanesRow + l)}};
+            // the warp's: the product and the carry are the first run's
             if (sub == 0) {
-                float4* o = &sm.pairs[q & 1][warp][l * 4];
-                o[0] = make_float4(RA.lo.x, lastB.lo.x, E.lo.x, 0.f);
-                o[1] = make_float4(RA.lo.y, lastB.lo.y, E.lo.y, 0.f);
-                o[2] = make_float4(RA.hi.x, lastB.hi.x, E.hi.x, 0.f);
-                o[3] = make_float4(RA.hi.y, lastB.hi.y, E.hi.y, 0.f);
+                float4* o = reinterpret_cast<float4*>(&sm.pairs[q & 1][warp][l * 4]);
+                o[0] = make_float4(RA.lo.x, E.lo.x, RA.lo.y, E.lo.y);
+                o[1] = make_float4(RA.hi.x, E.hi.x, RA.hi.y, E.hi.y);
             }
+            // the state is the last run's
+            if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&sm.states[q & 1][warp][l * 4]) = flat(B);
         }
         // The step's one barrier.  Past it: every warp's pair is there, nobody reads the stage before any more (its place in
         // the ring is free), and the bounds of the next stage are known.
         __syncthreads();
         float enter_c = carry, enter_h = saved;
-        if (warp < kColWarps) {
+        {
             if (threadIdx.x == 0) fetch(q + kDepth - 1);
+            float2 ae[kColWarps];
 #pragma unroll
-            for (int w = kColWarps - 1; w >= 0; --w) {
-                const float4 v = sm.pairs[q & 1][w][ch];
-                if (w == warp) enter_c = carry;
-                carry = (bd.warps_end >> w) & 1 ? v.z : fmaf(v.x, carry, v.z);
-                if (learn) through *= v.x;
-            }
-            reset |= bd.warps_end != 0;
+            for (int w = 0; w < kColWarps; ++w) ae[w] = sm.pairs[q & 1][w][ch];
             // the state at the tile's start, through the tile's warps before this one
 #pragma unroll
             for (int w = 0; w < kTileWarps - 1; ++w) {
                 const int v = warp / kTileWarps * kTileWarps + w;
                 if (v >= warp) break;
-                const float4 ab = sm.pairs[q & 1][v][ch];
-                enter_h = (bd.warps_start >> v) & 1 ? ab.y : fmaf(ab.x, enter_h, ab.y);
+                const float b = sm.states[q & 1][v][ch];
+                enter_h = (bd.warps_start >> v) & 1 ? b : fmaf(sm.pairs[q & 1][v][ch].x, enter_h, b);
             }
+            const uint32_t resets = bd.warps_end;
+#pragma unroll
+            for (int w = kColWarps - 1; w >= 0; --w) {
+                if (w == warp) enter_c = carry;
+                carry = fmaf(ae[w].x, carry, ae[w].y);
+                if (resets != 0 && ((resets >> w) & 1)) carry = ae[w].y;
+            }
+            if (learn)
+#pragma unroll
+                for (int w = 0; w < kColWarps; ++w) through *= ae[w].x;
+            reset |= resets != 0;
             fetch_saved(q + 1);
         }
         if (learn) {
@@ -324,61 +325,72 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             carry = sm.enter[ch];
             continue;
         }
-        if (warp == kColWarps) continue;
         auto spread = [&](float v) {
             return Quad{{__shfl_sync(0xffffffffu, v, l * 4), __shfl_sync(0xffffffffu, v, l * 4 + 1)},
                         {__shfl_sync(0xffffffffu, v, l * 4 + 2), __shfl_sync(0xffffffffu, v, l * 4 + 3)}};
         };
         Quad h = pick(started, exB, fma(exA, spread(enter_h), exB));
         Quad c = pick(ended, rxE, fma(rxA, spread(enter_c), rxE));
-        // states before each token, from the left; they take u's place
-#pragma unroll
-        for (int k = 0; k < kRun; ++k) {
-            if (!plain && ((starts >> k) & 1))
-                h = p.initial_state && on
-                        ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
-                        : all4(0.f);
-            const Quad next = fma(a[k], h, u[k]);
-            u[k] = h;
-            h = next;
-        }
-        // gradients, from the right
-        X* dx = static_cast<X*>(p.dx) + t * p.dx_stride + c0 + l * 4;
-        G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : t * p.da_stride + c0 + l * 4);
-        G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : t * p.db_stride + c0 + l * 4) : nullptr;
         float sums[kGates == kOneHead ? kRun : 1][2];
+        // The tokens once more; `whole`: all of them are there, with neither a start nor an end.
+        auto tokens = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+            // states before each token, from the left; they take u's place
 #pragma unroll
-        for (int k = kRun - 1; k >= 0; --k) {
-            const bool in = plain || k < n;
-            if (!plain && in && ((ends >> k) & 1))
-                c = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
-                                                           GDN_DTYPE_F32))
-                                    : all4(0.f);
-            const Quad g = add(widen(AX::get(stage, run, k, l)), c);
-            const Quad x = widen(AX::get(sx, run, k, l));
-            const Quad va = mul(g, u[k]), vb = mul(g, x);
-            Quad vx = g;
-            if constexpr (kHasB) {
-                if constexpr (kGates == kOneHead)
-                    vx = mul(g, shared_gate(hb, k));
-                else
-                    vx = mul(g, widen(AG::get(sb, run, k, l)));
+            for (int k = 0; k < kRun; ++k) {
+                if (!kWhole && ((starts >> k) & 1))
+                    h = p.initial_state && on
+                            ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
+                            : all4(0.f);
+                const Quad v = h;
+                if (k < kRun - 1) h = fma(a[k], h, u[k]);
+                u[k] = v;
             }
-            if (in) c = mul(a[k], g);
-            if (in && on) {
-                store_stream(reinterpret_cast<Pack<X>*>(dx + k * p.dx_stride), narrow(vx, X{}));
-                if constexpr (kGates == kPerChannel) {
-                    store_stream(reinterpret_cast<Pack<G>*>(da + k * p.da_stride), narrow(va, G{}));
-                    if constexpr (kHasB) store_stream(reinterpret_cast<Pack<G>*>(db + k * p.db_stride), narrow(vb, G{}));
+            // gradients, from the right
+            X* dx = static_cast<X*>(p.dx) + (t + kRun - 1) * p.dx_stride + c0 + l * 4;
+            G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.da_stride + c0 + l * 4);
+            G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.db_stride + c0 + l * 4) : nullptr;
+#pragma unroll
+            for (int k = kRun - 1; k >= 0; --k) {
+                const bool in = kWhole || k < n;
+                if (!kWhole && in && ((ends >> k) & 1))
+                    c = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
+                                                               GDN_DTYPE_F32))
+                                        : all4(0.f);
+                const Quad g = add(widen(AX::get(stage, run, k, l)), c);
+                const Quad va = mul(g, u[k]), vb = mul(g, widen(AX::get(sx, run, k, l)));
+                Quad vx = g;
+                if constexpr (kHasB) {
+                    if constexpr (kGates == kOneHead)
+                        vx = mul(g, shared_gate(hb, k));
+                    else
+                        vx = mul(g, widen(AG::get(sb, run, k, l)));
                 }
-                if (!plain && ((starts >> k) & 1) && p.d_initial)
-                    *reinterpret_cast<float4*>(p.d_initial + static_cast<int64_t>(bd.start_seq[run * kRun + k]) * p.C + c0 + l * 4) = flat(c);
+                if (in) c = mul(a[k], g);
+                if (in && on) {
+                    store_stream(reinterpret_cast<Pack<X>*>(dx), narrow(vx, X{}));
+                    if constexpr (kGates == kPerChannel) {
+                        store_stream(reinterpret_cast<Pack<G>*>(da), narrow(va, G{}));
+                        if constexpr (kHasB) store_stream(reinterpret_cast<Pack<G>*>(db), narrow(vb, G{}));
+                    }
+                    if (!kWhole && ((starts >> k) & 1) && p.d_initial)
+                        *reinterpret_cast<float4*>(p.d_initial + static_cast<int64_t>(bd.start_seq[run * kRun + k]) * p.C + c0 + l * 4) = flat(c);
+                }
+                dx -= p.dx_stride;
+                if constexpr (kGates == kPerChannel) {
+                    da -= p.da_stride;
+                    if constexpr (kHasB) db -= p.db_stride;
+                } else {
+                    const float2 sa = add2(va.lo, va.hi), sb2 = add2(vb.lo, vb.hi);
+                    sums[k][0] = sa.x + sa.y;
+                    sums[k][1] = sb2.x + sb2.y;
+                }
             }
-            if constexpr (kGates == kOneHead) {
-                sums[k][0] = (va.lo.x + va.lo.y) + (va.hi.x + va.hi.y);
-                sums[k][1] = (vb.lo.x + vb.lo.y) + (vb.hi.x + vb.hi.y);
-            }
-        }
+        };
+        if (plain)
+            tokens(std::true_type{});
+        else
+            tokens(std::false_type{});
         if constexpr (kGates == kOneHead) {
             // Over the run's lanes: each exchange halves the tokens that a lane has sums of, until it has one (kRun / lanes).
             static_assert(kRun % kLanesRow == 0, "every lane ends with tokens of its own");
@@ -437,15 +449,15 @@ cudaError_t launch_column_backward(const LinearParams& p, const Segments& seg, c
     return cudaGetLastError();
 }
 
-// Tokens of a run: 8, or 4 where the inputs of an element take 16 bytes and a stage would fill the ring.
-template <class X, class G>
+// Tokens of a run: 8, or 4 where gates per channel are fp32 and two stages of 8 would fill the ring.
+template <class G, int kGates>
 constexpr int backward_run() {
-    return sizeof(X) == 4 ? 4 : 8;
+    return kGates == kPerChannel && sizeof(G) == 4 ? 4 : 8;
 }
 
 template <class X, class G, int kGates>
 cudaError_t column_backward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
-    constexpr int R = kGates == kOneHead ? 8 : backward_run<X, G>();
+    constexpr int R = backward_run<G, kGates>();
     if (width == 32)
         return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R>>(p, seg, stream)
                    : launch_column_backward<X, G, kGates, false, Column<32, 8, R>>(p, seg, stream);
