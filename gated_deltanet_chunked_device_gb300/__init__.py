@@ -205,6 +205,25 @@ def gdn_prefill_cp_segments(plan, seq_lens, sm_count_hint: int = 0):
     return int(most), [int(segs[i]) for i in range(n)]
 
 
+class on_device:
+    """The raw current stream of a CUDA device, with that device current inside the block."""
+
+    __slots__ = ("index", "before")
+
+    def __init__(self, index):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
 def gdn_prefill_plan_destroy(plan) -> None:
     lib().gdn_prefill_plan_destroy(plan)
 

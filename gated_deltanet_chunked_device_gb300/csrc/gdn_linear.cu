@@ -1,10 +1,6 @@
-// gdn_linear.cu -- kernels of the gated linear recurrence (include/gdn_linear.h):
-//
-//     h_t = a_t h_{t-1} + b_t x_t
-//
-// One block of 128 threads per (sequence, head); a thread owns every 128th
-// channel of the head and walks the sequence's tokens.  Right for every case,
-// and as slow as the longest sequence.
+// gdn_linear.cu -- how runs of the gated linear recurrence go
+// (include/gdn_linear.h): which kernels, their workspace and maps; and the
+// decode step's kernel.
 #include <cudaTypedefs.h>
 
 #include "gdn_linear_column.cuh"
@@ -39,56 +35,86 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 constexpr int kThreads = 128;
 
-__device__ __forceinline__ void report(int32_t* status, int32_t bit) {
-    if (status) atomicOr(status, bit);
-}
-
-// The sequence's tokens [s, e); false (and reported) when cu_seqlens is malformed.
-__device__ __forceinline__ bool seq_range(const LinearParams& p, int64_t i, int64_t& s, int64_t& e) {
-    if (p.m > 0) {
-        s = i * p.m;
-        e = s + p.m;
-        return true;
+// One thread per sequence and 4 channels (adjacent ones with kVec, else one channel): its state stays in registers
+// through the tokens.
+template <class X, class G, bool kVec>
+__global__ void __launch_bounds__(kThreads) gdn_linear_decode_kernel(const LinearParams p) {
+    constexpr int V = kVec ? 4 : 1;
+    const int per_seq = p.C / V;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    const int64_t i = id / per_seq;
+    if (i >= p.N) return;
+    const int c = static_cast<int>(id % per_seq) * V;
+    const int64_t row = linear::state_row(p, i);
+    if (row < 0) return;
+    const int64_t off = row * p.state_stride + c;
+    const int gc = p.gate_div == 1 ? c : c / p.gate_div;
+    float h[4] = {0.f, 0.f, 0.f, 0.f};
+    if (p.initial_state) {
+        if constexpr (kVec)
+            state_load4(p.initial_state, off, p.state_dt, h);
+        else
+            h[0] = load1(p.initial_state, off, p.state_dt);
     }
-    if (!p.cu_seqlens) {
-        s = 0;
-        e = p.T;
-        return true;
-    }
-    s = load_index(p.cu_seqlens, p.cu_i64, i);
-    e = load_index(p.cu_seqlens, p.cu_i64, i + 1);
-    const bool ok = s >= 0 && s <= e && e <= p.T && (i > 0 || s == 0) && (i + 1 < p.N || e == p.T);
-    if (!ok) report(p.status, GDN_DEVICE_ERR_CU_SEQLENS);
-    return ok;
-}
-
-__device__ __forceinline__ bool seq_row(const LinearParams& p, int64_t i, int64_t& row) {
-    row = i;
-    if (!p.state_indices) return true;
-    row = load_index(p.state_indices, p.idx_i64, i);
-    if (row >= 0 && row < p.n_pool) return true;
-    report(p.status, GDN_DEVICE_ERR_STATE_INDEX_RANGE);
-    return false;
-}
-
-__global__ void __launch_bounds__(kThreads) gdn_linear_decode_kernel(LinearParams p) {
-    const int64_t i = blockIdx.x / p.H;
-    const int32_t h = static_cast<int32_t>(blockIdx.x % p.H);
-    int64_t s, e, row;
-    if (!seq_range(p, i, s, e) || !seq_row(p, i, row)) return;
-    for (int32_t d = threadIdx.x; d < p.D; d += kThreads) {
-        const int64_t c = static_cast<int64_t>(h) * p.D + d;
-        float st = p.initial_state ? load1(p.initial_state, row * p.state_stride + c, p.state_dt) : 0.f;
-        for (int64_t t = s; t < e; ++t) {
-            float u = load1(p.x, t * p.x_stride + c, p.x_dt);
-            if (p.b) u *= load1(p.b, t * p.b_stride + c / p.gate_div, p.gate_dt);
-            st = fmaf(load1(p.a, t * p.a_stride + c / p.gate_div, p.gate_dt), st, u);
-            store1(p.y, t * p.y_stride + c, p.x_dt, st);
-            if (p.tile_states && (t % GDN_LINEAR_TILE == GDN_LINEAR_TILE - 1 || t == p.T - 1))
-                p.tile_states[t / GDN_LINEAR_TILE * p.C + c] = st;
+    const X* x = static_cast<const X*>(p.x) + c;
+    const G* a = static_cast<const G*>(p.a) + gc;
+    const G* b = static_cast<const G*>(p.b) + gc;
+    X* y = static_cast<X*>(p.y) + c;
+#pragma unroll 4
+    for (int j = 0; j < p.m; ++j) {
+        const int64_t t = i * p.m + j;
+        float ga[4], u[4];
+        if constexpr (kVec) {
+            const linear::Pack<X> px = linear::load_stream(reinterpret_cast<const linear::Pack<X>*>(x + t * p.x_stride));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) u[k] = linear::to_f32(px.v[k]);
+            if (p.gate_div == 1) {
+                const linear::Pack<G> pa = linear::load_stream(reinterpret_cast<const linear::Pack<G>*>(a + t * p.a_stride));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) ga[k] = linear::to_f32(pa.v[k]);
+                if (p.b) {
+                    const linear::Pack<G> pb = linear::load_stream(reinterpret_cast<const linear::Pack<G>*>(b + t * p.b_stride));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) u[k] *= linear::to_f32(pb.v[k]);
+                }
+            } else {
+                ga[0] = ga[1] = ga[2] = ga[3] = linear::to_f32(a[t * p.a_stride]);
+                if (p.b) {
+                    const float s = linear::to_f32(b[t * p.b_stride]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) u[k] *= s;
+                }
+            }
+        } else {
+            u[0] = linear::to_f32(x[t * p.x_stride]);
+            ga[0] = linear::to_f32(a[t * p.a_stride]);
+            if (p.b) u[0] *= linear::to_f32(b[t * p.b_stride]);
         }
-        if (p.output_state) store1(p.output_state, row * p.state_stride + c, p.state_dt, st);
+#pragma unroll
+        for (int k = 0; k < V; ++k) h[k] = fmaf(ga[k], h[k], u[k]);
+        if constexpr (kVec) {
+            linear::store4<true>(y + t * p.y_stride, 0, 4, h);
+        } else {
+            linear::from_f32(h[0], y[t * p.y_stride]);
+        }
     }
+    if (p.output_state) {
+        if constexpr (kVec)
+            state_store4(p.output_state, off, p.state_dt, h);
+        else
+            store1(p.output_state, off, p.state_dt, h[0]);
+    }
+}
+
+template <class X, class G>
+cudaError_t decode_typed(const LinearParams& p, bool vec, cudaStream_t stream) {
+    const int64_t threads = static_cast<int64_t>(p.N) * (p.C / (vec ? 4 : 1)), blocks = (threads + kThreads - 1) / kThreads;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (vec)
+        gdn_linear_decode_kernel<X, G, true><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    else
+        gdn_linear_decode_kernel<X, G, false><<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(p);
+    return cudaGetLastError();
 }
 
 // Whether rows of this tensor can be read 4 elements at a time.
@@ -136,29 +162,60 @@ linear::Segments segments(const LinearParams& p, int run, int* width) {
     return s;
 }
 
-// The workspace as the kernels of columns take it.
-cudaError_t segment_space(const LinearParams& p, void* workspace, cudaStream_t stream, linear::Segments* seg) {
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    linear::ScanSpace& s = seg->space;
-    const size_t zeroed = 256 + sizeof(uint32_t) * s.nt * s.blocks, pairs = (zeroed + 255) / 256 * 256;
-    s.ticket = reinterpret_cast<uint32_t*>(ws);
-    s.flags = reinterpret_cast<uint32_t*>(ws + 256);
-    s.pairs = reinterpret_cast<float2*>(ws + pairs);
-    s.known = reinterpret_cast<float*>(ws + pairs + sizeof(float2) * s.nt * p.C);
-    return s.nt > 1 ? cudaMemsetAsync(ws, 0, zeroed, stream) : cudaSuccess;
+// How a run goes: by columns, or (rows that cannot be copied 16 bytes at a time, heads that do not fit a column) by tiles.
+struct Route {
+    bool column, vec;
+    int width;                 // of the columns
+    linear::Segments seg;      // columns
+    int64_t tiles, blocks;     // tiles
+    ScanLayout layout;
+    size_t sums;               // bytes of a head's sums, after the layout
+};
+
+void finish_route(const LinearParams& p, Route* r) {
+    r->tiles = tiles_of(p.T);
+    r->layout = r->column ? scan_layout(r->seg.space.nt, r->seg.space.blocks, p.C) : scan_layout(r->tiles, 4 * r->blocks, p.C);
 }
 
-// The workspace as the kernels take it; what has to start from zero is zeroed, where there is more than one tile.
-cudaError_t scan_space(const LinearParams& p, void* workspace, int64_t blocks, cudaStream_t stream, linear::ScanSpace* s) {
-    const ScanLayout l = scan_layout(p.T, p.C, p.gate_div != 1 ? p.D : 0);
+Route forward_route(const LinearParams& p) {
+    Route r{};
+    r.vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
+    r.column = r.vec && inputs_wide(p);
+    if (r.column) r.seg = segments(p, 8, &r.width);
+    r.blocks = (p.C + linear::kCols - 1) / linear::kCols;
+    finish_route(p, &r);
+    return r;
+}
+
+Route backward_route(const LinearParams& p) {
+    Route r{};
+    const int64_t head_dim = p.gate_div != 1 ? p.D : 0;
+    r.vec = rows_vector(p) && vector_of_4(p.dy, p.dy_stride, p.x_dt) && vector_of_4(p.dx, p.dx_stride, p.x_dt) &&
+            vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
+    if (p.gate_div == 1) r.vec = r.vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
+    if (r.vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
+        r.seg = segments(p, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);
+        r.column = p.gate_div == 1 || linear::one_head(p, r.width);
+    }
+    r.blocks = backward_blocks(p.C, head_dim);
+    r.sums = sums_bytes(p.T, p.C, head_dim, r.column ? r.width : linear::kCols);
+    finish_route(p, &r);
+    return r;
+}
+
+// The workspace as the kernels take it; what has to start from zero is zeroed, where anything is handed on.
+cudaError_t scan_space(const Route& r, void* workspace, cudaStream_t stream, linear::ScanSpace* s) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    s->nt = l.nt;
-    s->blocks = static_cast<uint32_t>(blocks);
+    if (!r.column) {
+        s->nt = r.tiles;
+        s->blocks = static_cast<uint32_t>(r.blocks);
+    }
+    if (r.layout.total == 0) return cudaSuccess;
     s->ticket = reinterpret_cast<uint32_t*>(ws);
     s->flags = reinterpret_cast<uint32_t*>(ws + 256);
-    s->pairs = reinterpret_cast<float2*>(ws + l.pairs);
-    s->known = reinterpret_cast<float*>(ws + l.known);
-    return l.nt > 1 ? cudaMemsetAsync(ws, 0, l.zeroed, stream) : cudaSuccess;
+    s->pairs = reinterpret_cast<float2*>(ws + r.layout.zeroed);
+    s->known = reinterpret_cast<float*>(ws + r.layout.known);
+    return cudaMemsetAsync(ws, 0, r.layout.zeroed, stream);
 }
 
 }  // namespace
@@ -183,55 +240,53 @@ int multiprocessors() {
     return n > 0 ? n : 1;
 }
 
+size_t linear_forward_workspace(const LinearParams& p) { return forward_route(p).layout.total; }
+
+size_t linear_backward_workspace(const LinearParams& p) {
+    const Route r = backward_route(p);
+    return r.layout.total + r.sums;
+}
+
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream) {
-    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
-    if (vec && inputs_wide(p)) {
-        int width;
-        linear::Segments seg = segments(p, 8, &width);
-        const cudaError_t e = segment_space(p, workspace, stream, &seg);
-        if (e != cudaSuccess) return e;
-        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, seg, width, stream);
-        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, seg, width, stream);
-        return launch_linear_column_forward_f32(p, seg, width, stream);
-    }
+    Route r = forward_route(p);
     linear::ScanSpace s{};
-    const cudaError_t e = scan_space(p, workspace, (p.C + linear::kCols - 1) / linear::kCols, stream, &s);
+    const cudaError_t e = scan_space(r, workspace, stream, r.column ? &r.seg.space : &s);
     if (e != cudaSuccess) return e;
+    if (r.column) {
+        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_forward_bf16(p, r.seg, r.width, stream);
+        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_forward_f16(p, r.seg, r.width, stream);
+        return launch_linear_column_forward_f32(p, r.seg, r.width, stream);
+    }
     if (p.tile_states) s.known = p.tile_states;
-    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, vec, stream);
-    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, vec, stream);
-    return launch_linear_forward_f32(p, s, vec, stream);
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_forward_bf16(p, s, r.vec, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_forward_f16(p, s, r.vec, stream);
+    return launch_linear_forward_f32(p, s, r.vec, stream);
 }
 
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream) {
-    LinearParams q = p;
-    const int64_t head_dim = p.gate_div != 1 ? p.D : 0;
-    q.scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + scan_layout(p.T, p.C, head_dim).sums);
-    bool vec = rows_vector(p) && vector_of_4(p.dy, p.dy_stride, p.x_dt) && vector_of_4(p.dx, p.dx_stride, p.x_dt) &&
-               vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
-    if (p.gate_div == 1) vec = vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
-    if (vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
-        int width;
-        linear::Segments seg = segments(p, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &width);
-        if (p.gate_div == 1 || linear::one_head(p, width)) {
-            const cudaError_t e = segment_space(p, workspace, stream, &seg);
-            if (e != cudaSuccess) return e;
-            if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_backward_bf16(q, seg, width, stream);
-            if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_backward_f16(q, seg, width, stream);
-            return launch_linear_column_backward_f32(q, seg, width, stream);
-        }
-    }
+    Route r = backward_route(p);
     linear::ScanSpace s{};
-    const cudaError_t e = scan_space(p, workspace, backward_blocks(p.C, head_dim), stream, &s);
+    const cudaError_t e = scan_space(r, workspace, stream, r.column ? &r.seg.space : &s);
     if (e != cudaSuccess) return e;
-    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_backward_bf16(q, s, vec, stream);
-    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_backward_f16(q, s, vec, stream);
-    return launch_linear_backward_f32(q, s, vec, stream);
+    LinearParams q = p;
+    if (r.sums > 0) q.scratch = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + r.layout.total);
+    if (r.column) {
+        if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_column_backward_bf16(q, r.seg, r.width, stream);
+        if (p.x_dt == GDN_DTYPE_F16) return launch_linear_column_backward_f16(q, r.seg, r.width, stream);
+        return launch_linear_column_backward_f32(q, r.seg, r.width, stream);
+    }
+    if (p.x_dt == GDN_DTYPE_BF16) return launch_linear_backward_bf16(q, s, r.vec, stream);
+    if (p.x_dt == GDN_DTYPE_F16) return launch_linear_backward_f16(q, s, r.vec, stream);
+    return launch_linear_backward_f32(q, s, r.vec, stream);
 }
 
 cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream) {
-    gdn_linear_decode_kernel<<<static_cast<unsigned>(static_cast<int64_t>(p.N) * p.H), kThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const bool vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt);
+    const bool wide_gates = p.gate_dt == GDN_DTYPE_F32;
+    if (p.x_dt == GDN_DTYPE_F32) return decode_typed<float, float>(p, vec, stream);
+    if (p.x_dt == GDN_DTYPE_BF16)
+        return wide_gates ? decode_typed<__nv_bfloat16, float>(p, vec, stream) : decode_typed<__nv_bfloat16, __nv_bfloat16>(p, vec, stream);
+    return wide_gates ? decode_typed<__half, float>(p, vec, stream) : decode_typed<__half, __half>(p, vec, stream);
 }
 
 }  // namespace gdn

@@ -73,26 +73,34 @@ inline int64_t backward_blocks(int64_t C, int64_t head_dim) {
     return (C + width - 1) / width;
 }
 
-// Workspace of the scans over T tokens and C channels: the ticket and the flags (zeroed before each run), what tiles
-// hand on, and the sums of heads wider than a block.
+// Sums that the blocks of a head leave per token, where a head has more than one: a block has `width` channels.
+inline size_t sums_bytes(int64_t T, int64_t C, int64_t head_dim, int64_t width) {
+    if (head_dim <= width) return 0;
+    return sizeof(float2) * static_cast<size_t>(T) * (C / head_dim) * ((head_dim + width - 1) / width);
+}
+
+// What `places` of a scan (tiles, or segments of columns) hand on: the ticket and the flags (zeroed before each run), the
+// pairs and the known states.
 struct ScanLayout {
-    size_t zeroed, pairs, known, sums, total;
-    int64_t nt, blocks;
+    size_t zeroed, known, total;
 };
 
-inline ScanLayout scan_layout(int64_t T, int64_t C, int64_t head_dim) {
+inline ScanLayout scan_layout(int64_t places, int64_t flags, int64_t C) {
     ScanLayout l{};
-    l.nt = T > 0 ? (T + GDN_LINEAR_TILE - 1) / GDN_LINEAR_TILE : 1;
-    l.blocks = backward_blocks(C, head_dim);  // the forward pass has no more
+    if (places < 2) return l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    l.zeroed = 256 + up(sizeof(uint32_t) * 4 * static_cast<size_t>(l.nt) * l.blocks);
-    l.pairs = l.zeroed;
-    l.known = l.pairs + up(sizeof(float2) * static_cast<size_t>(l.nt) * C);
-    l.sums = l.known + up(sizeof(float) * static_cast<size_t>(l.nt) * C);
-    l.total = l.sums;
-    if (head_dim > 16)  // a block has 16 channels or more
-        l.total += up(sizeof(float2) * static_cast<size_t>(T) * (C / head_dim) * ((head_dim + 15) / 16));
+    l.zeroed = 256 + up(sizeof(uint32_t) * static_cast<size_t>(places) * flags);
+    l.known = l.zeroed + up(sizeof(float2) * static_cast<size_t>(places) * C);
+    l.total = l.known + up(sizeof(float) * static_cast<size_t>(places) * C);
     return l;
+}
+
+inline int64_t tiles_of(int64_t T) { return T > 0 ? (T + GDN_LINEAR_TILE - 1) / GDN_LINEAR_TILE : 1; }
+
+// Any run's workspace with these bounds.  Columns have at most a twentieth of the tiles as segments, with a flag for
+// every 16 channels; tiles have 4 flags for every 128 channels, or fewer.
+inline size_t workspace_bound(int64_t T, int64_t C, int64_t head_dim) {
+    return scan_layout(tiles_of(T), 4 * backward_blocks(C, head_dim) + (C + 15) / 16, C).total + sums_bytes(T, C, head_dim, 16) + 256;
 }
 
 int multiprocessors();  // of the current device
@@ -101,7 +109,9 @@ int multiprocessors();  // of the current device
 // outside reads as zeros.
 bool encode_rows(CUtensorMap* map, const void* base, int32_t dt, int64_t stride, int64_t C, int64_t T, int width, int tokens);
 
-// workspace: scan_layout's total bytes
+// A run's workspace in bytes (at most workspace_bound of the plan's bounds), and the runs themselves.
+size_t linear_forward_workspace(const LinearParams& p);
+size_t linear_backward_workspace(const LinearParams& p);
 cudaError_t launch_linear_forward(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_backward(const LinearParams& p, void* workspace, cudaStream_t stream);
 cudaError_t launch_linear_decode(const LinearParams& p, cudaStream_t stream);

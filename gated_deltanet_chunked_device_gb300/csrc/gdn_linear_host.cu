@@ -30,6 +30,8 @@ bool tensor_ok(const void* p, gdn_dtype t, int64_t& stride, int64_t row) {
     return stride >= row;
 }
 
+bool workspace_ok(const void* p, size_t bytes, size_t needed) { return needed == 0 || (p && aligned(p, 16) && bytes >= needed); }
+
 enum class Run { kForward, kBackward, kDecode };
 
 // Checks the arguments that the runs share and fills the kernels' parameters.
@@ -131,13 +133,14 @@ gdn_status gdn_linear_plan(const gdn_linear_desc* desc, gdn_linear_plan_t* plan,
     if (d.max_total_tokens > 0x7fffffffLL - GDN_LINEAR_TILE) return GDN_ERR_UNSUPPORTED;
     if (!io_dtype(d.x_dtype) || !storage_dtype(d.state_dtype)) return GDN_ERR_UNSUPPORTED;
     if (d.gate_dtype != d.x_dtype && d.gate_dtype != GDN_DTYPE_F32) return GDN_ERR_UNSUPPORTED;
-    const gdn::ScanLayout scan = gdn::scan_layout(d.max_total_tokens, static_cast<int64_t>(d.num_heads) * d.head_dim,
-                                                  (d.flags & GDN_LINEAR_GATES_PER_HEAD) ? d.head_dim : 0);
-    if (scan.nt * scan.blocks > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;  // tiles of one launch
+    const int64_t C = static_cast<int64_t>(d.num_heads) * d.head_dim;
+    const int64_t head_dim = (d.flags & GDN_LINEAR_GATES_PER_HEAD) ? d.head_dim : 0;
+    // tiles of one launch
+    if (gdn::tiles_of(d.max_total_tokens) * gdn::backward_blocks(C, head_dim) > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
     gdn_linear_plan_s* p = new (std::nothrow) gdn_linear_plan_s;
     if (!p) return GDN_ERR_INVALID_ARG;
     p->desc = d;
-    p->workspace = scan.total;
+    p->workspace = gdn::workspace_bound(d.max_total_tokens, C, head_dim);
     *plan = p;
     *workspace_bytes = p->workspace;
     return GDN_OK;
@@ -145,13 +148,19 @@ gdn_status gdn_linear_plan(const gdn_linear_desc* desc, gdn_linear_plan_t* plan,
 
 void gdn_linear_plan_destroy(gdn_linear_plan_t plan) { delete plan; }
 
+size_t gdn_linear_run_workspace(gdn_linear_plan_t plan, const gdn_linear_args* args, int32_t backward) {
+    gdn::LinearParams p;
+    if (make_params(plan, args, backward ? Run::kBackward : Run::kForward, &p) != GDN_OK || p.N == 0) return 0;
+    return backward ? gdn::linear_backward_workspace(p) : gdn::linear_forward_workspace(p);
+}
+
 gdn_status gdn_linear_forward_run(gdn_linear_plan_t plan, const gdn_linear_args* args, void* workspace,
                                   size_t workspace_bytes, void* stream) {
     gdn::LinearParams p;
     const gdn_status st = make_params(plan, args, Run::kForward, &p);
     if (st != GDN_OK) return st;
-    if (!workspace || workspace_bytes < plan->workspace || !aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
     if (p.N == 0) return GDN_OK;
+    if (!workspace_ok(workspace, workspace_bytes, gdn::linear_forward_workspace(p))) return GDN_ERR_INVALID_ARG;
     return gdn::launch_linear_forward(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
@@ -160,8 +169,8 @@ gdn_status gdn_linear_backward_run(gdn_linear_plan_t plan, const gdn_linear_args
     gdn::LinearParams p;
     const gdn_status st = make_params(plan, args, Run::kBackward, &p);
     if (st != GDN_OK) return st;
-    if (!workspace || workspace_bytes < plan->workspace || !aligned(workspace, 16)) return GDN_ERR_INVALID_ARG;
     if (p.N == 0) return GDN_OK;
+    if (!workspace_ok(workspace, workspace_bytes, gdn::linear_backward_workspace(p))) return GDN_ERR_INVALID_ARG;
     return gdn::launch_linear_backward(p, workspace, static_cast<cudaStream_t>(stream)) == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

@@ -9,15 +9,16 @@ the work is done by the kernels of ``libgdn_prefill.so``.  :func:`gated_linear_r
 from __future__ import annotations
 
 import ctypes
+import struct
 import threading
 
 import torch
 
-from . import (DTYPE_F32, GdnError, _pow2_at_least, _ptr, _QKV_DTYPES, _STATE_DTYPES, lib)
+from . import DTYPE_F32, GdnError, _pow2_at_least, _QKV_DTYPES, _STATE_DTYPES, lib, on_device
 
 __all__ = ["gated_linear_recurrence", "gated_linear_recurrence_backward", "gated_linear_recurrence_decode", "LinearDesc",
            "LinearArgs", "LINEAR_FLAGS", "LINEAR_TILE", "gdn_linear_plan", "gdn_linear_plan_destroy",
-           "gdn_linear_forward_run", "gdn_linear_backward_run", "gdn_linear_decode_run"]
+           "gdn_linear_run_workspace", "gdn_linear_forward_run", "gdn_linear_backward_run", "gdn_linear_decode_run"]
 
 LINEAR_TILE = 64  # packed tokens a row of tile_states stands for
 LINEAR_FLAGS = {"HAS_B": 1 << 0, "GATES_PER_HEAD": 1 << 1, "HAS_INITIAL_STATE": 1 << 2, "OUTPUT_FINAL_STATE": 1 << 3,
@@ -44,18 +45,23 @@ class LinearArgs(ctypes.Structure):
                 ("db_stride", ctypes.c_int64)]
 
 
+# The bytes of a LinearArgs, in C's alignment: the calls below pack their arguments in one go.
+_pack = struct.Struct("@PPPqqqPiqPPqPiPPqPPqPPPPPqqq").pack
+
+
 def _register(L):
     """Argument types of the entry points (called once, when the library is loaded)."""
-    run = [ctypes.c_void_p, ctypes.POINTER(LinearArgs), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]
-    L.gdn_linear_plan.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(ctypes.c_void_p),
-                                  ctypes.POINTER(ctypes.c_size_t)]
+    vp, sz = ctypes.c_void_p, ctypes.c_size_t
+    L.gdn_linear_plan.argtypes = [ctypes.POINTER(LinearDesc), ctypes.POINTER(vp), ctypes.POINTER(sz)]
     L.gdn_linear_plan.restype = ctypes.c_int
-    L.gdn_linear_plan_destroy.argtypes = [ctypes.c_void_p]
+    L.gdn_linear_plan_destroy.argtypes = [vp]
     L.gdn_linear_plan_destroy.restype = None
+    L.gdn_linear_run_workspace.argtypes = [vp, vp, ctypes.c_int32]
+    L.gdn_linear_run_workspace.restype = sz
     for fn in (L.gdn_linear_forward_run, L.gdn_linear_backward_run):
-        fn.argtypes = run
+        fn.argtypes = [vp, vp, vp, sz, vp]
         fn.restype = ctypes.c_int
-    L.gdn_linear_decode_run.argtypes = [ctypes.c_void_p, ctypes.POINTER(LinearArgs), ctypes.c_int32, ctypes.c_void_p]
+    L.gdn_linear_decode_run.argtypes = [vp, vp, ctypes.c_int32, vp]
     L.gdn_linear_decode_run.restype = ctypes.c_int
 
 
@@ -71,16 +77,21 @@ def gdn_linear_plan_destroy(plan) -> None:
     lib().gdn_linear_plan_destroy(plan)
 
 
+def gdn_linear_run_workspace(plan, args: LinearArgs, backward: bool) -> int:
+    """Bytes of workspace that a run of these arguments needs (at most the plan's)."""
+    return lib().gdn_linear_run_workspace(plan, ctypes.byref(args), int(backward))
+
+
 def gdn_linear_forward_run(plan, args: LinearArgs, workspace_ptr, workspace_bytes: int, stream_ptr) -> int:
-    return lib().gdn_linear_forward_run(plan, args, workspace_ptr, workspace_bytes, stream_ptr)
+    return lib().gdn_linear_forward_run(plan, ctypes.byref(args), workspace_ptr, workspace_bytes, stream_ptr)
 
 
 def gdn_linear_backward_run(plan, args: LinearArgs, workspace_ptr, workspace_bytes: int, stream_ptr) -> int:
-    return lib().gdn_linear_backward_run(plan, args, workspace_ptr, workspace_bytes, stream_ptr)
+    return lib().gdn_linear_backward_run(plan, ctypes.byref(args), workspace_ptr, workspace_bytes, stream_ptr)
 
 
 def gdn_linear_decode_run(plan, args: LinearArgs, tokens_per_seq: int, stream_ptr) -> int:
-    return lib().gdn_linear_decode_run(plan, args, tokens_per_seq, stream_ptr)
+    return lib().gdn_linear_decode_run(plan, ctypes.byref(args), tokens_per_seq, stream_ptr)
 
 
 class _Plan:
@@ -88,11 +99,11 @@ class _Plan:
     stream that it runs on."""
 
     def __init__(self, desc):
-        st, self.handle, self.workspace_bytes = gdn_linear_plan(desc)
+        st, self.handle, _ = gdn_linear_plan(desc)
         if st != 0:
             self.handle = None
             raise GdnError(st, "gdn_linear_plan")
-        self.max_tokens, self.max_seqs = desc.max_total_tokens, desc.max_num_seqs
+        self.max_seqs = desc.max_num_seqs
 
     def __del__(self):
         try:
@@ -106,24 +117,21 @@ _plans = {}
 _plans_lock = threading.Lock()
 
 
-def _get_plan(key, T, N):
-    """key: (heads, dim, x dtype, gate dtype, state dtype, flags, power-of-two bound of the tokens)."""
+def _get_plan(H, D, x, a, state_dt, flags, T, N):
+    key = (H, D, x.dtype, a.dtype, state_dt, flags, T.bit_length())
     p = _plans.get(key)
     if p is None or p.max_seqs < N:
         with _plans_lock:
-            p = _Plan(LinearDesc(*key[:5], key[6], _pow2_at_least(N), key[5]))
+            p = _Plan(LinearDesc(H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], state_dt, (1 << T.bit_length()) - 1,
+                                 _pow2_at_least(N), flags))
             _plans[key] = p
     return p
 
 
 def _tokens(name, t, shape, dtype, device):
     """Checks a [T, ...] tensor; returns its token stride (0: dense)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError(f"{name} must be {dtype} {list(shape)} on cuda:{device}, not {t.dtype} {list(t.shape)} on {t.device}")
     if t.is_contiguous():
         return 0
     row = 1
@@ -137,124 +145,132 @@ def _tokens(name, t, shape, dtype, device):
 
 
 def _inputs(x, a, b):
-    """Checks x and the gates; returns T, H, D, flags and the token strides."""
-    if x.dim() != 3:
+    """Checks x and the gates; returns the device, T, H, D, flags and the token strides."""
+    shape = x.shape
+    if len(shape) != 3:
         raise ValueError("x must be [total_tokens, heads, head_dim]")
-    device = x.device
-    if device.type != "cuda":
+    if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor: this library has no CPU path")
-    T, H, D = shape = x.shape
-    if x.dtype not in _QKV_DTYPES:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    if a.dtype != x.dtype and a.dtype != torch.float32:
+    dtype, gdtype, device = x.dtype, a.dtype, x.get_device()
+    if dtype not in _QKV_DTYPES:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if gdtype is not dtype and gdtype is not torch.float32:
         raise ValueError("the gates must be float32 or of x's dtype")
-    flags = 0
-    if a.dim() == 2:
-        flags = _PER_HEAD
-        gshape = shape[:2]
-    else:
-        gshape = shape
-    xs = _tokens("x", x, shape, x.dtype, device)
-    as_ = _tokens("a", a, gshape, a.dtype, device)
+    T, H, D = shape
+    flags, gshape = (_PER_HEAD, (T, H)) if a.dim() == 2 else (0, shape)
+    xs = _tokens("x", x, shape, dtype, device)
+    as_ = _tokens("a", a, gshape, gdtype, device)
     bs = 0
     if b is not None:
         flags |= _HAS_B
-        bs = _tokens("b", b, gshape, a.dtype, device)
-    return T, H, D, flags, xs, as_, bs
+        bs = _tokens("b", b, gshape, gdtype, device)
+    return device, T, H, D, flags, xs, as_, bs
 
 
 def _sequences(cu_seqlens, device):
     """(N, flag) of cu_seqlens, or of one sequence without it."""
     if cu_seqlens is None:
         return 1, 0
-    if cu_seqlens.device != device or cu_seqlens.dim() != 1 or not cu_seqlens.is_contiguous() or cu_seqlens.numel() < 1:
-        raise ValueError(f"cu_seqlens must be a contiguous vector of N + 1 entries on {device}")
-    if cu_seqlens.dtype == torch.int32:
+    if cu_seqlens.dim() != 1 or cu_seqlens.get_device() != device or not cu_seqlens.is_contiguous() or not cu_seqlens.numel():
+        raise ValueError(f"cu_seqlens must be a contiguous vector of N + 1 entries on cuda:{device}")
+    if cu_seqlens.dtype is torch.int32:
         return cu_seqlens.numel() - 1, 0
-    if cu_seqlens.dtype == torch.int64:
+    if cu_seqlens.dtype is torch.int64:
         return cu_seqlens.numel() - 1, _CU_I64
     raise ValueError("cu_seqlens must be int32 or int64")
 
 
+def _state(name, t, H, D, device):
+    """Checks a state; returns its row stride (0: dense)."""
+    if t.dim() != 3 or t.shape[1] != H or t.shape[2] != D or t.get_device() != device:
+        raise ValueError(f"{name} must be [rows, {H}, {D}] on cuda:{device}")
+    if t.dtype not in _STATE_DTYPES:
+        raise ValueError(f"unsupported state dtype {t.dtype}")
+    if t.is_contiguous():
+        return 0
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or (t.shape[0] > 1 and t.stride(0) < H * D):
+        raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
 def _states(initial_state, output_state, state_indices, N, H, D, device):
     """Checks the states; returns (dtype code, row stride, pool rows, flags)."""
-    dt, stride, n_pool, flags = DTYPE_F32, 0, 0, 0
-    first = None
-    for name, t in (("initial_state", initial_state), ("output_state", output_state)):
-        if t is None:
-            continue
-        if t.device != device or t.dim() != 3 or t.shape[1] != H or t.shape[2] != D:
-            raise ValueError(f"{name} must be [rows, {H}, {D}] on {device}")
-        if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D) or (t.shape[0] > 1 and t.stride(0) < H * D):
-            raise ValueError(f"{name} must have contiguous rows that do not overlap")
-        if t.dtype not in _STATE_DTYPES:
-            raise ValueError(f"unsupported state dtype {t.dtype}")
+    flags, n_pool, first, stride = 0, 0, None, 0
+    if initial_state is not None:
+        flags, first = _HAS_INIT, initial_state
+        stride = _state("initial_state", initial_state, H, D, device)
+    if output_state is not None:
+        flags |= _FINAL
         if first is None:
-            first, dt, stride = t, _STATE_DTYPES[t.dtype], t.stride(0) if t.shape[0] > 1 else 0
-        elif t.dtype != first.dtype or t.shape != first.shape or (t.shape[0] > 1 and t.stride(0) != stride):
+            first, stride = output_state, _state("output_state", output_state, H, D, device)
+        elif output_state is not first and (_state("output_state", output_state, H, D, device) != stride or
+                                            output_state.dtype is not first.dtype or output_state.shape != first.shape):
             raise ValueError("initial_state and output_state must share shape, dtype and strides")
     if state_indices is not None:
         if first is None:
             raise ValueError("state_indices needs a state pool (initial_state and/or output_state)")
-        if state_indices.device != device or state_indices.shape != (N,) or not state_indices.is_contiguous():
-            raise ValueError(f"state_indices must be a contiguous vector of {N} entries on {device}")
-        flags = _HAS_IDX
-        if state_indices.dtype == torch.int64:
+        if state_indices.shape != (N,) or state_indices.get_device() != device or not state_indices.is_contiguous():
+            raise ValueError(f"state_indices must be a contiguous vector of {N} entries on cuda:{device}")
+        flags |= _HAS_IDX
+        if state_indices.dtype is torch.int64:
             flags |= _IDX_I64
-        elif state_indices.dtype != torch.int32:
+        elif state_indices.dtype is not torch.int32:
             raise ValueError("state_indices must be int32 or int64")
         n_pool = first.shape[0]
     elif first is not None and first.shape[0] != N:
         raise ValueError(f"the states must have {N} rows")
-    if initial_state is not None:
-        flags |= _HAS_INIT
-    if output_state is not None:
-        flags |= _FINAL
-    return dt, stride, n_pool, flags
+    return _STATE_DTYPES[first.dtype] if first is not None else DTYPE_F32, stride, n_pool, flags
 
 
 def _status_ptr(device_status, device):
     if device_status is None:
-        return None
-    if device_status.dtype != torch.int32 or device_status.device != device:
-        raise ValueError(f"device_status must be int32 on {device}")
+        return 0
+    if device_status.dtype is not torch.int32 or device_status.get_device() != device or not device_status.numel():
+        raise ValueError(f"device_status must be int32 on cuda:{device}")
     return device_status.data_ptr()
 
 
-def _run(fn, name, key, T, N, args, device):
-    p = _get_plan(key, T, N)
-    with torch.cuda.device(device):
-        ws = torch.empty(p.workspace_bytes, dtype=torch.uint8, device=device)
-        st = fn(p.handle, args, ws.data_ptr(), p.workspace_bytes, torch.cuda.current_stream(device).cuda_stream)
+def _addr(t):
+    return 0 if t is None else t.data_ptr()
+
+
+def _run(backward, plan, x, args):
+    """Runs an entry point on x's device and the caller's stream, with a workspace from torch's allocator."""
+    L, handle, ws, at = lib(), plan.handle, None, 0
+    with on_device(x.get_device()) as stream:
+        n = L.gdn_linear_run_workspace(handle, args, backward)
+        if n:
+            ws = x.new_empty(n, dtype=torch.uint8)
+            at = ws.data_ptr()
+        st = (L.gdn_linear_backward_run if backward else L.gdn_linear_forward_run)(handle, args, at, n, stream)
     if st != 0:
-        raise GdnError(st, name)
+        raise GdnError(st, "gdn_linear_backward_run" if backward else "gdn_linear_forward_run")
 
 
 def _new_states(initial_state, N, H, D, device):
     if initial_state is None:
         return torch.empty(N, H, D, dtype=torch.float32, device=device)
+    if initial_state.is_contiguous():
+        return torch.empty_like(initial_state)
     return torch.empty_strided(initial_state.shape, initial_state.stride(), dtype=initial_state.dtype, device=device)
 
 
 def _forward(x, a, b, initial_state, output_state, cu_seqlens, output, state_indices, tile_states, device_status):
-    T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
-    device = x.device
-    N, f = _sequences(cu_seqlens, device)
-    flags |= f
-    sdt, sstride, n_pool, f = _states(initial_state, output_state, state_indices, N, H, D, device)
-    flags |= f
+    device, T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
+    N, cf = _sequences(cu_seqlens, device)
+    sdt, sstride, n_pool, sf = _states(initial_state, output_state, state_indices, N, H, D, device)
     ys = 0
     if output is None:
-        output = torch.empty(T, H, D, dtype=x.dtype, device=device)
+        output = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         ys = _tokens("output", output, x.shape, x.dtype, device)
     if tile_states is not None and _tokens("tile_states", tile_states, (-(-T // LINEAR_TILE), H, D), torch.float32, device):
         raise ValueError("tile_states must be contiguous")
-    key = (H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], sdt, flags, _pow2_at_least(T, LINEAR_TILE))
-    args = LinearArgs(x.data_ptr(), a.data_ptr(), _ptr(b), xs, as_, bs, _ptr(cu_seqlens), N, T, _ptr(initial_state),
-                      _ptr(output_state), sstride, _ptr(state_indices), n_pool, _status_ptr(device_status, device),
-                      output.data_ptr(), ys, _ptr(tile_states))
-    _run(lib().gdn_linear_forward_run, "gdn_linear_forward_run", key, T, N, args, device)
+    plan = _get_plan(H, D, x, a, sdt, flags | cf | sf, T, N)
+    args = _pack(x.data_ptr(), a.data_ptr(), _addr(b), xs, as_, bs, _addr(cu_seqlens), N, T, _addr(initial_state),
+                 _addr(output_state), sstride, _addr(state_indices), n_pool, _status_ptr(device_status, device),
+                 output.data_ptr(), ys, _addr(tile_states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    _run(0, plan, x, args)
     return output
 
 
@@ -322,30 +338,26 @@ def gated_linear_recurrence_backward(dy, x, a, b=None, tile_states=None, initial
     what the forward run saved (not needed up to 64 tokens).  dx has x's type, da and db (None without b) the gates'
     type and shape; d_initial_state [N, H, D] is fp32 (None without initial_state).
     """
-    T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
-    device = x.device
-    N, f = _sequences(cu_seqlens, device)
-    flags |= f
-    sdt, sstride, _, f = _states(initial_state, None, None, N, H, D, device)
-    flags |= f
+    device, T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
+    N, cf = _sequences(cu_seqlens, device)
+    sdt, sstride, _, sf = _states(initial_state, None, None, N, H, D, device)
     dys = _tokens("dy", dy, x.shape, x.dtype, device)
     if tile_states is not None:
         if _tokens("tile_states", tile_states, (-(-T // LINEAR_TILE), H, D), torch.float32, device):
             raise ValueError("tile_states must be contiguous")
     elif T > LINEAR_TILE:
         raise ValueError("tile_states of the forward run are needed")
-    if d_final_state is not None and (d_final_state.shape != (N, H, D) or d_final_state.dtype != torch.float32 or
-                                      d_final_state.device != device or not d_final_state.is_contiguous()):
-        raise ValueError(f"d_final_state must be contiguous float32 [{N}, {H}, {D}] on {device}")
-    dx = torch.empty(T, H, D, dtype=x.dtype, device=device)
-    da = torch.empty(a.shape, dtype=a.dtype, device=device)
-    db = torch.empty(a.shape, dtype=a.dtype, device=device) if b is not None else None
-    d0 = torch.empty(N, H, D, dtype=torch.float32, device=device) if initial_state is not None else None
-    key = (H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], sdt, flags, _pow2_at_least(T, LINEAR_TILE))
-    args = LinearArgs(x.data_ptr(), a.data_ptr(), _ptr(b), xs, as_, bs, _ptr(cu_seqlens), N, T, _ptr(initial_state),
-                      None, sstride, None, 0, _status_ptr(device_status, device), None, 0, _ptr(tile_states),
-                      dy.data_ptr(), dys, _ptr(d_final_state), _ptr(d0), dx.data_ptr(), da.data_ptr(), _ptr(db))
-    _run(lib().gdn_linear_backward_run, "gdn_linear_backward_run", key, T, N, args, device)
+    if d_final_state is not None and _tokens("d_final_state", d_final_state, (N, H, D), torch.float32, device):
+        raise ValueError("d_final_state must be contiguous")
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    da = torch.empty(a.shape, dtype=a.dtype, device=x.device)
+    db = torch.empty_like(da) if b is not None else None
+    d0 = torch.empty(N, H, D, dtype=torch.float32, device=x.device) if initial_state is not None else None
+    plan = _get_plan(H, D, x, a, sdt, flags | cf | sf, T, N)
+    args = _pack(x.data_ptr(), a.data_ptr(), _addr(b), xs, as_, bs, _addr(cu_seqlens), N, T, _addr(initial_state), 0, sstride, 0, 0,
+                 _status_ptr(device_status, device), 0, 0, _addr(tile_states), dy.data_ptr(), dys, _addr(d_final_state), _addr(d0),
+                 dx.data_ptr(), da.data_ptr(), _addr(db), 0, 0, 0)
+    _run(1, plan, x, args)
     return dx, da, db, d0
 
 
@@ -354,8 +366,7 @@ def gated_linear_recurrence_decode(x, a, b=None, initial_state=None, state_indic
     """Decode step (or a short run of tokens) of :func:`gated_linear_recurrence`: N sequences of ``tokens_per_seq``
     tokens each, rows i * tokens_per_seq + j of x, a and b.  With ``state_indices`` the state is read from its pool row
     and written back in place (or to ``output_state``'s row).  Returns ``output`` or ``(output, final_state)``."""
-    T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
-    device = x.device
+    device, T, H, D, flags, xs, as_, bs = _inputs(x, a, b)
     m = int(tokens_per_seq)
     if m < 1 or T % m:
         raise ValueError("x must have N * tokens_per_seq rows")
@@ -368,20 +379,19 @@ def gated_linear_recurrence_decode(x, a, b=None, initial_state=None, state_indic
                 raise ValueError("state_indices needs the state pool as initial_state")
             output_state = initial_state
         else:
-            output_state = _new_states(initial_state, N, H, D, device)
-    sdt, sstride, n_pool, f = _states(initial_state, output_state, state_indices, N, H, D, device)
-    flags |= f
+            output_state = _new_states(initial_state, N, H, D, x.device)
+    sdt, sstride, n_pool, sf = _states(initial_state, output_state, state_indices, N, H, D, device)
     ys = 0
     if output is None:
-        output = torch.empty(T, H, D, dtype=x.dtype, device=device)
+        output = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     else:
         ys = _tokens("output", output, x.shape, x.dtype, device)
-    p = _get_plan((H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], sdt, flags, _pow2_at_least(T, LINEAR_TILE)), T, N)
-    args = LinearArgs(x.data_ptr(), a.data_ptr(), _ptr(b), xs, as_, bs, None, N, T, _ptr(initial_state),
-                      _ptr(output_state), sstride, _ptr(state_indices), n_pool, _status_ptr(device_status, device),
-                      output.data_ptr(), ys)
-    with torch.cuda.device(device):
-        st = lib().gdn_linear_decode_run(p.handle, args, m, torch.cuda.current_stream(device).cuda_stream)
+    plan = _get_plan(H, D, x, a, sdt, flags | sf, T, N)
+    args = _pack(x.data_ptr(), a.data_ptr(), _addr(b), xs, as_, bs, 0, N, T, _addr(initial_state), _addr(output_state), sstride,
+                 _addr(state_indices), n_pool, _status_ptr(device_status, device), output.data_ptr(), ys, 0, 0, 0, 0, 0, 0, 0, 0, 0,
+                 0, 0)
+    with on_device(device) as stream:
+        st = lib().gdn_linear_decode_run(plan.handle, args, m, stream)
     if st != 0:
         raise GdnError(st, "gdn_linear_decode_run")
     return (output, output_state) if output_final_state else output

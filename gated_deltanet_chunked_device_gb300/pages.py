@@ -9,10 +9,11 @@ tokens.  All of it is device memory that the caller owns.  The calls marshal arg
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from . import GdnError, lib
+from . import GdnError, lib, on_device
 
 __all__ = ["cache_reserve", "cache_fork", "cache_free", "cache_compact", "cache_copy", "PAGES_ERR", "PagesBook", "PagesBuffer"]
 
@@ -29,77 +30,86 @@ class PagesBuffer(ctypes.Structure):
     _fields_ = [("base", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("row_bytes", ctypes.c_int64)]
 
 
+_pack_book = struct.Struct("@PPPiii4x").pack  # the bytes of a PagesBook
+_buffer_packs = [struct.Struct("@" + "Pqq" * n).pack for n in range(MAX_BUFFERS + 1)]  # and of n PagesBuffers
+
+
 def _register(L):
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-    book, buf = ctypes.POINTER(PagesBook), ctypes.POINTER(PagesBuffer)
     L.gdn_pages_workspace_bytes.argtypes = [i32, i32, i32, i32]
     L.gdn_pages_workspace_bytes.restype = sz
-    L.gdn_pages_reserve_run.argtypes = [book, vp, vp, i32, vp, vp, vp, sz, vp]
-    L.gdn_pages_fork_run.argtypes = [book, buf, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
-    L.gdn_pages_free_run.argtypes = [book, vp, i32, vp, vp]
-    L.gdn_pages_compact_run.argtypes = [book, buf, i32, vp, vp, vp, vp, vp, vp, sz, vp]
-    L.gdn_pages_copy_run.argtypes = [buf, i32, buf, i32, i32, vp, vp, i32, vp, vp]
+    L.gdn_pages_reserve_run.argtypes = [vp, vp, vp, i32, vp, vp, vp, sz, vp]
+    L.gdn_pages_fork_run.argtypes = [vp, vp, i32, vp, vp, i32, i32, vp, vp, vp, sz, vp]
+    L.gdn_pages_free_run.argtypes = [vp, vp, i32, vp, vp]
+    L.gdn_pages_compact_run.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.gdn_pages_copy_run.argtypes = [vp, i32, vp, i32, i32, vp, vp, i32, vp, vp]
     for fn in (L.gdn_pages_reserve_run, L.gdn_pages_fork_run, L.gdn_pages_free_run, L.gdn_pages_compact_run, L.gdn_pages_copy_run):
         fn.restype = ctypes.c_int
 
 
 def _int32(name, t, shape, device):
-    if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on {device}")
+    if t.dtype is not torch.int32 or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 {list(shape)} on cuda:{device}")
     return t.data_ptr()
 
 
 def _book(table, refcounts, lengths):
-    device = table.device
-    if device.type != "cuda":
+    """Checks the bookkeeping; returns (device, packed book, sequences, pages a sequence, pages)."""
+    if not table.is_cuda:
         raise ValueError("table must be a CUDA tensor: this library has no CPU path")
     if table.dim() != 2 or refcounts.dim() != 1:
         raise ValueError("table must be [sequences, max_pages] and refcounts [pages]")
+    device = table.get_device()
     S, M = table.shape
     P, = refcounts.shape
-    return device, PagesBook(_int32("table", table, (S, M), device), _int32("refcounts", refcounts, (P,), device),
-                             None if lengths is None else _int32("lengths", lengths, (S,), device), S, M, P), S, M, P
+    return device, _pack_book(_int32("table", table, (S, M), device), _int32("refcounts", refcounts, (P,), device),
+                              0 if lengths is None else _int32("lengths", lengths, (S,), device), S, M, P), S, M, P
 
 
 def _buffers(name, pools, n_pages, device):
+    """Checks the buffers; returns them packed, and how many."""
     if isinstance(pools, torch.Tensor):
         pools = (pools,)
     if len(pools) > MAX_BUFFERS:
         raise ValueError(f"at most {MAX_BUFFERS} buffers")
-    out = (PagesBuffer * max(1, len(pools)))()
-    for b, t in zip(out, pools):
-        if t.device != device or t.dim() < 1 or (n_pages is not None and t.shape[0] != n_pages):
-            raise ValueError(f"{name} must be [{'pages' if n_pages is None else n_pages}, ...] on {device}")
+    out = []
+    for t in pools:
+        if t.get_device() != device or t.dim() < 1 or t.shape[0] != n_pages:
+            raise ValueError(f"{name} must be [{n_pages}, ...] on cuda:{device}")
         size = t.element_size()
         if t.is_contiguous():
-            row = t.numel() // t.shape[0] if t.shape[0] else 0
-            b.row_stride = row * size
+            row = stride = t.numel() // n_pages * size if n_pages else 0
         else:
             row = 1
             for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
                 if n > 1 and s != row:
                     raise ValueError(f"{name} must have contiguous rows")
                 row *= n
-            if t.shape[0] > 1 and t.stride(0) < row:
+            if n_pages > 1 and t.stride(0) < row:
                 raise ValueError(f"{name}'s rows must not overlap")
-            b.row_stride = max(t.stride(0), row) * size
-        b.base, b.row_bytes = t.data_ptr(), row * size
-    return out, len(pools)
+            stride, row = max(t.stride(0), row) * size, row * size
+        out += (t.data_ptr(), stride, row)
+    return _buffer_packs[len(pools)](*out), len(pools)
 
 
 def _status(device_status, device):
-    return None if device_status is None else _int32("device_status", device_status, device_status.shape, device)
+    if device_status is None:
+        return 0
+    if not device_status.numel():
+        raise ValueError("device_status must have an element")
+    return _int32("device_status", device_status, device_status.shape, device)
 
 
-def _call(name, device, *args, workspace=None):
-    with torch.cuda.device(device):
-        stream = torch.cuda.current_stream(device).cuda_stream
+def _call(name, like, args, workspace=None):
+    """Calls an entry point on `like`'s device and the caller's stream; workspace: the bounds to take one for."""
+    L = lib()
+    with on_device(like.get_device()) as stream:
         if workspace is None:
-            st = getattr(lib(), name)(*args, stream)
+            st = getattr(L, name)(*args, stream)
         else:
-            n = lib().gdn_pages_workspace_bytes(*workspace)
-            ws = torch.empty(n, dtype=torch.uint8, device=device)
-            st = getattr(lib(), name)(*args, ws.data_ptr(), n, stream)
+            n = L.gdn_pages_workspace_bytes(*workspace)
+            ws = like.new_empty(n, dtype=torch.uint8)
+            st = getattr(L, name)(*args, ws.data_ptr(), n, stream)
     if st != 0:
         raise GdnError(st, name)
 
@@ -110,9 +120,9 @@ def cache_reserve(table, refcounts, seqs, counts, device_status=None):
     which the free pages do not suffice, and those after it, get nothing (PAGES_ERR["NO_PAGES"])."""
     device, book, S, M, P = _book(table, refcounts, None)
     n = seqs.numel()
-    rows = torch.empty(n, M, dtype=torch.int32, device=device)
-    _call("gdn_pages_reserve_run", device, book, _int32("seqs", seqs, (n,), device), _int32("counts", counts, (n,), device), n,
-          rows.data_ptr(), _status(device_status, device), workspace=(S, M, P, n))
+    rows = table.new_empty((n, M))
+    _call("gdn_pages_reserve_run", table, (book, _int32("seqs", seqs, (n,), device), _int32("counts", counts, (n,), device), n,
+                                           rows.data_ptr(), _status(device_status, device)), (S, M, P, n))
     return rows
 
 
@@ -126,10 +136,10 @@ def cache_fork(pools, table, refcounts, parents, children, page_tokens=0, length
         raise ValueError("page_tokens needs lengths")
     n = children.numel()
     bufs, nb = _buffers("pools", pools, P, device)
-    rows = torch.empty(n, M, dtype=torch.int32, device=device)
-    _call("gdn_pages_fork_run", device, book, bufs, nb, _int32("parents", parents, (n,), device),
-          _int32("children", children, (n,), device), n, int(page_tokens), rows.data_ptr(), _status(device_status, device),
-          workspace=(S, M, P, n))
+    rows = table.new_empty((n, M))
+    _call("gdn_pages_fork_run", table, (book, bufs, nb, _int32("parents", parents, (n,), device),
+                                        _int32("children", children, (n,), device), n, int(page_tokens), rows.data_ptr(),
+                                        _status(device_status, device)), (S, M, P, n))
     return rows
 
 
@@ -137,7 +147,7 @@ def cache_free(table, refcounts, seqs, lengths=None, device_status=None):
     """Drops the sequences: a reference less on each of their pages, table entries -1, lengths 0."""
     device, book, _, _, _ = _book(table, refcounts, lengths)
     n = seqs.numel()
-    _call("gdn_pages_free_run", device, book, _int32("seqs", seqs, (n,), device), n, _status(device_status, device))
+    _call("gdn_pages_free_run", table, (book, _int32("seqs", seqs, (n,), device), n, _status(device_status, device)))
 
 
 def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, device_status=None):
@@ -148,11 +158,11 @@ def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, d
     table_out = table if table_out is None else table_out
     refcounts_out = refcounts if refcounts_out is None else refcounts_out
     bufs, nb = _buffers("pools", pools, P, device)
-    remap = torch.empty(P, dtype=torch.int32, device=device)
-    n_live = torch.empty(1, dtype=torch.int32, device=device)
-    _call("gdn_pages_compact_run", device, book, bufs, nb, _int32("table_out", table_out, (S, M), device),
-          _int32("refcounts_out", refcounts_out, (P,), device), remap.data_ptr(), n_live.data_ptr(), _status(device_status, device),
-          workspace=(S, M, P, 0))
+    remap = torch.empty_like(refcounts)
+    n_live = refcounts.new_empty(1)
+    _call("gdn_pages_compact_run", table, (book, bufs, nb, _int32("table_out", table_out, (S, M), device),
+                                           _int32("refcounts_out", refcounts_out, (P,), device), remap.data_ptr(),
+                                           n_live.data_ptr(), _status(device_status, device)), (S, M, P, 0))
     return remap, n_live
 
 
@@ -168,14 +178,14 @@ def cache_copy(src_pools, dst_pools, src, dst, device_status=None):
         raise ValueError("src_pools and dst_pools must have as many buffers")
     if not src_pools:
         return
-    device = src_pools[0].device
-    if device.type != "cuda":
+    device = src_pools[0].get_device()
+    if device < 0:
         raise ValueError("the pools must be CUDA tensors: this library has no CPU path")
     for s, d in zip(src_pools, dst_pools):
-        if s.dtype != d.dtype or s.shape[1:] != d.shape[1:]:
+        if s.dtype is not d.dtype or s.shape[1:] != d.shape[1:]:
             raise ValueError("a source and its destination must have rows of one type and shape")
     n_src, n_dst, n = src_pools[0].shape[0], dst_pools[0].shape[0], src.numel()
     sb, nb = _buffers("src_pools", src_pools, n_src, device)
     db, _ = _buffers("dst_pools", dst_pools, n_dst, device)
-    _call("gdn_pages_copy_run", device, sb, n_src, db, n_dst, nb, _int32("src", src, (n,), device), _int32("dst", dst, (n,), device),
-          n, _status(device_status, device))
+    _call("gdn_pages_copy_run", src_pools[0], (sb, n_src, db, n_dst, nb, _int32("src", src, (n,), device),
+                                               _int32("dst", dst, (n,), device), n, _status(device_status, device)))

@@ -125,6 +125,11 @@ typedef struct gdn_linear_args {
 gdn_status gdn_linear_plan(const gdn_linear_desc *desc, gdn_linear_plan_t *plan, size_t *workspace_bytes);
 void gdn_linear_plan_destroy(gdn_linear_plan_t plan);
 
+/* Bytes of workspace that the forward (backward != 0: the backward) run of
+ * these arguments needs on the current device: at most the plan's, and 0 for
+ * many (their workspace may be NULL).  0 for arguments that the run refuses. */
+size_t gdn_linear_run_workspace(gdn_linear_plan_t plan, const gdn_linear_args *args, int32_t backward);
+
 gdn_status gdn_linear_forward_run(gdn_linear_plan_t plan, const gdn_linear_args *args, void *workspace,
                                   size_t workspace_bytes, void *stream);
 

@@ -100,11 +100,29 @@ def test_runs_refuse_missing_outputs(op, kw):
 
 
 def test_workspace_is_checked():
+    """Runs that hand something on from block to block need a workspace: 16 channels of 200 tokens at an odd address."""
     st, plan, nbytes = gdn.gdn_linear_plan(desc())
-    for ws, n in ((None, nbytes), (1 << 22, nbytes - 1), ((1 << 22) + 8, nbytes)):
-        assert gdn.gdn_linear_forward_run(plan, gdn.LinearArgs(**GOOD), ws, n, None) == 1
-        assert gdn.gdn_linear_backward_run(plan, gdn.LinearArgs(**GOOD), ws, n, None) == 1
+    args = gdn.LinearArgs(**{**GOOD, "x": 4098, "total_tokens": 200})
+    for back, run in ((False, gdn.gdn_linear_forward_run), (True, gdn.gdn_linear_backward_run)):
+        n = gdn.gdn_linear_run_workspace(plan, args, back)
+        assert 0 < n <= nbytes
+        for ws, size in ((None, n), (1 << 22, n - 1), ((1 << 22) + 8, n)):
+            assert run(plan, args, ws, size, None) == 1
+    assert gdn.gdn_linear_run_workspace(plan, gdn.LinearArgs(**{**GOOD, "x": None}), False) == 0  # refused
     gdn.gdn_linear_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("T,H,D", [(1, 1, 1), (64, 1, 1), (65, 3, 7), (5000, 2, 128), (70000, 1, 16), (4096, 1, 4100), (999, 40, 96)])
+@pytest.mark.parametrize("per_head", [False, True])
+def test_a_runs_workspace_is_within_the_plans(T, H, D, per_head):
+    flags = gdn.LINEAR_FLAGS["GATES_PER_HEAD"] if per_head else 0
+    for kw in (dict(x_dtype=1, gate_dtype=1), dict(x_dtype=0, gate_dtype=0)):
+        st, plan, nbytes = gdn.gdn_linear_plan(desc(num_heads=H, head_dim=D, max_total_tokens=T, flags=flags, **kw))
+        for x in (4096, 4104, 4100):
+            args = gdn.LinearArgs(**{**GOOD, "x": x, "total_tokens": T})
+            for back in (False, True):
+                assert gdn.gdn_linear_run_workspace(plan, args, back) <= nbytes
+        gdn.gdn_linear_plan_destroy(plan)
 
 
 def test_states_and_pools_are_checked():

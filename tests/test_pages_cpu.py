@@ -18,7 +18,7 @@ def L():
 def book(**kw):
     d = dict(table=4096, refcounts=8192, lengths=12288, max_seqs=4, max_pages=3, n_pages=20)
     d.update(kw)
-    return gdn.PagesBook(**d)
+    return ctypes.byref(gdn.PagesBook(**d))
 
 
 def bufs(*rows):
