@@ -9,6 +9,7 @@ tokens.  All of it is device memory that the caller owns.  The calls marshal arg
 from __future__ import annotations
 
 import ctypes
+import functools
 import struct
 
 import torch
@@ -100,16 +101,20 @@ def _status(device_status, device):
     return _int32("device_status", device_status, device_status.shape, device)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(bounds):
+    return lib().gdn_pages_workspace_bytes(*bounds)
+
+
 def _call(name, like, args, workspace=None):
     """Calls an entry point on `like`'s device and the caller's stream; workspace: the bounds to take one for."""
-    L = lib()
     with on_device(like.get_device()) as stream:
         if workspace is None:
-            st = getattr(L, name)(*args, stream)
+            st = getattr(lib(), name)(*args, stream)
         else:
-            n = L.gdn_pages_workspace_bytes(*workspace)
-            ws = like.new_empty(n, dtype=torch.uint8)
-            st = getattr(L, name)(*args, ws.data_ptr(), n, stream)
+            n = _workspace_bytes(workspace)
+            ws = torch.empty(n, dtype=torch.uint8, device=like.device)
+            st = getattr(lib(), name)(*args, ws.data_ptr(), n, stream)
     if st != 0:
         raise GdnError(st, name)
 
@@ -120,7 +125,7 @@ def cache_reserve(table, refcounts, seqs, counts, device_status=None):
     which the free pages do not suffice, and those after it, get nothing (PAGES_ERR["NO_PAGES"])."""
     device, book, S, M, P = _book(table, refcounts, None)
     n = seqs.numel()
-    rows = table.new_empty((n, M))
+    rows = torch.empty(n, M, dtype=torch.int32, device=table.device)
     _call("gdn_pages_reserve_run", table, (book, _int32("seqs", seqs, (n,), device), _int32("counts", counts, (n,), device), n,
                                            rows.data_ptr(), _status(device_status, device)), (S, M, P, n))
     return rows
@@ -136,7 +141,7 @@ def cache_fork(pools, table, refcounts, parents, children, page_tokens=0, length
         raise ValueError("page_tokens needs lengths")
     n = children.numel()
     bufs, nb = _buffers("pools", pools, P, device)
-    rows = table.new_empty((n, M))
+    rows = torch.empty(n, M, dtype=torch.int32, device=table.device)
     _call("gdn_pages_fork_run", table, (book, bufs, nb, _int32("parents", parents, (n,), device),
                                         _int32("children", children, (n,), device), n, int(page_tokens), rows.data_ptr(),
                                         _status(device_status, device)), (S, M, P, n))
