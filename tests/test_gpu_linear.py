@@ -322,6 +322,17 @@ def test_decode(m, H, D, dtype, gate_dtype, gates):
     assert torch.equal(pool[rest], before[rest])
 
 
+@pytest.mark.parametrize("m", [1, 3, 9])
+@pytest.mark.parametrize("gate_dtype,gates", [("bf16", "channel"), ("f32", "channel"), ("f32", "head")])
+def test_decode_many_sequences(gate_dtype, gates, m):
+    """Enough of them for loads of 16 bytes, and more tokens than are loaded at a time."""
+    i = make([m] * 400, 16, 104, "bf16", gate_dtype, gates=gates, seed=26)
+    y, out = gdn.gated_linear_recurrence_decode(i["x"], i["a"], i["b"], initial_state=i["h0"], tokens_per_seq=m)
+    want = ref.forward(f64(i["x"]), f64(i["a"]), f64(i["b"]), i["cul"], f64(i["h0"]))
+    within("y", y, want[0], want[3], torch.bfloat16)
+    within("state", out, want[1], want[4])
+
+
 @pytest.mark.parametrize("state", [torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float8_e5m2])
 @pytest.mark.parametrize("D", [64, 9])
 def test_decode_state_types(state, D):
