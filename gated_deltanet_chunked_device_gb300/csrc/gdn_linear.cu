@@ -169,13 +169,13 @@ bool inputs_wide(const LinearParams& p) {
     return x && vector_of_16_bytes(p.a, p.a_stride, p.gate_dt, p.C) && vector_of_16_bytes(p.b, p.b_stride, p.gate_dt, p.C);
 }
 
-// Width and time segments of the columns, with runs of `run` tokens.
-linear::Segments segments(const LinearParams& p, int run, int* width) {
+// Width and time segments of the columns, for stages of `warps` warps with runs of `run` tokens.
+linear::Segments segments(const LinearParams& p, int warps, int run, int* width) {
     const int64_t sms = multiprocessors(), blocks32 = (p.C + 31) / 32;
     int64_t segs = sms / blocks32;
     *width = 5 * blocks32 < 3 * sms && segs < 3 ? 16 : 32;
     linear::Segments s{};
-    const int64_t tokens = 8 * (128 / *width) * run, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
+    const int64_t tokens = warps * (128 / *width) * run, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
     if (segs > n / 2) segs = n / 2;
     s.space.blocks = static_cast<uint32_t>((p.C + *width - 1) / *width);
     s.space.nt = 1;
@@ -208,7 +208,7 @@ Route forward_route(const LinearParams& p) {
     Route r{};
     r.vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
     r.column = r.vec && inputs_wide(p);
-    if (r.column) r.seg = segments(p, 8, &r.width);
+    if (r.column) r.seg = segments(p, linear::kForwardWarps, 8, &r.width);
     r.blocks = (p.C + linear::kCols - 1) / linear::kCols;
     finish_route(p, &r);
     return r;
@@ -221,7 +221,7 @@ Route backward_route(const LinearParams& p) {
             vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
     if (p.gate_div == 1) r.vec = r.vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
     if (r.vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
-        r.seg = segments(p, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);
+        r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);
         r.column = p.gate_div == 1 || linear::one_head(p, r.width);
     }
     r.blocks = backward_blocks(p.C, head_dim);

@@ -22,16 +22,19 @@
 namespace gdn {
 namespace linear {
 
-// A block's shape: W channels, NW warps, runs of R tokens.
-template <int W, int NW, int R>
+// A block's shape: W channels; NG groups of NW warps, which take the stages in turn; runs of R tokens.
+template <int W, int NW, int R, int NG = 1>
 struct Column {
-    static constexpr int kWidth = W, kRun = R;
+    static constexpr int kWidth = W, kRun = R, kGroups = NG;
     static constexpr int kLanesRow = W / 4;      // lanes that hold one token's channels
     static constexpr int kRuns = 32 / kLanesRow; // runs of tokens of a warp
     static constexpr int kWarpTokens = kRuns * kRun;
     static constexpr int kTokens = NW * kWarpTokens;
     static constexpr int kWarps = NW;
-    static constexpr int kThreads = 32 * NW;
+    static constexpr int kThreads = 32 * NW * NG;
+    // Places for what a stage hands to the next one.  A place is written again kHands stages later; by then the group that
+    // read it has gone on to another stage, all of it.
+    static constexpr int kHands = NG + 2;
 };
 
 constexpr int kRingBytes = 192 * 1024;           // shared memory of the ring, at most
@@ -281,6 +284,8 @@ struct ColumnMaps {
     CUtensorMap x, a, b, dy;
 };
 
+constexpr int kForwardWarps = 8, kForwardGroups = 2;
+
 // How gates are found: per channel; of one head for the block's channels (the head's channels are a multiple of them, and
 // rows of gates can be copied); or of any heads (4 channels of a lane share one), by plain loads.
 enum Gates { kPerChannel, kOneHead, kAnyHead };
@@ -292,13 +297,18 @@ struct ForwardShape {
     using AG = std::conditional_t<kGates == kOneHead, StageGates<G, Col>, StageArray<G, Col>>;
     static constexpr int kStageBytes = AX::kBytes + (kGates == kAnyHead ? 0 : kHasB ? 2 : 1) * AG::kBytes;
     static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
-    struct Tables {
+    struct Group {
         StageBounds<kTokens> bounds[3];
         alignas(16) float2 pairs[2][Col::kWarps][W];
-        float enter[W];
-        alignas(16) float kept[W];  // initial state of the last sequence that starts in the segment
+        alignas(16) float kept[W];  // initial state of the last sequence that starts in the segment's stages of this group
         int64_t kept_at;            // its first token
-        uint64_t full[kDepth];      // a stage's inputs have come
+    };
+    struct Tables {
+        Group groups[Col::kGroups];
+        float2 hand[Col::kHands][W];  // the state that enters a stage, and in steps that learn the gates' product so far
+        int32_t hand_reset[Col::kHands];
+        uint64_t full[kDepth];        // a stage's inputs have come
+        uint64_t handed[Col::kHands];
         uint32_t ticket;
     };
     static constexpr int kSmem = kDepth * kStageBytes + static_cast<int>(sizeof(Tables));
@@ -313,16 +323,21 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     using AX = typename Shape::AX;
     using AG = typename Shape::AG;
     constexpr int W = Shape::W, kTokens = Shape::kTokens, kDepth = Shape::kDepth, kRuns = Col::kRuns, kLanesRow = Col::kLanesRow;
-    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun;
+    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun, kGroups = Col::kGroups;
+    constexpr int kHands = Col::kHands;
     extern __shared__ __align__(1024) uint8_t ring[];
     typename Shape::Tables& sm = *reinterpret_cast<typename Shape::Tables*>(ring + kDepth * Shape::kStageBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int group = threadIdx.x / (32 * kColWarps), warp = threadIdx.x / 32 % kColWarps, lane = threadIdx.x % 32;
+    typename Shape::Group& gr = sm.groups[group];
+    const bool leader = warp == 0 && lane == 0;  // of the group
     const int sub = lane / kLanesRow, l = lane % kLanesRow, run = warp * kRuns + sub, ch = lane % W;
     const ScanSpace& sp = seg.space;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kDepth; ++i) mbar_init(&sm.full[i], 1);
+        for (int i = 0; i < kHands; ++i) mbar_init(&sm.handed[i], 1);
         fence_mbar_init();
-        sm.kept_at = -1;
+        mbar_arrive(&sm.handed[0]);  // nothing is handed to stage 0: its place's first turn is over
+        for (int i = 0; i < kGroups; ++i) sm.groups[i].kept_at = -1;
         if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
     __syncthreads();
@@ -400,16 +415,17 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     auto bounds = [&](int q) {
         if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, end);
-        if (q == 0 || q == stages) {
-            lo = from == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
+        if (q < kGroups || (q >= stages && q < stages + kGroups)) {
+            lo = t0 == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
             next = 0;
         }
+        StageBounds<kTokens>& b = gr.bounds[q / kGroups % 3];
         if (next > t1 && t1 == t0 + kTokens) {  // most stages
-            no_bounds(sm.bounds[q % 3], lane);
+            no_bounds(b, lane);
             return;
         }
         const bool write = q >= steps - stages;
-        lo += fill_bounds<kTokens, kWarpTokens>(p, lo, t0, t1, t1 == p.T, lane, sm.bounds[q % 3], [&](int64_t i) {
+        lo += fill_bounds<kTokens, kWarpTokens>(p, lo, t0, t1, t1 == p.T, lane, b, [&](int64_t i) {
             // an empty sequence's final state is its initial one
             if (!write || !p.output_state || p.output_state == p.initial_state) return;
             const int64_t row = state_row(p, i);
@@ -423,21 +439,26 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 
     if (threadIdx.x == 0)
         for (int q = 0; q < kDepth; ++q) fetch(q);
-    if (warp == kColWarps - 1) bounds(0);
-    if (warp == kColWarps - 2 && blk == 0) check_bounds(p, part, sp.nt, lane);
+    if (warp == kColWarps - 1) bounds(group);
+    if (group == 0 && warp == 0 && blk == 0) check_bounds(p, part, sp.nt, lane);
     __syncthreads();
-    float carry = 0.f, through = 1.f;  // of channel `ch`: the state (in steps that learn, from zero), the gates' product
-    bool reset = false;                // whether a sequence has started
     X* y = static_cast<X*>(p.y) + c0 + l * 4;
-    for (int q = 0; q < steps; ++q) {
-        const StageBounds<kTokens>& bd = sm.bounds[q % 3];
+    auto wait_hand = [&](int q) {
+        if (ok && !mbar_wait(&sm.handed[q % kHands], (q / kHands) & 1)) {
+            ok = false;
+            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+        }
+    };
+    for (int q = group; q < steps; q += kGroups) {
+        const StageBounds<kTokens>& bd = gr.bounds[q / kGroups % 3];
         const bool learn = twice && q < stages;
         const int64_t t = stage_start(q) + run * kRun;
+        if (twice && q >= stages && q < stages + kGroups) wait_hand(q);  // all that learns has been done: states are kept
         Quad a[kRun], u[kRun], A, B, exA, exB;
         uint32_t starts = 0;
         int n = kRun;
         bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
-        if (warp == kColWarps - 1) bounds(q + 1);
+        if (warp == kColWarps - 1) bounds(q + kGroups);
         {
             plain = (bd.plain >> warp) & 1;
             take(q);
@@ -481,13 +502,18 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                             // With states in place, a later segment may have written the row of a sequence that starts
                             // here by the time of the second pass: the last one to start, if any.  Its state is kept.
                             float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (twice && !learn && t + k == sm.kept_at)
-                                h0 = *reinterpret_cast<const float4*>(&sm.kept[l * 4]);
-                            else if (row >= 0)
+                            bool kept = false;
+                            if (twice && !learn)
+                                for (int i = 0; i < kGroups; ++i)
+                                    if (t + k == sm.groups[i].kept_at) {
+                                        h0 = *reinterpret_cast<const float4*>(&sm.groups[i].kept[l * 4]);
+                                        kept = true;
+                                    }
+                            if (!kept && row >= 0)
                                 h0 = state_quad_load(p.initial_state, row * p.state_stride + c0 + l * 4, p.state_dt);
                             if (learn && is_last_bit<kTokens>(bd.starts, run * kRun + k)) {
-                                *reinterpret_cast<float4*>(&sm.kept[l * 4]) = h0;
-                                sm.kept_at = t + k;
+                                *reinterpret_cast<float4*>(&gr.kept[l * 4]) = h0;
+                                gr.kept_at = t + k;
                             }
                             if (row >= 0) u[k] = fma(a[k], quad(h0), u[k]);
                         }
@@ -517,37 +543,43 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
             before = (rs & ((1u << sub) - 1u)) != 0;
             if (sub == kRuns - 1) {
-                float4* o = reinterpret_cast<float4*>(&sm.pairs[q & 1][warp][l * 4]);
+                float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
                 o[0] = make_float4(A.lo.x, B.lo.x, A.lo.y, B.lo.y);
                 o[1] = make_float4(A.hi.x, B.hi.x, A.hi.y, B.hi.y);
             }
         }
-        // The step's one barrier.  Past it: every warp's pair is there and every thread has its inputs of this stage, so its
-        // place in the ring is free; the bounds of the next stage are known.
-        __syncthreads();
-        float enter = carry;
-        {
-            if (threadIdx.x == 0) fetch(q + kDepth);
-            float2 ab[kColWarps];
+        // The group's one barrier of a step.  Past it: every warp's pair is there and every thread has its inputs of this
+        // stage, so its place in the ring is free; the bounds of the group's next stage are known.
+        named_bar_sync(1 + group, 32 * kColWarps);
+        if (leader) fetch(q + kDepth);
+        float2 ab[kColWarps];
 #pragma unroll
-            for (int w = 0; w < kColWarps; ++w) ab[w] = sm.pairs[q & 1][w][ch];
-            const uint32_t resets = bd.warps_start;
+        for (int w = 0; w < kColWarps; ++w) ab[w] = gr.pairs[q / kGroups & 1][w][ch];
+        const uint32_t resets = bd.warps_start;
+        // What the stage before hands on: the state (in steps that learn, from zero), and the gates' product.
+        float2 hand = make_float2(0.f, 1.f);
+        if (q > 0) {
+            wait_hand(q);
+            hand = sm.hand[q % kHands][ch];
+        }
+        float carry = hand.x, enter = carry;
 #pragma unroll
-            for (int w = 0; w < kColWarps; ++w) {
-                if (w == warp) enter = carry;
-                carry = fmaf(ab[w].x, carry, ab[w].y);
-                if (resets != 0 && ((resets >> w) & 1)) carry = ab[w].y;
-            }
-            if (learn)
+        for (int w = 0; w < kColWarps; ++w) {
+            if (w == warp) enter = carry;
+            carry = fmaf(ab[w].x, carry, ab[w].y);
+            if (resets != 0 && ((resets >> w) & 1)) carry = ab[w].y;
+        }
+        if (warp == 0) {
+            float through = hand.y;
+            bool reset = resets != 0;
+            if (learn) {
 #pragma unroll
                 for (int w = 0; w < kColWarps; ++w) through *= ab[w].x;
-            reset |= resets != 0;
-        }
-        if (learn) {
-            if (q < stages - 1) continue;
-            if (warp == 0) {  // hand the pair on, get the state that enters
-                const int c = c0 + lane;
-                uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
+                reset |= q > 0 && sm.hand_reset[q % kHands] != 0;
+            }
+            const int c = c0 + lane;
+            uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
+            if (learn && q == stages - 1) {  // the segment's pair goes on, the state that enters it comes
                 const bool lastpart = part == sp.nt - 1;
                 if (!lastpart) {
                     if (lane < cols) {
@@ -563,12 +595,17 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                     if (lane < cols) sp.known[part * p.C + c] = fmaf(through, h, carry);
                     publish(flags + part, kKnown, lane);
                 }
-                if (lane < W) sm.enter[lane] = h;
+                carry = h;
+            } else if (part == 0 && sp.nt > 1 && q == steps - 1) {  // the first segment's end state
+                if (lane < cols) sp.known[c] = carry;
+                publish(flags, kKnown, lane);
             }
-            __syncthreads();
-            carry = sm.enter[ch];
-            continue;
+            if (lane < W) sm.hand[(q + 1) % kHands][lane] = make_float2(carry, through);
+            if (lane == 0) sm.hand_reset[(q + 1) % kHands] = reset;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.handed[(q + 1) % kHands]);
         }
+        if (learn) continue;
         {
             const Quad e = {{__shfl_sync(0xffffffffu, enter, l * 4), __shfl_sync(0xffffffffu, enter, l * 4 + 1)},
                             {__shfl_sync(0xffffffffu, enter, l * 4 + 2), __shfl_sync(0xffffffffu, enter, l * 4 + 3)}};
@@ -602,10 +639,6 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
         }
     }
-    if (part == 0 && sp.nt > 1 && warp == 0) {  // the first segment's end state
-        if (lane < cols) sp.known[c0 + lane] = carry;
-        publish(sp.flags + static_cast<int64_t>(blk) * sp.nt, kKnown, lane);
-    }
 }
 
 template <class X, class G, int kGates, bool kHasB, class Col>
@@ -629,11 +662,12 @@ cudaError_t launch_column_forward(const LinearParams& p, const Segments& seg, cu
 
 template <class X, class G, int kGates>
 cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
+    constexpr int kWarps = kForwardWarps, kGroups = kForwardGroups;
     if (width == 32)
-        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, 8, 8>>(p, seg, stream)
-                   : launch_column_forward<X, G, kGates, false, Column<32, 8, 8>>(p, seg, stream);
-    return p.b ? launch_column_forward<X, G, kGates, true, Column<16, 8, 8>>(p, seg, stream)
-               : launch_column_forward<X, G, kGates, false, Column<16, 8, 8>>(p, seg, stream);
+        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, kWarps, 8, kGroups>>(p, seg, stream)
+                   : launch_column_forward<X, G, kGates, false, Column<32, kWarps, 8, kGroups>>(p, seg, stream);
+    return p.b ? launch_column_forward<X, G, kGates, true, Column<16, kWarps, 8, kGroups>>(p, seg, stream)
+               : launch_column_forward<X, G, kGates, false, Column<16, kWarps, 8, kGroups>>(p, seg, stream);
 }
 
 // Whether a block of `width` channels has one head, and its gates can be copied.
