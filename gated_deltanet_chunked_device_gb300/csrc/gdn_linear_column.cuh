@@ -90,6 +90,17 @@ __device__ __forceinline__ Quad shift_up(Quad v, int lanes) {
     return {{__shfl_up_sync(0xffffffffu, v.lo.x, lanes), __shfl_up_sync(0xffffffffu, v.lo.y, lanes)},
             {__shfl_up_sync(0xffffffffu, v.hi.x, lanes), __shfl_up_sync(0xffffffffu, v.hi.y, lanes)}};
 }
+// A gate: of four channels, or one that they share (gates of one head).
+__device__ __forceinline__ float mul(float a, float b) { return a * b; }
+__device__ __forceinline__ Quad mul(float a, Quad b) { return mul(all4(a), b); }
+__device__ __forceinline__ Quad fma(float a, Quad b, Quad c) { return fma(all4(a), b, c); }
+__device__ __forceinline__ float shift_up(float v, int lanes) { return __shfl_up_sync(0xffffffffu, v, lanes); }
+__device__ __forceinline__ float shift_down(float v, int lanes) { return __shfl_down_sync(0xffffffffu, v, lanes); }
+__device__ __forceinline__ void set_gate(float& g, float v) { g = v; }
+__device__ __forceinline__ void set_gate(Quad& g, float v) { g = all4(v); }
+__device__ __forceinline__ Quad of_channels(Quad g) { return g; }
+__device__ __forceinline__ Quad of_channels(float g) { return all4(g); }
+
 template <class T>
 __device__ __forceinline__ Quad widen(const Pack<T>& p) {
     return {{to_f32(p.v[0]), to_f32(p.v[1])}, {to_f32(p.v[2]), to_f32(p.v[3])}};
@@ -454,7 +465,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         const bool learn = twice && q < stages;
         const int64_t t = stage_start(q) + run * kRun;
         if (twice && q >= stages && q < stages + kGroups) wait_hand(q);  // all that learns has been done: states are kept
-        Quad a[kRun], u[kRun], A, B, exA, exB;
+        using Gate = std::conditional_t<kGates == kPerChannel, Quad, float>;
+        Gate a[kRun], A, exA;
+        Quad u[kRun], B, exB;
         uint32_t starts = 0;
         int n = kRun;
         bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
@@ -467,11 +480,11 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 u[k] = widen(px[k]);
                 if constexpr (kGates == kOneHead) {
                     const int from_lane = sub * kLanesRow + k % kLanesRow;
-                    a[k] = all4(__shfl_sync(0xffffffffu, ha[k / kLanesRow], from_lane));
-                    if constexpr (kHasB) u[k] = mul(u[k], all4(__shfl_sync(0xffffffffu, hb[k / kLanesRow], from_lane)));
+                    a[k] = __shfl_sync(0xffffffffu, ha[k / kLanesRow], from_lane);
+                    if constexpr (kHasB) u[k] = mul(__shfl_sync(0xffffffffu, hb[k / kLanesRow], from_lane), u[k]);
                 } else if constexpr (kGates == kAnyHead) {
-                    a[k] = all4(ha[k]);
-                    if constexpr (kHasB) u[k] = mul(u[k], all4(hb[k]));
+                    a[k] = ha[k];
+                    if constexpr (kHasB) u[k] = mul(hb[k], u[k]);
                 } else {
                     a[k] = widen(pa[k]);
                     if constexpr (kHasB) u[k] = mul(u[k], widen(pb[k]));
@@ -488,12 +501,12 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             } else {
                 n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
                 starts = run_bits<kRun>(bd.starts, run);
-                A = all4(1.f);
+                set_gate(A, 1.f);
                 B = all4(0.f);
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
                     if (k >= n) {
-                        a[k] = all4(1.f);
+                        set_gate(a[k], 1.f);
                         u[k] = all4(0.f);
                     }
                     if ((starts >> k) & 1) {
@@ -529,7 +542,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
                 const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
-                const Quad oa = shift_up(A, o * kLanesRow), ob = shift_up(B, o * kLanesRow);
+                const Gate oa = shift_up(A, o * kLanesRow);
+                const Quad ob = shift_up(B, o * kLanesRow);
                 if (sub >= o) {
                     B = pick(mine, B, fma(A, ob, B));
                     A = mul(A, oa);
@@ -538,14 +552,15 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             exA = shift_up(A, kLanesRow);
             exB = shift_up(B, kLanesRow);
             if (sub == 0) {
-                exA = all4(1.f);
+                set_gate(exA, 1.f);
                 exB = all4(0.f);
             }
             before = (rs & ((1u << sub) - 1u)) != 0;
             if (sub == kRuns - 1) {
                 float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
-                o[0] = make_float4(A.lo.x, B.lo.x, A.lo.y, B.lo.y);
-                o[1] = make_float4(A.hi.x, B.hi.x, A.hi.y, B.hi.y);
+                const Quad g = of_channels(A);
+                o[0] = make_float4(g.lo.x, B.lo.x, g.lo.y, B.lo.y);
+                o[1] = make_float4(g.hi.x, B.hi.x, g.hi.y, B.hi.y);
             }
         }
         // The group's one barrier of a step.  Past it: every warp's pair is there and every thread has its inputs of this

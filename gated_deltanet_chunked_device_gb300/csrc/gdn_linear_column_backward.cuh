@@ -139,7 +139,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         const int64_t t = stage_start(q) + run * kRun;
         const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
         const uint8_t *sa = stage + AX::kBytes, *sx = stage + Shape::kLearnBytes, *sb = sx + AX::kBytes;
-        Quad a[kRun], u[kRun], A, B = all4(0.f), E, exA, exB, rxA, rxE;
+        using Gate = std::conditional_t<kGates == kPerChannel, Quad, float>;
+        Gate a[kRun], A, exA, rxA;
+        Quad u[kRun], B = all4(0.f), E, exB, rxE;
         constexpr int kHeld = kGates == kOneHead ? (kRun + kLanesRow - 1) / kLanesRow : 1;
         float ha[kHeld], hb[kHeld];
         uint32_t starts = 0, ends = 0;
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         bool plain = true, started = false, ended = false;  // whether a sequence starts in the runs before, ends in those after
         // gates of one head: lane l of a run holds the run's token l
         auto shared_gate = [&](const float(&held)[kHeld], int k) {
-            return all4(__shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow));
+            return __shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow);
         };
         if (warp == kColWarps - 1) bounds(q + 1);
         {
@@ -177,13 +179,13 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                     u[k] = widen(AX::get(sx, run, k, l));
                     if constexpr (kHasB) {
                         if constexpr (kGates == kOneHead)
-                            u[k] = mul(u[k], shared_gate(hb, k));
+                            u[k] = mul(shared_gate(hb, k), u[k]);
                         else
                             u[k] = mul(u[k], widen(AG::get(sb, run, k, l)));
                     }
                 }
             }
-            A = all4(1.f);
+            set_gate(A, 1.f);
             E = all4(0.f);
             if (plain) {
 #pragma unroll
@@ -225,11 +227,12 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             // over the warp's runs: the carry from the right, the state from the left
             const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
             const uint32_t re = (bd.warps_end >> warp) & 1 ? runs_with<kRun, kRuns>(bd.ends, warp) : 0;
-            Quad RA = A;
+            Gate RA = A;
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
                 const bool mine = (re >> sub) & ((1u << o) - 1u);
-                const Quad oa = shift_down(RA, o * kLanesRow), oe = shift_down(E, o * kLanesRow);
+                const Gate oa = shift_down(RA, o * kLanesRow);
+                const Quad oe = shift_down(E, o * kLanesRow);
                 if (sub + o < kRuns) {
                     E = pick(mine, E, fma(RA, oe, E));
                     RA = mul(RA, oa);
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             rxA = shift_down(RA, kLanesRow);
             rxE = shift_down(E, kLanesRow);
             if (sub == kRuns - 1) {
-                rxA = all4(1.f);
+                set_gate(rxA, 1.f);
                 rxE = all4(0.f);
             }
             ended = (re >> (sub + 1)) != 0;
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 #pragma unroll
                 for (int o = 1; o < kRuns; o <<= 1) {
                     const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
-                    const Quad oa = shift_up(A, o * kLanesRow), ob = shift_up(B, o * kLanesRow);
+                    const Gate oa = shift_up(A, o * kLanesRow);
+                    const Quad ob = shift_up(B, o * kLanesRow);
                     if (sub >= o) {
                         B = pick(mine, B, fma(A, ob, B));
                         A = mul(A, oa);
@@ -255,7 +259,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 exA = shift_up(A, kLanesRow);
                 exB = shift_up(B, kLanesRow);
                 if (sub == 0) {
-                    exA = all4(1.f);
+                    set_gate(exA, 1.f);
                     exB = all4(0.f);
                 }
                 started = (rs & ((1u << sub) - 1u)) != 0;
@@ -263,8 +267,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             // the warp's: the product and the carry are the first run's
             if (sub == 0) {
                 float4* o = reinterpret_cast<float4*>(&sm.pairs[q & 1][warp][l * 4]);
-                o[0] = make_float4(RA.lo.x, E.lo.x, RA.lo.y, E.lo.y);
-                o[1] = make_float4(RA.hi.x, E.hi.x, RA.hi.y, E.hi.y);
+                const Quad g = of_channels(RA);
+                o[0] = make_float4(g.lo.x, E.lo.x, g.lo.y, E.lo.y);
+                o[1] = make_float4(g.hi.x, E.hi.x, g.hi.y, E.hi.y);
             }
             // the state is the last run's
             if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&sm.states[q & 1][warp][l * 4]) = flat(B);
@@ -362,7 +367,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 Quad vx = g;
                 if constexpr (kHasB) {
                     if constexpr (kGates == kOneHead)
-                        vx = mul(g, shared_gate(hb, k));
+                        vx = mul(shared_gate(hb, k), g);
                     else
                         vx = mul(g, widen(AG::get(sb, run, k, l)));
                 }
