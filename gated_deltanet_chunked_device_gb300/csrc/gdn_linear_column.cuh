@@ -185,34 +185,35 @@ struct StageBounds {
     int32_t start_seq[kTokens], end_seq[kTokens];
 };
 
-// Fills the bounds of tokens [t0, t1) (one warp); no entry of cu_seqlens before `lo` is at or past t0.  empty(i) is called
-// by the whole warp for every empty sequence.  Entries are taken as they are: a malformed cu_seqlens gives wrong bounds,
-// none outside.  Returns how many entries from `lo` on are before t1.
-template <int kTokens, int kWarpTokens, class Empty>
-__device__ __forceinline__ int64_t fill_bounds(const LinearParams& p, int64_t lo, int64_t t0, int64_t t1, bool last, int lane,
-                                               StageBounds<kTokens>& b, Empty empty) {
+// An entry of cu_seqlens, c at place i, with its neighbours: marks the token of [t0, t1) that starts a sequence with it,
+// and the one that ends the sequence before.  mark(start, sequence) is called for each.  Returns whether an empty sequence
+// lies at c.  Entries are taken as they are: a malformed cu_seqlens gives wrong bounds, none outside.
+template <int kTokens, class Mark>
+__device__ __forceinline__ bool mark_entry(const LinearParams& p, int64_t i, int64_t c, int64_t prev, int64_t next, int64_t t0, int64_t t1,
+                                           bool last, StageBounds<kTokens>& b, Mark mark) {
+    if (i < 0 || i > p.N || c < t0 || c > t1) return false;
+    if (i < p.N && c < t1 && next > c) {
+        b.start_seq[c - t0] = static_cast<int32_t>(i);
+        atomicOr(&b.starts[(c - t0) / 32], 1u << ((c - t0) % 32));
+        mark(true, i);
+    }
+    if (i > 0 && c > t0 && prev < c) {
+        b.end_seq[c - 1 - t0] = static_cast<int32_t>(i - 1);
+        atomicOr(&b.ends[(c - 1 - t0) / 32], 1u << ((c - 1 - t0) % 32));
+        mark(false, i - 1);
+    }
+    return i < p.N && next == c && (c < t1 || (last && c == t1));
+}
+
+template <int kTokens>
+__device__ __forceinline__ void clear_bounds(StageBounds<kTokens>& b, int lane) {
     if (lane < kTokens / 32) b.starts[lane] = b.ends[lane] = 0;
     __syncwarp();
-    int64_t moved = 0;
-    for (;; lo += 32) {
-        const int64_t i = lo + lane;
-        const int64_t c = i <= p.N ? cu_at(p, i) : t1 + 1;
-        const int64_t next = i < p.N ? cu_at(p, i + 1) : c, prev = i > 0 && i <= p.N ? cu_at(p, i - 1) : c;
-        const bool in = c >= t0 && c <= t1 && i <= p.N;
-        const bool start = in && c < t1 && next > c, end = in && c > t0 && prev < c;
-        const bool gap = in && i < p.N && next == c && (c < t1 || (last && c == t1));
-        if (start) {
-            b.start_seq[c - t0] = static_cast<int32_t>(i);
-            atomicOr(&b.starts[(c - t0) / 32], 1u << ((c - t0) % 32));
-        }
-        if (end) {
-            b.end_seq[c - 1 - t0] = static_cast<int32_t>(i - 1);
-            atomicOr(&b.ends[(c - 1 - t0) / 32], 1u << ((c - 1 - t0) % 32));
-        }
-        moved += __popc(__ballot_sync(0xffffffffu, i <= p.N && c < t1));
-        for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(lo + __ffs(m) - 1);
-        if (__any_sync(0xffffffffu, c > t1)) break;
-    }
+}
+
+// Which warps' tokens hold what was marked.
+template <int kTokens, int kWarpTokens>
+__device__ __forceinline__ void sum_up_bounds(int64_t t0, int64_t t1, int lane, StageBounds<kTokens>& b) {
     __syncwarp();
     uint32_t s = 0, e = 0;
     constexpr int kWords = kTokens / kWarpTokens;
@@ -234,8 +235,37 @@ __device__ __forceinline__ int64_t fill_bounds(const LinearParams& p, int64_t lo
         b.warps_end = we;
         b.plain = plain;
     }
-    return moved;
 }
+
+// Fills the bounds of tokens [t0, t1) (one warp) from memory; no entry of cu_seqlens before `lo` is at or past t0.
+// empty(i) is called by the whole warp for every empty sequence.
+template <int kTokens, int kWarpTokens, class Empty>
+__device__ __forceinline__ void fill_bounds(const LinearParams& p, int64_t lo, int64_t t0, int64_t t1, bool last, int lane,
+                                         StageBounds<kTokens>& b, Empty empty) {
+    clear_bounds<kTokens>(b, lane);
+    for (;; lo += 32) {
+        const int64_t i = lo + lane;
+        const int64_t c = i <= p.N ? cu_at(p, i) : t1 + 1;
+        const int64_t next = i < p.N ? cu_at(p, i + 1) : c, prev = i > 0 && i <= p.N ? cu_at(p, i - 1) : c;
+        const bool gap = mark_entry<kTokens>(p, i, c, prev, next, t0, t1, last, b, [](bool, int64_t) {});
+        for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(lo + __ffs(m) - 1);
+        if (__any_sync(0xffffffffu, c > t1)) break;
+    }
+    sum_up_bounds<kTokens, kWarpTokens>(t0, t1, lane, b);
+}
+
+// 32 entries of cu_seqlens in a warp's registers, a lane's at place `first` + lane (step = 1) or `first` - lane (step = -1).
+// Loaded a stage before they are looked at, so that a stage with bounds does not wait for memory.
+struct Window {
+    int64_t first, c;
+    __device__ __forceinline__ void load(const LinearParams& p, int64_t at, int step, int lane) {
+        first = at;
+        const int64_t i = at + step * lane;
+        c = i < 0 ? -1 : i <= p.N ? cu_at(p, i) : INT64_MAX;
+    }
+};
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 template <int kTokens>
 __device__ __forceinline__ void no_bounds(StageBounds<kTokens>& b, int lane) {
@@ -271,6 +301,15 @@ __device__ __forceinline__ uint32_t runs_with(const uint32_t* words, int warp) {
     uint32_t r = 0;
 #pragma unroll
     for (int i = 0; i < kRuns; ++i) r |= (run_bits<kRun>(words, warp * kRuns + i) ? 1u : 0u) << i;
+    return r;
+}
+
+// Which tokens of any of a warp's runs hold a bound: what a warp tests before it looks at its own run's.
+template <int kRun, int kRuns>
+__device__ __forceinline__ uint32_t any_run_bits(const uint32_t* words, int warp) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) r |= run_bits<kRun>(words, warp * kRuns + i);
     return r;
 }
 
@@ -422,30 +461,41 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
         }
     };
-    int64_t lo = 0, next = 0;  // the walk over cu_seqlens: entries before `lo` are before the tokens to come, entry `lo` is `next`
+    Window win{0, 0};  // from the last entry before the tokens to come on
     auto bounds = [&](int q) {
         if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, end);
-        if (q < kGroups || (q >= stages && q < stages + kGroups)) {
-            lo = t0 == 0 ? 0 : first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
-            next = 0;
-        }
+        if (q < kGroups || (q >= stages && q < stages + kGroups))
+            win.load(p, first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane) - 1, 1, lane);
         StageBounds<kTokens>& b = gr.bounds[q / kGroups % 3];
-        if (next > t1 && t1 == t0 + kTokens) {  // most stages
-            no_bounds(b, lane);
+        if (t1 == t0 + kTokens && !__any_sync(0xffffffffu, win.c >= t0 && win.c <= t1) && __any_sync(0xffffffffu, win.c > t1)) {
+            no_bounds(b, lane);  // most stages
             return;
         }
-        const bool write = q >= steps - stages;
-        lo += fill_bounds<kTokens, kWarpTokens>(p, lo, t0, t1, t1 == p.T, lane, b, [&](int64_t i) {
-            // an empty sequence's final state is its initial one
+        const bool write = q >= steps - stages, last = t1 == p.T;
+        auto empty = [&](int64_t i) {  // an empty sequence's final state is its initial one
             if (!write || !p.output_state || p.output_state == p.initial_state) return;
             const int64_t row = state_row(p, i);
             if (row < 0 || lane * 4 >= cols) return;
             const int64_t off = row * p.state_stride + c0 + lane * 4;
             state_quad_store(p.output_state, off, p.state_dt,
                              p.initial_state ? state_quad_load(p.initial_state, off, p.state_dt) : make_float4(0.f, 0.f, 0.f, 0.f));
-        });
-        next = lo <= p.N ? cu_at(p, lo) : INT64_MAX;
+        };
+        if (__shfl_sync(0xffffffffu, win.c, 31) > t1) {  // the window holds all of the stage's entries
+            clear_bounds<kTokens>(b, lane);
+            const int64_t next = __shfl_down_sync(0xffffffffu, win.c, 1), prev = __shfl_up_sync(0xffffffffu, win.c, 1);
+            const bool gap = lane > 0 && mark_entry<kTokens>(p, win.first + lane, win.c, prev, next, t0, t1, last, b, [&](bool start, int64_t i) {
+                if (start && p.initial_state && !p.state_indices)
+                    prefetch_l2(static_cast<const uint8_t*>(p.initial_state) + (i * p.state_stride + c0) * dtype_bytes(p.state_dt));
+            });
+            for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(win.first + __ffs(m) - 1);
+            sum_up_bounds<kTokens, kWarpTokens>(t0, t1, lane, b);
+            win.load(p, win.first + __popc(__ballot_sync(0xffffffffu, win.c < t1)) - 1, 1, lane);
+        } else {
+            const int64_t lo = first_entry(p, static_cast<int64_t>(p.N) + 1, t0, lane);
+            fill_bounds<kTokens, kWarpTokens>(p, lo, t0, t1, last, lane, b, empty);
+            win.load(p, first_entry(p, static_cast<int64_t>(p.N) + 1, t1, lane) - 1, 1, lane);
+        }
     };
 
     if (threadIdx.x == 0)
@@ -468,7 +518,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         using Gate = std::conditional_t<kGates == kPerChannel, Quad, float>;
         Gate a[kRun], A, exA;
         Quad u[kRun], B, exB;
-        uint32_t starts = 0;
+        uint32_t starts = 0, ends = 0;
         int n = kRun;
         bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
         if (warp == kColWarps - 1) bounds(q + kGroups);
@@ -490,26 +540,27 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                     if constexpr (kHasB) u[k] = mul(u[k], widen(pb[k]));
                 }
             }
-            if (plain) {
-                A = a[0];
-                B = u[0];
-#pragma unroll
-                for (int k = 1; k < kRun; ++k) {
-                    A = mul(A, a[k]);
-                    B = fma(a[k], B, u[k]);
-                }
-            } else {
+            set_gate(A, 1.f);
+            B = all4(0.f);
+            uint32_t any = 0;
+            if (!plain) {
                 n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
-                starts = run_bits<kRun>(bd.starts, run);
-                set_gate(A, 1.f);
-                B = all4(0.f);
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
-                    if (k >= n) {
-                        set_gate(a[k], 1.f);
-                        u[k] = all4(0.f);
-                    }
-                    if ((starts >> k) & 1) {
+                    if (k < n) continue;
+                    set_gate(a[k], 1.f);
+                    u[k] = all4(0.f);
+                }
+                starts = run_bits<kRun>(bd.starts, run);
+                ends = run_bits<kRun>(bd.ends, run);
+                any = any_run_bits<kRun, kRuns>(bd.starts, warp);
+            }
+            // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
+            auto compose = [&](auto whole) {
+                constexpr bool kWhole = decltype(whole)::value;
+#pragma unroll
+                for (int k = 0; k < kRun; ++k) {
+                    if (!kWhole && ((any >> k) & 1) && ((starts >> k) & 1)) {
                         if (p.initial_state && on) {
                             const int64_t row = state_row(p, bd.start_seq[run * kRun + k]);
                             // With states in place, a later segment may have written the row of a sequence that starts
@@ -530,13 +581,16 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                             }
                             if (row >= 0) u[k] = fma(a[k], quad(h0), u[k]);
                         }
-                        B = u[k];
-                    } else {
-                        A = mul(A, a[k]);
-                        B = fma(a[k], B, u[k]);
+                        B = all4(0.f);
                     }
+                    A = mul(A, a[k]);
+                    B = fma(a[k], B, u[k]);
                 }
-            }
+            };
+            if (plain)
+                compose(std::true_type{});
+            else
+                compose(std::false_type{});
             // over the warp's runs
             const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
 #pragma unroll
@@ -627,31 +681,30 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             Quad h = pick(before, exB, fma(exA, e, exB));
             if (!on) continue;
             X* out = y + t * p.y_stride;
-            if (plain) {
+            auto tokens = [&](auto whole) {
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
+                    if (!kWhole && ((starts >> k) & 1)) h = all4(0.f);
                     h = fma(a[k], h, u[k]);
-                    store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
+                    if (kWhole || k < n) store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
                     out += p.y_stride;
-                }
-                if (p.tile_states && (t + kRun) % kTile == 0)
-                    *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
-            } else {
-                const uint32_t ends = run_bits<kRun>(bd.ends, run);
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    if (k >= n) break;
-                    h = pick((starts >> k) & 1, u[k], fma(a[k], h, u[k]));
-                    store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
-                    out += p.y_stride;
-                    if (((ends >> k) & 1) && p.output_state) {
-                        const int64_t row = state_row(p, bd.end_seq[run * kRun + k]);
-                        if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
+                    if (!kWhole && ((ends >> k) & 1)) {
+                        if (p.output_state) {
+                            const int64_t row = state_row(p, bd.end_seq[run * kRun + k]);
+                            if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
+                        }
+                        if (p.tile_states && t + k == p.T - 1)
+                            *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = flat(h);
                     }
-                    if (p.tile_states && ((t + k) % kTile == kTile - 1 || t + k == p.T - 1))
-                        *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = flat(h);
                 }
-            }
+            };
+            if (plain)
+                tokens(std::true_type{});
+            else
+                tokens(std::false_type{});
+            if (p.tile_states && (t + kRun) % kTile == 0 && n == kRun)
+                *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
         }
     }
 }

@@ -87,33 +87,39 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         AX::fetch(stage + Shape::kLearnBytes, &maps.x, bar, c0, t0);
         if constexpr (kHasB) AG::fetch(stage + Shape::kLearnBytes + AX::kBytes, &maps.b, bar, at, t0);
     };
-    // The walk over cu_seqlens, from the right: entry `lo` is the first that is not before the tokens done, `at` its value,
-    // `before` the value of the one before it.
-    int64_t lo = 0, at = 0, before = 0;
+    Window win{0, 0};  // from the first entry past the tokens to come down
     auto bounds = [&](int q) {
         if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, p.T);
-        if (q == 0 || q == stages) {
-            lo = first_entry(p, static_cast<int64_t>(p.N) + 1, t1, lane);
-            at = before = t1;
-        }
+        if (q == 0 || q == stages) win.load(p, first_entry(p, static_cast<int64_t>(p.N) + 1, t1 + 1, lane), -1, lane);
         StageBounds<kTokens>& b = sm.bounds[q % 3];
-        if (before < t0 && at > t1 && t1 == t0 + kTokens) {  // most stages
-            no_bounds(b, lane);
+        if (t1 == t0 + kTokens && !__any_sync(0xffffffffu, win.c >= t0 && win.c <= t1) && __any_sync(0xffffffffu, win.c < t0)) {
+            no_bounds(b, lane);  // most stages
             return;
         }
-        const bool write = q >= steps - stages;
-        const int64_t from = first_entry(p, lo, t0, lane);
-        fill_bounds<kTokens, kWarpTokens>(p, from, t0, t1, t1 == p.T, lane, b, [&](int64_t i) {
-            // an empty sequence hands the gradient of its final state on
+        const bool write = q >= steps - stages, last = t1 == p.T;
+        auto empty = [&](int64_t i) {  // an empty sequence hands the gradient of its final state on
             if (!write || !p.d_initial || lane * 4 >= cols) return;
             const int64_t off = i * p.C + c0 + lane * 4;
             *reinterpret_cast<float4*>(p.d_initial + off) =
                 p.d_final ? *reinterpret_cast<const float4*>(p.d_final + off) : make_float4(0.f, 0.f, 0.f, 0.f);
-        });
-        lo = from;
-        at = lo <= p.N ? cu_at(p, lo) : INT64_MAX;
-        before = lo > 0 ? cu_at(p, lo - 1) : -1;
+        };
+        if (__shfl_sync(0xffffffffu, win.c, 31) < t0) {  // the window holds all of the stage's entries
+            clear_bounds<kTokens>(b, lane);
+            const int64_t prev = __shfl_down_sync(0xffffffffu, win.c, 1), next = __shfl_up_sync(0xffffffffu, win.c, 1);
+            const bool gap = lane > 0 && mark_entry<kTokens>(p, win.first - lane, win.c, prev, next, t0, t1, last, b, [&](bool start, int64_t i) {
+                if (start && p.initial_state)
+                    prefetch_l2(static_cast<const uint8_t*>(p.initial_state) + (i * p.state_stride + c0) * dtype_bytes(p.state_dt));
+                if (!start && p.d_final) prefetch_l2(p.d_final + i * p.C + c0);
+            });
+            for (uint32_t m = __ballot_sync(0xffffffffu, gap); m; m &= m - 1) empty(win.first - (__ffs(m) - 1));
+            sum_up_bounds<kTokens, kWarpTokens>(t0, t1, lane, b);
+            win.load(p, win.first - __popc(__ballot_sync(0xffffffffu, win.c > t0)) + 1, -1, lane);
+        } else {
+            const int64_t n = static_cast<int64_t>(p.N) + 1;
+            fill_bounds<kTokens, kWarpTokens>(p, first_entry(p, n, t0, lane), t0, t1, last, lane, b, empty);
+            win.load(p, first_entry(p, n, t0 + 1, lane), -1, lane);
+        }
     };
     // The state that enters this warp's tile (of channel `ch`), from the forward pass: one step ahead.
     float saved = 0.f;
@@ -147,6 +153,15 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         uint32_t starts = 0, ends = 0;
         int n = kRun;
         bool plain = true, started = false, ended = false;  // whether a sequence starts in the runs before, ends in those after
+        uint32_t any_start = 0, any_end = 0;
+        auto initial = [&](int k) {
+            if (!p.initial_state || !on) return all4(0.f);
+            return quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt));
+        };
+        auto final_gradient = [&](int k) {
+            if (!p.d_final || !on) return all4(0.f);
+            return quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4, GDN_DTYPE_F32));
+        };
         // gates of one head: lane l of a run holds the run's token l
         auto shared_gate = [&](const float(&held)[kHeld], int k) {
             return __shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow);
@@ -187,43 +202,36 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
             set_gate(A, 1.f);
             E = all4(0.f);
-            if (plain) {
-#pragma unroll
-                for (int k = kRun - 1; k >= 0; --k) {
-                    E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
-                    A = mul(A, a[k]);
-                }
-                if (!learn) {
-                    B = u[0];
-#pragma unroll
-                    for (int k = 1; k < kRun; ++k) B = fma(a[k], B, u[k]);
-                }
-            } else {
+            if (!plain) {
                 n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), p.T - t)));
+#pragma unroll
+                for (int k = 0; k < kRun; ++k)  // past the end, a carry goes through
+                    if (k >= n) set_gate(a[k], 1.f);
                 starts = run_bits<kRun>(bd.starts, run);
                 ends = run_bits<kRun>(bd.ends, run);
+                any_start = any_run_bits<kRun, kRuns>(bd.starts, warp);
+                any_end = any_run_bits<kRun, kRuns>(bd.ends, warp);
+            }
+            // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
+            auto compose = [&](auto whole) {
+                constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
                 for (int k = kRun - 1; k >= 0; --k) {
-                    if (k >= n) continue;
-                    if ((ends >> k) & 1)
-                        E = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
-                                                                   GDN_DTYPE_F32))
-                                            : all4(0.f);
+                    if (!kWhole && ((any_end >> k) & 1) && ((ends >> k) & 1)) E = final_gradient(k);
                     E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
                     A = mul(A, a[k]);
                 }
-                if (!learn) {
+                if (!learn)
 #pragma unroll
                     for (int k = 0; k < kRun; ++k) {
-                        if (k >= n) continue;
-                        if ((starts >> k) & 1)
-                            B = p.initial_state && on
-                                    ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
-                                    : all4(0.f);
+                        if (!kWhole && ((any_start >> k) & 1) && ((starts >> k) & 1)) B = initial(k);
                         B = fma(a[k], B, u[k]);
                     }
-                }
-            }
+            };
+            if (plain)
+                compose(std::true_type{});
+            else
+                compose(std::false_type{});
             // over the warp's runs: the carry from the right, the state from the left
             const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
             const uint32_t re = (bd.warps_end >> warp) & 1 ? runs_with<kRun, kRuns>(bd.ends, warp) : 0;
@@ -337,31 +345,24 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         Quad h = pick(started, exB, fma(exA, spread(enter_h), exB));
         Quad c = pick(ended, rxE, fma(rxA, spread(enter_c), rxE));
         float sums[kGates == kOneHead ? kRun : 1][2];
-        // The tokens once more; `whole`: all of them are there, with neither a start nor an end.
+        // The tokens once more.
         auto tokens = [&](auto whole) {
             constexpr bool kWhole = decltype(whole)::value;
-            // states before each token, from the left; they take u's place
+            // States before each, from the left; they take u's place.
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                if (!kWhole && ((starts >> k) & 1))
-                    h = p.initial_state && on
-                            ? quad(state_quad_load(p.initial_state, bd.start_seq[run * kRun + k] * p.state_stride + c0 + l * 4, p.state_dt))
-                            : all4(0.f);
+                if (!kWhole && ((any_start >> k) & 1) && ((starts >> k) & 1)) h = initial(k);
                 const Quad v = h;
                 if (k < kRun - 1) h = fma(a[k], h, u[k]);
                 u[k] = v;
             }
-            // gradients, from the right
+            // Gradients, from the right.
             X* dx = static_cast<X*>(p.dx) + (t + kRun - 1) * p.dx_stride + c0 + l * 4;
             G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.da_stride + c0 + l * 4);
             G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.db_stride + c0 + l * 4) : nullptr;
 #pragma unroll
             for (int k = kRun - 1; k >= 0; --k) {
-                const bool in = kWhole || k < n;
-                if (!kWhole && in && ((ends >> k) & 1))
-                    c = p.d_final && on ? quad(state_quad_load(p.d_final, static_cast<int64_t>(bd.end_seq[run * kRun + k]) * p.C + c0 + l * 4,
-                                                               GDN_DTYPE_F32))
-                                        : all4(0.f);
+                if (!kWhole && ((any_end >> k) & 1) && ((ends >> k) & 1)) c = final_gradient(k);
                 const Quad g = add(widen(AX::get(stage, run, k, l)), c);
                 const Quad va = mul(g, u[k]), vb = mul(g, widen(AX::get(sx, run, k, l)));
                 Quad vx = g;
@@ -371,16 +372,16 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                     else
                         vx = mul(g, widen(AG::get(sb, run, k, l)));
                 }
-                if (in) c = mul(a[k], g);
-                if (in && on) {
+                c = mul(a[k], g);
+                if ((kWhole || k < n) && on) {
                     store_stream(reinterpret_cast<Pack<X>*>(dx), narrow(vx, X{}));
                     if constexpr (kGates == kPerChannel) {
                         store_stream(reinterpret_cast<Pack<G>*>(da), narrow(va, G{}));
                         if constexpr (kHasB) store_stream(reinterpret_cast<Pack<G>*>(db), narrow(vb, G{}));
                     }
-                    if (!kWhole && ((starts >> k) & 1) && p.d_initial)
-                        *reinterpret_cast<float4*>(p.d_initial + static_cast<int64_t>(bd.start_seq[run * kRun + k]) * p.C + c0 + l * 4) = flat(c);
                 }
+                if (!kWhole && ((any_start >> k) & 1) && ((starts >> k) & 1) && on && p.d_initial)
+                    *reinterpret_cast<float4*>(p.d_initial + static_cast<int64_t>(bd.start_seq[run * kRun + k]) * p.C + c0 + l * 4) = flat(c);
                 dx -= p.dx_stride;
                 if constexpr (kGates == kPerChannel) {
                     da -= p.da_stride;
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 #pragma unroll
             for (int i = 0; i < kMine; ++i) {
                 const int k = l * kMine + i;
-                if (!plain && k >= n) continue;
+                if (k >= n) continue;
                 const int64_t tk = t + k;
                 if (pieces == 1) {
                     from_f32(sums[i][0], static_cast<G*>(p.da)[tk * p.da_stride + head]);

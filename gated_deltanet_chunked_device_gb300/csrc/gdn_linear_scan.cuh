@@ -503,7 +503,7 @@ struct BackwardSmem {
 // The carry goes from right to left: c_t = a_t (dy_t + c_{t+1}).  Tiles are taken from the right, and handed on as in
 // the forward pass; the states come from the left, from what the forward pass saved at the tiles' ends.
 template <class X, class G, bool kVec, bool kHead, bool kHasB>
-__global__ void __launch_bounds__(kThreads) gdn_linear_backward_kernel(const LinearParams p, const ScanSpace s) {
+__global__ void __launch_bounds__(kThreads, 2) gdn_linear_backward_kernel(const LinearParams p, const ScanSpace s) {
     __shared__ BackwardSmem<kVec, kHead> sm;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const bool multi = s.nt > 1;
@@ -733,6 +733,25 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_backward_kernel(const Lin
             sm.red[warp][0][k * 33 + lane] = (va[0] + va[1]) + (va[2] + va[3]);
             sm.red[warp][1][k * 33 + lane] = (vb[0] + vb[1]) + (vb[2] + vb[3]);
         } else if constexpr (kHead) {
+            if (heads <= 4) {  // a sum over the warp for each of them
+                for (int hd = 0; hd < heads; ++hd) {
+                    float sa = 0.f, sb = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int col = lane + 32 * j;
+                        const bool of = col < cols && col / wide == hd;
+                        sa += of ? va[j] : 0.f;
+                        sb += of ? vb[j] : 0.f;
+                    }
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) {
+                        sa += __shfl_xor_sync(0xffffffffu, sa, o);
+                        sb += __shfl_xor_sync(0xffffffffu, sb, o);
+                    }
+                    if (lane == 0 && t < t1) store_sums(t, hd, sa, sb);
+                }
+                continue;
+            }
             put4<kVec>(sm.red[warp][0], lane, va);
             put4<kVec>(sm.red[warp][1], lane, vb);
             __syncwarp();
