@@ -1,6 +1,7 @@
 // gdn_linear.cu -- how runs of the gated linear recurrence go
 // (include/gdn_linear.h): which kernels, their workspace and maps; and the
 // decode step's kernel.
+#include <atomic>
 #include <cudaTypedefs.h>
 
 #include "gdn_linear_column.cuh"
@@ -261,10 +262,13 @@ bool encode_rows(CUtensorMap* map, const void* base, int32_t dt, int64_t stride,
 }
 
 int multiprocessors() {
+    static std::atomic<int> known[64];  // a device's count does not change
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    return n > 0 ? n : 1;
+    if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return 1;
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 size_t linear_forward_workspace(const LinearParams& p) { return forward_route(p).layout.total; }

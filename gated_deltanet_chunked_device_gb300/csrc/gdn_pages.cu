@@ -10,7 +10,7 @@
 #include <climits>
 
 #include "../../include/gdn_pages.h"
-#include "gdn_internal.cuh"
+#include "gdn_linear.cuh"
 
 namespace {
 
@@ -550,12 +550,7 @@ BookParams make_book(const gdn_pages_book& b, int32_t n, void* workspace) {
     return p;
 }
 
-int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 1;
-    return n > 0 ? n : 1;
-}
+int sm_count() { return gdn::multiprocessors(); }
 
 // Bytes that rows of both buffers can be copied at a time.
 int32_t copy_unit(const gdn_pages_buffer& s, const gdn_pages_buffer& d) {

@@ -92,6 +92,40 @@ def test_in_place():
     assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("H,D", [(1, 32), (2, 17)])
+def test_in_place_over_many_segments(H, D):
+    i = make([4000, 1500], H, D, "bf16", seed=27)
+    y = gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=i["h0"], cu_seqlens=i["cu"])
+    for _ in range(5):
+        x = i["x"].clone()
+        gdn.gated_linear_recurrence(x, i["a"], i["b"], initial_state=i["h0"], cu_seqlens=i["cu"], output=x)
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("lens", [[512] * 20, [1, 2, 3] * 300, [0] * 50 + [300] + [0] * 70 + [1] * 90 + [0, 2000], [255, 257] * 8])
+@pytest.mark.parametrize("H,D,gates", [(1, 64, "channel"), (1, 64, "head"), (3, 6, "head")])
+def test_many_sequences(lens, H, D, gates):
+    """More bounds in a stage than a warp looks at at a time, and bounds at every place of a stage."""
+    i = make(lens, H, D, "f32", gates=gates, seed=28)
+    _, _, tiles = check_forward(i)
+    check_backward(i, tiles)
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements, and the last tokens as a short sequence with the state before them gives them: gates of 1/2
+    forget all but 2^-200 of what was 200 tokens ago, so the last 300 tokens alone have the same states to 2^-100."""
+    T, H, D, n = 70000, 256, 128, 300
+    x = torch.empty(T, H, D, dtype=torch.bfloat16, device="cuda").normal_()
+    a = torch.full((T, H), 0.5, device="cuda")
+    tiles = torch.empty(-(-T // 64), H, D, device="cuda")
+    y = gdn.gated_linear_recurrence(x, a, tile_states=tiles)
+    want = ref.forward(f64(x[-n:, :, :2]), f64(a[-n:]), None, [0, n])
+    within("y", y[-50:, :, :2], want[0][-50:], want[3][-50:] + 2.0 ** -100, torch.bfloat16)
+    dx = gdn.gated_linear_recurrence_backward(x, x, a, tile_states=tiles)[0]
+    val, err = ref.backward(f64(x[-n:, :, :2]), f64(x[-n:, :, :2]), f64(a[-n:]), None, [0, n])
+    within("dx", dx[-50:, :, :2], val["dx"][-50:], err["dx"][-50:], torch.bfloat16)
+
+
 @pytest.mark.parametrize("index", [torch.int32, torch.int64])
 @pytest.mark.parametrize("state", [torch.float32, torch.bfloat16, torch.float16, torch.float8_e4m3fn, torch.float8_e5m2])
 def test_pool(state, index):

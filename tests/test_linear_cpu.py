@@ -1,5 +1,7 @@
 """The gated linear recurrence without a GPU: the oracle's gradients against differences, and what the entry points refuse."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -146,6 +148,16 @@ def test_an_empty_batch_launches_nothing():
     assert gdn.gdn_linear_backward_run(plan, gdn.LinearArgs(), 1 << 22, nbytes, None) == 0
     assert gdn.gdn_linear_decode_run(plan, gdn.LinearArgs(), 1, None) == 0
     gdn.gdn_linear_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("header", ["gdn_linear.h", "gdn_pages.h"])
+def test_exports_every_declared_symbol(header):
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", header)) as f:
+        text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    names = re.findall(r"\b(gdn_\w+)\s*\(", text)
+    assert len(names) >= 6
+    for n in names:
+        assert hasattr(gdn.lib(), n), n
 
 
 def test_structs_match_the_header():
