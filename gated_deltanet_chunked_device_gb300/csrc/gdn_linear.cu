@@ -222,7 +222,7 @@ Route backward_route(const LinearParams& p) {
             vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
     if (p.gate_div == 1) r.vec = r.vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
     if (r.vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
-        r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);
+        r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);  // backward_run
         r.column = p.gate_div == 1 || linear::one_head(p, r.width);
     }
     r.blocks = backward_blocks(p.C, head_dim);

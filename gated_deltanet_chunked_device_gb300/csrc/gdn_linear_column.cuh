@@ -23,7 +23,7 @@ namespace gdn {
 namespace linear {
 
 // A block's shape: W channels; NG groups of NW warps, which take the stages in turn; runs of R tokens.
-template <int W, int NW, int R, int NG = 1>
+template <int W, int NW, int R, int NG>
 struct Column {
     static constexpr int kWidth = W, kRun = R, kGroups = NG;
     static constexpr int kLanesRow = W / 4;      // lanes that hold one token's channels

@@ -24,18 +24,24 @@ struct BackwardShape {
     // dy, a, x, b: the first two are what a pass that learns needs
     static constexpr int kLearnBytes = AX::kBytes + AG::kBytes;
     static constexpr int kStageBytes = 2 * AX::kBytes + (kHasB ? 2 : 1) * AG::kBytes;
-    static constexpr int kDepth = kRingBytes / kStageBytes < 4 ? kRingBytes / kStageBytes : 4;
-    struct Tables {
+    static constexpr int kDepth = kRingBytes / kStageBytes < 6 ? kRingBytes / kStageBytes : 6;
+    struct Group {
         StageBounds<kTokens> bounds[3];
         alignas(16) float2 pairs[2][Col::kWarps][W];  // a warp's tokens: product of the gates, carry from zero
         alignas(16) float states[2][Col::kWarps][W];  // and the state from zero
-        float enter[W];
+    };
+    struct Tables {
+        Group groups[Col::kGroups];
+        float2 hand[Col::kHands][W];  // the carry that enters a stage, and in steps that learn the gates' product so far
+        int32_t hand_reset[Col::kHands];
         uint64_t full[kDepth];
+        uint64_t handed[Col::kHands];
         uint32_t ticket;
     };
     static constexpr int kSmem = kDepth * kStageBytes + static_cast<int>(sizeof(Tables));
     static_assert(kDepth >= 2, "the next stage comes while one is worked on");
     static_assert(kStageBytes % 128 == 0 && alignof(Tables) == 16, "boxes and tables lie aligned");
+    static_assert(kSmem <= 227 * 1024, "shared memory of a block");
 };
 
 template <class X, class G, int kGates, bool kHasB, class Col>
@@ -45,16 +51,21 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     using AX = typename Shape::AX;
     using AG = typename Shape::AG;
     constexpr int W = Shape::W, kTokens = Shape::kTokens, kDepth = Shape::kDepth, kRuns = Col::kRuns, kLanesRow = Col::kLanesRow;
-    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun;
+    constexpr int kColWarps = Col::kWarps, kWarpTokens = Col::kWarpTokens, kRun = Col::kRun, kGroups = Col::kGroups;
+    constexpr int kHands = Col::kHands;
     constexpr int kTileWarps = kTile / kWarpTokens;  // warps whose tokens are a tile
     extern __shared__ __align__(1024) uint8_t ring[];
     typename Shape::Tables& sm = *reinterpret_cast<typename Shape::Tables*>(ring + kDepth * Shape::kStageBytes);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int group = threadIdx.x / (32 * kColWarps), warp = threadIdx.x / 32 % kColWarps, lane = threadIdx.x % 32;
+    typename Shape::Group& gr = sm.groups[group];
+    const bool leader = warp == 0 && lane == 0;  // of the group
     const int sub = lane / kLanesRow, l = lane % kLanesRow, run = warp * kRuns + sub, ch = lane % W;
     const ScanSpace& sp = seg.space;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kDepth; ++i) mbar_init(&sm.full[i], 1);
+        for (int i = 0; i < kHands; ++i) mbar_init(&sm.handed[i], 1);
         fence_mbar_init();
+        mbar_arrive(&sm.handed[0]);  // nothing is handed to stage 0: its place's first turn is over
         if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
     __syncthreads();
@@ -91,8 +102,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     auto bounds = [&](int q) {
         if (q >= max(steps, 1)) return;  // without tokens, the empty sequences
         const int64_t t0 = stage_start(q), t1 = min(t0 + kTokens, p.T);
-        if (q == 0 || q == stages) win.load(p, first_entry(p, static_cast<int64_t>(p.N) + 1, t1 + 1, lane), -1, lane);
-        StageBounds<kTokens>& b = sm.bounds[q % 3];
+        if (q < kGroups || (q >= stages && q < stages + kGroups))
+            win.load(p, first_entry(p, static_cast<int64_t>(p.N) + 1, t1 + 1, lane), -1, lane);
+        StageBounds<kTokens>& b = gr.bounds[q / kGroups % 3];
         if (t1 == t0 + kTokens && !__any_sync(0xffffffffu, win.c >= t0 && win.c <= t1) && __any_sync(0xffffffffu, win.c < t0)) {
             no_bounds(b, lane);  // most stages
             return;
@@ -130,17 +142,28 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         if (tile > 0 && tile * kTile < p.T) saved = p.tile_states[(tile - 1) * p.C + c0 + ch];
     };
 
+    // A stage's place in the ring is free when its group is done with it, which the group's next step shows: a place is
+    // fetched kGroups stages late.
+    constexpr int kAhead = kDepth - kGroups;
+    static_assert(kAhead >= kGroups, "every group has its next stage on the way");
     if (threadIdx.x == 0)
-        for (int q = 0; q < kDepth - 1; ++q) fetch(q);
-    if (warp == kColWarps - 1) bounds(0);
-    if (warp == kColWarps - 2 && blk == 0) check_bounds(p, part, sp.nt, lane);
-    fetch_saved(0);
+        for (int q = 0; q < kAhead; ++q) fetch(q);
+    if (warp == kColWarps - 1) bounds(group);
+    if (group == 0 && warp == 0 && blk == 0) check_bounds(p, part, sp.nt, lane);
+    fetch_saved(group);
     __syncthreads();
-    float carry = 0.f, through = 1.f;  // of channel `ch`: the carry (in steps that learn, from zero), the gates' product
-    bool reset = false, ok = true;     // whether a sequence has ended; until a wait runs out
+    bool ok = true;  // until a wait runs out
+    float2 own = make_float2(0.f, 1.f);
+    bool own_reset = false;
+    auto wait_hand = [&](int q) {
+        if (ok && !mbar_wait(&sm.handed[q % kHands], (q / kHands) & 1)) {
+            ok = false;
+            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+        }
+    };
     const int pieces = kGates == kOneHead ? p.D / W : 1, piece = kGates == kOneHead ? c0 % p.D / W : 0;
-    for (int q = 0; q < steps; ++q) {
-        const StageBounds<kTokens>& bd = sm.bounds[q % 3];
+    for (int q = group; q < steps; q += kGroups) {
+        const StageBounds<kTokens>& bd = gr.bounds[q / kGroups % 3];
         const bool learn = twice && q < stages;
         const int64_t t = stage_start(q) + run * kRun;
         const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
@@ -166,7 +189,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         auto shared_gate = [&](const float(&held)[kHeld], int k) {
             return __shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow);
         };
-        if (warp == kColWarps - 1) bounds(q + 1);
+        if (warp == kColWarps - 1) bounds(q + kGroups);
         {
             plain = (bd.plain >> warp) & 1;
             if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
@@ -274,49 +297,57 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
             // the warp's: the product and the carry are the first run's
             if (sub == 0) {
-                float4* o = reinterpret_cast<float4*>(&sm.pairs[q & 1][warp][l * 4]);
+                float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
                 const Quad g = of_channels(RA);
                 o[0] = make_float4(g.lo.x, E.lo.x, g.lo.y, E.lo.y);
                 o[1] = make_float4(g.hi.x, E.hi.x, g.hi.y, E.hi.y);
             }
             // the state is the last run's
-            if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&sm.states[q & 1][warp][l * 4]) = flat(B);
+            if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&gr.states[q / kGroups & 1][warp][l * 4]) = flat(B);
         }
-        // The step's one barrier.  Past it: every warp's pair is there, nobody reads the stage before any more (its place in
-        // the ring is free), and the bounds of the next stage are known.
-        __syncthreads();
-        float enter_c = carry, enter_h = saved;
-        {
-            if (threadIdx.x == 0) fetch(q + kDepth - 1);
-            float2 ae[kColWarps];
+        // The group's one barrier of a step.  Past it: every warp's pair is there, nobody of the group reads its stage before
+        // any more (its place in the ring is free), and the bounds of the group's next stage are known.
+        named_bar_sync(1 + group, 32 * kColWarps);
+        if (leader) fetch(q + kAhead);
+        float2 ae[kColWarps];
 #pragma unroll
-            for (int w = 0; w < kColWarps; ++w) ae[w] = sm.pairs[q & 1][w][ch];
-            // the state at the tile's start, through the tile's warps before this one
+        for (int w = 0; w < kColWarps; ++w) ae[w] = gr.pairs[q / kGroups & 1][w][ch];
+        // the state at the tile's start, through the tile's warps before this one
+        float enter_h = saved;
 #pragma unroll
-            for (int w = 0; w < kTileWarps - 1; ++w) {
-                const int v = warp / kTileWarps * kTileWarps + w;
-                if (v >= warp) break;
-                const float b = sm.states[q & 1][v][ch];
-                enter_h = (bd.warps_start >> v) & 1 ? b : fmaf(sm.pairs[q & 1][v][ch].x, enter_h, b);
-            }
-            const uint32_t resets = bd.warps_end;
-#pragma unroll
-            for (int w = kColWarps - 1; w >= 0; --w) {
-                if (w == warp) enter_c = carry;
-                carry = fmaf(ae[w].x, carry, ae[w].y);
-                if (resets != 0 && ((resets >> w) & 1)) carry = ae[w].y;
-            }
-            if (learn)
-#pragma unroll
-                for (int w = 0; w < kColWarps; ++w) through *= ae[w].x;
-            reset |= resets != 0;
-            fetch_saved(q + 1);
+        for (int w = 0; w < kTileWarps - 1; ++w) {
+            const int v = warp / kTileWarps * kTileWarps + w;
+            if (v >= warp) break;
+            const float b = gr.states[q / kGroups & 1][v][ch];
+            enter_h = (bd.warps_start >> v) & 1 ? b : fmaf(gr.pairs[q / kGroups & 1][v][ch].x, enter_h, b);
         }
-        if (learn) {
-            if (q < stages - 1) continue;
-            if (warp == 0) {  // hand the pair on, get the carry that enters
-                const int c = c0 + lane;
-                uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
+        fetch_saved(q + kGroups);
+        // What the stage to the right hands on: the carry (in steps that learn, from zero), and the gates' product.
+        const uint32_t resets = bd.warps_end;
+        // (One group keeps it itself.)
+        float2 hand = own;
+        if (kGroups > 1 && q > 0) {
+            wait_hand(q);
+            hand = sm.hand[q % kHands][ch];
+        }
+        float carry = hand.x, enter_c = carry;
+#pragma unroll
+        for (int w = kColWarps - 1; w >= 0; --w) {
+            if (w == warp) enter_c = carry;
+            carry = fmaf(ae[w].x, carry, ae[w].y);
+            if (resets != 0 && ((resets >> w) & 1)) carry = ae[w].y;
+        }
+        float through = hand.y;
+        if (learn)
+#pragma unroll
+            for (int w = 0; w < kColWarps; ++w) through *= ae[w].x;
+        own = make_float2(carry, through);
+        own_reset |= resets != 0;
+        if (warp == 0 && (kGroups > 1 || sp.nt > 1)) {
+            const bool reset = kGroups == 1 ? own_reset : resets != 0 || (learn && q > 0 && sm.hand_reset[q % kHands] != 0);
+            const int c = c0 + lane;
+            uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
+            if (learn && q == stages - 1) {  // the segment's pair goes on, the carry that enters it comes
                 const bool lastpart = part == sp.nt - 1;
                 if (!lastpart) {
                     if (lane < cols) {
@@ -332,12 +363,23 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                     if (lane < cols) sp.known[part * p.C + c] = fmaf(through, v, carry);
                     publish(flags + part, kKnown, lane);
                 }
-                if (lane < W) sm.enter[lane] = v;
+                carry = v;
+            } else if (part == 0 && sp.nt > 1 && q == steps - 1) {  // the first segment's carry
+                if (lane < cols) sp.known[c] = carry;
+                publish(flags, kKnown, lane);
             }
-            __syncthreads();
-            carry = sm.enter[ch];
-            continue;
+            if (lane < W) sm.hand[(q + 1) % kHands][lane] = make_float2(carry, through);
+            if constexpr (kGroups > 1) {
+                if (lane == 0) sm.hand_reset[(q + 1) % kHands] = reset;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm.handed[(q + 1) % kHands]);
+            }
         }
+        if (kGroups == 1 && learn && q == stages - 1) {
+            named_bar_sync(1, 32 * kColWarps);
+            own = sm.hand[(q + 1) % kHands][ch];
+        }
+        if (learn) continue;
         auto spread = [&](float v) {
             return Quad{{__shfl_sync(0xffffffffu, v, l * 4), __shfl_sync(0xffffffffu, v, l * 4 + 1)},
                         {__shfl_sync(0xffffffffu, v, l * 4 + 2), __shfl_sync(0xffffffffu, v, l * 4 + 3)}};
@@ -358,8 +400,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
             // Gradients, from the right.
             X* dx = static_cast<X*>(p.dx) + (t + kRun - 1) * p.dx_stride + c0 + l * 4;
-            G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.da_stride + c0 + l * 4);
-            G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.db_stride + c0 + l * 4) : nullptr;
+            [[maybe_unused]] G* da = static_cast<G*>(p.da) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.da_stride + c0 + l * 4);
+            [[maybe_unused]] G* db = kHasB ? static_cast<G*>(p.db) + (kGates == kOneHead ? 0 : (t + kRun - 1) * p.db_stride + c0 + l * 4) : nullptr;
 #pragma unroll
             for (int k = kRun - 1; k >= 0; --k) {
                 if (!kWhole && ((any_end >> k) & 1) && ((ends >> k) & 1)) c = final_gradient(k);
@@ -427,10 +469,6 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
         }
     }
-    if (part == 0 && sp.nt > 1 && warp == 0) {  // the first segment's carry
-        if (lane < cols) sp.known[c0 + lane] = carry;
-        publish(sp.flags + static_cast<int64_t>(blk) * sp.nt, kKnown, lane);
-    }
 }
 
 template <class X, class G, int kGates, bool kHasB, class Col>
@@ -461,14 +499,21 @@ constexpr int backward_run() {
     return kGates == kPerChannel && sizeof(G) == 4 ? 4 : 8;
 }
 
+// Groups of 8 warps: two, where 128 registers a thread hold a run (of 8 tokens with gates per channel they do not), and the
+// ring four stages (fp32 throughout: fewer).
+template <class X, class G, int kGates>
+constexpr int backward_groups() {
+    return sizeof(X) == 4 || (kGates == kPerChannel && sizeof(G) == 2) ? 1 : 2;
+}
+
 template <class X, class G, int kGates>
 cudaError_t column_backward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
-    constexpr int R = backward_run<G, kGates>();
+    constexpr int R = backward_run<G, kGates>(), NG = backward_groups<X, G, kGates>();
     if (width == 32)
-        return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R>>(p, seg, stream)
-                   : launch_column_backward<X, G, kGates, false, Column<32, 8, R>>(p, seg, stream);
-    return p.b ? launch_column_backward<X, G, kGates, true, Column<16, 8, R>>(p, seg, stream)
-               : launch_column_backward<X, G, kGates, false, Column<16, 8, R>>(p, seg, stream);
+        return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R, NG>>(p, seg, stream)
+                   : launch_column_backward<X, G, kGates, false, Column<32, 8, R, NG>>(p, seg, stream);
+    return p.b ? launch_column_backward<X, G, kGates, true, Column<16, 8, R, NG>>(p, seg, stream)
+               : launch_column_backward<X, G, kGates, false, Column<16, 8, R, NG>>(p, seg, stream);
 }
 
 template <class X, class G>
