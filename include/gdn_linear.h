@@ -43,8 +43,8 @@
  * An empty sequence's final state is its initial state, and its
  * d_initial_state its d_final_state.
  *
- * Gates may have any value.  The scan forms products of the a of at most 64
- * successive tokens; these have to stay finite in fp32, which |a| <= 4
+ * Gates may have any value.  The scan forms products of the a of up to 64
+ * successive tokens; these have to stay finite in fp32, which |a| < 4
  * guarantees.  A state that is not finite stays within its own sequence.
  * y may be x itself (same stride); other overlaps of outputs with inputs are
  * not allowed, except output_state with initial_state.

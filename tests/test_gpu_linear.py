@@ -231,12 +231,24 @@ def test_what_is_not_finite_stays_in_its_sequence(bad):
 
 @pytest.mark.parametrize("value", [0.0, 1.0, -1.0, 4.0, 1e-30])
 def test_gates_of_any_value(value):
-    """Zero forgets, one sums up, four is the largest for which the products of 64 gates are sure to be finite."""
+    """Zero forgets, one sums up, gates of less than four have finite products over 64 tokens (here 60 of four)."""
     n = 60 if value == 4.0 else 300
     i = make([n, 2], 2, 16, "f32", seed=10)
     i["a"].fill_(value)
     _, _, tiles = check_forward(i)
     check_backward(i, tiles)
+
+
+def test_gates_above_one_without_inputs():
+    """Gates whose product over a segment is infinite, and nothing for them to grow: the states stay zero until the inputs
+    come, in the last tokens."""
+    i = make([6000], 1, 32, "f32", states=False, seed=29)
+    i["a"].fill_(1.25)
+    i["x"][:5990] = 0
+    y = gdn.gated_linear_recurrence(i["x"], i["a"], i["b"])
+    assert not y[:5990].any()
+    want = ref.forward(f64(i["x"][5990:]), f64(i["a"][5990:]), f64(i["b"][5990:]), [0, 10])
+    within("y", y[5990:], want[0], want[3])
 
 
 def test_growing_states_over_tiles():
