@@ -97,8 +97,8 @@ inline ScanLayout scan_layout(int64_t places, int64_t flags, int64_t C) {
 
 inline int64_t tiles_of(int64_t T) { return T > 0 ? (T + GDN_LINEAR_TILE - 1) / GDN_LINEAR_TILE : 1; }
 
-// Any run's workspace with these bounds.  Columns have at most a twentieth of the tiles as segments, with a flag for
-// every 16 channels; tiles have 4 flags for every 128 channels, or fewer.
+// Any run's workspace with these bounds.  Columns have at most a quarter of the tiles as segments, with a flag for every 16
+// channels; tiles have 4 flags for every 128 channels, or fewer.
 inline size_t workspace_bound(int64_t T, int64_t C, int64_t head_dim) {
     return scan_layout(tiles_of(T), 4 * backward_blocks(C, head_dim) + (C + 15) / 16, C).total + sums_bytes(T, C, head_dim, 16) + 256;
 }

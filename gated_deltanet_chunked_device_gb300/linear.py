@@ -21,6 +21,7 @@ __all__ = ["gated_linear_recurrence", "gated_linear_recurrence_backward", "gated
            "gdn_linear_run_workspace", "gdn_linear_forward_run", "gdn_linear_backward_run", "gdn_linear_decode_run"]
 
 LINEAR_TILE = 64  # packed tokens a row of tile_states stands for
+_MAX_TOKENS = 0x7fffffff - LINEAR_TILE  # of any plan
 LINEAR_FLAGS = {"HAS_B": 1 << 0, "GATES_PER_HEAD": 1 << 1, "HAS_INITIAL_STATE": 1 << 2, "OUTPUT_FINAL_STATE": 1 << 3,
                 "HAS_STATE_INDICES": 1 << 4, "CU_SEQLENS_I64": 1 << 5, "STATE_INDICES_I64": 1 << 6}
 _HAS_B, _PER_HEAD, _HAS_INIT, _FINAL, _HAS_IDX, _CU_I64, _IDX_I64 = (1 << i for i in range(7))
@@ -122,8 +123,8 @@ def _get_plan(H, D, x, a, state_dt, flags, T, N):
     p = _plans.get(key)
     if p is None or p.max_seqs < N:
         with _plans_lock:
-            p = _Plan(LinearDesc(H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], state_dt, (1 << T.bit_length()) - 1,
-                                 _pow2_at_least(N), flags))
+            p = _Plan(LinearDesc(H, D, _QKV_DTYPES[x.dtype], _QKV_DTYPES[a.dtype], state_dt,
+                                 min((1 << T.bit_length()) - 1, _MAX_TOKENS), _pow2_at_least(N), flags))
             _plans[key] = p
     return p
 
