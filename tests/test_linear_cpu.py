@@ -114,7 +114,8 @@ def test_workspace_is_checked():
     gdn.gdn_linear_plan_destroy(plan)
 
 
-@pytest.mark.parametrize("T,H,D", [(1, 1, 1), (64, 1, 1), (65, 3, 7), (5000, 2, 128), (70000, 1, 16), (4096, 1, 4100), (999, 40, 96)])
+@pytest.mark.parametrize("T,H,D", [(1, 1, 1), (64, 1, 1), (65, 3, 7), (5000, 2, 128), (70000, 1, 16), (4096, 1, 4100), (999, 40, 96),
+                                   (4096, 64, 16), (1000, 4, 80), (512, 8, 48)])
 @pytest.mark.parametrize("per_head", [False, True])
 def test_a_runs_workspace_is_within_the_plans(T, H, D, per_head):
     flags = gdn.LINEAR_FLAGS["GATES_PER_HEAD"] if per_head else 0
@@ -125,6 +126,13 @@ def test_a_runs_workspace_is_within_the_plans(T, H, D, per_head):
             for back in (False, True):
                 assert gdn.gdn_linear_run_workspace(plan, args, back) <= nbytes
         gdn.gdn_linear_plan_destroy(plan)
+
+
+@pytest.mark.parametrize("T", [0, 1, 2**30 - 1, 2**30, 2**31 - 65])
+def test_python_plans_for_all_lengths(T):
+    x = torch.empty(0, dtype=torch.bfloat16)
+    plan = gdn.linear._get_plan(1, 16, x, x, 0, 0, T, 1)
+    assert plan.handle and plan is gdn.linear._get_plan(1, 16, x, x, 0, 0, T, 1)
 
 
 def test_states_and_pools_are_checked():
