@@ -176,10 +176,11 @@ bool inputs_wide(const LinearParams& p) {
 //   - Fewer columns, but too many for three segments each: columns of 16 (32768 x 2048 117 us, with columns of 32 166 us).
 //   - Fewer still: as many time segments as the SMs hold (32768 x 1024 86 us, in one segment 164 us).  With two segments the
 //     second pass over the later one would cost what the halves save.
-linear::Segments segments(const LinearParams& p, int warps, int run, int* width) {
+// narrow: columns of 16 whatever the number (backward_route).
+linear::Segments segments(const LinearParams& p, int warps, int run, bool narrow, int* width) {
     const int64_t sms = multiprocessors(), blocks32 = (p.C + 31) / 32;
     int64_t segs = sms / blocks32;
-    *width = 5 * blocks32 < 3 * sms && segs < 3 ? 16 : 32;
+    *width = narrow || (5 * blocks32 < 3 * sms && segs < 3) ? 16 : 32;
     linear::Segments s{};
     const int64_t tokens = warps * (128 / *width) * run, n = p.T > 0 ? (p.T + tokens - 1) / tokens : 1;
     if (segs > n / 2) segs = n / 2;
@@ -214,7 +215,7 @@ Route forward_route(const LinearParams& p) {
     Route r{};
     r.vec = rows_vector(p) && vector_of_4(p.y, p.y_stride, p.x_dt) && vector_of_4(p.tile_states, 0, GDN_DTYPE_F32);
     r.column = r.vec && inputs_wide(p);
-    if (r.column) r.seg = segments(p, linear::kForwardWarps, 8, &r.width);
+    if (r.column) r.seg = segments(p, linear::kForwardWarps, 8, false, &r.width);
     r.blocks = (p.C + linear::kCols - 1) / linear::kCols;
     finish_route(p, &r);
     return r;
@@ -227,7 +228,12 @@ Route backward_route(const LinearParams& p) {
             vector_of_4(p.d_final, 0, GDN_DTYPE_F32) && vector_of_4(p.d_initial, 0, GDN_DTYPE_F32);
     if (p.gate_div == 1) r.vec = r.vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
     if (r.vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
-        r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, &r.width);  // backward_run
+        // Sums of heads of 16, 48, 80 channels fit columns of 16 alone, which have no time segments: taken where the columns
+        // are blocks for two fifths of the SMs, or the batch is short (52 heads of 80, 32768 tokens: 343 us, tiles 1157;
+        // 64 heads of 16, 4096 tokens: 35, tiles 42; 32 heads of 16, 512 tokens: 17, tiles 23; but 32768 tokens: 201, tiles 126).
+        const bool narrow = p.gate_div != 1 && p.D % 32 != 0 && p.D % 16 == 0 &&
+                            (5 * ((p.C + 31) / 32) >= multiprocessors() || p.T <= 2048);
+        r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, narrow, &r.width);  // backward_run
         r.column = p.gate_div == 1 || linear::one_head(p, r.width);
     }
     r.blocks = backward_blocks(p.C, head_dim);

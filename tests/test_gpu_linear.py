@@ -27,6 +27,7 @@ LENS = {
     "long": [3001], "long_two": [1000, 1411], "all_empty": [0, 0, 0], "none": [0],
 }
 SHAPES = [(2, 128), (3, 100), (1, 1), (5, 7), (2, 64), (1, 300), (3, 8), (2, 4)]
+HEADS = [(8, 16), (4, 80), (8, 48), (16, 144), (4, 32)]  # of which a column holds one, or a part
 
 
 @pytest.mark.parametrize("gates", ["channel", "head"])
@@ -43,6 +44,14 @@ def test_lengths(lens, gates):
 @pytest.mark.parametrize("dtype,gate_dtype", [("bf16", "bf16"), ("f16", "f16"), ("f32", "f32"), ("bf16", "f32"), ("f16", "f32")])
 def test_types_and_shapes(dtype, gate_dtype, H, D, gates, has_b):
     i = make([70, 1, 0, 129], H, D, dtype, gate_dtype, gates=gates, has_b=has_b, seed=2)
+    _, _, tiles = check_forward(i)
+    check_backward(i, tiles)
+
+
+@pytest.mark.parametrize("H,D", HEADS)
+@pytest.mark.parametrize("dtype,gate_dtype", [("bf16", "bf16"), ("f32", "f32"), ("f16", "f32")])
+def test_heads_in_columns(dtype, gate_dtype, H, D):
+    i = make([300, 5, 0, 420], H, D, dtype, gate_dtype, gates="head", seed=30)
     _, _, tiles = check_forward(i)
     check_backward(i, tiles)
 
