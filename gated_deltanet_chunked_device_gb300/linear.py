@@ -241,7 +241,7 @@ def _run(backward, plan, x, args):
     with on_device(x.get_device()) as stream:
         n = L.gdn_linear_run_workspace(handle, args, backward)
         if n:
-            ws = x.new_empty(n, dtype=torch.uint8)
+            ws = torch.empty(n, dtype=torch.uint8, device=x.device)
             at = ws.data_ptr()
         st = (L.gdn_linear_backward_run if backward else L.gdn_linear_forward_run)(handle, args, at, n, stream)
     if st != 0:

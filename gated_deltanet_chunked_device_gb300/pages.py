@@ -164,7 +164,7 @@ def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, d
     refcounts_out = refcounts if refcounts_out is None else refcounts_out
     bufs, nb = _buffers("pools", pools, P, device)
     remap = torch.empty_like(refcounts)
-    n_live = refcounts.new_empty(1)
+    n_live = torch.empty(1, dtype=torch.int32, device=refcounts.device)
     _call("gdn_pages_compact_run", table, (book, bufs, nb, _int32("table_out", table_out, (S, M), device),
                                            _int32("refcounts_out", refcounts_out, (P,), device), remap.data_ptr(),
                                            n_live.data_ptr(), _status(device_status, device)), (S, M, P, 0))
