@@ -208,7 +208,7 @@ struct Route {
 
 void finish_route(const LinearParams& p, Route* r) {
     r->tiles = tiles_of(p.T);
-    r->layout = r->column ? scan_layout(r->seg.space.nt, r->seg.space.blocks, p.C) : scan_layout(r->tiles, 4 * r->blocks, p.C);
+    r->layout = r->column ? scan_layout(r->seg.space.nt, r->seg.space.blocks, p.C, true) : scan_layout(r->tiles, 4 * r->blocks, p.C, false);
 }
 
 Route forward_route(const LinearParams& p) {
@@ -254,6 +254,7 @@ cudaError_t scan_space(const Route& r, void* workspace, cudaStream_t stream, lin
     s->flags = reinterpret_cast<uint32_t*>(ws + 256);
     s->pairs = reinterpret_cast<float2*>(ws + r.layout.zeroed);
     s->known = reinterpret_cast<float*>(ws + r.layout.known);
+    s->exponents = reinterpret_cast<int32_t*>(ws + r.layout.exponents);
     return cudaMemsetAsync(ws, 0, r.layout.zeroed, stream);
 }
 

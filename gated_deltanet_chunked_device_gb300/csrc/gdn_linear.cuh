@@ -80,18 +80,19 @@ inline size_t sums_bytes(int64_t T, int64_t C, int64_t head_dim, int64_t width) 
 }
 
 // What `places` of a scan (tiles, or segments of columns) hand on: the ticket and the flags (zeroed before each run), the
-// pairs and the known states.
+// pairs, the known states and (segments) the exponents of the pairs' products.
 struct ScanLayout {
-    size_t zeroed, known, total;
+    size_t zeroed, known, exponents, total;
 };
 
-inline ScanLayout scan_layout(int64_t places, int64_t flags, int64_t C) {
+inline ScanLayout scan_layout(int64_t places, int64_t flags, int64_t C, bool segments) {
     ScanLayout l{};
     if (places < 2) return l;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     l.zeroed = 256 + up(sizeof(uint32_t) * static_cast<size_t>(places) * flags);
     l.known = l.zeroed + up(sizeof(float2) * static_cast<size_t>(places) * C);
-    l.total = l.known + up(sizeof(float) * static_cast<size_t>(places) * C);
+    l.total = l.exponents = l.known + up(sizeof(float) * static_cast<size_t>(places) * C);
+    if (segments) l.total += up(sizeof(int32_t) * static_cast<size_t>(places) * C);
     return l;
 }
 
@@ -100,7 +101,7 @@ inline int64_t tiles_of(int64_t T) { return T > 0 ? (T + GDN_LINEAR_TILE - 1) / 
 // Any run's workspace with these bounds.  Columns have at most a quarter of the tiles as segments, with a flag for every 16
 // channels; tiles have 4 flags for every 128 channels, or fewer.
 inline size_t workspace_bound(int64_t T, int64_t C, int64_t head_dim) {
-    return scan_layout(tiles_of(T), 4 * backward_blocks(C, head_dim) + (C + 15) / 16, C).total + sums_bytes(T, C, head_dim, 16) + 256;
+    return scan_layout(tiles_of(T), 4 * backward_blocks(C, head_dim) + (C + 15) / 16, C, false).total + sums_bytes(T, C, head_dim, 16) + 256;
 }
 
 int multiprocessors();  // of the current device

@@ -37,10 +37,14 @@
 namespace gdn {
 namespace linear {
 
-// A block's shape: W channels; NG groups of NW warps, which take the stages in turn; runs of R tokens.
-template <int W, int NW, int R, int NG>
+// A block's shape: W channels; NG groups of NW warps, which take the stages in turn; runs of R tokens; S: one of several time
+// segments (of columns of 32 alone, a lane a channel).  In kernels of their own, since what segments need costs the others
+// registers and instruction cache (64 sequences of 512 tokens x 4096: 208 us, in one kernel 235).
+template <int W, int NW, int R, int NG, bool S = false>
 struct Column {
     static constexpr int kWidth = W, kRun = R, kGroups = NG;
+    static constexpr bool kSegments = S;
+    static_assert(!S || W == 32, "a lane a channel");
     static constexpr int kLanesRow = W / 4;      // lanes that hold one token's channels
     static constexpr int kRuns = 32 / kLanesRow; // runs of tokens of a warp
     static constexpr int kWarpTokens = kRuns * kRun;
@@ -370,8 +374,9 @@ struct ForwardShape {
     };
     struct Tables {
         Group groups[Col::kGroups];
-        float2 hand[Col::kHands][W];  // the state that enters a stage, and in steps that learn the gates' product so far
+        float hand[Col::kHands][W];   // the state that enters a stage
         int32_t hand_reset[Col::kHands];
+        Product product[Col::kGroups][W];  // of the gates of a group's steps that learn
         uint64_t full[kDepth];        // a stage's inputs have come
         uint64_t handed[Col::kHands];
         uint32_t ticket;
@@ -403,18 +408,19 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         fence_mbar_init();
         mbar_arrive(&sm.handed[0]);  // nothing is handed to stage 0: its place's first turn is over
         for (int i = 0; i < kGroups; ++i) sm.groups[i].kept_at = -1;
-        if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
+        if (Col::kSegments) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
+    if (Col::kSegments && threadIdx.x < kGroups * W) sm.product[threadIdx.x / W][threadIdx.x % W] = Product{1.f, 0};
     __syncthreads();
-    const uint32_t ticket = sp.nt > 1 ? sm.ticket : blockIdx.x;
-    const int64_t part = ticket / sp.blocks;
-    const uint32_t blk = ticket % sp.blocks;
+    const uint32_t ticket = Col::kSegments ? sm.ticket : blockIdx.x;
+    const int64_t part = Col::kSegments ? ticket / sp.blocks : 0;
+    const uint32_t blk = Col::kSegments ? ticket % sp.blocks : ticket;
     const int c0 = static_cast<int>(blk) * W, cols = min(W, p.C - c0);
     const int64_t from = part == 0 ? 0 : (seg.first + (part - 1) * seg.stages) * static_cast<int64_t>(kTokens);
-    const int64_t end = part == sp.nt - 1 ? p.T : (seg.first + part * seg.stages) * static_cast<int64_t>(kTokens);
+    const int64_t end = !Col::kSegments || part == sp.nt - 1 ? p.T : (seg.first + part * seg.stages) * static_cast<int64_t>(kTokens);
     const int stages = static_cast<int>(max(static_cast<int64_t>(1), (end - from + kTokens - 1) / kTokens));
     // A later segment learns what it does to a state in steps 0 .. stages - 1.
-    const bool twice = part > 0;
+    const bool twice = Col::kSegments && part > 0;
     const int steps = p.T == 0 ? 0 : twice ? 2 * stages : stages;
     const bool on = l * 4 < cols;
 
@@ -640,13 +646,19 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kColWarps; ++w) ab[w] = gr.pairs[q / kGroups & 1][w][ch];
         const uint32_t resets = bd.warps_start;
-        // What the stage before hands on: the state (in steps that learn, from zero), and the gates' product.
-        float2 hand = make_float2(0.f, 1.f);
+        if (learn && warp == 0) {  // before the wait, so that the next stage does not wait for it
+            float factors[kColWarps];
+#pragma unroll
+            for (int w = 0; w < kColWarps; ++w) factors[w] = ab[w].x;
+            sm.product[group][lane] = times(sm.product[group][lane], product_of(factors));
+        }
+        // What the stage before hands on: the state (in steps that learn, from zero).
+        float carry = 0.f;
         if (q > 0) {
             wait_hand(q);
-            hand = sm.hand[q % kHands][ch];
+            carry = sm.hand[q % kHands][ch];
         }
-        float carry = hand.x, enter = carry;
+        float enter = carry;
 #pragma unroll
         for (int w = 0; w < kColWarps; ++w) {
             if (w == warp) enter = carry;
@@ -654,37 +666,36 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             if (resets != 0 && ((resets >> w) & 1)) carry = ab[w].y;
         }
         if (warp == 0) {
-            float through = hand.y;
-            bool reset = resets != 0;
-            if (learn) {
-#pragma unroll
-                for (int w = 0; w < kColWarps; ++w) through *= ab[w].x;
-                reset |= q > 0 && sm.hand_reset[q % kHands] != 0;
-            }
+            const bool reset = resets != 0 || (learn && q > 0 && sm.hand_reset[q % kHands] != 0);
             const int c = c0 + lane;
             uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
             if (learn && q == stages - 1) {  // the segment's pair goes on, the state that enters it comes
                 const bool lastpart = part == sp.nt - 1;
+                Product whole = sm.product[0][lane];
+                for (int i = 1; i < kGroups; ++i) whole = times(whole, sm.product[i][lane]);
+                whole = folded(whole);
                 if (!lastpart) {
                     if (lane < cols) {
-                        if (reset)
+                        if (reset) {
                             sp.known[part * p.C + c] = carry;
-                        else
-                            sp.pairs[part * p.C + c] = make_float2(through, carry);
+                        } else {
+                            sp.pairs[part * p.C + c] = make_float2(whole.m, carry);
+                            sp.exponents[part * p.C + c] = whole.e;
+                        }
                     }
                     publish(flags + part, reset ? kKnown : kPair, lane);
                 }
-                const float h = look_back(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
+                const float h = look_back<true>(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
                 if (!lastpart && !reset) {
-                    if (lane < cols) sp.known[part * p.C + c] = pass_on(through, h, carry);
+                    if (lane < cols) sp.known[part * p.C + c] = pass_on(whole, h, carry);
                     publish(flags + part, kKnown, lane);
                 }
                 carry = h;
-            } else if (part == 0 && sp.nt > 1 && q == steps - 1) {  // the first segment's end state
+            } else if (Col::kSegments && part == 0 && q == steps - 1) {  // the first segment's end state
                 if (lane < cols) sp.known[c] = carry;
                 publish(flags, kKnown, lane);
             }
-            if (lane < W) sm.hand[(q + 1) % kHands][lane] = make_float2(carry, through);
+            if (lane < W) sm.hand[(q + 1) % kHands][lane] = carry;
             if (lane == 0) sm.hand_reset[(q + 1) % kHands] = reset;
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.handed[(q + 1) % kHands]);
@@ -746,6 +757,9 @@ cudaError_t launch_column_forward(const LinearParams& p, const Segments& seg, cu
 template <class X, class G, int kGates>
 cudaError_t column_forward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
     constexpr int kWarps = kForwardWarps, kGroups = kForwardGroups;
+    if (seg.space.nt > 1)
+        return p.b ? launch_column_forward<X, G, kGates, true, Column<32, kWarps, 8, kGroups, true>>(p, seg, stream)
+                   : launch_column_forward<X, G, kGates, false, Column<32, kWarps, 8, kGroups, true>>(p, seg, stream);
     if (width == 32)
         return p.b ? launch_column_forward<X, G, kGates, true, Column<32, kWarps, 8, kGroups>>(p, seg, stream)
                    : launch_column_forward<X, G, kGates, false, Column<32, kWarps, 8, kGroups>>(p, seg, stream);

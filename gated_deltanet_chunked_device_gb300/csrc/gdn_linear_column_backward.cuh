@@ -43,8 +43,9 @@ struct BackwardShape {
     };
     struct Tables {
         Group groups[Col::kGroups];
-        float2 hand[Col::kHands][W];  // the carry that enters a stage, and in steps that learn the gates' product so far
+        float hand[Col::kHands][W];   // the carry that enters a stage
         int32_t hand_reset[Col::kHands];
+        Product product[Col::kGroups][W];  // of the gates of a group's steps that learn
         uint64_t full[kDepth];
         uint64_t handed[Col::kHands];
         uint32_t ticket;
@@ -77,19 +78,20 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         for (int i = 0; i < kHands; ++i) mbar_init(&sm.handed[i], 1);
         fence_mbar_init();
         mbar_arrive(&sm.handed[0]);  // nothing is handed to stage 0: its place's first turn is over
-        if (sp.nt > 1) sm.ticket = atomicAdd(sp.ticket, 1u);
+        if (Col::kSegments) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
+    if (Col::kSegments && threadIdx.x < kGroups * W) sm.product[threadIdx.x / W][threadIdx.x % W] = Product{1.f, 0};
     __syncthreads();
-    const uint32_t ticket = sp.nt > 1 ? sm.ticket : blockIdx.x;
-    const int64_t part = ticket / sp.blocks;  // segments are counted from the right
-    const uint32_t blk = ticket % sp.blocks;
+    const uint32_t ticket = Col::kSegments ? sm.ticket : blockIdx.x;
+    const int64_t part = Col::kSegments ? ticket / sp.blocks : 0;  // segments are counted from the right
+    const uint32_t blk = Col::kSegments ? ticket % sp.blocks : ticket;
     const int c0 = static_cast<int>(blk) * W, cols = min(W, p.C - c0);
     // stages of the whole axis are counted from the left; this segment has [left, right)
     const int64_t all = max(static_cast<int64_t>(1), (p.T + kTokens - 1) / kTokens);
     const int64_t right = part == 0 ? all : all - seg.first - (part - 1) * seg.stages;
-    const int64_t left = part == sp.nt - 1 ? 0 : all - seg.first - part * seg.stages;
+    const int64_t left = !Col::kSegments || part == sp.nt - 1 ? 0 : all - seg.first - part * seg.stages;
     const int stages = static_cast<int>(right - left);
-    const bool twice = part > 0;
+    const bool twice = Col::kSegments && part > 0;
     const int steps = p.T == 0 ? 0 : twice ? 2 * stages : stages;
     const bool on = l * 4 < cols;
     const int head = c0 / p.D;
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     fetch_saved(group);
     __syncthreads();
     bool ok = true;  // until a wait runs out
-    float2 own = make_float2(0.f, 1.f);
+    float own = 0.f;
     bool own_reset = false;
     auto wait_hand = [&](int q) {
         if (ok && !mbar_wait(&sm.handed[q % kHands], (q / kHands) & 1)) {
@@ -333,53 +335,60 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             enter_h = (bd.warps_start >> v) & 1 ? b : fmaf(gr.pairs[q / kGroups & 1][v][ch].x, enter_h, b);
         }
         fetch_saved(q + kGroups);
-        // What the stage to the right hands on: the carry (in steps that learn, from zero), and the gates' product.
+        if (learn && warp == 0) {  // before the wait, so that the next stage does not wait for it
+            float factors[kColWarps];
+#pragma unroll
+            for (int w = 0; w < kColWarps; ++w) factors[w] = ae[w].x;
+            sm.product[group][lane] = times(sm.product[group][lane], product_of(factors));
+        }
+        // What the stage to the right hands on: the carry (in steps that learn, from zero).
         const uint32_t resets = bd.warps_end;
         // (One group keeps it itself.)
-        float2 hand = own;
+        float carry = own;
         if (kGroups > 1 && q > 0) {
             wait_hand(q);
-            hand = sm.hand[q % kHands][ch];
+            carry = sm.hand[q % kHands][ch];
         }
-        float carry = hand.x, enter_c = carry;
+        float enter_c = carry;
 #pragma unroll
         for (int w = kColWarps - 1; w >= 0; --w) {
             if (w == warp) enter_c = carry;
             carry = fmaf(ae[w].x, carry, ae[w].y);
             if (resets != 0 && ((resets >> w) & 1)) carry = ae[w].y;
         }
-        float through = hand.y;
-        if (learn)
-#pragma unroll
-            for (int w = 0; w < kColWarps; ++w) through *= ae[w].x;
-        own = make_float2(carry, through);
+        own = carry;
         own_reset |= resets != 0;
-        if (warp == 0 && (kGroups > 1 || sp.nt > 1)) {
+        if (warp == 0 && (kGroups > 1 || Col::kSegments)) {
             const bool reset = kGroups == 1 ? own_reset : resets != 0 || (learn && q > 0 && sm.hand_reset[q % kHands] != 0);
             const int c = c0 + lane;
             uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
             if (learn && q == stages - 1) {  // the segment's pair goes on, the carry that enters it comes
                 const bool lastpart = part == sp.nt - 1;
+                Product whole = sm.product[0][lane];
+                for (int i = 1; i < kGroups; ++i) whole = times(whole, sm.product[i][lane]);
+                whole = folded(whole);
                 if (!lastpart) {
                     if (lane < cols) {
-                        if (reset)
+                        if (reset) {
                             sp.known[part * p.C + c] = carry;
-                        else
-                            sp.pairs[part * p.C + c] = make_float2(through, carry);
+                        } else {
+                            sp.pairs[part * p.C + c] = make_float2(whole.m, carry);
+                            sp.exponents[part * p.C + c] = whole.e;
+                        }
                     }
                     publish(flags + part, reset ? kKnown : kPair, lane);
                 }
-                const float v = look_back(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
+                const float v = look_back<true>(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
                 if (!lastpart && !reset) {
-                    if (lane < cols) sp.known[part * p.C + c] = pass_on(through, v, carry);
+                    if (lane < cols) sp.known[part * p.C + c] = pass_on(whole, v, carry);
                     publish(flags + part, kKnown, lane);
                 }
                 carry = v;
-            } else if (part == 0 && sp.nt > 1 && q == steps - 1) {  // the first segment's carry
+            } else if (Col::kSegments && part == 0 && q == steps - 1) {  // the first segment's carry
                 if (lane < cols) sp.known[c] = carry;
                 publish(flags, kKnown, lane);
             }
-            if (lane < W) sm.hand[(q + 1) % kHands][lane] = make_float2(carry, through);
+            if (lane < W) sm.hand[(q + 1) % kHands][lane] = carry;
             if constexpr (kGroups > 1) {
                 if (lane == 0) sm.hand_reset[(q + 1) % kHands] = reset;
                 __syncwarp();
@@ -520,6 +529,9 @@ constexpr int backward_groups() {
 template <class X, class G, int kGates>
 cudaError_t column_backward_gates(const LinearParams& p, const Segments& seg, int width, cudaStream_t stream) {
     constexpr int R = backward_run<G, kGates>(), NG = backward_groups<X, G, kGates>();
+    if (seg.space.nt > 1)
+        return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R, NG, true>>(p, seg, stream)
+                   : launch_column_backward<X, G, kGates, false, Column<32, 8, R, NG, true>>(p, seg, stream);
     if (width == 32)
         return p.b ? launch_column_backward<X, G, kGates, true, Column<32, 8, R, NG>>(p, seg, stream)
                    : launch_column_backward<X, G, kGates, false, Column<32, 8, R, NG>>(p, seg, stream);

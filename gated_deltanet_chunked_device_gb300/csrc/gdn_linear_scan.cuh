@@ -236,11 +236,12 @@ __device__ __forceinline__ void check_bounds(const LinearParams& p, int64_t f, i
     if (bad) report(p.status, GDN_DEVICE_ERR_CU_SEQLENS);
 }
 
-// What tiles hand on, in the workspace.
+// What tiles, or time segments of columns, hand on, in the workspace.
 struct ScanSpace {
     uint32_t* ticket;              // next tile: tiles are taken in order, so whom one waits for has started
-    uint32_t* flags;               // [4 channel quarters of a block][blocks][nt]: kPair, then kKnown
+    uint32_t* flags;               // [blocks][4 channel quarters of a block][nt] (columns: [blocks][nt]): kPair, then kKnown
     float2* pairs;                 // [nt][C] (A, B)
+    int32_t* exponents;            // [nt][C] columns: A is pairs' times 2^this
     float* known;                  // [nt][C] end states in the scan's direction
     int64_t nt;
     uint32_t blocks;
@@ -264,14 +265,68 @@ __device__ __forceinline__ void publish(uint32_t* flag, uint32_t what, int lane)
     if (lane == 0) store_release(flag, what);
 }
 
-// h through a stretch of tokens.  Over a whole time segment the product of gates above one may be infinite; a state of
-// zero stays zero all the same (any other one would have overflowed token by token too).
+// h through a tile's tokens.
 __device__ __forceinline__ float pass_on(float a, float h, float b) { return h == 0.f ? b : fmaf(a, h, b); }
+
+// A product of any number of gates, m 2^e with |m| in [1/2, 1) (or 0, or not finite): that of a whole time segment may leave
+// fp32's range, or fall below it and come back, where no state does.
+struct Product {
+    float m;
+    int e;
+};
+
+// Of a few factors: their fractions are brought to [1/2, 1) each, so that none waits for another.  (What is not finite has no
+// exponent to speak of, and is not asked for it.)
+template <int kN>
+__device__ __forceinline__ Product product_of(const float (&a)[kN]) {
+    Product p{1.f, 0};
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        int e;
+        p.m *= frexpf(a[i], &e);
+        p.e += e;
+    }
+    return p;
+}
+__device__ __forceinline__ Product times(Product p, Product q) {
+    int e;
+    const float f = frexpf(p.m * q.m, &e);
+    return {f, p.e + q.e + e};
+}
+
+// The same product with an exponent of 0 where fp32 holds it without loss, as most do.
+__device__ __forceinline__ Product folded(Product p) {
+    return isfinite(p.m) && p.e >= -125 && p.e <= 127 ? Product{ldexpf(p.m, p.e), 0} : p;
+}
+
+// h through a time segment, fmaf(A, h, b) with one rounding whatever the exponent (76 segments of 64 channels, 32768
+// tokens: 26 us, without the first two lines 28).
+__device__ __forceinline__ float pass_on(Product a, float h, float b) {
+    if (a.e == 0 || !isfinite(a.m) || !isfinite(h)) return pass_on(a.m, h, b);
+    if (a.e < -300) return b;  // less than half of the least number, for any h
+    // the exponents' sum is shared between two factors that both are in range, unless the product is far out of it
+    int e;
+    const float f = frexpf(h, &e);
+    const int sum = min(max(a.e + e, -250), 252), half = sum / 2;
+    return fmaf(ldexpf(a.m, half), ldexpf(f, sum - half), b);
+}
+
+// The pair of place `row` of the scan, and h through it.
+template <bool kSegments>
+__device__ __forceinline__ auto load_pair(const ScanSpace& s, int64_t row, int C, int c) {
+    const float2 ab = __ldcg(s.pairs + row * C + c);
+    if constexpr (kSegments)
+        return make_float4(ab.x, ab.y, __int_as_float(__ldcg(s.exponents + row * C + c)), 0.f);
+    else
+        return ab;
+}
+__device__ __forceinline__ float through_pair(float2 ab, float h) { return pass_on(ab.x, h, ab.y); }
+__device__ __forceinline__ float through_pair(float4 ab, float h) { return pass_on(Product{ab.x, __float_as_int(ab.z)}, h, ab.y); }
 
 // The state that enters place `f` of the scan (f >= 1) for channel c, by one warp for 32 channels: from the nearest
 // place whose end state is known, through the pairs of the places after it.  Places are numbered in the scan's
-// direction; at(f) gives a place's row in pairs and known.
-template <class At>
+// direction; at(f) gives a place's row in pairs and known.  kSegments: places are time segments, with exponents.
+template <bool kSegments, class At>
 __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpace& s, const uint32_t* flags, int64_t f, int c, int lane,
                                            At at) {
     const bool on = c < p.C;
@@ -294,16 +349,13 @@ __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpac
     float h = __ldcg(s.known + at(f - 1 - dist) * p.C + c);
     int d = dist - 1;
     for (; d >= 3; d -= 4) {
-        float2 ab[4];
+        decltype(load_pair<kSegments>(s, 0, 0, 0)) ab[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) ab[j] = __ldcg(s.pairs + at(f - 1 - d + j) * p.C + c);
+        for (int j = 0; j < 4; ++j) ab[j] = load_pair<kSegments>(s, at(f - 1 - d + j), p.C, c);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h = pass_on(ab[j].x, h, ab[j].y);
+        for (int j = 0; j < 4; ++j) h = through_pair(ab[j], h);
     }
-    for (; d >= 0; --d) {
-        const float2 ab = __ldcg(s.pairs + at(f - 1 - d) * p.C + c);
-        h = pass_on(ab.x, h, ab.y);
-    }
+    for (; d >= 0; --d) h = through_pair(load_pair<kSegments>(s, at(f - 1 - d), p.C, c), h);
     return h;
 }
 
@@ -444,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_forward_kernel(const Line
             }
             if (!last) publish(flags + f, known ? kKnown : kPair, lane);
             if (f > 0 && !(reset_lo & 1)) {
-                h = look_back(p, s, flags, f, c, lane, [](int64_t k) { return k; });
+                h = look_back<false>(p, s, flags, f, c, lane, [](int64_t k) { return k; });
                 if (!known) {
                     if (c < p.C) s.known[f * p.C + c] = pass_on(ta, h, tb);
                     if (!last) publish(flags + f, kKnown, lane);
@@ -652,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 2) gdn_linear_backward_kernel(const 
             }
             if (!first) publish(flags + r, known ? kKnown : kPair, lane);
             if (r > 0 && !(sm.bounds.ends[1] >> 31)) {
-                carry = look_back(p, s, flags, r, valid ? c : p.C, lane, [&](int64_t k) { return s.nt - 1 - k; });
+                carry = look_back<false>(p, s, flags, r, valid ? c : p.C, lane, [&](int64_t k) { return s.nt - 1 - k; });
                 if (!known && !first) {
                     if (valid) s.known[f * p.C + c] = pass_on(ta, carry, tc);
                     publish(flags + r, kKnown, lane);

@@ -44,8 +44,11 @@
  * d_initial_state its d_final_state.
  *
  * Gates may have any value.  The scan forms products of the a of up to 64
- * successive tokens; these have to stay finite in fp32, which |a| < 4
- * guarantees.  A state that is not finite stays within its own sequence.
+ * successive tokens in fp32; these have to stay finite, which |a| < 4
+ * guarantees, and bits of them that fall below 2^-149 are lost.  Products over
+ * longer stretches have an exponent of their own.  The error of a result is
+ * that of a sum of its terms' absolute values, which has to stay finite as
+ * well.  A state that is not finite stays within its own sequence.
  * y may be x itself (same stride); other overlaps of outputs with inputs are
  * not allowed, except output_state with initial_state.
  *
