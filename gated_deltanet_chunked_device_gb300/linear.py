@@ -283,19 +283,20 @@ class _Recurrence(torch.autograd.Function):
         final = _new_states(initial_state, N, H, D, x.device) if output_final_state else None
         tiles = torch.empty(-(-T // LINEAR_TILE), H, D, dtype=torch.float32, device=x.device)
         y = _forward(x, a, b, initial_state, final, cu_seqlens, None, None, tiles, device_status)
-        ctx.save_for_backward(x, a, b, initial_state, cu_seqlens, tiles, device_status)
+        ctx.save_for_backward(x, a, b, initial_state, cu_seqlens, tiles)
+        ctx.device_status = device_status  # written to, never read: the caller may clear it in between
         return y, final
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy, d_final):
-        x, a, b, initial_state, cu_seqlens, tiles, status = ctx.saved_tensors
+        x, a, b, initial_state, cu_seqlens, tiles = ctx.saved_tensors
         if dy is None:
             dy = torch.zeros_like(x)
         dx, da, db, d0 = gated_linear_recurrence_backward(
             dy.contiguous(), x, a, b, tile_states=tiles, initial_state=initial_state,
             d_final_state=None if d_final is None else d_final.float().contiguous(), cu_seqlens=cu_seqlens,
-            device_status=status)
+            device_status=ctx.device_status)
         if d0 is not None:
             d0 = d0.to(initial_state.dtype) if ctx.needs_input_grad[3] else None
         return dx, da, db, d0, None, None, None
