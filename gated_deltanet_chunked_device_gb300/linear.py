@@ -14,7 +14,7 @@ import threading
 
 import torch
 
-from . import DTYPE_F32, GdnError, _pow2_at_least, _QKV_DTYPES, _STATE_DTYPES, lib, on_device
+from . import DTYPE_F32, GdnError, _pow2_at_least, _QKV_DTYPES, _STATE_DTYPES, lib, mark_written, on_device
 
 __all__ = ["gated_linear_recurrence", "gated_linear_recurrence_backward", "gated_linear_recurrence_decode", "LinearDesc",
            "LinearArgs", "LINEAR_FLAGS", "LINEAR_TILE", "gdn_linear_plan", "gdn_linear_plan_destroy",
@@ -272,6 +272,7 @@ def _forward(x, a, b, initial_state, output_state, cu_seqlens, output, state_ind
                  _addr(output_state), sstride, _addr(state_indices), n_pool, _status_ptr(device_status, device),
                  output.data_ptr(), ys, _addr(tile_states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     _run(0, plan, x, args)
+    mark_written(output, output_state, tile_states)
     return output
 
 
@@ -396,4 +397,5 @@ def gated_linear_recurrence_decode(x, a, b=None, initial_state=None, state_indic
         st = lib().gdn_linear_decode_run(plan.handle, args, m, stream)
     if st != 0:
         raise GdnError(st, "gdn_linear_decode_run")
+    mark_written(output, output_state)
     return (output, output_state) if output_final_state else output

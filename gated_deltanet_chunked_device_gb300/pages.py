@@ -14,7 +14,7 @@ import struct
 
 import torch
 
-from . import GdnError, lib, on_device
+from . import GdnError, lib, mark_written, on_device
 
 __all__ = ["cache_reserve", "cache_fork", "cache_free", "cache_compact", "cache_copy", "PAGES_ERR", "PagesBook", "PagesBuffer"]
 
@@ -67,10 +67,13 @@ def _book(table, refcounts, lengths):
                               0 if lengths is None else _int32("lengths", lengths, (S,), device), S, M, P), S, M, P
 
 
+def _as_list(pools):
+    return (pools,) if isinstance(pools, torch.Tensor) else pools
+
+
 def _buffers(name, pools, n_pages, device):
     """Checks the buffers; returns them packed, and how many."""
-    if isinstance(pools, torch.Tensor):
-        pools = (pools,)
+    pools = _as_list(pools)
     if len(pools) > MAX_BUFFERS:
         raise ValueError(f"at most {MAX_BUFFERS} buffers")
     out = []
@@ -128,6 +131,7 @@ def cache_reserve(table, refcounts, seqs, counts, device_status=None):
     rows = torch.empty(n, M, dtype=torch.int32, device=table.device)
     _call("gdn_pages_reserve_run", table, (book, _int32("seqs", seqs, (n,), device), _int32("counts", counts, (n,), device), n,
                                            rows.data_ptr(), _status(device_status, device)), (S, M, P, n))
+    mark_written(table, refcounts)
     return rows
 
 
@@ -145,6 +149,7 @@ def cache_fork(pools, table, refcounts, parents, children, page_tokens=0, length
     _call("gdn_pages_fork_run", table, (book, bufs, nb, _int32("parents", parents, (n,), device),
                                         _int32("children", children, (n,), device), n, int(page_tokens), rows.data_ptr(),
                                         _status(device_status, device)), (S, M, P, n))
+    mark_written(table, refcounts, lengths, *_as_list(pools))
     return rows
 
 
@@ -153,6 +158,7 @@ def cache_free(table, refcounts, seqs, lengths=None, device_status=None):
     device, book, _, _, _ = _book(table, refcounts, lengths)
     n = seqs.numel()
     _call("gdn_pages_free_run", table, (book, _int32("seqs", seqs, (n,), device), n, _status(device_status, device)))
+    mark_written(table, refcounts, lengths)
 
 
 def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, device_status=None):
@@ -168,6 +174,7 @@ def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, d
     _call("gdn_pages_compact_run", table, (book, bufs, nb, _int32("table_out", table_out, (S, M), device),
                                            _int32("refcounts_out", refcounts_out, (P,), device), remap.data_ptr(),
                                            n_live.data_ptr(), _status(device_status, device)), (S, M, P, 0))
+    mark_written(table_out, refcounts_out, *_as_list(pools))
     return remap, n_live
 
 
@@ -175,10 +182,7 @@ def cache_copy(src_pools, dst_pools, src, dst, device_status=None):
     """Row ``src[i]`` of each buffer of ``src_pools`` to row ``dst[i]`` of the buffer of the same place in ``dst_pools``
     (checkpoints into a state pool, for one); pairs with a negative index are skipped.  No row is named twice in ``dst``,
     and none is both read and written."""
-    if isinstance(src_pools, torch.Tensor):
-        src_pools = (src_pools,)
-    if isinstance(dst_pools, torch.Tensor):
-        dst_pools = (dst_pools,)
+    src_pools, dst_pools = _as_list(src_pools), _as_list(dst_pools)
     if len(src_pools) != len(dst_pools):
         raise ValueError("src_pools and dst_pools must have as many buffers")
     if not src_pools:
@@ -194,3 +198,4 @@ def cache_copy(src_pools, dst_pools, src, dst, device_status=None):
     db, _ = _buffers("dst_pools", dst_pools, n_dst, device)
     _call("gdn_pages_copy_run", src_pools[0], (sb, n_src, db, n_dst, nb, _int32("src", src, (n,), device),
                                                _int32("dst", dst, (n,), device), n, _status(device_status, device)))
+    mark_written(*dst_pools)

@@ -35,3 +35,57 @@ def test_the_status_may_be_cleared_before_the_backward_pass():
     status.zero_()
     y.sum().backward()
     assert int(status) & gdn.DEVICE_ERR["CU_SEQLENS"]
+
+
+WRITES = {
+    "output": lambda i, t: gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], cu_seqlens=i["cu"], output=i["x"]),
+    "output_state": lambda i, t: gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=i["h0"], output_state=i["h0"],
+                                                             output_final_state=True, cu_seqlens=i["cu"]),
+    "tile_states": lambda i, t: gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], cu_seqlens=i["cu"], tile_states=t),
+    "decode_output": lambda i, t: gdn.gated_linear_recurrence_decode(i["x"], i["a"], i["b"], output=i["x"]),
+    "decode_state": lambda i, t: gdn.gated_linear_recurrence_decode(
+        i["x"][:2], i["a"][:2], i["b"][:2], initial_state=i["h0"], state_indices=torch.tensor([1, 0], dtype=torch.int32, device="cuda")),
+    "decode_output_state": lambda i, t: gdn.gated_linear_recurrence_decode(i["x"][:2], i["a"][:2], i["b"][:2], output_state=i["h0"]),
+}
+
+
+@pytest.mark.parametrize("how", list(WRITES))
+def test_overwriting_a_saved_tensor_is_noticed(how):
+    """What a call writes into a caller's tensor counts as a change in place: a backward pass that saved the tensor refuses to
+    compute gradients from the new values.  Reading it changes nothing."""
+    i = make([64, 6], 2, 16, "f32", seed=32)
+    t = torch.ones(2, 2, 16, device="cuda", requires_grad=True)
+    saved = {"output": "x", "decode_output": "x", "tile_states": None}.get(how, "h0")
+    kept = i["x"] if saved == "x" else i["h0"] if saved == "h0" else t.detach()
+    w = torch.ones_like(kept, requires_grad=True)
+    loss = (w * kept).sum()  # saves `kept` for w's gradient
+    gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=i["h0"], cu_seqlens=i["cu"])  # reads
+    loss.backward(retain_graph=True)
+    with torch.no_grad():
+        WRITES[how](i, kept)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+
+
+def test_a_recurrence_notices_that_its_initial_state_was_overwritten():
+    i = make([64, 6], 2, 16, "f32", seed=33)
+    a = i["a"].clone().requires_grad_()
+    y = gdn.gated_linear_recurrence(i["x"], a, i["b"], initial_state=i["h0"], cu_seqlens=i["cu"])
+    with torch.no_grad():
+        gdn.gated_linear_recurrence_decode(i["x"][:2], i["a"][:2], i["b"][:2], initial_state=i["h0"],
+                                           state_indices=torch.tensor([1, 0], dtype=torch.int32, device="cuda"))
+    with pytest.raises(RuntimeError, match="inplace"):
+        y.sum().backward()
+
+
+def test_inference_mode():
+    """Tensors without a version: the calls work on them as on others."""
+    i = make([64, 6], 2, 16, "f32", seed=34)
+    want = gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=i["h0"], cu_seqlens=i["cu"], output_final_state=True)
+    with torch.inference_mode():
+        pool, out, tiles = i["h0"].clone(), torch.empty_like(i["x"]), torch.empty(2, 2, 16, device="cuda")
+        gdn.gated_linear_recurrence(i["x"], i["a"], i["b"], initial_state=pool, output_state=pool, output_final_state=True,
+                                    cu_seqlens=i["cu"], output=out, tile_states=tiles)
+        assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
+        y, _ = gdn.gated_linear_recurrence_decode(i["x"][:2], i["a"][:2], i["b"][:2], initial_state=pool, output_state=pool)
+        torch.testing.assert_close(y, i["a"][:2] * want[1] + i["b"][:2] * i["x"][:2], rtol=0, atol=2 ** -18)  # terms below 16, four roundings
