@@ -245,6 +245,7 @@ Route backward_route(const LinearParams& p) {
 // The workspace as the kernels take it; what has to start from zero is zeroed, where anything is handed on.
 cudaError_t scan_space(const Route& r, void* workspace, cudaStream_t stream, linear::ScanSpace* s) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    s->wait_cycles = linear::kWaitCycles;
     if (!r.column) {
         s->nt = r.tiles;
         s->blocks = static_cast<uint32_t>(r.blocks);

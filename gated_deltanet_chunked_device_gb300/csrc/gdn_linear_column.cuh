@@ -175,6 +175,14 @@ struct StageArray {
     static __device__ __forceinline__ Pack<T> get(const uint8_t* stage, int run, int k, int l) {
         return *reinterpret_cast<const Pack<T>*>(stage + (run * kRun + k) * kRow + l * 4 * static_cast<int>(sizeof(T)));
     }
+    // What a thread reads of a stage becomes NaN: its copies have not come.
+    static __device__ __forceinline__ void spoil(uint8_t* stage, int run, int l) {
+        Pack<T> nan;
+        memset(&nan, 0xff, sizeof(nan));
+#pragma unroll 1
+        for (int k = 0; k < kRun; ++k)
+            *reinterpret_cast<Pack<T>*>(stage + (run * kRun + k) * kRow + l * 4 * static_cast<int>(sizeof(T))) = nan;
+    }
 };
 
 // A stage of gates per head: the 16 bytes of each token's gates that hold the block's head.
@@ -348,6 +356,14 @@ struct Segments {
     int32_t first, stages;         // stages of the first segment, and of the others
 };
 
+// At the end of a block that gave up a wait: what copies are under way get time to land, before the block's shared memory goes
+// (one thread).  A place's phase that is under way is of one parity, and of the other the wait is over at once.
+template <int kDepth>
+__device__ __forceinline__ void drain(uint64_t (&full)[kDepth], long long cycles) {
+    for (int i = 0; i < kDepth; ++i)
+        for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait(&full[i], parity, cycles / 8);
+}
+
 // Maps of the inputs for tiled copies (not of gates of any heads).
 struct ColumnMaps {
     CUtensorMap x, a, b, dy;
@@ -447,7 +463,12 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     Pack<X> px[kRun];
     Pack<G> pa[kGates == kPerChannel ? kRun : 1], pb[kGates == kPerChannel ? kRun : 1];
     float ha[kHeld], hb[kHeld];
-    bool ok = true;  // until a wait runs out
+    bool ok = true;  // until a wait runs out; then what this thread adds to the results is NaN
+    auto wait = [&](uint64_t* bar, uint32_t parity, long long cycles) {
+        if (!ok || mbar_wait(bar, parity, cycles)) return;
+        ok = false;
+        report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+    };
     auto take = [&](int q) {
         if (kGates == kAnyHead) {
             const int64_t t = stage_start(q) + run * kRun;
@@ -459,11 +480,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 if constexpr (kHasB) hb[k] = to_f32(gb[(t + k) * p.b_stride]);
             }
         }
-        if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
-            ok = false;
-            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
-        }
-        const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
+        wait(&sm.full[q % kDepth], (q / kDepth) & 1, copy_wait(sp.wait_cycles));
+        if (!ok) AX::spoil(stage, run, l);
         const uint8_t *sa = stage + AX::kBytes, *sb = sa + AG::kBytes;
 #pragma unroll
         for (int k = 0; k < kRun; ++k) {
@@ -525,12 +544,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     if (group == 0 && warp == 0 && blk == 0) check_bounds(p, part, sp.nt, lane);
     __syncthreads();
     X* y = static_cast<X*>(p.y) + c0 + l * 4;
-    auto wait_hand = [&](int q) {
-        if (ok && !mbar_wait(&sm.handed[q % kHands], (q / kHands) & 1)) {
-            ok = false;
-            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
-        }
-    };
+    auto wait_hand = [&](int q) { wait(&sm.handed[q % kHands], (q / kHands) & 1, hand_wait(sp.wait_cycles)); };
     for (int q = group; q < steps; q += kGroups) {
         const StageBounds<kTokens>& bd = gr.bounds[q / kGroups % 3];
         const bool learn = twice && q < stages;
@@ -641,7 +655,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         // The group's one barrier of a step.  Past it: every warp's pair is there and every thread has its inputs of this
         // stage, so its place in the ring is free; the bounds of the group's next stage are known.
         named_bar_sync(1 + group, 32 * kColWarps);
-        if (leader) fetch(q + kDepth);
+        if (leader && ok) fetch(q + kDepth);
         float2 ab[kColWarps];
 #pragma unroll
         for (int w = 0; w < kColWarps; ++w) ab[w] = gr.pairs[q / kGroups & 1][w][ch];
@@ -656,7 +670,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         float carry = 0.f;
         if (q > 0) {
             wait_hand(q);
-            carry = sm.hand[q % kHands][ch];
+            carry = ok ? sm.hand[q % kHands][ch] : nanf("");
         }
         float enter = carry;
 #pragma unroll
@@ -733,6 +747,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                 *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
         }
     }
+    if (leader && !ok) drain(sm.full, sp.wait_cycles);
 }
 
 template <class X, class G, int kGates, bool kHasB, class Col>

@@ -165,22 +165,22 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
     if (group == 0 && warp == 0 && blk == 0) check_bounds(p, part, sp.nt, lane);
     fetch_saved(group);
     __syncthreads();
-    bool ok = true;  // until a wait runs out
+    bool ok = true;  // until a wait runs out; then what this thread adds to the results is NaN
+    auto wait = [&](uint64_t* bar, uint32_t parity, long long cycles) {
+        if (!ok || mbar_wait(bar, parity, cycles)) return;
+        ok = false;
+        report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+    };
     float own = 0.f;
     bool own_reset = false;
-    auto wait_hand = [&](int q) {
-        if (ok && !mbar_wait(&sm.handed[q % kHands], (q / kHands) & 1)) {
-            ok = false;
-            report(p.status, GDN_DEVICE_ERR_TIMEOUT);
-        }
-    };
+    auto wait_hand = [&](int q) { wait(&sm.handed[q % kHands], (q / kHands) & 1, hand_wait(sp.wait_cycles)); };
     const int pieces = kGates == kOneHead ? p.D / W : 1, piece = kGates == kOneHead ? c0 % p.D / W : 0;
     for (int q = group; q < steps; q += kGroups) {
         const StageBounds<kTokens>& bd = gr.bounds[q / kGroups % 3];
         const bool learn = twice && q < stages;
         const int64_t t = stage_start(q) + run * kRun;
-        const uint8_t* stage = ring + q % kDepth * Shape::kStageBytes;
-        const uint8_t *sa = stage + AX::kBytes, *sx = stage + Shape::kLearnBytes, *sb = sx + AX::kBytes;
+        uint8_t *stage = ring + q % kDepth * Shape::kStageBytes, *sx = stage + Shape::kLearnBytes;
+        const uint8_t *sa = stage + AX::kBytes, *sb = sx + AX::kBytes;
         using Gate = std::conditional_t<kGates == kPerChannel, Quad, float>;
         Gate a[kRun], A, exA, rxA;
         Quad u[kRun], B = all4(0.f), E, exB, rxE;
@@ -205,9 +205,10 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         if (warp == kColWarps - 1) bounds(q + kGroups);
         {
             plain = (bd.plain >> warp) & 1;
-            if (ok && !mbar_wait(&sm.full[q % kDepth], (q / kDepth) & 1)) {
-                ok = false;
-                report(p.status, GDN_DEVICE_ERR_TIMEOUT);
+            wait(&sm.full[q % kDepth], (q / kDepth) & 1, copy_wait(sp.wait_cycles));
+            if (!ok) {
+                AX::spoil(stage, run, l);
+                if (!learn) AX::spoil(sx, run, l);
             }
             if constexpr (kGates == kOneHead) {
 #pragma unroll
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         // The group's one barrier of a step.  Past it: every warp's pair is there, nobody of the group reads its stage before
         // any more (its place in the ring is free), and the bounds of the group's next stage are known.
         named_bar_sync(1 + group, 32 * kColWarps);
-        if (leader) fetch(q + kAhead);
+        if (leader && ok) fetch(q + kAhead);
         float2 ae[kColWarps];
 #pragma unroll
         for (int w = 0; w < kColWarps; ++w) ae[w] = gr.pairs[q / kGroups & 1][w][ch];
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         float carry = own;
         if (kGroups > 1 && q > 0) {
             wait_hand(q);
-            carry = sm.hand[q % kHands][ch];
+            carry = ok ? sm.hand[q % kHands][ch] : nanf("");
         }
         float enter_c = carry;
 #pragma unroll
@@ -489,6 +490,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             }
         }
     }
+    if (leader && !ok) drain(sm.full, sp.wait_cycles);
 }
 
 template <class X, class G, int kGates, bool kHasB, class Col>

@@ -37,7 +37,14 @@ constexpr int kCols = 128;             // channels of a block
 constexpr int kWarps = 8;
 constexpr int kSegTokens = kTile / kWarps;
 constexpr int kThreads = 32 * kWarps;
-constexpr long long kWaitCycles = 4000000000LL;  // about two seconds
+
+// Limits of waits, in SM clocks.  For another block (a look-back) about two seconds; within a block, for copies half of that.
+// Warps that wait for one that may itself wait for both, in turn, have the most patience: none gives up while what it waits for
+// may still come.  What a wait should have brought is NaN once it has run out, for all that depends on it.
+constexpr long long kWaitCycles = 4000000000LL;
+__host__ __device__ constexpr long long copy_wait(long long wait) { return wait / 2; }
+__host__ __device__ constexpr long long hand_wait(long long wait) { return 2 * wait; }
+static_assert(hand_wait(kWaitCycles) > kWaitCycles + copy_wait(kWaitCycles), "a hand-over comes after a look-back and a copy");
 
 template <class T>
 struct alignas(4 * sizeof(T)) Pack {
@@ -245,6 +252,7 @@ struct ScanSpace {
     float* known;                  // [nt][C] end states in the scan's direction
     int64_t nt;
     uint32_t blocks;
+    long long wait_cycles;         // limit of a look-back; the others follow from it
 };
 
 constexpr uint32_t kPair = 1, kKnown = 2;
@@ -326,6 +334,7 @@ __device__ __forceinline__ float through_pair(float4 ab, float h) { return pass_
 // The state that enters place `f` of the scan (f >= 1) for channel c, by one warp for 32 channels: from the nearest
 // place whose end state is known, through the pairs of the places after it.  Places are numbered in the scan's
 // direction; at(f) gives a place's row in pairs and known.  kSegments: places are time segments, with exponents.
+// NaN when the wait runs out: handed on, it reaches whatever depends on it, and nobody after waits for long.
 template <bool kSegments, class At>
 __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpace& s, const uint32_t* flags, int64_t f, int c, int lane,
                                            At at) {
@@ -339,9 +348,9 @@ __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpac
         dist = known ? __ffs(known) - 1 : 32;
         // all nearer places have their pairs
         if (dist < 32 && (~any & ((1u << dist) - 1)) == 0) break;
-        if (clock64() - t0 > kWaitCycles) {
+        if (__any_sync(0xffffffffu, clock64() - t0 > s.wait_cycles)) {
             if (lane == 0) report(p.status, GDN_DEVICE_ERR_TIMEOUT);
-            return 0.f;
+            return nanf("");
         }
     }
     __syncwarp();

@@ -312,7 +312,8 @@ def gated_linear_recurrence(x, a, b=None, initial_state=None, output_final_state
     (int32 or int64) bounds the sequences (None: one sequence); ``initial_state`` and ``output_state`` are [N, H, D], or
     pools addressed by ``state_indices``, and may be one buffer.  ``tile_states`` [ceil(T / 64), H, D] fp32, when given,
     receives what :func:`gated_linear_recurrence_backward` needs.  ``device_status`` (int32) receives the error bits of
-    device data.  Returns ``output`` or ``(output, final_state)``.
+    device data (``DEVICE_ERR``); without it such errors go unreported, and the outputs are unspecified where they occur.  (A
+    wait inside a kernel that ran out, "TIMEOUT", leaves NaN in all that depends on it.)  Returns ``output`` or ``(output, final_state)``.
 
     Differentiable in x, a, b and initial_state when called without output, output_state, state_indices and
     tile_states.

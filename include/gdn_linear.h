@@ -61,7 +61,10 @@
  * GDN_DEVICE_ERR_STATE_INDEX_RANGE and GDN_DEVICE_ERR_TIMEOUT are OR-ed into
  * args.device_status, when it is given; the outputs are then unspecified).  A
  * state index outside [0, n_pool) is not followed.  Two sequences that name
- * one pool row race on it.
+ * one pool row race on it.  Waits of one block for another, or for its copies,
+ * have a limit of one to four seconds.  After one that ran out
+ * (GDN_DEVICE_ERR_TIMEOUT) the run ends, and outputs and states that depend
+ * on what did not come are NaN, with device_status or without it.
  */
 #ifndef GDN_LINEAR_H
 #define GDN_LINEAR_H
