@@ -224,12 +224,6 @@ class on_device:
             torch.cuda.set_device(self.before)
 
 
-def mark_written(*tensors) -> None:
-    """Tells autograd that a kernel has changed these tensors (None: none) in place, so that a backward pass that saved one
-    of them refuses to go on with other values."""
-    torch.autograd.graph.increment_version([t for t in tensors if t is not None])
-
-
 def gdn_prefill_plan_destroy(plan) -> None:
     lib().gdn_prefill_plan_destroy(plan)
 

@@ -13,8 +13,9 @@ import struct
 import threading
 
 import torch
+from torch.autograd.graph import increment_version
 
-from . import DTYPE_F32, GdnError, _pow2_at_least, _QKV_DTYPES, _STATE_DTYPES, lib, mark_written, on_device
+from . import DTYPE_F32, GdnError, _pow2_at_least, _QKV_DTYPES, _STATE_DTYPES, lib, on_device
 
 __all__ = ["gated_linear_recurrence", "gated_linear_recurrence_backward", "gated_linear_recurrence_decode", "LinearDesc",
            "LinearArgs", "LINEAR_FLAGS", "LINEAR_TILE", "gdn_linear_plan", "gdn_linear_plan_destroy",
@@ -231,6 +232,12 @@ def _status_ptr(device_status, device):
     return device_status.data_ptr()
 
 
+def _written(*tensors):
+    """Tells autograd what a kernel has changed in place (None: nothing), so that a backward pass that saved one of these tensors
+    refuses to go on with other values."""
+    increment_version([t for t in tensors if t is not None])
+
+
 def _addr(t):
     return 0 if t is None else t.data_ptr()
 
@@ -272,7 +279,7 @@ def _forward(x, a, b, initial_state, output_state, cu_seqlens, output, state_ind
                  _addr(output_state), sstride, _addr(state_indices), n_pool, _status_ptr(device_status, device),
                  output.data_ptr(), ys, _addr(tile_states), 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
     _run(0, plan, x, args)
-    mark_written(output, output_state, tile_states)
+    _written(output, output_state, tile_states)
     return output
 
 
@@ -398,5 +405,5 @@ def gated_linear_recurrence_decode(x, a, b=None, initial_state=None, state_indic
         st = lib().gdn_linear_decode_run(plan.handle, args, m, stream)
     if st != 0:
         raise GdnError(st, "gdn_linear_decode_run")
-    mark_written(output, output_state)
+    _written(output, output_state)
     return (output, output_state) if output_final_state else output

@@ -13,8 +13,9 @@ import functools
 import struct
 
 import torch
+from torch.autograd.graph import increment_version
 
-from . import GdnError, lib, mark_written, on_device
+from . import GdnError, lib, on_device
 
 __all__ = ["cache_reserve", "cache_fork", "cache_free", "cache_compact", "cache_copy", "PAGES_ERR", "PagesBook", "PagesBuffer"]
 
@@ -110,7 +111,8 @@ def _workspace_bytes(bounds):
 
 
 def _call(name, like, args, workspace=None):
-    """Calls an entry point on `like`'s device and the caller's stream; workspace: the bounds to take one for."""
+    """Calls an entry point on `like`'s device and the caller's stream; workspace: the bounds to take one for.  What it changes
+    in place its caller tells autograd (increment_version), so that a backward pass that saved it refuses to go on."""
     with on_device(like.get_device()) as stream:
         if workspace is None:
             st = getattr(lib(), name)(*args, stream)
@@ -131,7 +133,7 @@ def cache_reserve(table, refcounts, seqs, counts, device_status=None):
     rows = torch.empty(n, M, dtype=torch.int32, device=table.device)
     _call("gdn_pages_reserve_run", table, (book, _int32("seqs", seqs, (n,), device), _int32("counts", counts, (n,), device), n,
                                            rows.data_ptr(), _status(device_status, device)), (S, M, P, n))
-    mark_written(table, refcounts)
+    increment_version((table, refcounts))
     return rows
 
 
@@ -149,7 +151,7 @@ def cache_fork(pools, table, refcounts, parents, children, page_tokens=0, length
     _call("gdn_pages_fork_run", table, (book, bufs, nb, _int32("parents", parents, (n,), device),
                                         _int32("children", children, (n,), device), n, int(page_tokens), rows.data_ptr(),
                                         _status(device_status, device)), (S, M, P, n))
-    mark_written(table, refcounts, lengths, *_as_list(pools))
+    increment_version((table, refcounts, *_as_list(pools)) if lengths is None else (table, refcounts, lengths, *_as_list(pools)))
     return rows
 
 
@@ -158,7 +160,7 @@ def cache_free(table, refcounts, seqs, lengths=None, device_status=None):
     device, book, _, _, _ = _book(table, refcounts, lengths)
     n = seqs.numel()
     _call("gdn_pages_free_run", table, (book, _int32("seqs", seqs, (n,), device), n, _status(device_status, device)))
-    mark_written(table, refcounts, lengths)
+    increment_version((table, refcounts) if lengths is None else (table, refcounts, lengths))
 
 
 def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, device_status=None):
@@ -174,7 +176,7 @@ def cache_compact(pools, table, refcounts, table_out=None, refcounts_out=None, d
     _call("gdn_pages_compact_run", table, (book, bufs, nb, _int32("table_out", table_out, (S, M), device),
                                            _int32("refcounts_out", refcounts_out, (P,), device), remap.data_ptr(),
                                            n_live.data_ptr(), _status(device_status, device)), (S, M, P, 0))
-    mark_written(table_out, refcounts_out, *_as_list(pools))
+    increment_version((table_out, refcounts_out, *_as_list(pools)))
     return remap, n_live
 
 
@@ -198,4 +200,4 @@ def cache_copy(src_pools, dst_pools, src, dst, device_status=None):
     db, _ = _buffers("dst_pools", dst_pools, n_dst, device)
     _call("gdn_pages_copy_run", src_pools[0], (sb, n_src, db, n_dst, nb, _int32("src", src, (n,), device),
                                                _int32("dst", dst, (n,), device), n, _status(device_status, device)))
-    mark_written(*dst_pools)
+    increment_version(dst_pools)
