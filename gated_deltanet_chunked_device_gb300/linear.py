@@ -293,6 +293,7 @@ class _Recurrence(torch.autograd.Function):
         y = _forward(x, a, b, initial_state, final, cu_seqlens, None, None, tiles, device_status)
         ctx.save_for_backward(x, a, b, initial_state, cu_seqlens, tiles)
         ctx.device_status = device_status  # written to, never read: the caller may clear it in between
+        ctx.set_materialize_grads(False)  # a final state that the loss does not use has no gradient to be read
         return y, final
 
     @staticmethod

@@ -89,3 +89,23 @@ def test_inference_mode():
         assert torch.equal(out, want[0]) and torch.equal(pool, want[1])
         y, _ = gdn.gated_linear_recurrence_decode(i["x"][:2], i["a"][:2], i["b"][:2], initial_state=pool, output_state=pool)
         torch.testing.assert_close(y, i["a"][:2] * want[1] + i["b"][:2] * i["x"][:2], rtol=0, atol=2 ** -18)  # terms below 16, four roundings
+
+
+@pytest.mark.parametrize("uses", ["y", "final", "both"])
+def test_what_the_loss_does_not_use_has_no_gradient(uses, monkeypatch):
+    """An unused final state is not made up as zeros for the backward pass to read; gradients through either output alone."""
+    i = make([70, 0, 9], 2, 16, "f32", seed=35)
+    seen = []
+    backward = gdn.linear.gated_linear_recurrence_backward
+    monkeypatch.setattr(gdn.linear, "gated_linear_recurrence_backward",
+                        lambda *args, **kw: seen.append(kw["d_final_state"] is None) or backward(*args, **kw))
+    leaf = {k: i[k].clone().requires_grad_() for k in ("x", "a", "b", "h0")}
+    y, final = gdn.gated_linear_recurrence(leaf["x"], leaf["a"], leaf["b"], initial_state=leaf["h0"], output_final_state=True,
+                                           cu_seqlens=i["cu"])
+    loss = ((y * i["dy"]).sum() if uses != "final" else 0) + ((final * i["df"]).sum() if uses != "y" else 0)
+    loss.backward()
+    assert seen == [uses == "y"]
+    dy = np.zeros(y.shape) if uses == "final" else f64(i["dy"])
+    val, err = ref.backward(dy, *(f64(i[k]) for k in ("x", "a", "b")), i["cul"], f64(i["h0"]), None if uses == "y" else f64(i["df"]))
+    for name, e in (("x", "dx"), ("a", "da"), ("b", "db"), ("h0", "d0")):
+        within(name, leaf[name].grad, val[e], err[e])
