@@ -361,4 +361,6 @@ cudaError_t launch_cp_final(const CpParams& p, cudaStream_t stream);
 size_t chunk_bf16_smem_bytes();
 size_t plan_workspace_bytes(gdn_prefill_plan_t plan);
 
+int multiprocessors();  // of the current device (gdn_linear.cu)
+
 }  // namespace gdn

@@ -104,8 +104,6 @@ inline size_t workspace_bound(int64_t T, int64_t C, int64_t head_dim) {
     return scan_layout(tiles_of(T), 4 * backward_blocks(C, head_dim) + (C + 15) / 16, C, false).total + sums_bytes(T, C, head_dim, 16) + 256;
 }
 
-int multiprocessors();  // of the current device
-
 // A map of T rows of C elements, `stride` elements apart, for boxes of `width` elements of `tokens` rows; what lies
 // outside reads as zeros.
 bool encode_rows(CUtensorMap* map, const void* base, int32_t dt, int64_t stride, int64_t C, int64_t T, int width, int tokens);

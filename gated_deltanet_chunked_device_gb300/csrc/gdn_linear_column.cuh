@@ -557,100 +557,98 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         int n = kRun;
         bool plain = true, before = false;  // before: whether a sequence starts in the warp's runs before this one
         if (warp == kColWarps - 1) bounds(q + kGroups);
-        {
-            plain = (bd.plain >> warp) & 1;
-            take(q);
+        plain = (bd.plain >> warp) & 1;
+        take(q);
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            u[k] = widen(px[k]);
+            if constexpr (kGates == kOneHead) {
+                const int from_lane = sub * kLanesRow + k % kLanesRow;
+                a[k] = __shfl_sync(0xffffffffu, ha[k / kLanesRow], from_lane);
+                if constexpr (kHasB) u[k] = mul(__shfl_sync(0xffffffffu, hb[k / kLanesRow], from_lane), u[k]);
+            } else if constexpr (kGates == kAnyHead) {
+                a[k] = ha[k];
+                if constexpr (kHasB) u[k] = mul(hb[k], u[k]);
+            } else {
+                a[k] = widen(pa[k]);
+                if constexpr (kHasB) u[k] = mul(u[k], widen(pb[k]));
+            }
+        }
+        set_gate(A, 1.f);
+        B = all4(0.f);
+        uint32_t any = 0;
+        if (!plain) {
+            n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                u[k] = widen(px[k]);
-                if constexpr (kGates == kOneHead) {
-                    const int from_lane = sub * kLanesRow + k % kLanesRow;
-                    a[k] = __shfl_sync(0xffffffffu, ha[k / kLanesRow], from_lane);
-                    if constexpr (kHasB) u[k] = mul(__shfl_sync(0xffffffffu, hb[k / kLanesRow], from_lane), u[k]);
-                } else if constexpr (kGates == kAnyHead) {
-                    a[k] = ha[k];
-                    if constexpr (kHasB) u[k] = mul(hb[k], u[k]);
-                } else {
-                    a[k] = widen(pa[k]);
-                    if constexpr (kHasB) u[k] = mul(u[k], widen(pb[k]));
-                }
+                if (k < n) continue;
+                set_gate(a[k], 1.f);
+                u[k] = all4(0.f);
             }
-            set_gate(A, 1.f);
-            B = all4(0.f);
-            uint32_t any = 0;
-            if (!plain) {
-                n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), end - t)));
+            starts = run_bits<kRun>(bd.starts, run);
+            ends = run_bits<kRun>(bd.ends, run);
+            any = any_run_bits<kRun, kRuns>(bd.starts, warp);
+        }
+        // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
+        auto compose = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    if (k < n) continue;
-                    set_gate(a[k], 1.f);
-                    u[k] = all4(0.f);
-                }
-                starts = run_bits<kRun>(bd.starts, run);
-                ends = run_bits<kRun>(bd.ends, run);
-                any = any_run_bits<kRun, kRuns>(bd.starts, warp);
-            }
-            // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
-            auto compose = [&](auto whole) {
-                constexpr bool kWhole = decltype(whole)::value;
-#pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    if (!kWhole && ((any >> k) & 1) && ((starts >> k) & 1)) {
-                        if (p.initial_state && on) {
-                            const int64_t row = state_row(p, bd.start_seq[run * kRun + k]);
-                            // With states in place, a later segment may have written the row of a sequence that starts
-                            // here by the time of the second pass: the last one to start, if any.  Its state is kept.
-                            float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
-                            bool kept = false;
-                            if (twice && !learn)
-                                for (int i = 0; i < kGroups; ++i)
-                                    if (t + k == sm.groups[i].kept_at) {
-                                        h0 = *reinterpret_cast<const float4*>(&sm.groups[i].kept[l * 4]);
-                                        kept = true;
-                                    }
-                            if (!kept && row >= 0)
-                                h0 = state_quad_load(p.initial_state, row * p.state_stride + c0 + l * 4, p.state_dt);
-                            if (learn && is_last_bit<kTokens>(bd.starts, run * kRun + k)) {
-                                *reinterpret_cast<float4*>(&gr.kept[l * 4]) = h0;
-                                gr.kept_at = t + k;
-                            }
-                            if (row >= 0) u[k] = fma(a[k], quad(h0), u[k]);
+            for (int k = 0; k < kRun; ++k) {
+                if (!kWhole && ((any >> k) & 1) && ((starts >> k) & 1)) {
+                    if (p.initial_state && on) {
+                        const int64_t row = state_row(p, bd.start_seq[run * kRun + k]);
+                        // With states in place, a later segment may have written the row of a sequence that starts
+                        // here by the time of the second pass: the last one to start, if any.  Its state is kept.
+                        float4 h0 = make_float4(0.f, 0.f, 0.f, 0.f);
+                        bool kept = false;
+                        if (twice && !learn)
+                            for (int i = 0; i < kGroups; ++i)
+                                if (t + k == sm.groups[i].kept_at) {
+                                    h0 = *reinterpret_cast<const float4*>(&sm.groups[i].kept[l * 4]);
+                                    kept = true;
+                                }
+                        if (!kept && row >= 0)
+                            h0 = state_quad_load(p.initial_state, row * p.state_stride + c0 + l * 4, p.state_dt);
+                        if (learn && is_last_bit<kTokens>(bd.starts, run * kRun + k)) {
+                            *reinterpret_cast<float4*>(&gr.kept[l * 4]) = h0;
+                            gr.kept_at = t + k;
                         }
-                        B = all4(0.f);
+                        if (row >= 0) u[k] = fma(a[k], quad(h0), u[k]);
                     }
-                    A = mul(A, a[k]);
-                    B = fma(a[k], B, u[k]);
+                    B = all4(0.f);
                 }
-            };
-            if (plain)
-                compose(std::true_type{});
-            else
-                compose(std::false_type{});
-            // over the warp's runs
-            const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
+                A = mul(A, a[k]);
+                B = fma(a[k], B, u[k]);
+            }
+        };
+        if (plain)
+            compose(std::true_type{});
+        else
+            compose(std::false_type{});
+        // over the warp's runs
+        const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
 #pragma unroll
-            for (int o = 1; o < kRuns; o <<= 1) {
-                const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
-                const Gate oa = shift_up(A, o * kLanesRow);
-                const Quad ob = shift_up(B, o * kLanesRow);
-                if (sub >= o) {
-                    B = pick(mine, B, fma(A, ob, B));
-                    A = mul(A, oa);
-                }
+        for (int o = 1; o < kRuns; o <<= 1) {
+            const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
+            const Gate oa = shift_up(A, o * kLanesRow);
+            const Quad ob = shift_up(B, o * kLanesRow);
+            if (sub >= o) {
+                B = pick(mine, B, fma(A, ob, B));
+                A = mul(A, oa);
             }
-            exA = shift_up(A, kLanesRow);
-            exB = shift_up(B, kLanesRow);
-            if (sub == 0) {
-                set_gate(exA, 1.f);
-                exB = all4(0.f);
-            }
-            before = (rs & ((1u << sub) - 1u)) != 0;
-            if (sub == kRuns - 1) {
-                float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
-                const Quad g = of_channels(A);
-                o[0] = make_float4(g.lo.x, B.lo.x, g.lo.y, B.lo.y);
-                o[1] = make_float4(g.hi.x, B.hi.x, g.hi.y, B.hi.y);
-            }
+        }
+        exA = shift_up(A, kLanesRow);
+        exB = shift_up(B, kLanesRow);
+        if (sub == 0) {
+            set_gate(exA, 1.f);
+            exB = all4(0.f);
+        }
+        before = (rs & ((1u << sub) - 1u)) != 0;
+        if (sub == kRuns - 1) {
+            float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
+            const Quad g = of_channels(A);
+            o[0] = make_float4(g.lo.x, B.lo.x, g.lo.y, B.lo.y);
+            o[1] = make_float4(g.hi.x, B.hi.x, g.hi.y, B.hi.y);
         }
         // The group's one barrier of a step.  Past it: every warp's pair is there and every thread has its inputs of this
         // stage, so its place in the ring is free; the bounds of the group's next stage are known.
@@ -715,37 +713,35 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             if (lane == 0) mbar_arrive(&sm.handed[(q + 1) % kHands]);
         }
         if (learn) continue;
-        {
-            const Quad e = {{__shfl_sync(0xffffffffu, enter, l * 4), __shfl_sync(0xffffffffu, enter, l * 4 + 1)},
-                            {__shfl_sync(0xffffffffu, enter, l * 4 + 2), __shfl_sync(0xffffffffu, enter, l * 4 + 3)}};
-            Quad h = pick(before, exB, fma(exA, e, exB));
-            if (!on) continue;
-            X* out = y + t * p.y_stride;
-            auto tokens = [&](auto whole) {
-                constexpr bool kWhole = decltype(whole)::value;
+        const Quad e = {{__shfl_sync(0xffffffffu, enter, l * 4), __shfl_sync(0xffffffffu, enter, l * 4 + 1)},
+                        {__shfl_sync(0xffffffffu, enter, l * 4 + 2), __shfl_sync(0xffffffffu, enter, l * 4 + 3)}};
+        Quad h = pick(before, exB, fma(exA, e, exB));
+        if (!on) continue;
+        X* out = y + t * p.y_stride;
+        auto tokens = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-                for (int k = 0; k < kRun; ++k) {
-                    if (!kWhole && ((starts >> k) & 1)) h = all4(0.f);
-                    h = fma(a[k], h, u[k]);
-                    if (kWhole || k < n) store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
-                    out += p.y_stride;
-                    if (!kWhole && ((ends >> k) & 1)) {
-                        if (p.output_state) {
-                            const int64_t row = state_row(p, bd.end_seq[run * kRun + k]);
-                            if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
-                        }
-                        if (p.tile_states && t + k == p.T - 1)
-                            *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = flat(h);
+            for (int k = 0; k < kRun; ++k) {
+                if (!kWhole && ((starts >> k) & 1)) h = all4(0.f);
+                h = fma(a[k], h, u[k]);
+                if (kWhole || k < n) store_stream(reinterpret_cast<Pack<X>*>(out), narrow(h, X{}));
+                out += p.y_stride;
+                if (!kWhole && ((ends >> k) & 1)) {
+                    if (p.output_state) {
+                        const int64_t row = state_row(p, bd.end_seq[run * kRun + k]);
+                        if (row >= 0) state_quad_store(p.output_state, row * p.state_stride + c0 + l * 4, p.state_dt, flat(h));
                     }
+                    if (p.tile_states && t + k == p.T - 1)
+                        *reinterpret_cast<float4*>(p.tile_states + (t + k) / kTile * p.C + c0 + l * 4) = flat(h);
                 }
-            };
-            if (plain)
-                tokens(std::true_type{});
-            else
-                tokens(std::false_type{});
-            if (p.tile_states && (t + kRun) % kTile == 0 && n == kRun)
-                *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
-        }
+            }
+        };
+        if (plain)
+            tokens(std::true_type{});
+        else
+            tokens(std::false_type{});
+        if (p.tile_states && (t + kRun) % kTile == 0 && n == kRun)
+            *reinterpret_cast<float4*>(p.tile_states + t / kTile * p.C + c0 + l * 4) = flat(h);
     }
     if (leader && !ok) drain(sm.full, sp.wait_cycles);
 }

@@ -203,122 +203,120 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             return __shfl_sync(0xffffffffu, held[k / kLanesRow], sub * kLanesRow + k % kLanesRow);
         };
         if (warp == kColWarps - 1) bounds(q + kGroups);
-        {
-            plain = (bd.plain >> warp) & 1;
-            wait(&sm.full[q % kDepth], (q / kDepth) & 1, copy_wait(sp.wait_cycles));
-            if (!ok) {
-                AX::spoil(stage, run, l);
-                if (!learn) AX::spoil(sx, run, l);
-            }
-            if constexpr (kGates == kOneHead) {
+        plain = (bd.plain >> warp) & 1;
+        wait(&sm.full[q % kDepth], (q / kDepth) & 1, copy_wait(sp.wait_cycles));
+        if (!ok) {
+            AX::spoil(stage, run, l);
+            if (!learn) AX::spoil(sx, run, l);
+        }
+        if constexpr (kGates == kOneHead) {
 #pragma unroll
-                for (int i = 0; i < kHeld; ++i) {
-                    const int tok = run * kRun + min(i * kLanesRow + l, kRun - 1);
-                    ha[i] = AG::get(sa, tok, head);
-                    if (kHasB && !learn) hb[i] = AG::get(sb, tok, head);
-                }
+            for (int i = 0; i < kHeld; ++i) {
+                const int tok = run * kRun + min(i * kLanesRow + l, kRun - 1);
+                ha[i] = AG::get(sa, tok, head);
+                if (kHasB && !learn) hb[i] = AG::get(sb, tok, head);
             }
+        }
+#pragma unroll
+        for (int k = 0; k < kRun; ++k) {
+            if constexpr (kGates == kOneHead)
+                a[k] = shared_gate(ha, k);
+            else
+                a[k] = widen(AG::get(sa, run, k, l));
+        }
+        if (!learn) {
 #pragma unroll
             for (int k = 0; k < kRun; ++k) {
-                if constexpr (kGates == kOneHead)
-                    a[k] = shared_gate(ha, k);
-                else
-                    a[k] = widen(AG::get(sa, run, k, l));
+                u[k] = widen(AX::get(sx, run, k, l));
+                if constexpr (kHasB) {
+                    if constexpr (kGates == kOneHead)
+                        u[k] = mul(shared_gate(hb, k), u[k]);
+                    else
+                        u[k] = mul(u[k], widen(AG::get(sb, run, k, l)));
+                }
             }
-            if (!learn) {
+        }
+        set_gate(A, 1.f);
+        E = all4(0.f);
+        if (!plain) {
+            n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), p.T - t)));
+#pragma unroll
+            for (int k = 0; k < kRun; ++k)  // past the end, a carry goes through
+                if (k >= n) set_gate(a[k], 1.f);
+            starts = run_bits<kRun>(bd.starts, run);
+            ends = run_bits<kRun>(bd.ends, run);
+            any_start = any_run_bits<kRun, kRuns>(bd.starts, warp);
+            any_end = any_run_bits<kRun, kRuns>(bd.ends, warp);
+        }
+        // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
+        auto compose = [&](auto whole) {
+            constexpr bool kWhole = decltype(whole)::value;
+#pragma unroll
+            for (int k = kRun - 1; k >= 0; --k) {
+                if (!kWhole && ((any_end >> k) & 1) && ((ends >> k) & 1)) E = final_gradient(k);
+                E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
+                A = mul(A, a[k]);
+            }
+            if (!learn)
 #pragma unroll
                 for (int k = 0; k < kRun; ++k) {
-                    u[k] = widen(AX::get(sx, run, k, l));
-                    if constexpr (kHasB) {
-                        if constexpr (kGates == kOneHead)
-                            u[k] = mul(shared_gate(hb, k), u[k]);
-                        else
-                            u[k] = mul(u[k], widen(AG::get(sb, run, k, l)));
-                    }
+                    if (!kWhole && ((any_start >> k) & 1) && ((starts >> k) & 1)) B = initial(k);
+                    B = fma(a[k], B, u[k]);
                 }
+        };
+        if (plain)
+            compose(std::true_type{});
+        else
+            compose(std::false_type{});
+        // over the warp's runs: the carry from the right, the state from the left
+        const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
+        const uint32_t re = (bd.warps_end >> warp) & 1 ? runs_with<kRun, kRuns>(bd.ends, warp) : 0;
+        Gate RA = A;
+#pragma unroll
+        for (int o = 1; o < kRuns; o <<= 1) {
+            const bool mine = (re >> sub) & ((1u << o) - 1u);
+            const Gate oa = shift_down(RA, o * kLanesRow);
+            const Quad oe = shift_down(E, o * kLanesRow);
+            if (sub + o < kRuns) {
+                E = pick(mine, E, fma(RA, oe, E));
+                RA = mul(RA, oa);
             }
-            set_gate(A, 1.f);
-            E = all4(0.f);
-            if (!plain) {
-                n = static_cast<int>(min(static_cast<int64_t>(kRun), max(static_cast<int64_t>(0), p.T - t)));
-#pragma unroll
-                for (int k = 0; k < kRun; ++k)  // past the end, a carry goes through
-                    if (k >= n) set_gate(a[k], 1.f);
-                starts = run_bits<kRun>(bd.starts, run);
-                ends = run_bits<kRun>(bd.ends, run);
-                any_start = any_run_bits<kRun, kRuns>(bd.starts, warp);
-                any_end = any_run_bits<kRun, kRuns>(bd.ends, warp);
-            }
-            // `whole`: all of the warp's tokens are there, with neither a start nor an end: code without a branch.
-            auto compose = [&](auto whole) {
-                constexpr bool kWhole = decltype(whole)::value;
-#pragma unroll
-                for (int k = kRun - 1; k >= 0; --k) {
-                    if (!kWhole && ((any_end >> k) & 1) && ((ends >> k) & 1)) E = final_gradient(k);
-                    E = mul(a[k], add(widen(AX::get(stage, run, k, l)), E));
-                    A = mul(A, a[k]);
-                }
-                if (!learn)
-#pragma unroll
-                    for (int k = 0; k < kRun; ++k) {
-                        if (!kWhole && ((any_start >> k) & 1) && ((starts >> k) & 1)) B = initial(k);
-                        B = fma(a[k], B, u[k]);
-                    }
-            };
-            if (plain)
-                compose(std::true_type{});
-            else
-                compose(std::false_type{});
-            // over the warp's runs: the carry from the right, the state from the left
-            const uint32_t rs = (bd.warps_start >> warp) & 1 ? runs_with<kRun, kRuns>(bd.starts, warp) : 0;
-            const uint32_t re = (bd.warps_end >> warp) & 1 ? runs_with<kRun, kRuns>(bd.ends, warp) : 0;
-            Gate RA = A;
+        }
+        rxA = shift_down(RA, kLanesRow);
+        rxE = shift_down(E, kLanesRow);
+        if (sub == kRuns - 1) {
+            set_gate(rxA, 1.f);
+            rxE = all4(0.f);
+        }
+        ended = (re >> (sub + 1)) != 0;
+        if (!learn) {
 #pragma unroll
             for (int o = 1; o < kRuns; o <<= 1) {
-                const bool mine = (re >> sub) & ((1u << o) - 1u);
-                const Gate oa = shift_down(RA, o * kLanesRow);
-                const Quad oe = shift_down(E, o * kLanesRow);
-                if (sub + o < kRuns) {
-                    E = pick(mine, E, fma(RA, oe, E));
-                    RA = mul(RA, oa);
+                const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
+                const Gate oa = shift_up(A, o * kLanesRow);
+                const Quad ob = shift_up(B, o * kLanesRow);
+                if (sub >= o) {
+                    B = pick(mine, B, fma(A, ob, B));
+                    A = mul(A, oa);
                 }
             }
-            rxA = shift_down(RA, kLanesRow);
-            rxE = shift_down(E, kLanesRow);
-            if (sub == kRuns - 1) {
-                set_gate(rxA, 1.f);
-                rxE = all4(0.f);
-            }
-            ended = (re >> (sub + 1)) != 0;
-            if (!learn) {
-#pragma unroll
-                for (int o = 1; o < kRuns; o <<= 1) {
-                    const bool mine = (rs >> max(0, sub - o + 1)) & ((1u << o) - 1u);
-                    const Gate oa = shift_up(A, o * kLanesRow);
-                    const Quad ob = shift_up(B, o * kLanesRow);
-                    if (sub >= o) {
-                        B = pick(mine, B, fma(A, ob, B));
-                        A = mul(A, oa);
-                    }
-                }
-                exA = shift_up(A, kLanesRow);
-                exB = shift_up(B, kLanesRow);
-                if (sub == 0) {
-                    set_gate(exA, 1.f);
-                    exB = all4(0.f);
-                }
-                started = (rs & ((1u << sub) - 1u)) != 0;
-            }
-            // the warp's: the product and the carry are the first run's
+            exA = shift_up(A, kLanesRow);
+            exB = shift_up(B, kLanesRow);
             if (sub == 0) {
-                float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
-                const Quad g = of_channels(RA);
-                o[0] = make_float4(g.lo.x, E.lo.x, g.lo.y, E.lo.y);
-                o[1] = make_float4(g.hi.x, E.hi.x, g.hi.y, E.hi.y);
+                set_gate(exA, 1.f);
+                exB = all4(0.f);
             }
-            // the state is the last run's
-            if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&gr.states[q / kGroups & 1][warp][l * 4]) = flat(B);
+            started = (rs & ((1u << sub) - 1u)) != 0;
         }
+        // the warp's: the product and the carry are the first run's
+        if (sub == 0) {
+            float4* o = reinterpret_cast<float4*>(&gr.pairs[q / kGroups & 1][warp][l * 4]);
+            const Quad g = of_channels(RA);
+            o[0] = make_float4(g.lo.x, E.lo.x, g.lo.y, E.lo.y);
+            o[1] = make_float4(g.hi.x, E.hi.x, g.hi.y, E.hi.y);
+        }
+        // the state is the last run's
+        if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&gr.states[q / kGroups & 1][warp][l * 4]) = flat(B);
         // The group's one barrier of a step.  Past it: every warp's pair is there, nobody of the group reads its stage before
         // any more (its place in the ring is free), and the bounds of the group's next stage are known.
         named_bar_sync(1 + group, 32 * kColWarps);

@@ -15,7 +15,7 @@
 #include <climits>
 
 #include "../../include/gdn_pages.h"
-#include "gdn_linear.cuh"
+#include "gdn_internal.cuh"
 
 namespace {
 
@@ -556,8 +556,6 @@ BookParams make_book(const gdn_pages_book& b, int32_t n, void* workspace) {
     return p;
 }
 
-int sm_count() { return gdn::multiprocessors(); }
-
 // Bytes that rows of both buffers can be copied at a time.
 int32_t copy_unit(const gdn_pages_buffer& s, const gdn_pages_buffer& d) {
     const uintptr_t all = reinterpret_cast<uintptr_t>(s.base) | reinterpret_cast<uintptr_t>(d.base) |
@@ -592,7 +590,7 @@ cudaError_t launch_copy_of(const gdn_pages_buffer* src, int32_t src_pages, const
     p.count = count;
     p.n = n;
     p.status = status;
-    const int64_t units = rows > entries ? rows : entries, cap = 8 * sm_count();
+    const int64_t units = rows > entries ? rows : entries, cap = 8 * gdn::multiprocessors();
     gdn_pages_copy_kernel<kMax><<<static_cast<unsigned>(units < cap ? units : cap), kCopyThreads, 0, stream>>>(p);
     return cudaGetLastError();
 }
