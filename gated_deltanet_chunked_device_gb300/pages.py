@@ -145,6 +145,8 @@ def cache_fork(pools, table, refcounts, parents, children, page_tokens=0, length
     device, book, S, M, P = _book(table, refcounts, lengths)
     if page_tokens and lengths is None:
         raise ValueError("page_tokens needs lengths")
+    if page_tokens > 0x7fffffff:
+        raise ValueError("page_tokens must fit 32 bits")
     n = children.numel()
     bufs, nb = _buffers("pools", pools, P, device)
     rows = torch.empty(n, M, dtype=torch.int32, device=table.device)

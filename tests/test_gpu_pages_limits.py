@@ -92,3 +92,15 @@ def test_past_all_limits_at_once(page_tokens):
     assert p.m.status & ERR["NO_PAGES"]
     p.free(rng.integers(0, S, 3000).tolist())
     p.compact()
+
+
+def test_page_tokens_past_32_bits_are_refused():
+    """Not taken modulo 2^32, by which 2^32 + 4 tokens a page would be 4."""
+    p = empty_pair(3, 2, 6)
+    p.reserve([0], [2])
+    lengths(p, [0], 7)
+    for n in (1 << 31, (1 << 32) + 4, 1 << 70):
+        with pytest.raises(ValueError, match="page_tokens"):
+            p.fork([0], [1], n)
+    p.fork([0], [1], 0x7fffffff)  # one page, partly filled
+    assert p.m.table[1].tolist() == [2, -1]
