@@ -171,10 +171,10 @@ bool inputs_wide(const LinearParams& p) {
 }
 
 // Width and time segments of the columns, for stages of `warps` warps with runs of `run` tokens.
-//   - Columns of 32 channels, where they are blocks for three fifths of the SMs or more: 32768 x 4096 168 us, with columns of
-//     16 240 us (rows of 32 bytes).
-//   - Fewer columns, but too many for three segments each: columns of 16 (32768 x 2048 117 us, with columns of 32 166 us).
-//   - Fewer still: as many time segments as the SMs hold (32768 x 1024 86 us, in one segment 164 us).  With two segments the
+//   - Columns of 32 channels, where they are blocks for three fifths of the SMs or more: 32768 x 4096 172 us, with columns of
+//     16 212 us (rows of 32 bytes).
+//   - Fewer columns, but too many for three segments each: columns of 16 (32768 x 2048 107 us, with columns of 32 134 us).
+//   - Fewer still: as many time segments as the SMs hold (32768 x 1024 89 us, in one segment 134 us).  With two segments the
 //     second pass over the later one would cost what the halves save.
 // narrow: columns of 16 whatever the number (backward_route).
 linear::Segments segments(const LinearParams& p, int warps, int run, bool narrow, int* width) {
@@ -229,8 +229,8 @@ Route backward_route(const LinearParams& p) {
     if (p.gate_div == 1) r.vec = r.vec && vector_of_4(p.da, p.da_stride, p.gate_dt) && vector_of_4(p.db, p.db_stride, p.gate_dt);
     if (r.vec && inputs_wide(p) && vector_of_16_bytes(p.dy, p.dy_stride, p.x_dt, p.C)) {
         // Sums of heads of 16, 48, 80 channels fit columns of 16 alone, which have no time segments: taken where the columns
-        // are blocks for two fifths of the SMs, or the batch is short (52 heads of 80, 32768 tokens: 343 us, tiles 1157;
-        // 64 heads of 16, 4096 tokens: 35, tiles 42; 32 heads of 16, 512 tokens: 17, tiles 23; but 32768 tokens: 201, tiles 126).
+        // are blocks for two fifths of the SMs, or the batch is short (52 heads of 80, 32768 tokens: 329 us, tiles 1238;
+        // 64 heads of 16, 4096 tokens: 28, tiles 30; 32 heads of 16, 512 tokens: 8, tiles 15; but 32768 tokens: 184, tiles 122).
         const bool narrow = p.gate_div != 1 && p.D % 32 != 0 && p.D % 16 == 0 &&
                             (5 * ((p.C + 31) / 32) >= multiprocessors() || p.T <= 2048);
         r.seg = segments(p, 8, p.gate_div == 1 && p.gate_dt == GDN_DTYPE_F32 ? 4 : 8, narrow, &r.width);  // backward_run

@@ -8,19 +8,21 @@
 // tokens; the state stays in it from stage to stage (of 256 tokens, or 512),
 // so blocks hand nothing to one another, and the next stages are on their way
 // into a ring in shared memory by tiled copies.  With 4096 channels that is 128
-// blocks, and they fill HBM: 32768 tokens, bf16, gates per channel 168 us, 6.4
-// TB/s, 0.94 of a measured copy; with fp32 gates 246 us, 0.97.
+// blocks, and they fill HBM: 32768 tokens, bf16, gates per channel 166 us, 6.5
+// TB/s, 0.95 of a measured copy; with fp32 gates 239 us, 0.99.
 //
 // In a stage a thread composes 8 successive tokens of 4 channels (h_out = A
 // h_in + B, see gdn_linear_scan.cuh; two channels an instruction), the runs of
 // a warp's lanes are composed by shuffles, the warps through shared memory;
 // then every thread goes over its tokens once more from their true state.
 // Its inputs stay in registers in between: one read of shared memory.  That
-// is 480 instructions a warp and stage, and where fewer bytes come with an
-// element (gates per head: 118 us, 0.68) they bound it, not HBM: hence two
-// groups of 8 warps that take the stages in turn, so that one composes while
-// the other stores (145 us with one group), and handing the state on through
-// shared memory takes one wait and 8 fused multiply-adds.
+// is 430 to 560 instructions a warp and stage.  Where fewer bytes come with an
+// element (gates per head: 108 us, 0.74) nothing is full: 52 % of the issue
+// slots, no pipe above 33 %, and 24 of the 152 SMs without a block; what is left
+// is the latency of a stage's steps.  Hence two groups of 8 warps that take the
+// stages in turn, so that one composes while the other stores (145 us with one
+// group), and handing the state on through shared memory takes one wait and 8
+// fused multiply-adds.
 //
 // Tried and slower (32768 x 4096, bf16): inputs fetched by the threads
 // themselves, 16 bytes each (197 us: the copies' instructions and L1's tags);
@@ -349,8 +351,8 @@ __device__ __forceinline__ bool is_last_bit(const uint32_t* words, int at) {
 }
 
 // Time segments of a column, where there are too few columns for the GPU's SMs.  Segments after the first go over their
-// tokens twice: once to learn what they do to a state, and, when the state that enters is known, once more (from L2,
-// mostly).
+// tokens twice: once to learn what they do to a state, and, when the state that enters is known, once more (from HBM,
+// mostly: 368 MB read for 201 MB of inputs of 32768 x 1024, bf16).
 struct Segments {
     ScanSpace space;               // nt = segments; flags [blocks][nt]
     int32_t first, stages;         // stages of the first segment, and of the others

@@ -13,13 +13,14 @@
 // memory twice, so that a run's registers are its gates, u = b x and the
 // states that take u's place.
 //
-// 32768 x 4096: 338 us in bf16 with gates per channel (0.82 of a measured
-// copy), 461 us with fp32 gates (0.94), 542 us in fp32; with gates per head 238
-// us (0.51): there a warp's 950 instructions a stage bound it, a fifth of them
-// the sums over a head's channels, which are exact to their order: over a
-// thread's 4 channels, over a run's lanes by exchanges that halve the tokens a
-// lane has sums of, and over the blocks of a head by a small kernel (9 us), in
-// place of atomics whose order would change the result.
+// 32768 x 4096: 312 us in bf16 with gates per channel (0.89 of a measured
+// copy), 458 us with fp32 gates (0.95), 554 us in fp32 (1.0); with gates per
+// head 224 us (0.54).  There nothing is full: 59 % of the issue slots, no pipe
+// above 36 %, and 24 of the 152 SMs without a block.  A fifth of a warp's 960
+// instructions a stage are the sums over a head's channels, which have a fixed
+// order: over a thread's 4 channels, over a run's lanes by exchanges that halve
+// the tokens a lane has sums of, and over the blocks of a head by a small
+// kernel (9 us), in place of atomics whose order would change the result.
 #pragma once
 
 #include "gdn_linear_column.cuh"
