@@ -83,3 +83,31 @@ def test_a_state_of_zero_or_of_little(first):
         assert torch.isfinite(y[:n - 40]).all() and torch.isinf(y[n:]).all()
     else:
         assert not y.any()
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+@pytest.mark.parametrize("H,D,per", [(1, 32, "channel"), (8, 32, "head"), (8, 12, "head"), (2, 17, "channel"), (16, 128, "channel"), (20, 100, "head")])
+def test_what_is_not_finite_stays_in_its_sequence(H, D, per, bad):
+    """Over many segments, stages and tiles: inputs, gates and states of one sequence that are not finite leave the bits of the
+    others as they are, in both directions."""
+    i = make([1700, 900, 1, 2100], H, D, "f32", gates=per, seed=42)
+    tiles = torch.empty(-(-i["T"] // 64), H, D, device="cuda")
+
+    def run(j):
+        y, final = gdn.gated_linear_recurrence(j["x"], j["a"], j["b"], initial_state=j["h0"], cu_seqlens=j["cu"],
+                                               output_final_state=True, tile_states=tiles)
+        return (y, *gdn.gated_linear_recurrence_backward(j["dy"], j["x"], j["a"], j["b"], tiles, j["h0"], j["df"], j["cu"])[:3]), \
+            (final, gdn.gated_linear_recurrence_backward(j["dy"], j["x"], j["a"], j["b"], tiles, j["h0"], j["df"], j["cu"])[3])
+
+    clean = run(i)
+    for where in ("x", "a", "h0", "df", "dy"):
+        j = dict(i)
+        j[where] = i[where].clone()
+        for at in ((1, 2) if where in ("h0", "df") else (1700, 2150, 2599, 2600)):  # of the second and third sequence
+            j[where][at] = bad
+        got = run(j)
+        for n in (0, 3):
+            s, e = i["cul"][n], i["cul"][n + 1]
+            assert all(torch.equal(g[s:e], w[s:e]) for g, w in zip(got[0], clean[0])), (where, n)
+            assert all(torch.equal(g[n], w[n]) for g, w in zip(got[1], clean[1])), (where, n)
+        assert not torch.isfinite(got[0][2 if where in ("dy", "df") else 0][1700:2600]).all()
