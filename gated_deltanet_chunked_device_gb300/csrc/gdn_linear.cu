@@ -174,7 +174,7 @@ bool inputs_wide(const LinearParams& p) {
 //   - Columns of 32 channels, where they are blocks for three fifths of the SMs or more: 32768 x 4096 172 us, with columns of
 //     16 212 us (rows of 32 bytes).
 //   - Fewer columns, but too many for three segments each: columns of 16 (32768 x 2048 107 us, with columns of 32 134 us).
-//   - Fewer still: as many time segments as the SMs hold (32768 x 1024 89 us, in one segment 134 us).  With two segments the
+//   - Fewer still: as many time segments as the SMs hold (32768 x 1024 87 us, in one segment 134 us).  With two segments the
 //     second pass over the later one would cost what the halves save.
 // narrow: columns of 16 whatever the number (backward_route).
 linear::Segments segments(const LinearParams& p, int warps, int run, bool narrow, int* width) {

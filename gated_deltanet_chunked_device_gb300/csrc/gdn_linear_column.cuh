@@ -394,7 +394,7 @@ struct ForwardShape {
         Group groups[Col::kGroups];
         float hand[Col::kHands][W];   // the state that enters a stage
         int32_t hand_reset[Col::kHands];
-        Product product[Col::kGroups][W];  // of the gates of a group's steps that learn
+        Product product[Col::kSegments ? Col::kGroups * Col::kWarps : 1][W];  // of the gates of a warp's steps that learn
         uint64_t full[kDepth];        // a stage's inputs have come
         uint64_t handed[Col::kHands];
         uint32_t ticket;
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         for (int i = 0; i < kGroups; ++i) sm.groups[i].kept_at = -1;
         if (Col::kSegments) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
-    if (Col::kSegments && threadIdx.x < kGroups * W) sm.product[threadIdx.x / W][threadIdx.x % W] = Product{1.f, 0};
+    if (Col::kSegments) sm.product[threadIdx.x / 32][lane] = Product{1.f, 0};
     __syncthreads();
     const uint32_t ticket = Col::kSegments ? sm.ticket : blockIdx.x;
     const int64_t part = Col::kSegments ? ticket / sp.blocks : 0;
@@ -652,6 +652,11 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             o[0] = make_float4(g.lo.x, B.lo.x, g.lo.y, B.lo.y);
             o[1] = make_float4(g.hi.x, B.hi.x, g.hi.y, B.hi.y);
         }
+        if (learn) {
+            __syncwarp();
+            Product& mine = sm.product[threadIdx.x / 32][lane];
+            mine = times(mine, gr.pairs[q / kGroups & 1][warp][lane].x);
+        }
         // The group's one barrier of a step.  Past it: every warp's pair is there and every thread has its inputs of this
         // stage, so its place in the ring is free; the bounds of the group's next stage are known.
         named_bar_sync(1 + group, 32 * kColWarps);
@@ -660,12 +665,6 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
 #pragma unroll
         for (int w = 0; w < kColWarps; ++w) ab[w] = gr.pairs[q / kGroups & 1][w][ch];
         const uint32_t resets = bd.warps_start;
-        if (learn && warp == 0) {  // before the wait, so that the next stage does not wait for it
-            float factors[kColWarps];
-#pragma unroll
-            for (int w = 0; w < kColWarps; ++w) factors[w] = ab[w].x;
-            sm.product[group][lane] = times(sm.product[group][lane], product_of(factors));
-        }
         // What the stage before hands on: the state (in steps that learn, from zero).
         float carry = 0.f;
         if (q > 0) {
@@ -685,8 +684,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
             if (learn && q == stages - 1) {  // the segment's pair goes on, the state that enters it comes
                 const bool lastpart = part == sp.nt - 1;
-                Product whole = sm.product[0][lane];
-                for (int i = 1; i < kGroups; ++i) whole = times(whole, sm.product[i][lane]);
+                Product whole{1.f, 0};
+                for (int i = 0; i < kGroups * kColWarps; ++i) whole = times(whole, sm.product[i][lane]);
                 whole = folded(whole);
                 if (!lastpart) {
                     if (lane < cols) {
@@ -697,7 +696,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                             sp.exponents[part * p.C + c] = whole.e;
                         }
                     }
-                    publish(flags + part, reset ? kKnown : kPair, lane);
+                    const bool scaled = __any_sync(0xffffffffu, whole.e != 0);
+                    publish(flags + part, reset ? kKnown : scaled ? kScaledPair : kPair, lane);
                 }
                 const float h = look_back<true>(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
                 if (!lastpart && !reset) {

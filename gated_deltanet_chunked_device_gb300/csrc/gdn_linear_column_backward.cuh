@@ -46,7 +46,7 @@ struct BackwardShape {
         Group groups[Col::kGroups];
         float hand[Col::kHands][W];   // the carry that enters a stage
         int32_t hand_reset[Col::kHands];
-        Product product[Col::kGroups][W];  // of the gates of a group's steps that learn
+        Product product[Col::kSegments ? Col::kGroups * Col::kWarps : 1][W];  // of the gates of a warp's steps that learn
         uint64_t full[kDepth];
         uint64_t handed[Col::kHands];
         uint32_t ticket;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         mbar_arrive(&sm.handed[0]);  // nothing is handed to stage 0: its place's first turn is over
         if (Col::kSegments) sm.ticket = atomicAdd(sp.ticket, 1u);
     }
-    if (Col::kSegments && threadIdx.x < kGroups * W) sm.product[threadIdx.x / W][threadIdx.x % W] = Product{1.f, 0};
+    if (Col::kSegments) sm.product[threadIdx.x / 32][lane] = Product{1.f, 0};
     __syncthreads();
     const uint32_t ticket = Col::kSegments ? sm.ticket : blockIdx.x;
     const int64_t part = Col::kSegments ? ticket / sp.blocks : 0;  // segments are counted from the right
@@ -318,6 +318,11 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         }
         // the state is the last run's
         if (kTileWarps > 1 && !learn && sub == kRuns - 1) *reinterpret_cast<float4*>(&gr.states[q / kGroups & 1][warp][l * 4]) = flat(B);
+        if (learn) {
+            __syncwarp();
+            Product& mine = sm.product[threadIdx.x / 32][lane];
+            mine = times(mine, gr.pairs[q / kGroups & 1][warp][lane].x);
+        }
         // The group's one barrier of a step.  Past it: every warp's pair is there, nobody of the group reads its stage before
         // any more (its place in the ring is free), and the bounds of the group's next stage are known.
         named_bar_sync(1 + group, 32 * kColWarps);
@@ -335,12 +340,6 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             enter_h = (bd.warps_start >> v) & 1 ? b : fmaf(gr.pairs[q / kGroups & 1][v][ch].x, enter_h, b);
         }
         fetch_saved(q + kGroups);
-        if (learn && warp == 0) {  // before the wait, so that the next stage does not wait for it
-            float factors[kColWarps];
-#pragma unroll
-            for (int w = 0; w < kColWarps; ++w) factors[w] = ae[w].x;
-            sm.product[group][lane] = times(sm.product[group][lane], product_of(factors));
-        }
         // What the stage to the right hands on: the carry (in steps that learn, from zero).
         const uint32_t resets = bd.warps_end;
         // (One group keeps it itself.)
@@ -364,8 +363,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
             uint32_t* flags = sp.flags + static_cast<int64_t>(blk) * sp.nt;
             if (learn && q == stages - 1) {  // the segment's pair goes on, the carry that enters it comes
                 const bool lastpart = part == sp.nt - 1;
-                Product whole = sm.product[0][lane];
-                for (int i = 1; i < kGroups; ++i) whole = times(whole, sm.product[i][lane]);
+                Product whole{1.f, 0};
+                for (int i = 0; i < kGroups * kColWarps; ++i) whole = times(whole, sm.product[i][lane]);
                 whole = folded(whole);
                 if (!lastpart) {
                     if (lane < cols) {
@@ -376,7 +375,8 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
                             sp.exponents[part * p.C + c] = whole.e;
                         }
                     }
-                    publish(flags + part, reset ? kKnown : kPair, lane);
+                    const bool scaled = __any_sync(0xffffffffu, whole.e != 0);
+                    publish(flags + part, reset ? kKnown : scaled ? kScaledPair : kPair, lane);
                 }
                 const float v = look_back<true>(p, sp, flags, part, lane < cols ? c : p.C, lane, [](int64_t k) { return k; });
                 if (!lastpart && !reset) {

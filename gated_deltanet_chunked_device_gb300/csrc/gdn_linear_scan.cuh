@@ -246,7 +246,7 @@ __device__ __forceinline__ void check_bounds(const LinearParams& p, int64_t f, i
 // What tiles, or time segments of columns, hand on, in the workspace.
 struct ScanSpace {
     uint32_t* ticket;              // next tile: tiles are taken in order, so whom one waits for has started
-    uint32_t* flags;               // [blocks][4 channel quarters of a block][nt] (columns: [blocks][nt]): kPair, then kKnown
+    uint32_t* flags;               // [blocks][4 channel quarters of a block][nt] (columns: [blocks][nt]): a pair, then kKnown
     float2* pairs;                 // [nt][C] (A, B)
     int32_t* exponents;            // [nt][C] columns: A is pairs' times 2^this
     float* known;                  // [nt][C] end states in the scan's direction
@@ -255,7 +255,7 @@ struct ScanSpace {
     long long wait_cycles;         // limit of a look-back; the others follow from it
 };
 
-constexpr uint32_t kPair = 1, kKnown = 2;
+constexpr uint32_t kPair = 1, kKnown = 2, kScaledPair = 3;  // a pair; an end state; a pair some of whose exponents are not 0
 
 __device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
     uint32_t v;
@@ -283,18 +283,11 @@ struct Product {
     int e;
 };
 
-// Of a few factors: their fractions are brought to [1/2, 1) each, so that none waits for another.  (What is not finite has no
-// exponent to speak of, and is not asked for it.)
-template <int kN>
-__device__ __forceinline__ Product product_of(const float (&a)[kN]) {
-    Product p{1.f, 0};
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-        int e;
-        p.m *= frexpf(a[i], &e);
-        p.e += e;
-    }
-    return p;
+// (What is not finite has no exponent to speak of, and is not asked for it.)
+__device__ __forceinline__ Product times(Product p, float a) {
+    int e;
+    const float f = frexpf(p.m * a, &e);
+    return {f, p.e + e};
 }
 __device__ __forceinline__ Product times(Product p, Product q) {
     int e;
@@ -307,8 +300,7 @@ __device__ __forceinline__ Product folded(Product p) {
     return isfinite(p.m) && p.e >= -125 && p.e <= 127 ? Product{ldexpf(p.m, p.e), 0} : p;
 }
 
-// h through a time segment, fmaf(A, h, b) with one rounding whatever the exponent (76 segments of 64 channels, 32768
-// tokens: 26 us, without the first two lines 28).
+// h through a time segment, fmaf(A, h, b) with one rounding whatever the exponent.
 __device__ __forceinline__ float pass_on(Product a, float h, float b) {
     if (a.e == 0 || !isfinite(a.m) || !isfinite(h)) return pass_on(a.m, h, b);
     if (a.e < -300) return b;  // less than half of the least number, for any h
@@ -319,17 +311,32 @@ __device__ __forceinline__ float pass_on(Product a, float h, float b) {
     return fmaf(ldexpf(a.m, half), ldexpf(f, sum - half), b);
 }
 
-// The pair of place `row` of the scan, and h through it.
-template <bool kSegments>
-__device__ __forceinline__ auto load_pair(const ScanSpace& s, int64_t row, int C, int c) {
-    const float2 ab = __ldcg(s.pairs + row * C + c);
-    if constexpr (kSegments)
-        return make_float4(ab.x, ab.y, __int_as_float(__ldcg(s.exponents + row * C + c)), 0.f);
-    else
-        return ab;
+// h through the pairs of `n` places, the last of which is f - 1, in token order.  kScaled: with their exponents.
+template <bool kScaled, class At>
+__device__ __forceinline__ float through_pairs(const ScanSpace& s, int64_t f, int n, float h, int C, int c, At at) {
+    auto load = [&](int d, float2& ab, int& e) {
+        const int64_t i = at(f - 1 - d) * C + c;
+        ab = __ldcg(s.pairs + i);
+        e = kScaled ? __ldcg(s.exponents + i) : 0;
+    };
+    auto pass = [&](float2 ab, int e) { h = kScaled ? pass_on(Product{ab.x, e}, h, ab.y) : pass_on(ab.x, h, ab.y); };
+    int d = n - 1;
+    for (; d >= 3; d -= 4) {
+        float2 ab[4];
+        int e[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load(d - j, ab[j], e[j]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pass(ab[j], e[j]);
+    }
+    for (; d >= 0; --d) {
+        float2 ab;
+        int e;
+        load(d, ab, e);
+        pass(ab, e);
+    }
+    return h;
 }
-__device__ __forceinline__ float through_pair(float2 ab, float h) { return pass_on(ab.x, h, ab.y); }
-__device__ __forceinline__ float through_pair(float4 ab, float h) { return pass_on(Product{ab.x, __float_as_int(ab.z)}, h, ab.y); }
 
 // The state that enters place `f` of the scan (f >= 1) for channel c, by one warp for 32 channels: from the nearest
 // place whose end state is known, through the pairs of the places after it.  Places are numbered in the scan's
@@ -341,10 +348,12 @@ __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpac
     const bool on = c < p.C;
     const long long t0 = clock64();
     int dist;
+    uint32_t scaled;
     while (true) {
         const int64_t k = f - 1 - lane;
         const uint32_t flag = k >= 0 ? load_acquire(flags + k) : kKnown;
         const uint32_t known = __ballot_sync(0xffffffffu, flag == kKnown), any = __ballot_sync(0xffffffffu, flag != 0);
+        scaled = __ballot_sync(0xffffffffu, flag == kScaledPair);
         dist = known ? __ffs(known) - 1 : 32;
         // all nearer places have their pairs
         if (dist < 32 && (~any & ((1u << dist) - 1)) == 0) break;
@@ -356,16 +365,8 @@ __device__ __forceinline__ float look_back(const LinearParams& p, const ScanSpac
     __syncwarp();
     if (!on) return 0.f;
     float h = __ldcg(s.known + at(f - 1 - dist) * p.C + c);
-    int d = dist - 1;
-    for (; d >= 3; d -= 4) {
-        decltype(load_pair<kSegments>(s, 0, 0, 0)) ab[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) ab[j] = load_pair<kSegments>(s, at(f - 1 - d + j), p.C, c);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h = through_pair(ab[j], h);
-    }
-    for (; d >= 0; --d) h = through_pair(load_pair<kSegments>(s, at(f - 1 - d), p.C, c), h);
-    return h;
+    if (kSegments && scaled & ((1u << dist) - 1)) return through_pairs<true>(s, f, dist, h, p.C, c, at);
+    return through_pairs<false>(s, f, dist, h, p.C, c, at);
 }
 
 struct ForwardSmem {
