@@ -516,9 +516,9 @@ __global__ void __launch_bounds__(Col::kThreads, 1)
         }
         const bool write = q >= steps - stages, last = t1 == p.T;
         auto empty = [&](int64_t i) {  // an empty sequence's final state is its initial one
-            if (!write || !p.output_state || p.output_state == p.initial_state) return;
-            const int64_t row = state_row(p, i);
-            if (row < 0 || lane * 4 >= cols) return;
+            if (!write) return;
+            const int64_t row = state_row(p, i);  // looked at, and reported, whether or not there is anything to copy
+            if (row < 0 || !p.output_state || p.output_state == p.initial_state || lane * 4 >= cols) return;
             const int64_t off = row * p.state_stride + c0 + lane * 4;
             state_quad_store(p.output_state, off, p.state_dt,
                              p.initial_state ? state_quad_load(p.initial_state, off, p.state_dt) : make_float4(0.f, 0.f, 0.f, 0.f));

@@ -429,9 +429,8 @@ __global__ void __launch_bounds__(kThreads) gdn_linear_forward_kernel(const Line
     if (warp == 0) {
         find_bounds(p, t0, t1, last, lane, sm.bounds, [&](int64_t i) {
             // an empty sequence's final state is its initial one
-            if (!p.output_state || (p.output_state == p.initial_state)) return;
-            const int64_t row = state_row(p, i);
-            if (row < 0 || !on) return;
+            const int64_t row = state_row(p, i);  // looked at, and reported, whether or not there is anything to copy
+            if (row < 0 || !p.output_state || p.output_state == p.initial_state || !on) return;
             float v[4] = {0.f, 0.f, 0.f, 0.f};
             if (p.initial_state) state_load<kVec>(p.initial_state, row * p.state_stride + c0, p.state_dt, lane, cols, v);
             state_store<kVec>(p.output_state, row * p.state_stride + c0, p.state_dt, lane, cols, v);
