@@ -138,6 +138,7 @@ def lib():
                 L.gdn_status_string.restype = ctypes.c_char_p
                 linear._register(L)
                 pages._register(L)
+                attention._register(L)
                 _lib = L
     return _lib
 
@@ -545,7 +546,9 @@ def read_chunk_map(plan: _Plan, ws: torch.Tensor, num_seqs: int):
 
 
 from . import linear, pages  # noqa: E402 - they need the names above
+from . import attention  # noqa: E402
 from .linear import *  # noqa: E402,F401,F403
 from .pages import *  # noqa: E402,F401,F403
+from .attention import *  # noqa: E402,F401,F403
 
-__all__ += linear.__all__ + pages.__all__
+__all__ += linear.__all__ + pages.__all__ + attention.__all__

@@ -1,0 +1,465 @@
+// gdn_attention.cu -- attention over a paged cache (include/gdn_attention.h):
+// host side, the kernel on CUDA cores, and the join of units that were cut.
+#include "gdn_attention.cuh"
+
+namespace gdn {
+namespace {
+
+// ------------------------------------------------------------------------------------------------ CUDA cores
+// Every type, head size and layout: 64 rows of a unit against tiles of 64 keys, all of it fp32, one pass with a running maximum
+// and sum for each row.  256 threads as 16 x 16: a thread has 4 rows by 4 keys of the scores (keys tx + 16 c) and 4 rows by 4 x kCols
+// channels of the result (channels 4 tx + 64 c).
+constexpr int kRows = 64, kKeys = 64, kThreads = 256;
+
+__device__ __forceinline__ float wide(float x) { return x; }
+__device__ __forceinline__ float wide(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float wide(__half x) { return __half2float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void put(__half* p, float x) { *p = __float2half_rn(x); }
+
+template <class E, int V>
+struct alignas(sizeof(E) * V) Vec {
+    E e[V];
+};
+
+// Floats from row to row in shared memory: a multiple of 4 that is 4 more than one of 32, so that 16-byte accesses of successive
+// rows fall into different banks.
+__host__ __device__ inline int row_floats(int D) { return (D + 3) / 4 * 4 % 32 == 4 ? (D + 3) / 4 * 4 : (D + 31) / 32 * 32 + 4; }
+
+size_t simple_smem(int D) { return sizeof(float) * (3 * kRows * row_floats(D) + kRows * (kKeys + 4)) + kKeys * 2 * sizeof(int64_t); }
+
+template <class E, int kVec, int kCols>
+__global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid_constant__ AttnParams p) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ AttnScan<kThreads> scan;
+    const int D = p.c.head_dim, D4 = (D + 3) / 4 * 4, S = row_floats(D);
+    float* q_s = reinterpret_cast<float*>(smem);
+    float* k_s = q_s + kRows * S;
+    float* v_s = k_s + kKeys * S;
+    float* w_s = v_s + kKeys * S;                                          // [kRows][kKeys + 4]
+    int64_t* off_s = reinterpret_cast<int64_t*>(w_s + kRows * (kKeys + 4)); // offset of a key's row of k and of v; -1: no page
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int32_t block = blockIdx.x;
+    if (tid == 0) p.joins[2 * block] = make_int4(0, 0, 0, 0);
+    AttnWalk walk;
+    walk.begin(attn_start<kThreads>(p, block, gridDim.x, scan));
+    AttnPart a;
+    uint32_t err = 0;
+    while (walk.next(p, a)) {
+        const int rows = a.tokens * a.heads;
+        __syncthreads();
+        for (int i = tid; i < kRows * D4; i += kThreads) {
+            const int r = i / D4, d = i - r * D4;
+            float x = 0.f;
+            if (r < rows && d < D) {
+                const int t = r / a.heads, g = r - t * a.heads;
+                x = wide(static_cast<const E*>(p.q)[(a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D + d]);
+            }
+            q_s[r * S + d] = x;
+        }
+        // each row's keys: [lo, hi)
+        int32_t lo[4], hi[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            const int64_t pos = static_cast<int64_t>(a.pos0) + r / a.heads;
+            hi[i] = r < rows ? (p.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys) : 0;
+            lo[i] = p.window ? static_cast<int32_t>(max(pos - p.window + 1, int64_t{0})) : 0;
+        }
+        float m[4], l[4], acc[4][4 * kCols];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4 * kCols; ++c) acc[i][c] = 0.f;
+        }
+        for (int32_t tile = a.tile0; tile < a.tile1; ++tile) {
+            const int64_t key0 = static_cast<int64_t>(tile) * kKeys;
+            if (tid < kKeys) {
+                const int64_t key = key0 + tid;
+                int64_t ko = -1, vo = -1;
+                if (key < a.keys) {
+                    const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + key / p.b.page_tokens];
+                    if (page < 0 || page >= p.b.n_pages) {
+                        err |= GDN_PAGES_ERR_PAGE;
+                    } else {
+                        const int64_t slot = key % p.b.page_tokens;
+                        ko = page * p.c.k_page_stride + slot * p.c.k_token_stride + a.kv_head * p.c.k_head_stride;
+                        vo = page * p.c.v_page_stride + slot * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
+                    }
+                }
+                off_s[2 * tid] = ko;
+                off_s[2 * tid + 1] = vo;
+            }
+            __syncthreads();
+            const int pieces = D4 / kVec;  // with kVec = 4, D is a multiple of 4
+            for (int i = tid; i < kKeys * pieces; i += kThreads) {
+                const int r = i / pieces, d = (i - r * pieces) * kVec;
+                const int64_t ko = off_s[2 * r], vo = off_s[2 * r + 1];
+                Vec<E, kVec> k{}, v{};
+                if (ko >= 0 && d < D) {
+                    k = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.k) + ko + d);
+                    v = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.v) + vo + d);
+                }
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    k_s[r * S + d + j] = ko >= 0 && d < D ? wide(k.e[j]) : 0.f;
+                    v_s[r * S + d + j] = ko >= 0 && d < D ? wide(v.e[j]) : 0.f;
+                }
+            }
+            __syncthreads();
+            if (4 * (ty & ~1) < rows) {  // by whole warps: they shuffle
+                float s[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+                for (int d = 0; d < D4; d += 4) {
+                    float4 x[4], y[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(q_s + (4 * ty + i) * S + d);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) y[c] = *reinterpret_cast<const float4*>(k_s + (tx + 16 * c) * S + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            s[i][c] = fmaf(x[i].x, y[c].x, s[i][c]);
+                            s[i][c] = fmaf(x[i].y, y[c].y, s[i][c]);
+                            s[i][c] = fmaf(x[i].z, y[c].z, s[i][c]);
+                            s[i][c] = fmaf(x[i].w, y[c].w, s[i][c]);
+                        }
+                }
+                bool cut = false;  // some of the tile's keys are hidden from some of this thread's rows
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int64_t key = key0 + tx + 16 * c;
+                    const bool there = off_s[2 * (tx + 16 * c)] >= 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool seen = there && key >= lo[i] && key < hi[i];
+                        s[i][c] = seen ? s[i][c] * p.scale_log2 : -INFINITY;
+                        cut |= !seen;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float top = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+                    for (int d = 8; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+                    const float now = fmaxf(m[i], top), base = now == -INFINITY ? 0.f : now;
+                    const float keep = exp2f(m[i] - base);
+                    float sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const float w = exp2f(s[i][c] - base);
+                        sum += w;
+                        w_s[(4 * ty + i) * (kKeys + 4) + tx + 16 * c] = w;
+                    }
+                    for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
+                    m[i] = now;
+                    l[i] = l[i] * keep + sum;
+#pragma unroll
+                    for (int c = 0; c < 4 * kCols; ++c) acc[i][c] *= keep;
+                }
+                cut = __any_sync(~0u, cut);
+                __syncwarp();
+                if (!cut) {
+                    for (int k = 0; k < kKeys; k += 4) {
+                        float4 w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(w_s + (4 * ty + i) * (kKeys + 4) + k);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int c = 0; c < kCols; ++c) {
+                                if (4 * tx + 64 * c >= D4) break;
+                                const float4 v = *reinterpret_cast<const float4*>(v_s + (k + j) * S + 4 * tx + 64 * c);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float u = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
+                                    acc[i][4 * c] = fmaf(u, v.x, acc[i][4 * c]);
+                                    acc[i][4 * c + 1] = fmaf(u, v.y, acc[i][4 * c + 1]);
+                                    acc[i][4 * c + 2] = fmaf(u, v.z, acc[i][4 * c + 2]);
+                                    acc[i][4 * c + 3] = fmaf(u, v.w, acc[i][4 * c + 3]);
+                                }
+                            }
+                    }
+                } else {  // a hidden key's value is left out, not taken times zero: it may be infinite or NaN
+                    for (int k = 0; k < kKeys; ++k) {
+                        const int64_t key = key0 + k;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if (key < lo[i] || key >= hi[i]) continue;
+                            const float u = w_s[(4 * ty + i) * (kKeys + 4) + k];
+#pragma unroll
+                            for (int c = 0; c < kCols; ++c) {
+                                if (4 * tx + 64 * c >= D4) break;
+                                const float4 v = *reinterpret_cast<const float4*>(v_s + k * S + 4 * tx + 64 * c);
+                                acc[i][4 * c] = fmaf(u, v.x, acc[i][4 * c]);
+                                acc[i][4 * c + 1] = fmaf(u, v.y, acc[i][4 * c + 1]);
+                                acc[i][4 * c + 2] = fmaf(u, v.z, acc[i][4 * c + 2]);
+                                acc[i][4 * c + 3] = fmaf(u, v.w, acc[i][4 * c + 3]);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        const bool whole = a.tile0 == a.first && a.tile1 == a.last;
+        const int32_t slot = attn_slot(a, block);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * ty + i;
+            if (r >= rows) continue;
+            const int t = r / a.heads, g = r - t * a.heads;
+            if (whole) {
+                E* o = static_cast<E*>(p.o) + (a.row0 + t) * p.o_stride + static_cast<int64_t>(a.head0 + g) * D;
+                const float by = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+                for (int c = 0; c < 4 * kCols; ++c) {
+                    const int d = 4 * tx + 64 * (c / 4) + c % 4;
+                    if (d < D) put(o + d, acc[i][c] * by);
+                }
+                if (p.lse && tx == 0)
+                    p.lse[(a.row0 + t) * p.heads + a.head0 + g] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * 0.69314718055994531f;
+            } else {
+                const int64_t at = static_cast<int64_t>(slot) * (p.unit_tokens * p.group) + r;
+#pragma unroll
+                for (int c = 0; c < 4 * kCols; ++c) {
+                    const int d = 4 * tx + 64 * (c / 4) + c % 4;
+                    if (d < D) p.part_o[at * D + d] = acc[i][c];
+                }
+                if (tx == 0) p.part_ml[at] = make_float2(m[i], l[i]);
+            }
+        }
+        if (tid == 0 && a.tile0 == a.first && a.tile1 < a.last) attn_note_join(p, a, block, walk.at.share);
+    }
+    kv_report(p.b.device_status, err);
+}
+
+template <class E, int kVec, int kCols>
+cudaError_t launch_simple(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
+    const size_t smem = simple_smem(p.c.head_dim);
+    auto kernel = attention_simple_kernel<E, kVec, kCols>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kThreads, smem, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t launch_simple_typed(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
+    const int64_t strides[] = {p.c.k_page_stride, p.c.k_token_stride, p.c.k_head_stride,
+                               p.c.v_page_stride, p.c.v_token_stride, p.c.v_head_stride, p.c.head_dim};
+    bool vec = reinterpret_cast<uintptr_t>(p.c.k) % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(p.c.v) % (4 * sizeof(E)) == 0;
+    for (int64_t s : strides) vec = vec && s % 4 == 0;
+    const int D = p.c.head_dim;
+    if (D <= 64) return vec ? launch_simple<E, 4, 1>(p, blocks, stream) : launch_simple<E, 1, 1>(p, blocks, stream);
+    if (D <= 128) return vec ? launch_simple<E, 4, 2>(p, blocks, stream) : launch_simple<E, 1, 2>(p, blocks, stream);
+    return vec ? launch_simple<E, 4, 4>(p, blocks, stream) : launch_simple<E, 1, 4>(p, blocks, stream);
+}
+
+// ------------------------------------------------------------------------------------------------ the join
+// A warp a row: the parts' results, each with its own maximum, weighted to the largest one, in the parts' order.
+constexpr int kJoinWarps = 8;
+
+template <class E>
+__global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnParams p) {
+    const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), block = blockIdx.x;
+    const int4 head = p.joins[2 * block];
+    if (head.x == 0 || r >= head.y * head.w) return;
+    const int4 first = p.joins[2 * block + 1];
+    const int64_t row0 = (static_cast<int64_t>(first.y) << 32) | static_cast<uint32_t>(first.x);
+    const int parts = head.x, D = p.c.head_dim;
+    const int64_t rows = p.unit_tokens * p.group;
+    // the unit's first part is in this block's odd slot, the others in the even ones of the blocks after it
+    auto place = [&](int k) { return (k == 0 ? 2 * static_cast<int64_t>(block) + 1 : 2 * (static_cast<int64_t>(block) + k)) * rows + r; };
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_ml[place(k)].x);
+    for (int d = 16; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, acc[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+        const int64_t at = place(k);
+        const float2 ml = p.part_ml[at];
+        const float by = exp2f(ml.x - base);
+        sum = fmaf(ml.y, by, sum);
+        if (by == 0.f) continue;  // a part that sees nothing adds nothing
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int d = lane + 32 * c;
+            if (d < D) acc[c] = fmaf(p.part_o[at * D + d], by, acc[c]);
+        }
+    }
+    const int t = r / head.w, g = r - t * head.w;
+    E* o = static_cast<E*>(p.o) + (row0 + t) * p.o_stride + static_cast<int64_t>(head.z + g) * D;
+    const float by = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int d = lane + 32 * c;
+        if (d < D) put(o + d, acc[c] * by);
+    }
+    if (p.lse && lane == 0)
+        p.lse[(row0 + t) * p.heads + head.z + g] = sum == 0.f ? -INFINITY : (base + log2f(sum)) * 0.69314718055994531f;
+}
+
+// ------------------------------------------------------------------------------------------------ host side
+bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
+
+// Pages, tokens and heads of rows of D elements that do not overlap: from the smallest stride on, each has to pass the span of the
+// smaller ones.
+bool apart(int64_t pages, int64_t page_stride, int64_t tokens, int64_t token_stride, int64_t heads, int64_t head_stride, int64_t D) {
+    int64_t n[3] = {pages, tokens, heads}, s[3] = {page_stride, token_stride, head_stride};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (s[j] < s[i]) {
+                int64_t t = s[i];
+                s[i] = s[j], s[j] = t;
+                t = n[i];
+                n[i] = n[j], n[j] = t;
+            }
+    int64_t span = D;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (s[i] < span) return false;
+        int64_t more;
+        if (__builtin_mul_overflow(n[i] - 1, s[i], &more) || __builtin_add_overflow(span, more, &span) || span > (1LL << 56)) return false;
+    }
+    return true;
+}
+
+struct Route {
+    AttnParams p;
+    int32_t blocks, rows;
+};
+
+gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, const gdn_attention_args* args, Route* out) {
+    const gdn_status st = kv_check(batch, cache);
+    if (st != GDN_OK) return st;
+    if (!args) return GDN_ERR_INVALID_ARG;
+    gdn_attention_args a = *args;
+    const gdn_kv_cache& c = *cache;
+    if (a.heads < 1 || a.heads % c.kv_heads || a.window < 0 || !(a.scale == a.scale) || a.scale - a.scale != 0.f) return GDN_ERR_INVALID_ARG;
+    if (c.head_dim > GDN_ATTENTION_MAX_DIM || static_cast<int64_t>(a.heads) * c.head_dim > (1 << 20)) return GDN_ERR_UNSUPPORTED;
+    const int64_t row = static_cast<int64_t>(a.heads) * c.head_dim;
+    if (a.q_stride == 0) a.q_stride = row;
+    if (a.output_stride == 0) a.output_stride = row;
+    if (batch->total_tokens > 0 && (!a.q || !a.output || !aligned(a.q, dtype_bytes(c.dtype)) || !aligned(a.output, dtype_bytes(c.dtype)) ||
+                                    a.q_stride < row || a.output_stride < row))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned(a.lse, 4)) return GDN_ERR_INVALID_ARG;
+    Route r{};
+    AttnParams& p = r.p;
+    p.b = *batch;
+    p.c = c;
+    p.q = a.q;
+    p.o = a.output;
+    p.lse = a.lse;
+    p.q_stride = a.q_stride;
+    p.o_stride = a.output_stride;
+    p.heads = a.heads;
+    p.per_kv = a.heads / c.kv_heads;
+    p.causal = a.causal != 0;
+    p.window = a.window;
+    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.pieces = (p.per_kv + kRows - 1) / kRows;
+    p.group = (p.per_kv + p.pieces - 1) / p.pieces;
+    p.unit_tokens = kRows / p.group;
+    p.tile = kKeys;
+    p.min_steps = 2;
+    r.rows = p.unit_tokens * p.group;
+    r.blocks = multiprocessors() * (simple_smem(c.head_dim) <= 110 * 1024 ? 2 : 1);
+    *out = r;
+    return GDN_OK;
+}
+
+size_t up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+gdn_status kv_check(const gdn_kv_batch* batch, const gdn_kv_cache* cache) {
+    if (!batch || !cache) return GDN_ERR_INVALID_ARG;
+    const gdn_kv_batch& b = *batch;
+    const gdn_kv_cache& c = *cache;
+    if (b.num_seqs < 0 || b.total_tokens < 0 || b.max_seqs < 0 || b.max_pages < 0 || b.n_pages < 0 || b.page_tokens < 1)
+        return GDN_ERR_INVALID_ARG;
+    if (b.total_tokens > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (c.kv_heads < 1 || c.head_dim < 1) return GDN_ERR_INVALID_ARG;
+    if (c.dtype != GDN_DTYPE_F32 && c.dtype != GDN_DTYPE_BF16 && c.dtype != GDN_DTYPE_F16) return GDN_ERR_UNSUPPORTED;
+    if (!b.cu_seqlens && (b.tokens_per_seq < 1 || static_cast<int64_t>(b.num_seqs) * b.tokens_per_seq != b.total_tokens))
+        return GDN_ERR_INVALID_ARG;
+    if (!b.seqs && b.num_seqs > b.max_seqs) return GDN_ERR_INVALID_ARG;
+    if (b.num_seqs > 0) {
+        if (!b.lengths || (!b.table && b.max_pages > 0) || (b.n_pages > 0 && (!c.k || !c.v))) return GDN_ERR_INVALID_ARG;
+        if (!aligned(b.lengths, 4) || !aligned(b.table, 4) || !aligned(b.seqs, 4) || !aligned(b.cu_seqlens, b.cu_i64 ? 8 : 4) ||
+            !aligned(b.device_status, 4) || !aligned(c.k, dtype_bytes(c.dtype)) || !aligned(c.v, dtype_bytes(c.dtype)))
+            return GDN_ERR_INVALID_ARG;
+    }
+    if (!apart(b.n_pages, c.k_page_stride, b.page_tokens, c.k_token_stride, c.kv_heads, c.k_head_stride, c.head_dim) ||
+        !apart(b.n_pages, c.v_page_stride, b.page_tokens, c.v_token_stride, c.kv_heads, c.v_head_stride, c.head_dim))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+size_t attn_workspace(int32_t blocks, int32_t rows, int32_t D) {
+    const size_t slots = 2 * static_cast<size_t>(blocks);
+    return up(slots * sizeof(int4)) + up(slots * rows * sizeof(float2)) + up(slots * rows * D * sizeof(float));
+}
+
+void attn_place(AttnParams* p, void* workspace, int32_t blocks, int32_t rows) {
+    const size_t slots = 2 * static_cast<size_t>(blocks);
+    uint8_t* w = static_cast<uint8_t*>(workspace);
+    p->joins = reinterpret_cast<int4*>(w);
+    w += up(slots * sizeof(int4));
+    p->part_ml = reinterpret_cast<float2*>(w);
+    w += up(slots * rows * sizeof(float2));
+    p->part_o = reinterpret_cast<float*>(w);
+}
+
+cudaError_t launch_attention_simple(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
+    if (p.c.dtype == GDN_DTYPE_F32) return launch_simple_typed<float>(p, blocks, stream);
+    if (p.c.dtype == GDN_DTYPE_BF16) return launch_simple_typed<__nv_bfloat16>(p, blocks, stream);
+    return launch_simple_typed<__half>(p, blocks, stream);
+}
+
+cudaError_t launch_attention_join(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
+    const dim3 grid(blocks, (p.unit_tokens * p.group + kJoinWarps - 1) / kJoinWarps);
+    if (p.c.dtype == GDN_DTYPE_F32)
+        attention_join_kernel<float><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
+    else if (p.c.dtype == GDN_DTYPE_BF16)
+        attention_join_kernel<__nv_bfloat16><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
+    else
+        attention_join_kernel<__half><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace gdn
+
+extern "C" {
+
+size_t gdn_attention_workspace(const gdn_kv_batch* batch, const gdn_kv_cache* cache, const gdn_attention_args* args) {
+    gdn::Route r;
+    if (gdn::make_route(batch, cache, args, &r) != GDN_OK || batch->total_tokens == 0 || batch->num_seqs == 0) return 0;
+    return gdn::attn_workspace(r.blocks, r.rows, r.p.c.head_dim);
+}
+
+gdn_status gdn_attention_run(const gdn_kv_batch* batch, const gdn_kv_cache* cache, const gdn_attention_args* args, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+    gdn::Route r;
+    const gdn_status st = gdn::make_route(batch, cache, args, &r);
+    if (st != GDN_OK) return st;
+    if (batch->total_tokens == 0 || batch->num_seqs == 0) return GDN_OK;
+    if (!workspace || !gdn::aligned(workspace, 16) || workspace_bytes < gdn::attn_workspace(r.blocks, r.rows, r.p.c.head_dim))
+        return GDN_ERR_INVALID_ARG;
+    gdn::attn_place(&r.p, workspace, r.blocks, r.rows);
+    cudaError_t e = gdn::launch_attention_simple(r.p, r.blocks, static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) e = gdn::launch_attention_join(r.p, r.blocks, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // extern "C"
