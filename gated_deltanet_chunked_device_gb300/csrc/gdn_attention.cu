@@ -1,6 +1,9 @@
 // gdn_attention.cu -- attention over a paged cache (include/gdn_attention.h):
 // host side, the kernel on CUDA cores, and the join of units that were cut.
-#include "gdn_attention.cuh"
+#include <cmath>
+#include <cudaTypedefs.h>
+
+#include "gdn_attention_tc.cuh"
 
 namespace gdn {
 namespace {
@@ -335,8 +338,95 @@ bool apart(int64_t pages, int64_t page_stride, int64_t tokens, int64_t token_str
 
 struct Route {
     AttnParams p;
+    attn_tc::TcParams tc;          // streams > 0
     int32_t blocks, rows;
+    int32_t streams;               // row tiles of the tensor core kernel; 0: CUDA cores
 };
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ok ? f : nullptr);
+    }();
+    return fn;
+}
+
+// A map of 16-bit elements for boxes of 64 channels, swizzled in rows of 128 bytes; what lies outside reads as zeros.  strides:
+// elements of all dimensions but the first.
+bool encode(CUtensorMap* map, const void* base, gdn_dtype dtype, int rank, const int64_t* dims, const int64_t* strides, const int32_t* box) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t n[4], s[3];
+    cuuint32_t b[4], es[4] = {1, 1, 1, 1};
+    for (int i = 0; i < rank; ++i) {
+        n[i] = static_cast<cuuint64_t>(dims[i]);
+        b[i] = static_cast<cuuint32_t>(box[i]);
+        // a dimension of one has no step, and its stride may be anything
+        if (i > 0) s[i - 1] = static_cast<cuuint64_t>(dims[i] > 1 ? strides[i - 1] * 2 : (dims[0] + 7) / 8 * 16);
+    }
+    return enc(map, dtype == GDN_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), n,
+               s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether the tensor cores can take a call: 16-bit types whose rows tiled copies can fetch (addresses and strides of 16 bytes, below
+// 2^40), pages of boxes of at least 8 tokens (the swizzle's period).
+bool tc_fits(const AttnParams& p) {
+    const gdn_kv_cache& c = p.c;
+    if (c.dtype == GDN_DTYPE_F32 || p.b.n_pages < 1 || p.b.page_tokens % 8 || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(p.q, 16))
+        return false;
+    auto fits = [](int64_t n, int64_t stride) { return n <= 1 || (stride % 8 == 0 && stride < (1LL << 39)); };
+    return fits(p.b.n_pages, c.k_page_stride) && fits(p.b.page_tokens, c.k_token_stride) && fits(c.kv_heads, c.k_head_stride) &&
+           fits(p.b.n_pages, c.v_page_stride) && fits(p.b.page_tokens, c.v_token_stride) && fits(c.kv_heads, c.v_head_stride) &&
+           fits(p.b.total_tokens, p.q_stride) && fits(p.heads, c.head_dim);
+}
+
+// The tensor cores' shape.  Two row tiles a unit pay where a sequence has, on the average, rows for more than one.
+void tc_route(Route* r) {
+    AttnParams& p = r->p;
+    const int D = p.c.head_dim, rows = attn_tc::kRowTile;
+    p.pieces = (p.per_kv + rows - 1) / rows;
+    p.group = (p.per_kv + p.pieces - 1) / p.pieces;
+    r->streams = D <= 128 && p.b.total_tokens * p.per_kv > static_cast<int64_t>(p.b.num_seqs) * rows ? 2 : 1;
+    p.tile = 128;
+    attn_tc::TcParams& t = r->tc;
+    t.row_tokens = rows / p.group;
+    p.unit_tokens = r->streams * t.row_tokens;
+    t.box_keys = p.tile;
+    while (p.b.page_tokens % t.box_keys) t.box_keys /= 2;
+    t.boxes = p.tile / t.box_keys;
+    // Heads of more than 128 channels run as 256: what lies behind them reads as zeros.
+    t.k_steps = D > 128 ? 8 : (D + 15) / 16;
+    const bool f16 = p.c.dtype == GDN_DTYPE_F16;
+    t.idesc_qk = idesc_16bit_f32(rows, p.tile, false, false, p.scale_log2 < 0.f, f16);
+    t.idesc_pv = idesc_16bit_f32(rows, 16 * t.k_steps, false, true, false, f16);
+    // Scores of keys that are not seen are -infinity, which has to survive the scaling: zero becomes a scale that any finite score vanishes in.
+    t.scale_log2 = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    t.out_vec = D % 8 == 0 && p.o_stride % 8 == 0 && aligned(p.o, 16);
+    r->blocks = multiprocessors();
+    r->rows = p.unit_tokens * p.group;
+    t.a = p;
+}
+
+cudaError_t launch_tc(const Route& r, cudaStream_t stream) {
+    const AttnParams& p = r.p;
+    const gdn_kv_cache& c = p.c;
+    CUtensorMap maps[3];
+    const int64_t q_dims[3] = {c.head_dim, p.heads, p.b.total_tokens}, q_strides[2] = {c.head_dim, p.q_stride};
+    const int32_t q_box[3] = {64, p.group, r.tc.row_tokens}, kv_box[4] = {64, r.tc.box_keys, 1, 1};
+    const int64_t kv_dims[4] = {c.head_dim, p.b.page_tokens, c.kv_heads, p.b.n_pages};
+    const int64_t k_strides[3] = {c.k_token_stride, c.k_head_stride, c.k_page_stride}, v_strides[3] = {c.v_token_stride, c.v_head_stride, c.v_page_stride};
+    if (!encode(maps, p.q, c.dtype, 3, q_dims, q_strides, q_box) || !encode(maps + 1, c.k, c.dtype, 4, kv_dims, k_strides, kv_box) ||
+        !encode(maps + 2, c.v, c.dtype, 4, kv_dims, v_strides, kv_box))
+        return cudaErrorInvalidValue;
+    attn_tc::TcParams t = r.tc;
+    t.a = p;
+    return c.dtype == GDN_DTYPE_BF16 ? launch_attention_tc_bf16(t, maps, r.streams, r.blocks, stream)
+                                     : launch_attention_tc_f16(t, maps, r.streams, r.blocks, stream);
+}
 
 gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, const gdn_attention_args* args, Route* out) {
     const gdn_status st = kv_check(batch, cache);
@@ -374,6 +464,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
     r.blocks = multiprocessors() * (simple_smem(c.head_dim) <= 110 * 1024 ? 2 : 1);
+    if (tc_fits(p)) tc_route(&r);
     *out = r;
     return GDN_OK;
 }
@@ -457,8 +548,9 @@ gdn_status gdn_attention_run(const gdn_kv_batch* batch, const gdn_kv_cache* cach
     if (!workspace || !gdn::aligned(workspace, 16) || workspace_bytes < gdn::attn_workspace(r.blocks, r.rows, r.p.c.head_dim))
         return GDN_ERR_INVALID_ARG;
     gdn::attn_place(&r.p, workspace, r.blocks, r.rows);
-    cudaError_t e = gdn::launch_attention_simple(r.p, r.blocks, static_cast<cudaStream_t>(stream));
-    if (e == cudaSuccess) e = gdn::launch_attention_join(r.p, r.blocks, static_cast<cudaStream_t>(stream));
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = r.streams ? gdn::launch_tc(r, s) : gdn::launch_attention_simple(r.p, r.blocks, s);
+    if (e == cudaSuccess) e = gdn::launch_attention_join(r.p, r.blocks, s);
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 

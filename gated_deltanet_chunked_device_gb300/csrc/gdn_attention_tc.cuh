@@ -1,0 +1,744 @@
+// gdn_attention_tc.cuh -- attention over a paged cache on the tensor cores (bf16 and fp16).
+//
+// A unit's rows (token, head of the group) are the 128 rows of tcgen05 products; grouped heads and speculated tokens fill them
+// where tokens alone would not.  Keys and values come by tiled copies, a box a page (or piece of one), straight from the caller's
+// cache in any strides; what lies outside a page, a head or the cache reads as zeros.  Per tile of keys:
+//
+//     S = Q K^T               fp32 in TMEM
+//     P = exp2(S - m)         a thread a row, from TMEM to registers and back as 16-bit pairs over S
+//     O += P V                P from TMEM, O fp32 in TMEM
+//
+// m is the row's running maximum, raised (and O and the sum l scaled down) only when it has grown by more than 2^8: P stays
+// below 2^8 (fp16: 2^15, from an offset of 2^7 that lifts small weights out of fp16's subnormals), and any m gives the same
+// quotient.  P is rounded to 16 bits for the product, relative to itself; l sums the unrounded weights in fp32.
+//
+// Two shapes.  kStreams = 2, for many rows: two row tiles against the same keys, each with a warpgroup of its own for the
+// exponentials, so that the tensor cores work on one while the other's are computed.  kStreams = 1, for few rows, or heads of
+// 256: one row tile, the scores of the next keys ahead of the exponentials of the present ones; what counts there is the stream of
+// keys and values, 160 KB of which are on their way at any time.
+//
+// Warps: 0 finds the work and copies, 1 issues the products, 2 owns TMEM, 3 notes cut units, 4.. exponentials and results.
+#pragma once
+
+#include <type_traits>
+
+#include "gdn_attention.cuh"
+#include "sm103_ptx.cuh"
+
+namespace gdn {
+namespace attn_tc {
+
+constexpr int kRowTile = 128;
+constexpr float kGrowth = 8.f;      // log2 of how far a row's maximum may fall behind
+constexpr int kParts = 4;           // parts handed from the producer to the others ahead
+
+template <int kDim, int kStreams>
+struct Shape {
+    static_assert(kDim == 64 || kDim == 128 || (kDim == 256 && kStreams == 1), "TMEM holds no more");
+    static constexpr int kKeys = 128;                                // keys a tile
+    static constexpr int kHalves = kDim == 256 ? 2 : 1;              // stages a tile of keys or values takes: 128 channels each at most
+    static constexpr int kChunks = kDim / 64 / kHalves;              // swizzled columns of 64 channels in a stage
+    static constexpr int kQBytes = kHalves * kChunks * kRowTile * 128;
+    static constexpr int kKvBytes = kChunks * kKeys * 128;
+    static constexpr int kQSlots = kStreams == 1 && kDim < 256 ? 2 : 1;  // units whose Q is there
+    static constexpr int kQTiles = kQSlots * kStreams;
+    static constexpr int kStages = (224 * 1024 - kQTiles * kQBytes) / kKvBytes;
+    static constexpr int kTileBytes = kQTiles * kQBytes + kStages * kKvBytes;
+    static constexpr int kThreads = 128 + 128 * kStreams;
+    static constexpr uint32_t kTmemO = 256;                          // S slots at columns 0 and 128
+};
+
+// What the launch adds to AttnParams.
+struct TcParams {
+    AttnParams a;
+    int32_t row_tokens;            // tokens a row tile
+    int32_t box_keys;              // keys a box: what pages and tiles have in common
+    int32_t boxes;                 // of a tile, along the keys
+    int32_t k_steps;               // steps of 16 channels a stage
+    uint32_t idesc_qk, idesc_pv;
+    float scale_log2;              // positive: a negative scale negates Q in the product
+    int32_t out_vec;               // results can be written 16 bytes at a time
+};
+
+template <class S>
+struct Misc {
+    uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
+    uint64_t part_full[kParts], part_empty[kParts], drain;
+    uint32_t stage_mask[S::kStages], slot_mask[2];
+    uint32_t tmem;
+    int32_t abort;
+    AttnPart parts[kParts];
+    AttnScan<S::kThreads> scan;
+};
+
+template <class S>
+constexpr size_t smem_bytes() { return S::kTileBytes + sizeof(Misc<S>); }
+
+// Waits with a limit of about a second; the first that runs out makes all others give up.
+static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait_sleep(bar, parity, 1000)) {
+        if (*static_cast<volatile int32_t*>(abort)) return false;
+        if (clock64() - t0 > 2000000000LL) {
+            *static_cast<volatile int32_t*>(abort) = 1;
+            kv_report(status, GDN_DEVICE_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// By a whole warp: all of its lanes go on, or none.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
+    return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status));
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint64_t both(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_both(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_both(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+template <class E>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (sizeof(E) == 2 && std::is_same<E, __half>::value)
+        return pack_f16x2(lo, hi);
+    else
+        return pack_bf16x2(lo, hi);
+}
+__device__ __forceinline__ float wide16(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float wide16(__half x) { return __half2float(x); }
+template <class E>
+__device__ __forceinline__ E narrow16(float x) {
+    if constexpr (std::is_same<E, __half>::value)
+        return __float2half_rn(x);
+    else
+        return __float2bfloat16_rn(x);
+}
+
+// Tiles of row tile s of a part that some of its rows see (what lies behind, only later rows see).
+__device__ __forceinline__ int32_t stream_end(const TcParams& p, const AttnPart& a, int s, int32_t keys_a_tile) {
+    const int32_t t1 = min(a.tokens, (s + 1) * p.row_tokens);
+    if (s * p.row_tokens >= a.tokens) return a.tile0;
+    if (!p.a.causal) return a.tile1;
+    const int64_t hi = min(max(static_cast<int64_t>(a.pos0) + t1, int64_t{0}), static_cast<int64_t>(a.keys));
+    return max(a.tile0, static_cast<int32_t>(min(static_cast<int64_t>(a.tile1), (hi + keys_a_tile - 1) / keys_a_tile)));
+}
+
+// Where a row's result goes.
+template <class E>
+struct RowOut {
+    E* o;                          // whole units
+    float* lse;
+    float* part;                   // parts
+    float2* ml;
+};
+
+template <class E>
+__device__ __forceinline__ RowOut<E> row_out(const AttnParams& p, const AttnPart& a, int32_t block, int t, int g) {
+    RowOut<E> r{};
+    const int D = p.c.head_dim;
+    if (a.tile0 == a.first && a.tile1 == a.last) {
+        r.o = static_cast<E*>(p.o) + (a.row0 + t) * p.o_stride + static_cast<int64_t>(a.head0 + g) * D;
+        if (p.lse) r.lse = p.lse + (a.row0 + t) * p.heads + a.head0 + g;
+    } else {
+        const int64_t at = static_cast<int64_t>(attn_slot(a, block)) * (p.unit_tokens * p.group) + t * a.heads + g;
+        r.part = p.part_o + at * D;
+        r.ml = p.part_ml + at;
+    }
+    return r;
+}
+
+// One row from the keys that it sees, by a warp: where a hidden value that is not finite (taken times zero by the product) has
+// spoilt the row.  m is the row's maximum as used, l its sum.
+template <class E>
+__device__ __noinline__ void exact_row(const AttnParams& p, const AttnPart& a, int t, int g, int32_t lo, int32_t hi, float m, float l,
+                                       int32_t block, int lane) {
+    const int D = p.c.head_dim;
+    const E* q = static_cast<const E*>(p.q) + (a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D;
+    float x[8], acc[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        x[c] = lane + 32 * c < D ? wide16(q[lane + 32 * c]) : 0.f;
+        acc[c] = 0.f;
+    }
+    const int64_t from = max(static_cast<int64_t>(a.tile0) * p.tile, static_cast<int64_t>(lo));
+    const int64_t upto = min(static_cast<int64_t>(a.tile1) * p.tile, static_cast<int64_t>(hi));
+    for (int64_t key = from; key < upto; ++key) {
+        const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + key / p.b.page_tokens];
+        if (page < 0 || page >= p.b.n_pages) continue;
+        const int64_t in = key % p.b.page_tokens;
+        const E* k = static_cast<const E*>(p.c.k) + page * p.c.k_page_stride + in * p.c.k_token_stride + a.kv_head * p.c.k_head_stride;
+        const E* v = static_cast<const E*>(p.c.v) + page * p.c.v_page_stride + in * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
+        float s = 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (lane + 32 * c < D) s = fmaf(x[c], wide16(k[lane + 32 * c]), s);
+        for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
+        const float w = exp2f(fmaf(s, p.scale_log2, -m));
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (lane + 32 * c < D) acc[c] = fmaf(w, wide16(v[lane + 32 * c]), acc[c]);
+    }
+    const RowOut<E> out = row_out<E>(p, a, block, t, g);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+        const int d = lane + 32 * c;
+        if (d >= D) break;
+        if (out.o)
+            out.o[d] = narrow16<E>(l == 0.f ? 0.f : acc[c] / l);
+        else
+            out.part[d] = acc[c];
+    }
+}
+
+// A row's result without keys (zero), or after a wait that ran out (NaN).
+template <class E>
+__device__ __noinline__ void fill_row(const AttnParams& p, const AttnPart& a, int t, int g, float value, int32_t block) {
+    const RowOut<E> out = row_out<E>(p, a, block, t, g);
+    for (int d = 0; d < p.c.head_dim; ++d) {
+        if (out.o)
+            out.o[d] = narrow16<E>(value);
+        else
+            out.part[d] = value;
+    }
+    if (out.lse) *out.lse = value == 0.f ? -INFINITY : value;
+    if (out.ml) *out.ml = make_float2(value == 0.f ? -INFINITY : 0.f, value);
+}
+
+// ------------------------------------------------------------------------------------------------ warp 0: work and copies
+template <class S, int kStreams>
+__device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUtensorMap* map_k, const CUtensorMap* map_v, Misc<S>& sh,
+                        uint8_t* q_s, uint8_t* kv_s, int lane) {
+    const AttnParams& ap = p.a;
+    const int32_t pt = ap.b.page_tokens;
+    int32_t* status = ap.b.device_status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    AttnWalk walk;
+    walk.begin(sh.scan.start);
+    AttnPart a{};
+    uint32_t n = 0, qn = 0, err = 0;
+    bool ok = true;
+
+    // Lane b: the page of a tile's box b and the box's first token in it; the cache's end, which reads as zeros, without one.
+    struct Boxes {
+        int32_t page, token;
+        uint32_t mask;             // boxes whose page is there, or that lie behind the sequence
+    };
+    auto look_up = [&](int32_t tile) {
+        Boxes x{ap.b.n_pages, 0, ~0u};
+        const int64_t key = static_cast<int64_t>(tile) * S::kKeys + lane * p.box_keys;
+        bool bad = false;
+        if (lane < p.boxes && key < a.keys) {
+            const int64_t i = key / pt;
+            x.token = static_cast<int32_t>(key - i * pt);
+            x.page = ap.b.table[static_cast<int64_t>(a.table_row) * ap.b.max_pages + i];
+            bad = x.page < 0 || x.page >= ap.b.n_pages;
+            if (bad) x.page = ap.b.n_pages;
+        }
+        x.mask = ~__ballot_sync(~0u, bad);
+        if (x.mask != ~0u) err |= GDN_PAGES_ERR_PAGE;
+        return x;
+    };
+    auto load_half = [&](const CUtensorMap* map, const Boxes& x, int half) {
+        const uint32_t st = n % S::kStages, use = n / S::kStages;
+        if (use > 0 && !wait(sh.kv_empty + st, (use - 1) & 1)) return false;
+        if (elect_one()) {
+            sh.stage_mask[st] = x.mask;
+            mbar_arrive_expect_tx(sh.kv_full + st, S::kKvBytes);
+        }
+        __syncwarp();
+        for (int b = 0; b < p.boxes; ++b) {
+            const int32_t page = __shfl_sync(~0u, x.page, b), token = __shfl_sync(~0u, x.token, b);
+            if (elect_one()) {
+#pragma unroll
+                for (int c = 0; c < S::kChunks; ++c)
+                    tma_load_4d(kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + b * p.box_keys * 128, map, sh.kv_full + st,
+                                (half * S::kChunks + c) * 64, token, a.kv_head, page);
+            }
+            __syncwarp();
+        }
+        ++n;
+        return true;
+    };
+    auto load = [&](const CUtensorMap* map, const Boxes& x) {
+        for (int half = 0; half < S::kHalves; ++half)
+            if (!load_half(map, x, half)) return false;
+        return true;
+    };
+
+    for (uint32_t k = 0; ok; ++k) {
+        const bool more = walk.next(ap, a);
+        if (!more) a.tokens = 0;
+        if (k >= kParts && !wait(sh.part_empty + k % kParts, (k / kParts - 1) & 1)) break;
+        if (elect_one()) {
+            sh.parts[k % kParts] = a;
+            mbar_arrive(sh.part_full + k % kParts);
+        }
+        __syncwarp();
+        if (!more) break;
+        if (a.first == a.last) continue;
+        const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
+        if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
+        const int active = a.tokens > p.row_tokens ? kStreams : 1;
+        if (elect_one()) {
+            constexpr int kAll = S::kHalves * S::kChunks;
+            mbar_arrive_expect_tx(sh.q_full + slot, active * kAll * ap.group * p.row_tokens * 128);
+            for (int s = 0; s < active; ++s)
+#pragma unroll
+                for (int c = 0; c < kAll; ++c)
+                    tma_load_3d(q_s + (slot + s) * S::kQBytes + c * (kRowTile * 128), map_q, sh.q_full + slot, c * 64, a.head0,
+                                static_cast<int32_t>(a.row0 + s * p.row_tokens));
+        }
+        __syncwarp();
+        ++qn;
+        Boxes now = look_up(a.tile0);
+        if (kStreams == 1) ok = load(map_k, now);
+        for (int32_t tile = a.tile0; ok && tile < a.tile1; ++tile) {
+            const bool next = tile + 1 < a.tile1;
+            Boxes then = now;
+            if (next) then = look_up(tile + 1);
+            if (kStreams == 2)
+                ok = load(map_k, now) && load(map_v, now);
+            else
+                ok = (!next || load(map_k, then)) && load(map_v, now);
+            now = then;
+        }
+    }
+    if (lane == 0) kv_report(status, err);
+    if (*static_cast<volatile int32_t*>(&sh.abort)) {  // no copy may be under way when the block ends
+        for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) mbar_wait(sh.kv_full + i % S::kStages, i / S::kStages & 1);
+        for (uint32_t i = qn > S::kQSlots ? qn - S::kQSlots : 0; i < qn; ++i) mbar_wait(sh.q_full + i % S::kQSlots, i / S::kQSlots & 1);
+    }
+}
+
+// ------------------------------------------------------------------------------------------------ warp 1: products
+// The whole warp goes through it, converged, so that addresses and descriptors stay in uniform registers; one lane issues.  What is
+// issued completes in order, so that a product may overwrite the S whose P an earlier one reads.
+template <class S, int kStreams>
+__device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, uint32_t tmem, int lane) {
+    int32_t* status = p.a.b.device_status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    const uint32_t q_at = smem_u32(q_s), kv_at = smem_u32(kv_s);
+    uint32_t n = 0, qn = 0, g = 0, seen0 = 0, seen1 = 0;
+
+    // S in slot `slot` (+)= row tile q times the keys of stage st; with the last half the slot's mask goes along.
+    auto scores = [&](int slot, uint32_t q, uint32_t st, int half) {
+        const uint64_t dq = desc_kmajor_sw128(q_at + q * S::kQBytes + half * (S::kChunks * kRowTile * 128));
+        const uint64_t dk = desc_kmajor_sw128(kv_at + st * S::kKvBytes);
+#pragma unroll
+        for (int i = 0; i < S::kChunks * 4; ++i)
+            if (i < p.k_steps)
+                mma_ss_elect(tmem + slot * 128, dq + ((i / 4) * (kRowTile * 128) + (i % 4) * 32) / 16,
+                            dk + ((i / 4) * (S::kKeys * 128) + (i % 4) * 32) / 16, p.idesc_qk, half > 0 || i > 0);
+        if (half == S::kHalves - 1) {
+            mma_commit_elect(sh.s_full + slot);
+            if (lane == 0) {
+                sh.slot_mask[slot] = sh.stage_mask[st];
+                mbar_arrive(sh.s_full + slot);
+            }
+            __syncwarp();
+        }
+    };
+    // O of stream s (+)= P in slot `slot` times the values of stage st.
+    auto values = [&](int slot, int s, uint32_t st, int half, bool add) {
+        const uint64_t dv = desc_mnmajor_sw128(kv_at + st * S::kKvBytes, S::kKeys * 128);
+#pragma unroll
+        for (int i = 0; i < S::kKeys / 16; ++i)
+            mma_ts_elect(tmem + S::kTmemO + (s + half) * 128, tmem + slot * 128 + i * 8, dv + i * (2048 / 16), p.idesc_pv, add || i > 0);
+        if (half == S::kHalves - 1) mma_commit_elect(sh.pv_done + s);
+    };
+    // The sequence's last tile: what its page holds behind the sequence may be anything, and a weight of zero does not make nothing
+    // of it.  The exponentials of this tile are under way meanwhile.
+    auto clear_tail = [&](const AttnPart& a, int32_t tile, uint32_t st) {
+        const int64_t held = a.keys - static_cast<int64_t>(tile) * S::kKeys;
+        if (held >= S::kKeys) return;
+#pragma unroll
+        for (int c = 0; c < S::kChunks; ++c)
+            for (int i = static_cast<int>(held) * 8 + lane; i < S::kKeys * 8; i += 32)
+                *reinterpret_cast<uint4*>(kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+    };
+    auto arrived = [&](uint32_t at) { return wait(sh.kv_full + at % S::kStages, at / S::kStages & 1); };
+    auto run = [&]() {
+        for (uint32_t k = 0;; ++k) {
+            if (!wait(sh.part_full + k % kParts, k / kParts & 1)) return;
+            const AttnPart a = sh.parts[k % kParts];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.part_empty + k % kParts);
+            __syncwarp();
+            if (a.tokens == 0) return;
+            if (a.first == a.last) continue;
+            const uint32_t slot = qn % S::kQSlots;
+            if (!wait(sh.q_full + slot, qn / S::kQSlots & 1)) return;
+            ++qn;
+            const int32_t count = a.tile1 - a.tile0;
+            if constexpr (kStreams == 2) {
+                const int32_t end0 = stream_end(p, a, 0, S::kKeys) - a.tile0, end1 = stream_end(p, a, 1, S::kKeys) - a.tile0;
+                if (!arrived(n)) return;
+                tc_fence_after();
+                if (end0 > 0) scores(0, 0, n % S::kStages, 0);
+                if (end1 > 0) scores(1, 1, n % S::kStages, 0);
+                mma_commit_elect(sh.kv_empty + n % S::kStages);
+                if (count == 1) mma_commit_elect(sh.q_empty + slot);
+                ++n;
+                for (int32_t j = 0; j < count; ++j) {
+                    const uint32_t v_at = n % S::kStages, k_at = (n + 1) % S::kStages;
+                    const bool next = j + 1 < count;
+                    if (!arrived(n) || (next && !arrived(n + 1))) return;
+                    clear_tail(a, a.tile0 + j, v_at);
+                    if (j < end0) {
+                        if (!wait(sh.p_full + 0, seen0++ & 1)) return;
+                        tc_fence_after();
+                        values(0, 0, v_at, 0, j > 0);
+                    }
+                    if (j + 1 < end0) scores(0, 0, k_at, 0);
+                    if (j < end1) {
+                        if (!wait(sh.p_full + 1, seen1++ & 1)) return;
+                        tc_fence_after();
+                        values(1, 1, v_at, 0, j > 0);
+                    }
+                    if (j + 1 < end1) scores(1, 1, k_at, 0);
+                    mma_commit_elect(sh.kv_empty + v_at);
+                    if (next) mma_commit_elect(sh.kv_empty + k_at);
+                    if (j + 2 == count) mma_commit_elect(sh.q_empty + slot);
+                    n += next ? 2 : 1;
+                }
+            } else {
+                auto all_scores = [&](int s_slot) {
+                    for (int half = 0; half < S::kHalves; ++half, ++n) {
+                        if (!arrived(n)) return false;
+                        tc_fence_after();
+                        scores(s_slot, slot, n % S::kStages, half);
+                        mma_commit_elect(sh.kv_empty + n % S::kStages);
+                    }
+                    return true;
+                };
+                if (!all_scores(g & 1)) return;
+                if (count == 1) mma_commit_elect(sh.q_empty + slot);
+                for (int32_t j = 0; j < count; ++j, ++g) {
+                    if (j + 1 < count && !all_scores((g + 1) & 1)) return;
+                    if (j + 2 == count) mma_commit_elect(sh.q_empty + slot);
+                    for (int half = 0; half < S::kHalves; ++half, ++n) {
+                        if (!arrived(n)) return;
+                        clear_tail(a, a.tile0 + j, n % S::kStages);
+                        if (half == 0 && !wait(sh.p_full + (g & 1), g / 2 & 1)) return;
+                        tc_fence_after();
+                        values(g & 1, 0, n % S::kStages, half, j > 0);
+                        mma_commit_elect(sh.kv_empty + n % S::kStages);
+                    }
+                }
+            }
+        }
+    };
+    run();
+    __syncwarp();
+    mma_commit_elect(&sh.drain);  // no product may be under way when TMEM is given back
+    mbar_wait(&sh.drain, 0);
+}
+
+// ------------------------------------------------------------------------------------------------ warps 4..: exponentials, results
+template <class E, class S, int kDim, int kStreams>
+__device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int stream, int warp, int lane, int32_t block) {
+    constexpr float kOffset = std::is_same<E, __half>::value ? 7.f : 0.f;
+    const AttnParams& ap = p.a;
+    const int D = ap.c.head_dim;
+    int32_t* status = ap.b.device_status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    const int row = warp * 32 + lane, tile_t = row / ap.group, g = row - tile_t * ap.group, t = stream * p.row_tokens + tile_t;
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+    const uint32_t o_at = tmem + lanes + S::kTmemO + stream * 128;
+    uint32_t count = 0;            // tiles of this stream so far
+    uint32_t k = 0;
+    bool ok = true;
+    for (; ok; ++k) {
+        ok = wait(sh.part_full + k % kParts, k / kParts & 1);
+        if (!ok) break;
+        const AttnPart a = sh.parts[k % kParts];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.part_empty + k % kParts);
+        if (a.tokens == 0) break;
+        const bool mine = tile_t < p.row_tokens && t < a.tokens && g < a.heads;
+        if (a.first == a.last) {
+            if (mine) fill_row<E>(ap, a, t, g, 0.f, block);
+            continue;
+        }
+        const int64_t pos = static_cast<int64_t>(a.pos0) + t;
+        const int32_t hi = ap.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
+        const int32_t lo = ap.window ? static_cast<int32_t>(max(pos - ap.window + 1, int64_t{0})) : 0;
+        const bool live = __any_sync(~0u, mine);
+        const int32_t tiles = kStreams == 2 ? stream_end(p, a, stream, S::kKeys) - a.tile0 : a.tile1 - a.tile0;
+        float m = -INFINITY, l = 0.f;  // the maximum as used, less the offset; the sum of weights relative to it
+        for (int32_t j = 0; j < tiles; ++j, ++count) {
+            const uint32_t slot = kStreams == 2 ? stream : count & 1;
+            const uint32_t parity = kStreams == 2 ? count & 1 : count / 2 & 1;
+            ok = wait(sh.s_full + slot, parity);
+            if (!ok) break;
+            tc_fence_after();
+            float shrink = 1.f;
+            if (live) {
+                const uint32_t s_at = tmem + lanes + slot * 128;
+                uint32_t s[S::kKeys];
+#pragma unroll
+                for (int c = 0; c < S::kKeys; c += 32) tmem_ld32(s_at + c, s + c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < S::kKeys; c += 32) tmem_regs_ready32(s + c);
+                const int64_t key0 = static_cast<int64_t>(a.tile0 + j) * S::kKeys;
+                const uint32_t mask = sh.slot_mask[slot];
+                const bool clean = !mine || (lo <= key0 && key0 + S::kKeys <= hi);
+                if (!__all_sync(~0u, clean)) {
+                    const int from = static_cast<int>(max(lo - key0, int64_t{0}));
+                    const int upto = static_cast<int>(min(hi - key0, static_cast<int64_t>(S::kKeys)));
+#pragma unroll
+                    for (int c = 0; c < S::kKeys; ++c)
+                        if (c < from || c >= upto) s[c] = 0xff800000u;  // -infinity
+                }
+                if (mask != ~0u) {
+#pragma unroll
+                    for (int c = 0; c < S::kKeys; ++c)
+                        if (!(mask >> (c / p.box_keys) & 1)) s[c] = 0xff800000u;
+                }
+                float top[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(s[c]);
+#pragma unroll
+                for (int c = 4; c < S::kKeys; ++c) top[c % 4] = fmaxf(top[c % 4], __uint_as_float(s[c]));
+                const float x = fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale_log2, -kOffset);
+                if (mine && (x > m + kGrowth || m == -INFINITY)) {
+                    shrink = m == -INFINITY ? 0.f : exp2_fast(m - x);
+                    m = x;
+                    l *= shrink;
+                }
+                __syncwarp();
+                const float base = m == -INFINITY ? 0.f : m;
+                const uint64_t by = both(p.scale_log2, p.scale_log2), less = both(-base, -base);
+                uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        float e[4];
+                        split(fma_both(both(__uint_as_float(s[64 * h + c]), __uint_as_float(s[64 * h + c + 1])), by, less), e[0], e[1]);
+                        split(fma_both(both(__uint_as_float(s[64 * h + c + 2]), __uint_as_float(s[64 * h + c + 3])), by, less), e[2], e[3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e[i] = exp2_fast(e[i]);
+                        sum0 = add_both(sum0, both(e[0], e[1]));
+                        sum1 = add_both(sum1, both(e[2], e[3]));
+                        w[c / 2] = pack16<E>(e[0], e[1]);
+                        w[c / 2 + 1] = pack16<E>(e[2], e[3]);
+                    }
+                    tmem_st32(s_at + 32 * h, w);
+                }
+                float s0, s1, s2, s3;
+                split(sum0, s0, s1);
+                split(sum1, s2, s3);
+                l += (s0 + s1) + (s2 + s3);
+            }
+            if (j > 0) {
+                ok = wait(sh.pv_done + stream, (count - 1) & 1);
+                if (!ok) break;
+                if (__any_sync(~0u, shrink != 1.f)) {
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_wait(o_at + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st32(o_at + c, o);
+                    }
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.p_full + slot);
+        }
+        if (!ok) break;
+        if (tiles > 0) {
+            ok = wait(sh.pv_done + stream, (count - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+        }
+        if (!live) continue;
+        const RowOut<E> out = row_out<E>(ap, a, block, t, g);
+        const float scale = out.o ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+        float finite = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            if (tiles > 0) {
+                tmem_ld32_wait(o_at + c, o);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = 0;
+            }
+            if (mine) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < D) finite = fmaf(__uint_as_float(o[i]), 0.f, finite);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+                if (out.o) {
+                    if (p.out_vec) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 8)
+                            if (c + i < D)
+                                *reinterpret_cast<uint4*>(out.o + c + i) =
+                                    make_uint4(pack16<E>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                               pack16<E>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
+                                               pack16<E>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
+                                               pack16<E>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < D) out.o[c + i] = narrow16<E>(__uint_as_float(o[i]));
+                    }
+                } else if (D % 4 == 0) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+                        if (c + i < D) *reinterpret_cast<uint4*>(out.part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (c + i < D) out.part[c + i] = __uint_as_float(o[i]);
+                }
+            }
+            __syncwarp();
+        }
+        tc_fence_before();
+        if (mine) {
+            if (out.lse) *out.lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+            if (out.ml) *out.ml = make_float2(m, l);
+        }
+        unsigned spoilt = __ballot_sync(~0u, mine && finite != 0.f && l - l == 0.f);
+        while (spoilt) {
+            const int from = __ffs(spoilt) - 1;
+            spoilt &= spoilt - 1;
+            __syncwarp();
+            exact_row<E>(ap, a, __shfl_sync(~0u, t, from), __shfl_sync(~0u, g, from), __shfl_sync(~0u, lo, from), __shfl_sync(~0u, hi, from),
+                         __shfl_sync(~0u, m, from), __shfl_sync(~0u, l, from), block, lane);
+        }
+    }
+    if (!ok) {  // what a wait that ran out has left undone
+        AttnWalk walk;
+        walk.begin(sh.scan.start);
+        AttnPart a;
+        for (uint32_t i = 0; walk.next(ap, a); ++i)
+            if (i >= k && tile_t < p.row_tokens && t < a.tokens && g < a.heads) fill_row<E>(ap, a, t, g, __int_as_float(0x7fffffff), block);
+    }
+}
+
+template <class E, int kDim, int kStreams>
+__global__ void __launch_bounds__(128 + 128 * kStreams, 1)
+    attention_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v) {
+    using S = Shape<kDim, kStreams>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint8_t* q_s = smem;
+    uint8_t* kv_s = smem + S::kQTiles * S::kQBytes;
+    Misc<S>& sh = *reinterpret_cast<Misc<S>*>(smem + S::kTileBytes);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t block = blockIdx.x;
+    if (tid == 0) {
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(sh.kv_full + i, 1);
+            mbar_init(sh.kv_empty + i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.q_full + i, 1);
+            mbar_init(sh.q_empty + i, 1);
+            mbar_init(sh.s_full + i, 2);     // the product, and the slot's mask
+            mbar_init(sh.p_full + i, 4);     // a warpgroup's warps
+            mbar_init(sh.pv_done + i, 1);
+        }
+        for (int i = 0; i < kParts; ++i) {
+            mbar_init(sh.part_full + i, 1);
+            mbar_init(sh.part_empty + i, 1 + 4 * kStreams);
+        }
+        mbar_init(&sh.drain, 1);
+        sh.abort = 0;
+        fence_mbar_init();
+        prefetch_tensormap(&map_q);
+        prefetch_tensormap(&map_k);
+        prefetch_tensormap(&map_v);
+    }
+    if (warp == 2) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    attn_start<S::kThreads>(p.a, block, gridDim.x, sh.scan);  // and the barriers are there for all
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    if (warp < 4) {
+        if (warp == 0) {
+            produce<S, kStreams>(p, &map_q, &map_k, &map_v, sh, q_s, kv_s, lane);
+        } else if (warp == 1) {
+            multiply<S, kStreams>(p, sh, q_s, kv_s, tmem, lane);
+        } else if (warp == 3 && lane == 0) {
+            p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
+            AttnWalk walk;
+            walk.begin(sh.scan.start);
+            AttnPart a;
+            while (walk.next(p.a, a))
+                if (a.tile0 == a.first && a.tile1 < a.last) attn_note_join(p.a, a, block, walk.at.share);
+        }
+    } else {
+        exponentiate<E, S, kDim, kStreams>(p, sh, tmem, (warp - 4) / 4, warp & 3, lane, block);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <class E, int kDim, int kStreams>
+cudaError_t launch_shape(const TcParams& p, const CUtensorMap* maps, int32_t blocks, cudaStream_t stream) {
+    using S = Shape<kDim, kStreams>;
+    static_assert(smem_bytes<S>() <= 227 * 1024, "shared memory");
+    auto kernel = attention_tc_kernel<E, kDim, kStreams>;
+    constexpr int bytes = static_cast<int>(smem_bytes<S>());
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, S::kThreads, bytes, stream>>>(p, maps[0], maps[1], maps[2]);
+    return cudaGetLastError();
+}
+
+template <class E>
+cudaError_t launch_typed(const TcParams& p, const CUtensorMap* maps, int streams, int32_t blocks, cudaStream_t stream) {
+    const int D = p.a.c.head_dim;
+    if (D > 128) return launch_shape<E, 256, 1>(p, maps, blocks, stream);
+    if (D > 64)
+        return streams == 2 ? launch_shape<E, 128, 2>(p, maps, blocks, stream) : launch_shape<E, 128, 1>(p, maps, blocks, stream);
+    return streams == 2 ? launch_shape<E, 64, 2>(p, maps, blocks, stream) : launch_shape<E, 64, 1>(p, maps, blocks, stream);
+}
+
+}  // namespace attn_tc
+
+cudaError_t launch_attention_tc_bf16(const attn_tc::TcParams& p, const CUtensorMap* maps, int streams, int32_t blocks, cudaStream_t stream);
+cudaError_t launch_attention_tc_f16(const attn_tc::TcParams& p, const CUtensorMap* maps, int streams, int32_t blocks, cudaStream_t stream);
+
+}  // namespace gdn

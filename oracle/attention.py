@@ -50,16 +50,15 @@ def attend(q, k_cache, v_cache, table, lengths, seqs, lens, scale, causal=True, 
             if window:
                 seen &= keys > p - window
             if seen.any():
-                k, v = (c[page[seen], keys[seen] % pt] for c in (k_cache, v_cache))
-                for h in range(H):
-                    kh, vh = k[:, h // (H // Hk)], v[:, h // (H // Hk)]
-                    x = scale * (kh @ q[t, h])
-                    top = x.max()
-                    w = np.exp(x - top)
-                    total = w.sum()
-                    out[t, h], lse[t, h] = w @ vh / total, top + np.log(total)
-                    size[t, h] = w @ np.abs(vh) / total
-                    products[t, h] = (abs(scale) * (np.abs(kh) @ np.abs(q[t, h]))).max()
-                    count[t, h] = len(x)
+                k, v = (c[page[seen], keys[seen] % pt].transpose(1, 0, 2) for c in (k_cache, v_cache))  # [kv_heads, keys, D]
+                x = scale * np.matmul(q[t].reshape(Hk, H // Hk, D), k.transpose(0, 2, 1))
+                top = x.max(-1, keepdims=True)
+                w = np.exp(x - top)
+                total = w.sum(-1, keepdims=True)
+                out[t] = (np.matmul(w, v) / total).reshape(H, D)
+                size[t] = (np.matmul(w, np.abs(v)) / total).reshape(H, D)
+                lse[t] = (top + np.log(total)).reshape(H)
+                products[t] = (abs(scale) * np.matmul(np.abs(q[t]).reshape(Hk, H // Hk, D), np.abs(k).transpose(0, 2, 1))).max(-1).reshape(H)
+                count[t] = x.shape[-1]
             t += 1
     return out, lse, size, products, count

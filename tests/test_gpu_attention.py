@@ -182,6 +182,25 @@ def test_many_sequences():
         Cache(lens, past, 2, 1, 64, 16, dtype).check()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D,tokens", [(64, 1), (128, 1), (128, 2), (256, 1)])
+def test_many_units_a_block(dtype, D, tokens):
+    """Each block goes through several sequences with several tiles and a partly filled last one."""
+    g = torch.Generator().manual_seed(D + tokens)
+    past = torch.randint(0, 1300, (320,), generator=g).tolist()
+    Cache([tokens] * 320, past, 4, 2, D, 16, dtype, seed=D).check(tokens=tokens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page_tokens", [(64, 16), (128, 64), (256, 64)])
+def test_many_units_of_many_rows_a_block(dtype, D, page_tokens):
+    """The same for chunks of tokens: units of several hundred rows, whole ones and cut ones."""
+    g = torch.Generator().manual_seed(D)
+    lens = torch.randint(0, 60, (60,), generator=g).tolist()
+    past = torch.randint(0, 1000, (60,), generator=g).tolist()
+    Cache(lens, past, 32, 2, D, page_tokens, dtype, seed=D).check()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("heads,kv_heads", [(4, 1), (16, 2)])
