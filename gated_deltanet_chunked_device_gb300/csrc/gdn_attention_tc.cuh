@@ -17,7 +17,7 @@
 // 256: one row tile, the scores of the next keys ahead of the exponentials of the present ones; what counts there is the stream of
 // keys and values, 160 KB of which are on their way at any time.
 //
-// Warps: 0 finds the work and copies, 1 issues the products, 2 owns TMEM, 3 notes cut units, 4.. exponentials and results.
+// Warps: 0 finds the work and copies, 1 (and 2) issue the products, 2 owns TMEM, 3 notes cut units, 4.. exponentials and results.
 #pragma once
 
 #include <type_traits>
@@ -62,8 +62,8 @@ struct TcParams {
 
 template <class S>
 struct Misc {
-    uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
-    uint64_t part_full[kParts], part_empty[kParts], drain;
+    uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2];
+    uint64_t part_full[kParts], part_empty[kParts], tail_done, turn[2], drain[2];
     uint32_t stage_mask[S::kStages], slot_mask[2];
     uint32_t tmem;
     int32_t abort;
@@ -75,7 +75,7 @@ template <class S>
 constexpr size_t smem_bytes() { return S::kTileBytes + sizeof(Misc<S>); }
 
 // Waits with a limit of about a second; the first that runs out makes all others give up.
-static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
     const long long t0 = clock64();
     while (!mbar_try_wait_sleep(bar, parity, 1000)) {
         if (*static_cast<volatile int32_t*>(abort)) return false;
@@ -92,6 +92,9 @@ static __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, in
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
     return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status));
 }
+
+// The lowest n bits, n of any size and sign.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -168,7 +171,7 @@ __device__ __forceinline__ RowOut<E> row_out(const AttnParams& p, const AttnPart
 // One row from the keys that it sees, by a warp: where a hidden value that is not finite (taken times zero by the product) has
 // spoilt the row.  m is the row's maximum as used, l its sum.
 template <class E>
-__device__ __noinline__ void exact_row(const AttnParams& p, const AttnPart& a, int t, int g, int32_t lo, int32_t hi, float m, float l,
+__device__ __forceinline__ void exact_row(const AttnParams& p, const AttnPart& a, int t, int g, int32_t lo, int32_t hi, float m, float l,
                                        int32_t block, int lane) {
     const int D = p.c.head_dim;
     const E* q = static_cast<const E*>(p.q) + (a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D;
@@ -210,7 +213,7 @@ __device__ __noinline__ void exact_row(const AttnParams& p, const AttnPart& a, i
 
 // A row's result without keys (zero), or after a wait that ran out (NaN).
 template <class E>
-__device__ __noinline__ void fill_row(const AttnParams& p, const AttnPart& a, int t, int g, float value, int32_t block) {
+__device__ __forceinline__ void fill_row(const AttnParams& p, const AttnPart& a, int t, int g, float value, int32_t block) {
     const RowOut<E> out = row_out<E>(p, a, block, t, g);
     for (int d = 0; d < p.c.head_dim; ++d) {
         if (out.o)
@@ -220,6 +223,70 @@ __device__ __noinline__ void fill_row(const AttnParams& p, const AttnPart& a, in
     }
     if (out.lse) *out.lse = value == 0.f ? -INFINITY : value;
     if (out.ml) *out.ml = make_float2(value == 0.f ? -INFINITY : 0.f, value);
+}
+
+// A row of products issued from a converged warp, one lane chosen once: kSteps steps of 16 channels of row tiles and keys (chunks of 64
+// channels, 16 KB each), and four steps of 16 keys of weights and values.  (Issued one by one, each with an election of its own
+// and its descriptors made in between, they cost the issuing warp more time than the tensor cores.)
+template <int kSteps>
+__device__ __forceinline__ void issue_scores(uint32_t d, uint64_t q, uint64_t k, uint32_t idesc, uint32_t add) {
+    if constexpr (kSteps == 8)
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 1024;\n\tadd.s64 b, %2, 1024;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 1026;\n\tadd.s64 b, %2, 1026;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 1028;\n\tadd.s64 b, %2, 1028;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 1030;\n\tadd.s64 b, %2, 1030;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "}"
+            ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(add)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred e, p, t;\n\t.reg .b64 a, b;\n\t"
+            "elect.sync _|e, 0xffffffff;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "setp.eq.b32 t, 0, 0;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+            "add.s64 a, %1, 2;\n\tadd.s64 b, %2, 2;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 4;\n\tadd.s64 b, %2, 4;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "add.s64 a, %1, 6;\n\tadd.s64 b, %2, 6;\n\t"
+            "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+            "}"
+            ::"r"(d), "l"(q), "l"(k), "r"(idesc), "r"(add)
+            : "memory");
+}
+__device__ __forceinline__ void issue_values(uint32_t d, uint32_t w, uint64_t v, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, t;\n\t.reg .b64 b;\n\t.reg .b32 a;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+        "add.s32 a, %1, 8;\n\tadd.s64 b, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s32 a, %1, 16;\n\tadd.s64 b, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "add.s32 a, %1, 24;\n\tadd.s64 b, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+        "}"
+        ::"r"(d), "r"(w), "l"(v), "r"(idesc), "r"(add)
+        : "memory");
 }
 
 // ------------------------------------------------------------------------------------------------ warp 0: work and copies
@@ -236,50 +303,51 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
     uint32_t n = 0, qn = 0, err = 0;
     bool ok = true;
 
-    // Lane b: the page of a tile's box b and the box's first token in it; the cache's end, which reads as zeros, without one.
+    // Lane i: the page of box i of the `span` tiles from `tile` on, and the box's first token in it; loaded well before it is used.
+    const int span = 32 / p.boxes;
     struct Boxes {
         int32_t page, token;
-        uint32_t mask;             // boxes whose page is there, or that lie behind the sequence
+        bool inside;               // before the sequence's end
     };
     auto look_up = [&](int32_t tile) {
-        Boxes x{ap.b.n_pages, 0, ~0u};
+        Boxes x{0, 0, false};
         const int64_t key = static_cast<int64_t>(tile) * S::kKeys + lane * p.box_keys;
-        bool bad = false;
-        if (lane < p.boxes && key < a.keys) {
-            const int64_t i = key / pt;
-            x.token = static_cast<int32_t>(key - i * pt);
+        if (key < a.keys && tile + lane / p.boxes < a.tile1) {
+            const int32_t i = static_cast<int32_t>(key) / pt;
+            x.inside = true;
+            x.token = static_cast<int32_t>(key) - i * pt;
             x.page = ap.b.table[static_cast<int64_t>(a.table_row) * ap.b.max_pages + i];
-            bad = x.page < 0 || x.page >= ap.b.n_pages;
-            if (bad) x.page = ap.b.n_pages;
         }
-        x.mask = ~__ballot_sync(~0u, bad);
-        if (x.mask != ~0u) err |= GDN_PAGES_ERR_PAGE;
         return x;
     };
-    auto load_half = [&](const CUtensorMap* map, const Boxes& x, int half) {
+    // What is behind the sequence or has no page is fetched from behind the cache's end, which reads as zeros.
+    auto settle = [&](Boxes& x) {
+        const bool bad = x.inside && (x.page < 0 || x.page >= ap.b.n_pages);
+        if (!x.inside || bad) x.page = ap.b.n_pages;
+        if (bad) err |= GDN_PAGES_ERR_PAGE;
+        return ~__ballot_sync(~0u, bad);  // boxes that have a page, or need none
+    };
+    // Tile i of the span.
+    auto load_half = [&](const CUtensorMap* map, const Boxes& x, uint32_t mask, int i, int half) {
         const uint32_t st = n % S::kStages, use = n / S::kStages;
         if (use > 0 && !wait(sh.kv_empty + st, (use - 1) & 1)) return false;
         if (elect_one()) {
-            sh.stage_mask[st] = x.mask;
+            sh.stage_mask[st] = mask >> (i * p.boxes) | ~0u << p.boxes;
             mbar_arrive_expect_tx(sh.kv_full + st, S::kKvBytes);
         }
         __syncwarp();
-        for (int b = 0; b < p.boxes; ++b) {
-            const int32_t page = __shfl_sync(~0u, x.page, b), token = __shfl_sync(~0u, x.token, b);
-            if (elect_one()) {
-#pragma unroll
-                for (int c = 0; c < S::kChunks; ++c)
-                    tma_load_4d(kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + b * p.box_keys * 128, map, sh.kv_full + st,
-                                (half * S::kChunks + c) * 64, token, a.kv_head, page);
-            }
-            __syncwarp();
-        }
+        const int b = lane / S::kChunks, c = lane % S::kChunks;  // at most 16 boxes of 2 chunks
+        const int32_t page = __shfl_sync(~0u, x.page, (i * p.boxes + b) & 31), token = __shfl_sync(~0u, x.token, (i * p.boxes + b) & 31);
+        if (b < p.boxes)
+            tma_load_4d(kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + b * p.box_keys * 128, map, sh.kv_full + st,
+                        (half * S::kChunks + c) * 64, token, a.kv_head, page);
+        __syncwarp();
         ++n;
         return true;
     };
-    auto load = [&](const CUtensorMap* map, const Boxes& x) {
+    auto load = [&](const CUtensorMap* map, const Boxes& x, uint32_t mask, int i) {
         for (int half = 0; half < S::kHalves; ++half)
-            if (!load_half(map, x, half)) return false;
+            if (!load_half(map, x, mask, i, half)) return false;
         return true;
     };
 
@@ -308,75 +376,109 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         }
         __syncwarp();
         ++qn;
-        Boxes now = look_up(a.tile0);
-        if (kStreams == 1) ok = load(map_k, now);
-        for (int32_t tile = a.tile0; ok && tile < a.tile1; ++tile) {
-            const bool next = tile + 1 < a.tile1;
-            Boxes then = now;
-            if (next) then = look_up(tile + 1);
-            if (kStreams == 2)
-                ok = load(map_k, now) && load(map_v, now);
-            else
-                ok = (!next || load(map_k, then)) && load(map_v, now);
-            now = then;
+        // Two spans of pages: the one that keys are fetched from (kStreams == 1: a tile ahead of the values), and the next one.
+        Boxes ahead = look_up(a.tile0), keys = ahead, vals = ahead;
+        uint32_t key_mask = 0, val_mask = 0;
+        auto load_keys = [&](int32_t j) {
+            const int i = j % span;
+            if (i == 0) {
+                keys = ahead;
+                ahead = look_up(a.tile0 + j + span);
+                key_mask = settle(keys);
+            }
+            return load(map_k, keys, key_mask, i);
+        };
+        const int32_t tiles = a.tile1 - a.tile0;
+        if (kStreams == 1) ok = load_keys(0);
+        for (int32_t j = 0; ok && j < tiles; ++j) {
+            if (kStreams == 2) ok = load_keys(j);
+            if (j % span == 0) {  // the values' pages are those of the keys, before these go on
+                vals = keys;
+                val_mask = key_mask;
+            }
+            if (kStreams == 1 && j + 1 < tiles) ok = load_keys(j + 1);
+            ok = ok && load(map_v, vals, val_mask, j % span);
         }
     }
-    if (lane == 0) kv_report(status, err);
+    kv_report(status, err);
     if (*static_cast<volatile int32_t*>(&sh.abort)) {  // no copy may be under way when the block ends
         for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) mbar_wait(sh.kv_full + i % S::kStages, i / S::kStages & 1);
         for (uint32_t i = qn > S::kQSlots ? qn - S::kQSlots : 0; i < qn; ++i) mbar_wait(sh.q_full + i % S::kQSlots, i / S::kQSlots & 1);
     }
 }
 
-// ------------------------------------------------------------------------------------------------ warp 1: products
-// The whole warp goes through it, converged, so that addresses and descriptors stay in uniform registers; one lane issues.  What is
-// issued completes in order, so that a product may overwrite the S whose P an earlier one reads.
+// ------------------------------------------------------------------------------------------------ warps 1 and 2: products
+// A warp a stream.  All of it goes through this converged, so that addresses and descriptors stay in uniform registers; one lane issues.
+// What a warp issues completes in order, so that a product may overwrite the S whose P an earlier one reads.  (One warp for both
+// streams was what bound the kernel: waits, barriers and bookkeeping between two rows of products cost it more than the products.)
 template <class S, int kStreams>
-__device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, uint32_t tmem, int lane) {
+__device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, uint32_t tmem, int stream, int lane) {
     int32_t* status = p.a.b.device_status;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
-    const uint32_t q_at = smem_u32(q_s), kv_at = smem_u32(kv_s);
-    uint32_t n = 0, qn = 0, g = 0, seen0 = 0, seen1 = 0;
+    const uint64_t dq0 = desc_kmajor_sw128(smem_u32(q_s) + stream * S::kQBytes), dk0 = desc_kmajor_sw128(smem_u32(kv_s));
+    const uint64_t dv0 = desc_mnmajor_sw128(smem_u32(kv_s), S::kKeys * 128);
+    const bool full = p.k_steps == S::kChunks * 4;
+    const uint32_t o_at = tmem + S::kTmemO + stream * 128;
+    uint32_t st = 0, ph = 0, qn = 0, g = 0, seen = 0, tails = 0, turns = 0;  // stage and its phase; units; tiles
 
-    // S in slot `slot` (+)= row tile q times the keys of stage st; with the last half the slot's mask goes along.
-    auto scores = [&](int slot, uint32_t q, uint32_t st, int half) {
-        const uint64_t dq = desc_kmajor_sw128(q_at + q * S::kQBytes + half * (S::kChunks * kRowTile * 128));
-        const uint64_t dk = desc_kmajor_sw128(kv_at + st * S::kKvBytes);
-#pragma unroll
-        for (int i = 0; i < S::kChunks * 4; ++i)
-            if (i < p.k_steps)
-                mma_ss_elect(tmem + slot * 128, dq + ((i / 4) * (kRowTile * 128) + (i % 4) * 32) / 16,
-                            dk + ((i / 4) * (S::kKeys * 128) + (i % 4) * 32) / 16, p.idesc_qk, half > 0 || i > 0);
+    auto arrived = [&]() { return wait(sh.kv_full + st, ph); };
+    auto arrived_next = [&]() { return st + 1 == S::kStages ? wait(sh.kv_full, ph ^ 1) : wait(sh.kv_full + st + 1, ph); };
+    // The two warps take turns, so that the tensor cores finish one stream's products while the other's exponentials are computed;
+    // first come, first served, they end up in step, with both waiting for either.
+    auto turn = [&]() {
+        const bool mine = stream == 0 && turns == 0;
+        const uint32_t phase = turns++ - (stream == 0 ? 1 : 0);
+        return mine || wait(sh.turn + stream, phase & 1);
+    };
+    auto pass = [&]() {
+        if (lane == 0) mbar_arrive(sh.turn + 1 - stream);
+        __syncwarp();
+    };
+    auto advance = [&]() {
+        if (++st == S::kStages) {
+            st = 0;
+            ph ^= 1;
+        }
+    };
+    // S in slot `slot` (+)= row tile q times the keys of the present stage; with the last half the slot's mask goes along.
+    auto scores = [&](int slot, uint32_t q, int half) {
+        const uint32_t mask = sh.stage_mask[st];
+        const uint64_t dq = dq0 + (q * S::kQBytes + half * (S::kChunks * kRowTile * 128)) / 16, dk = dk0 + st * (S::kKvBytes / 16);
+        if (full)
+            issue_scores<S::kChunks * 4>(tmem + slot * 128, dq, dk, p.idesc_qk, half > 0);
+        else
+            for (int i = 0; i < p.k_steps; ++i)
+                mma_ss_elect(tmem + slot * 128, dq + (i / 4) * 1024 + (i % 4) * 2, dk + (i / 4) * 1024 + (i % 4) * 2, p.idesc_qk, i > 0);
         if (half == S::kHalves - 1) {
             mma_commit_elect(sh.s_full + slot);
             if (lane == 0) {
-                sh.slot_mask[slot] = sh.stage_mask[st];
+                sh.slot_mask[slot] = mask;
                 mbar_arrive(sh.s_full + slot);
             }
             __syncwarp();
         }
+        mma_commit_elect(sh.kv_empty + st);
     };
-    // O of stream s (+)= P in slot `slot` times the values of stage st.
-    auto values = [&](int slot, int s, uint32_t st, int half, bool add) {
-        const uint64_t dv = desc_mnmajor_sw128(kv_at + st * S::kKvBytes, S::kKeys * 128);
-#pragma unroll
-        for (int i = 0; i < S::kKeys / 16; ++i)
-            mma_ts_elect(tmem + S::kTmemO + (s + half) * 128, tmem + slot * 128 + i * 8, dv + i * (2048 / 16), p.idesc_pv, add || i > 0);
-        if (half == S::kHalves - 1) mma_commit_elect(sh.pv_done + s);
+    // O (+)= P in slot `slot`, the first or the last 64 keys of it, times the values of the present stage.
+    auto values = [&](int slot, int half, int keys64, bool add) {
+        issue_values(o_at + half * 128, tmem + slot * 128 + keys64 * 32, dv0 + st * (S::kKvBytes / 16) + keys64 * (64 * 128 / 16), p.idesc_pv, add);
     };
-    // The sequence's last tile: what its page holds behind the sequence may be anything, and a weight of zero does not make nothing
-    // of it.  The exponentials of this tile are under way meanwhile.
-    auto clear_tail = [&](const AttnPart& a, int32_t tile, uint32_t st) {
-        const int64_t held = a.keys - static_cast<int64_t>(tile) * S::kKeys;
-        if (held >= S::kKeys) return;
-#pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
-            for (int i = static_cast<int>(held) * 8 + lane; i < S::kKeys * 8; i += 32)
-                *reinterpret_cast<uint4*>(kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+    auto skip = [&]() {  // a stage that this stream has no use for
+        if (lane == 0) mbar_arrive(sh.kv_empty + st);
         __syncwarp();
     };
-    auto arrived = [&](uint32_t at) { return wait(sh.kv_full + at % S::kStages, at / S::kStages & 1); };
+    // The sequence's last tile: what its page holds behind the sequence may be anything, and a weight of zero does not make nothing of
+    // it.  The warps take turns row by row.  The exponentials of this tile are under way meanwhile.
+    auto clear_tail = [&](int held) {
+        for (int i = held + stream; i < S::kKeys; i += kStreams)
+            for (int c = lane; c < S::kChunks * 8; c += 32)
+                *reinterpret_cast<uint4*>(kv_s + st * S::kKvBytes + c / 8 * (S::kKeys * 128) + i * 128 + c % 8 * 16) = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (kStreams == 1) return true;
+        if (lane == 0) mbar_arrive(&sh.tail_done);
+        return wait(&sh.tail_done, tails++ & 1);
+    };
     auto run = [&]() {
         for (uint32_t k = 0;; ++k) {
             if (!wait(sh.part_full + k % kParts, k / kParts & 1)) return;
@@ -390,44 +492,54 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
             if (!wait(sh.q_full + slot, qn / S::kQSlots & 1)) return;
             ++qn;
             const int32_t count = a.tile1 - a.tile0;
+            const int held = static_cast<int>(min(a.keys - static_cast<int64_t>(a.tile1 - 1) * S::kKeys, int64_t{S::kKeys}));  // of the last tile
             if constexpr (kStreams == 2) {
-                const int32_t end0 = stream_end(p, a, 0, S::kKeys) - a.tile0, end1 = stream_end(p, a, 1, S::kKeys) - a.tile0;
-                if (!arrived(n)) return;
+                const int32_t end = stream_end(p, a, stream, S::kKeys) - a.tile0;
+                if (!arrived() || !turn()) return;
                 tc_fence_after();
-                if (end0 > 0) scores(0, 0, n % S::kStages, 0);
-                if (end1 > 0) scores(1, 1, n % S::kStages, 0);
-                mma_commit_elect(sh.kv_empty + n % S::kStages);
-                if (count == 1) mma_commit_elect(sh.q_empty + slot);
-                ++n;
+                if (end > 0)
+                    scores(stream, 0, 0);
+                else
+                    skip();
+                pass();
+                if (count == 1) mma_commit_elect(sh.q_empty);
+                advance();
                 for (int32_t j = 0; j < count; ++j) {
-                    const uint32_t v_at = n % S::kStages, k_at = (n + 1) % S::kStages;
                     const bool next = j + 1 < count;
-                    if (!arrived(n) || (next && !arrived(n + 1))) return;
-                    clear_tail(a, a.tile0 + j, v_at);
-                    if (j < end0) {
-                        if (!wait(sh.p_full + 0, seen0++ & 1)) return;
+                    if (!arrived()) return;
+                    if (!next && held < S::kKeys && !clear_tail(held)) return;
+                    if (next && !arrived_next()) return;
+                    if (j < end && !wait(sh.p_half + stream, seen & 1)) return;
+                    if (!turn()) return;
+                    if (j < end) {
                         tc_fence_after();
-                        values(0, 0, v_at, 0, j > 0);
-                    }
-                    if (j + 1 < end0) scores(0, 0, k_at, 0);
-                    if (j < end1) {
-                        if (!wait(sh.p_full + 1, seen1++ & 1)) return;
+                        values(stream, 0, 0, j > 0);
+                        if (!wait(sh.p_full + stream, seen++ & 1)) return;
                         tc_fence_after();
-                        values(1, 1, v_at, 0, j > 0);
+                        values(stream, 0, 1, true);
+                        if (j + 1 == end) mma_commit_elect(sh.pv_done + stream);
+                        mma_commit_elect(sh.kv_empty + st);
+                    } else {
+                        skip();
                     }
-                    if (j + 1 < end1) scores(1, 1, k_at, 0);
-                    mma_commit_elect(sh.kv_empty + v_at);
-                    if (next) mma_commit_elect(sh.kv_empty + k_at);
-                    if (j + 2 == count) mma_commit_elect(sh.q_empty + slot);
-                    n += next ? 2 : 1;
+                    advance();
+                    if (next) {
+                        if (j + 1 < end)
+                            scores(stream, 0, 0);
+                        else
+                            skip();
+                        if (j + 2 == count) mma_commit_elect(sh.q_empty);
+                        advance();
+                    }
+                    pass();
                 }
             } else {
                 auto all_scores = [&](int s_slot) {
-                    for (int half = 0; half < S::kHalves; ++half, ++n) {
-                        if (!arrived(n)) return false;
+                    for (int half = 0; half < S::kHalves; ++half) {
+                        if (!arrived()) return false;
                         tc_fence_after();
-                        scores(s_slot, slot, n % S::kStages, half);
-                        mma_commit_elect(sh.kv_empty + n % S::kStages);
+                        scores(s_slot, slot, half);
+                        advance();
                     }
                     return true;
                 };
@@ -436,13 +548,17 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
                 for (int32_t j = 0; j < count; ++j, ++g) {
                     if (j + 1 < count && !all_scores((g + 1) & 1)) return;
                     if (j + 2 == count) mma_commit_elect(sh.q_empty + slot);
-                    for (int half = 0; half < S::kHalves; ++half, ++n) {
-                        if (!arrived(n)) return;
-                        clear_tail(a, a.tile0 + j, n % S::kStages);
-                        if (half == 0 && !wait(sh.p_full + (g & 1), g / 2 & 1)) return;
-                        tc_fence_after();
-                        values(g & 1, 0, n % S::kStages, half, j > 0);
-                        mma_commit_elect(sh.kv_empty + n % S::kStages);
+                    for (int half = 0; half < S::kHalves; ++half) {
+                        if (!arrived()) return;
+                        if (j + 1 == count && held < S::kKeys && !clear_tail(held)) return;
+                        for (int h = 0; h < 2; ++h) {
+                            if (half == 0 && !wait((h ? sh.p_full : sh.p_half) + (g & 1), g / 2 & 1)) return;
+                            tc_fence_after();
+                            values(g & 1, half, h, h > 0 || j > 0);
+                        }
+                        if (half == S::kHalves - 1) mma_commit_elect(sh.pv_done + (g & 1));
+                        mma_commit_elect(sh.kv_empty + st);
+                        advance();
                     }
                 }
             }
@@ -450,8 +566,8 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
     };
     run();
     __syncwarp();
-    mma_commit_elect(&sh.drain);  // no product may be under way when TMEM is given back
-    mbar_wait(&sh.drain, 0);
+    mma_commit_elect(sh.drain + stream);  // no product may be under way when TMEM is given back
+    mbar_wait(sh.drain + stream, 0);
 }
 
 // ------------------------------------------------------------------------------------------------ warps 4..: exponentials, results
@@ -465,7 +581,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
     const int row = warp * 32 + lane, tile_t = row / ap.group, g = row - tile_t * ap.group, t = stream * p.row_tokens + tile_t;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_at = tmem + lanes + S::kTmemO + stream * 128;
-    uint32_t count = 0;            // tiles of this stream so far
+    uint32_t count = 0, done = 0;  // tiles, and parts with tiles, of this stream so far
     uint32_t k = 0;
     bool ok = true;
     for (; ok; ++k) {
@@ -484,6 +600,9 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
         const int32_t hi = ap.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
         const int32_t lo = ap.window ? static_cast<int32_t>(max(pos - ap.window + 1, int64_t{0})) : 0;
         const bool live = __any_sync(~0u, mine);
+        // tiles that every row of this warp sees whole: [clean0, clean1)
+        const int32_t clean0 = __reduce_max_sync(~0u, mine ? static_cast<int32_t>((static_cast<int64_t>(lo) + S::kKeys - 1) / S::kKeys) : 0);
+        const int32_t clean1 = __reduce_min_sync(~0u, mine ? hi / S::kKeys : 0x7fffffff);
         const int32_t tiles = kStreams == 2 ? stream_end(p, a, stream, S::kKeys) - a.tile0 : a.tile1 - a.tile0;
         float m = -INFINITY, l = 0.f;  // the maximum as used, less the offset; the sum of weights relative to it
         for (int32_t j = 0; j < tiles; ++j, ++count) {
@@ -492,7 +611,6 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
             ok = wait(sh.s_full + slot, parity);
             if (!ok) break;
             tc_fence_after();
-            float shrink = 1.f;
             if (live) {
                 const uint32_t s_at = tmem + lanes + slot * 128;
                 uint32_t s[S::kKeys];
@@ -501,15 +619,18 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < S::kKeys; c += 32) tmem_regs_ready32(s + c);
-                const int64_t key0 = static_cast<int64_t>(a.tile0 + j) * S::kKeys;
                 const uint32_t mask = sh.slot_mask[slot];
-                const bool clean = !mine || (lo <= key0 && key0 + S::kKeys <= hi);
-                if (!__all_sync(~0u, clean)) {
+                if (a.tile0 + j < clean0 || a.tile0 + j >= clean1) {
+                    const int64_t key0 = static_cast<int64_t>(a.tile0 + j) * S::kKeys;
                     const int from = static_cast<int>(max(lo - key0, int64_t{0}));
-                    const int upto = static_cast<int>(min(hi - key0, static_cast<int64_t>(S::kKeys)));
+                    const int upto = static_cast<int>(max(min(hi - key0, static_cast<int64_t>(S::kKeys)), int64_t{0}));
 #pragma unroll
-                    for (int c = 0; c < S::kKeys; ++c)
-                        if (c < from || c >= upto) s[c] = 0xff800000u;  // -infinity
+                    for (int w = 0; w < S::kKeys; w += 32) {
+                        const uint32_t bits = low_bits(upto - w) & ~low_bits(from - w);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(bits >> c & 1)) s[w + c] = 0xff800000u;  // -infinity
+                    }
                 }
                 if (mask != ~0u) {
 #pragma unroll
@@ -522,12 +643,31 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
 #pragma unroll
                 for (int c = 4; c < S::kKeys; ++c) top[c % 4] = fmaxf(top[c % 4], __uint_as_float(s[c]));
                 const float x = fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale_log2, -kOffset);
-                if (mine && (x > m + kGrowth || m == -INFINITY)) {
-                    shrink = m == -INFINITY ? 0.f : exp2_fast(m - x);
-                    m = x;
+                const bool raise = mine && x > m + kGrowth;
+                const bool rescale = __any_sync(~0u, raise);
+                float shrink = 1.f;
+                if (rescale) {
+                    const float now = raise ? x : m;
+                    shrink = raise ? exp2_fast(m - now) : 1.f;  // 0 for a row's first keys
+                    m = now;
                     l *= shrink;
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (j > 0 && rescale) {
+                    // With two streams S came after the last product on O; with one it may still be under way.
+                    if (kStreams == 1) {
+                        ok = wait(sh.pv_done + (count - 1 & 1), (count - 1) / 2 & 1);
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_wait(o_at + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st32(o_at + c, o);
+                    }
+                }
                 const float base = m == -INFINITY ? 0.f : m;
                 const uint64_t by = both(p.scale_log2, p.scale_log2), less = both(-base, -base);
                 uint64_t sum0 = 0, sum1 = 0;
@@ -547,35 +687,32 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
                         w[c / 2 + 1] = pack16<E>(e[2], e[3]);
                     }
                     tmem_st32(s_at + 32 * h, w);
+                    if (h == 0) {
+                        tmem_wait_st();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sh.p_half + slot);
+                    }
                 }
                 float s0, s1, s2, s3;
                 split(sum0, s0, s1);
                 split(sum1, s2, s3);
                 l += (s0 + s1) + (s2 + s3);
             }
-            if (j > 0) {
-                ok = wait(sh.pv_done + stream, (count - 1) & 1);
-                if (!ok) break;
-                if (__any_sync(~0u, shrink != 1.f)) {
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_ld32_wait(o_at + c, o);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
-                        tmem_st32(o_at + c, o);
-                    }
-                }
-            }
+            if (!ok) break;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(sh.p_full + slot);
+            if (lane == 0) {
+                if (!live) mbar_arrive(sh.p_half + slot);
+                mbar_arrive(sh.p_full + slot);
+            }
         }
         if (!ok) break;
         if (tiles > 0) {
-            ok = wait(sh.pv_done + stream, (count - 1) & 1);
+            // Two streams: a phase a part.  One: a phase a tile, on two barriers in turn: a wait tells a phase only from its neighbours,
+            // and the product before the last may be under way, or both may be done.
+            ok = kStreams == 1 ? wait(sh.pv_done + (count - 1 & 1), (count - 1) / 2 & 1) : wait(sh.pv_done + stream, done++ & 1);
             if (!ok) break;
             tc_fence_after();
         }
@@ -662,20 +799,25 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(sh.kv_full + i, 1);
-            mbar_init(sh.kv_empty + i, 1);
+            mbar_init(sh.kv_empty + i, kStreams);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.q_full + i, 1);
-            mbar_init(sh.q_empty + i, 1);
+            mbar_init(sh.q_empty + i, kStreams);
             mbar_init(sh.s_full + i, 2);     // the product, and the slot's mask
-            mbar_init(sh.p_full + i, 4);     // a warpgroup's warps
+            mbar_init(sh.p_half + i, 4);     // a warpgroup's warps
+            mbar_init(sh.p_full + i, 4);
             mbar_init(sh.pv_done + i, 1);
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(sh.part_full + i, 1);
-            mbar_init(sh.part_empty + i, 1 + 4 * kStreams);
+            mbar_init(sh.part_empty + i, 5 * kStreams);
         }
-        mbar_init(&sh.drain, 1);
+        mbar_init(&sh.tail_done, 2);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(sh.turn + i, 1);
+            mbar_init(sh.drain + i, 1);
+        }
         sh.abort = 0;
         fence_mbar_init();
         prefetch_tensormap(&map_q);
@@ -691,10 +833,11 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     if (warp < 4) {
+        if constexpr (kStreams == 2) regs_dec<80>();
         if (warp == 0) {
             produce<S, kStreams>(p, &map_q, &map_k, &map_v, sh, q_s, kv_s, lane);
-        } else if (warp == 1) {
-            multiply<S, kStreams>(p, sh, q_s, kv_s, tmem, lane);
+        } else if (warp <= kStreams) {
+            multiply<S, kStreams>(p, sh, q_s, kv_s, tmem, warp - 1, lane);
         } else if (warp == 3 && lane == 0) {
             p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
             AttnWalk walk;
@@ -704,6 +847,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
                 if (a.tile0 == a.first && a.tile1 < a.last) attn_note_join(p.a, a, block, walk.at.share);
         }
     } else {
+        if constexpr (kStreams == 2) regs_inc<208>();  // 128 x 80 + 256 x 208 of the 384 x 168 registers that the block has
         exponentiate<E, S, kDim, kStreams>(p, sh, tmem, (warp - 4) / 4, warp & 3, lane, block);
     }
     __syncwarp();
