@@ -2,6 +2,7 @@
 // host side, the kernel on CUDA cores, and the join of units that were cut.
 #include <cmath>
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 #include "gdn_attention_tc.cuh"
 
@@ -26,6 +27,9 @@ struct alignas(sizeof(E) * V) Vec {
     E e[V];
 };
 
+// The lowest n bits, n of any size and sign.
+__device__ __forceinline__ uint64_t low_bits64(int64_t n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
 // Floats from row to row in shared memory: a multiple of 4 that is 4 more than one of 32, so that 16-byte accesses of successive
 // rows fall into different banks.
 __host__ __device__ inline int row_floats(int D) { return (D + 3) / 4 * 4 % 32 == 4 ? (D + 3) / 4 * 4 : (D + 31) / 32 * 32 + 4; }
@@ -33,9 +37,10 @@ __host__ __device__ inline int row_floats(int D) { return (D + 3) / 4 * 4 % 32 =
 size_t simple_smem(int D) { return sizeof(float) * (3 * kRows * row_floats(D) + kRows * (kKeys + 4)) + kKeys * 2 * sizeof(int64_t); }
 
 template <class E, int kVec, int kCols>
-__global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1) attention_simple_kernel(const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ AttnScan<kThreads> scan;
+    __shared__ uint32_t there_s[2];        // the keys of a tile that have a page, a bit a key
     const int D = p.c.head_dim, D4 = (D + 3) / 4 * 4, S = row_floats(D);
     float* q_s = reinterpret_cast<float*>(smem);
     float* k_s = q_s + kRows * S;
@@ -44,30 +49,27 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
     int64_t* off_s = reinterpret_cast<int64_t*>(w_s + kRows * (kKeys + 4)); // offset of a key's row of k and of v; -1: no page
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int32_t block = blockIdx.x;
+    griddep_launch_dependents();  // the join's blocks, which wait for this kernel's end
     if (tid == 0) p.joins[2 * block] = make_int4(0, 0, 0, 0);
     AttnWalk walk;
     walk.begin(attn_start<kThreads>(p, block, gridDim.x, scan));
     AttnPart a;
     uint32_t err = 0;
+    const int warp = tid >> 5, lane = tid & 31, pieces = D4 / kVec;  // with kVec = 4, D is a multiple of 4
     while (walk.next(p, a)) {
         const int rows = a.tokens * a.heads;
         __syncthreads();
-        for (int i = tid; i < kRows * D4; i += kThreads) {
-            const int r = i / D4, d = i - r * D4;
-            float x = 0.f;
-            if (r < rows && d < D) {
-                const int t = r / a.heads, g = r - t * a.heads;
-                x = wide(static_cast<const E*>(p.q)[(a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D + d]);
-            }
-            q_s[r * S + d] = x;
+        for (int r = warp; r < kRows; r += kThreads / 32) {
+            const int t = r / a.heads, g = r - t * a.heads;
+            const E* q = static_cast<const E*>(p.q) + (a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D;
+            for (int d = lane; d < D4; d += 32) q_s[r * S + d] = r < rows && d < D ? wide(q[d]) : 0.f;
         }
         // each row's keys: [lo, hi)
         int32_t lo[4], hi[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int r = 4 * ty + i;
-            const int64_t pos = static_cast<int64_t>(a.pos0) + r / a.heads;
-            hi[i] = r < rows ? (p.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys) : 0;
+            const int64_t pos = static_cast<int64_t>(a.pos0) + (4 * ty + i) / a.heads;
+            hi[i] = p.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
             lo[i] = p.window ? static_cast<int32_t>(max(pos - p.window + 1, int64_t{0})) : 0;
         }
         float m[4], l[4], acc[4][4 * kCols];
@@ -84,32 +86,62 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
                 const int64_t key = key0 + tid;
                 int64_t ko = -1, vo = -1;
                 if (key < a.keys) {
-                    const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + key / p.b.page_tokens];
+                    const int32_t at = static_cast<int32_t>(key) / p.b.page_tokens, slot = static_cast<int32_t>(key) - at * p.b.page_tokens;
+                    const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + at];
                     if (page < 0 || page >= p.b.n_pages) {
                         err |= GDN_PAGES_ERR_PAGE;
                     } else {
-                        const int64_t slot = key % p.b.page_tokens;
                         ko = page * p.c.k_page_stride + slot * p.c.k_token_stride + a.kv_head * p.c.k_head_stride;
                         vo = page * p.c.v_page_stride + slot * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
                     }
                 }
                 off_s[2 * tid] = ko;
                 off_s[2 * tid + 1] = vo;
+                const unsigned there = __ballot_sync(~0u, ko >= 0);
+                if (lane == 0) there_s[warp] = there;
             }
             __syncthreads();
-            const int pieces = D4 / kVec;  // with kVec = 4, D is a multiple of 4
-            for (int i = tid; i < kKeys * pieces; i += kThreads) {
-                const int r = i / pieces, d = (i - r * pieces) * kVec;
-                const int64_t ko = off_s[2 * r], vo = off_s[2 * r + 1];
-                Vec<E, kVec> k{}, v{};
-                if (ko >= 0 && d < D) {
-                    k = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.k) + ko + d);
-                    v = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.v) + vo + d);
+            // Keys and values, a warp a row; rows that are not there are zero.
+            if constexpr (kVec == 4 && sizeof(E) == 4) {
+                for (int r = warp; r < kKeys; r += kThreads / 32) {
+                    const int64_t ko = off_s[2 * r], vo = off_s[2 * r + 1];
+                    for (int d = 4 * lane; d < D; d += 128) {
+                        if (ko >= 0) {
+                            cp_async16(k_s + r * S + d, static_cast<const E*>(p.c.k) + ko + d);
+                            cp_async16(v_s + r * S + d, static_cast<const E*>(p.c.v) + vo + d);
+                        } else {
+                            *reinterpret_cast<float4*>(k_s + r * S + d) = *reinterpret_cast<float4*>(v_s + r * S + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        }
+                    }
                 }
+                cp_async_commit();
+                cp_async_wait<0>();
+            } else {
+                for (int d0 = 0; d0 < pieces; d0 += 32) {
+                    const int d = (d0 + lane) * kVec;
+                    const bool in = d < D;
+#pragma unroll 2
+                    for (int r0 = warp; r0 < kKeys; r0 += 4 * (kThreads / 32)) {
+                        Vec<E, kVec> k[4]{}, v[4]{};
+                        bool ok[4];
 #pragma unroll
-                for (int j = 0; j < kVec; ++j) {
-                    k_s[r * S + d + j] = ko >= 0 && d < D ? wide(k.e[j]) : 0.f;
-                    v_s[r * S + d + j] = ko >= 0 && d < D ? wide(v.e[j]) : 0.f;
+                        for (int u = 0; u < 4; ++u) {
+                            const int64_t ko = off_s[2 * (r0 + 8 * u)], vo = off_s[2 * (r0 + 8 * u) + 1];
+                            ok[u] = in && ko >= 0;
+                            if (ok[u]) {
+                                k[u] = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.k) + ko + d);
+                                v[u] = *reinterpret_cast<const Vec<E, kVec>*>(static_cast<const E*>(p.c.v) + vo + d);
+                            }
+                        }
+#pragma unroll
+                        for (int u = 0; u < 4; ++u)
+#pragma unroll
+                            for (int j = 0; j < kVec; ++j)
+                                if (d + j < D4) {
+                                    k_s[(r0 + 8 * u) * S + d + j] = ok[u] ? wide(k[u].e[j]) : 0.f;
+                                    v_s[(r0 + 8 * u) * S + d + j] = ok[u] ? wide(v[u].e[j]) : 0.f;
+                                }
+                    }
                 }
             }
             __syncthreads();
@@ -119,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) s[i][c] = 0.f;
+#pragma unroll 2
                 for (int d = 0; d < D4; d += 4) {
                     float4 x[4], y[4];
 #pragma unroll
@@ -135,21 +168,25 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
                             s[i][c] = fmaf(x[i].w, y[c].w, s[i][c]);
                         }
                 }
-                bool cut = false;  // some of the tile's keys are hidden from some of this thread's rows
+                // The keys of the tile that each row sees, a bit a key; rows behind the unit's end see all that is there.
+                const uint64_t there = there_s[0] | static_cast<uint64_t>(there_s[1]) << 32;
+                uint64_t seen[4];
+                bool cut = there != ~0ull;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int64_t key = key0 + tx + 16 * c;
-                    const bool there = off_s[2 * (tx + 16 * c)] >= 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool seen = there && key >= lo[i] && key < hi[i];
-                        s[i][c] = seen ? s[i][c] * p.scale_log2 : -INFINITY;
-                        cut |= !seen;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    seen[i] = there;
+                    if (4 * ty + i < rows) seen[i] &= low_bits64(hi[i] - key0) & ~low_bits64(lo[i] - key0);
+                    cut |= seen[i] != ~0ull;
                 }
+                cut = __any_sync(~0u, cut);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) s[i][c] = !cut || seen[i] >> (tx + 16 * c) & 1 ? s[i][c] * p.scale_log2 : -INFINITY;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     float top = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
                     for (int d = 8; d; d /= 2) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
                     const float now = fmaxf(m[i], top), base = now == -INFINITY ? 0.f : now;
                     const float keep = exp2f(m[i] - base);
@@ -160,19 +197,22 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
                         sum += w;
                         w_s[(4 * ty + i) * (kKeys + 4) + tx + 16 * c] = w;
                     }
-                    for (int d = 8; d; d /= 2) sum += __shfl_xor_sync(~0u, sum, d);
                     m[i] = now;
-                    l[i] = l[i] * keep + sum;
+                    l[i] = l[i] * keep + sum;  // of this thread's keys; the 16 threads of a row join at the unit's end
 #pragma unroll
                     for (int c = 0; c < 4 * kCols; ++c) acc[i][c] *= keep;
                 }
-                cut = __any_sync(~0u, cut);
                 __syncwarp();
-                if (!cut) {
+                auto values = [&](auto some) {  // some: a hidden key's value is left out, not taken times zero: it may be infinite or NaN
+#pragma unroll 2
                     for (int k = 0; k < kKeys; k += 4) {
                         float4 w[4];
+                        uint32_t bits[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(w_s + (4 * ty + i) * (kKeys + 4) + k);
+                        for (int i = 0; i < 4; ++i) {
+                            w[i] = *reinterpret_cast<const float4*>(w_s + (4 * ty + i) * (kKeys + 4) + k);
+                            bits[i] = static_cast<uint32_t>(seen[i] >> k);
+                        }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -182,35 +222,27 @@ __global__ void __launch_bounds__(kThreads) attention_simple_kernel(const __grid
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const float u = j == 0 ? w[i].x : j == 1 ? w[i].y : j == 2 ? w[i].z : w[i].w;
-                                    acc[i][4 * c] = fmaf(u, v.x, acc[i][4 * c]);
-                                    acc[i][4 * c + 1] = fmaf(u, v.y, acc[i][4 * c + 1]);
-                                    acc[i][4 * c + 2] = fmaf(u, v.z, acc[i][4 * c + 2]);
-                                    acc[i][4 * c + 3] = fmaf(u, v.w, acc[i][4 * c + 3]);
+                                    if (!some.value || bits[i] >> j & 1) {
+                                        acc[i][4 * c] = fmaf(u, v.x, acc[i][4 * c]);
+                                        acc[i][4 * c + 1] = fmaf(u, v.y, acc[i][4 * c + 1]);
+                                        acc[i][4 * c + 2] = fmaf(u, v.z, acc[i][4 * c + 2]);
+                                        acc[i][4 * c + 3] = fmaf(u, v.w, acc[i][4 * c + 3]);
+                                    }
                                 }
                             }
                     }
-                } else {  // a hidden key's value is left out, not taken times zero: it may be infinite or NaN
-                    for (int k = 0; k < kKeys; ++k) {
-                        const int64_t key = key0 + k;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (key < lo[i] || key >= hi[i]) continue;
-                            const float u = w_s[(4 * ty + i) * (kKeys + 4) + k];
-#pragma unroll
-                            for (int c = 0; c < kCols; ++c) {
-                                if (4 * tx + 64 * c >= D4) break;
-                                const float4 v = *reinterpret_cast<const float4*>(v_s + k * S + 4 * tx + 64 * c);
-                                acc[i][4 * c] = fmaf(u, v.x, acc[i][4 * c]);
-                                acc[i][4 * c + 1] = fmaf(u, v.y, acc[i][4 * c + 1]);
-                                acc[i][4 * c + 2] = fmaf(u, v.z, acc[i][4 * c + 2]);
-                                acc[i][4 * c + 3] = fmaf(u, v.w, acc[i][4 * c + 3]);
-                            }
-                        }
-                    }
-                }
+                };
+                if (cut)
+                    values(std::true_type());
+                else
+                    values(std::false_type());
             }
             __syncthreads();
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int d = 8; d; d /= 2) l[i] += __shfl_xor_sync(~0u, l[i], d);
         const bool whole = a.tile0 == a.first && a.tile1 == a.last;
         const int32_t slot = attn_slot(a, block);
 #pragma unroll
@@ -272,6 +304,7 @@ constexpr int kJoinWarps = 8;
 template <class E>
 __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const __grid_constant__ AttnParams p) {
     const int lane = threadIdx.x & 31, r = blockIdx.y * kJoinWarps + (threadIdx.x >> 5), block = blockIdx.x;
+    griddep_wait();
     const int4 head = p.joins[2 * block];
     if (head.x == 0 || r >= head.y * head.w) return;
     const int4 first = p.joins[2 * block + 1];
@@ -287,16 +320,28 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
     float sum = 0.f, acc[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] = 0.f;
-    for (int k = 0; k < parts; ++k) {
-        const int64_t at = place(k);
-        const float2 ml = p.part_ml[at];
-        const float by = exp2f(ml.x - base);
-        sum = fmaf(ml.y, by, sum);
-        if (by == 0.f) continue;  // a part that sees nothing adds nothing
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+        // 32 parts' weights at a time, a lane each; their sums of values eight loads ahead
+        const float2 ml = k0 + lane < parts ? p.part_ml[place(k0 + lane)] : make_float2(-INFINITY, 0.f);
+        const float mine = exp2f(ml.x - base);
+        float more = ml.y * mine;
+        for (int d = 16; d; d /= 2) more += __shfl_xor_sync(~0u, more, d);
+        sum += more;
+        const int some = min(32, parts - k0);
+        for (int k1 = 0; k1 < some; k1 += 4) {
+            float x[4][8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const int d = lane + 32 * c;
-            if (d < D) acc[c] = fmaf(p.part_o[at * D + d], by, acc[c]);
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                    x[k][c] = k1 + k < some && lane + 32 * c < D ? p.part_o[place(k0 + k1 + k) * D + lane + 32 * c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float by = __shfl_sync(~0u, mine, (k1 + k) & 31);
+                if (k1 + k < some && by != 0.f)  // a part that sees nothing adds nothing
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) acc[c] = fmaf(x[k][c], by, acc[c]);
+            }
         }
     }
     const int t = r / head.w, g = r - t * head.w;
@@ -463,7 +508,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.tile = kKeys;
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
-    r.blocks = multiprocessors() * (simple_smem(c.head_dim) <= 110 * 1024 ? 2 : 1);
+    r.blocks = multiprocessors() * (c.head_dim <= 128 ? 2 : 1);
     if (tc_fits(p)) tc_route(&r);
     *out = r;
     return GDN_OK;
@@ -519,14 +564,18 @@ cudaError_t launch_attention_simple(const AttnParams& p, int32_t blocks, cudaStr
 }
 
 cudaError_t launch_attention_join(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
-    const dim3 grid(blocks, (p.unit_tokens * p.group + kJoinWarps - 1) / kJoinWarps);
-    if (p.c.dtype == GDN_DTYPE_F32)
-        attention_join_kernel<float><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
-    else if (p.c.dtype == GDN_DTYPE_BF16)
-        attention_join_kernel<__nv_bfloat16><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
-    else
-        attention_join_kernel<__half><<<grid, 32 * kJoinWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(blocks, (p.unit_tokens * p.group + kJoinWarps - 1) / kJoinWarps);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its blocks are there when the parts' kernel ends
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (p.c.dtype == GDN_DTYPE_F32) return cudaLaunchKernelEx(&cfg, attention_join_kernel<float>, p);
+    if (p.c.dtype == GDN_DTYPE_BF16) return cudaLaunchKernelEx(&cfg, attention_join_kernel<__nv_bfloat16>, p);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<__half>, p);
 }
 
 }  // namespace gdn

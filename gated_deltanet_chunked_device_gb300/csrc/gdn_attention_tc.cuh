@@ -796,6 +796,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     Misc<S>& sh = *reinterpret_cast<Misc<S>*>(smem + S::kTileBytes);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t block = blockIdx.x;
+    griddep_launch_dependents();  // the join's blocks, which wait for this kernel's end
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(sh.kv_full + i, 1);
