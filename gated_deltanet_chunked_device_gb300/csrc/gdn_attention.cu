@@ -417,16 +417,27 @@ bool encode(CUtensorMap* map, const void* base, gdn_dtype dtype, int rank, const
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the tensor cores can take a call: 16-bit types whose rows tiled copies can fetch (addresses and strides of 16 bytes, below
-// 2^40), pages of boxes of at least 8 tokens (the swizzle's period).
-bool tc_fits(const AttnParams& p) {
+// Whether tiled copies can fetch a call's rows: addresses and strides of 16 bytes, below 2^40, pages of boxes of at least 8 tokens
+// (the swizzle's period).
+bool tiles_fit(const AttnParams& p) {
     const gdn_kv_cache& c = p.c;
-    if (c.dtype == GDN_DTYPE_F32 || p.b.n_pages < 1 || p.b.page_tokens % 8 || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(p.q, 16))
+    if (p.b.page_tokens % 8 || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(p.q, 16))
         return false;
     auto fits = [](int64_t n, int64_t stride) { return n <= 1 || (stride % 8 == 0 && stride < (1LL << 39)); };
     return fits(p.b.n_pages, c.k_page_stride) && fits(p.b.page_tokens, c.k_token_stride) && fits(c.kv_heads, c.k_head_stride) &&
            fits(p.b.n_pages, c.v_page_stride) && fits(p.b.page_tokens, c.v_token_stride) && fits(c.kv_heads, c.v_head_stride) &&
            fits(p.b.total_tokens, p.q_stride) && fits(p.heads, c.head_dim);
+}
+
+// The widest piece of 16, 8, 4 or 2 bytes that divides every row, stride and address.
+int widest_piece(const AttnParams& p) {
+    const gdn_kv_cache& c = p.c;
+    int64_t all = 16 | reinterpret_cast<intptr_t>(p.q) | reinterpret_cast<intptr_t>(c.k) | reinterpret_cast<intptr_t>(c.v) | 2 * c.head_dim;
+    if (p.b.total_tokens > 1) all |= 2 * p.q_stride;
+    if (p.b.n_pages > 1) all |= 2 * (c.k_page_stride | c.v_page_stride);
+    if (p.b.page_tokens > 1) all |= 2 * (c.k_token_stride | c.v_token_stride);
+    if (c.kv_heads > 1) all |= 2 * (c.k_head_stride | c.v_head_stride);
+    return static_cast<int>(all & -all);
 }
 
 // The tensor cores' shape.  Two row tiles a unit pay where a sequence has, on the average, rows for more than one.
@@ -440,8 +451,9 @@ void tc_route(Route* r) {
     attn_tc::TcParams& t = r->tc;
     t.row_tokens = rows / p.group;
     p.unit_tokens = r->streams * t.row_tokens;
+    t.plain = tiles_fit(p) ? 0 : widest_piece(p);
     t.box_keys = p.tile;
-    while (p.b.page_tokens % t.box_keys) t.box_keys /= 2;
+    while (!t.plain && p.b.page_tokens % t.box_keys) t.box_keys /= 2;
     t.boxes = p.tile / t.box_keys;
     // Heads of more than 128 channels run as 256: what lies behind them reads as zeros.
     t.k_steps = D > 128 ? 8 : (D + 15) / 16;
@@ -459,13 +471,14 @@ void tc_route(Route* r) {
 cudaError_t launch_tc(const Route& r, cudaStream_t stream) {
     const AttnParams& p = r.p;
     const gdn_kv_cache& c = p.c;
-    CUtensorMap maps[3];
+    CUtensorMap maps[3]{};
     const int64_t q_dims[3] = {c.head_dim, p.heads, p.b.total_tokens}, q_strides[2] = {c.head_dim, p.q_stride};
     const int32_t q_box[3] = {64, p.group, r.tc.row_tokens}, kv_box[4] = {64, r.tc.box_keys, 1, 1};
     const int64_t kv_dims[4] = {c.head_dim, p.b.page_tokens, c.kv_heads, p.b.n_pages};
     const int64_t k_strides[3] = {c.k_token_stride, c.k_head_stride, c.k_page_stride}, v_strides[3] = {c.v_token_stride, c.v_head_stride, c.v_page_stride};
-    if (!encode(maps, p.q, c.dtype, 3, q_dims, q_strides, q_box) || !encode(maps + 1, c.k, c.dtype, 4, kv_dims, k_strides, kv_box) ||
-        !encode(maps + 2, c.v, c.dtype, 4, kv_dims, v_strides, kv_box))
+    if (!r.tc.plain &&
+        (!encode(maps, p.q, c.dtype, 3, q_dims, q_strides, q_box) || !encode(maps + 1, c.k, c.dtype, 4, kv_dims, k_strides, kv_box) ||
+         !encode(maps + 2, c.v, c.dtype, 4, kv_dims, v_strides, kv_box)))
         return cudaErrorInvalidValue;
     attn_tc::TcParams t = r.tc;
     t.a = p;
@@ -509,7 +522,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
     r.blocks = multiprocessors() * (c.head_dim <= 128 ? 2 : 1);
-    if (tc_fits(p)) tc_route(&r);
+    if (c.dtype != GDN_DTYPE_F32 && batch->n_pages > 0) tc_route(&r);  // fp32 would lose its last 13 bits there
     *out = r;
     return GDN_OK;
 }

@@ -17,7 +17,10 @@
 // 256: one row tile, the scores of the next keys ahead of the exponentials of the present ones; what counts there is the stream of
 // keys and values, 160 KB of which are on their way at any time.
 //
-// Warps: 0 finds the work and copies, 1 (and 2) issue the products, 2 owns TMEM, 3 notes cut units, 4.. exponentials and results.
+// Where tiled copies cannot fetch the rows (pages of sizes that no multiple of 8 is, heads of 100 channels) warps 0 and 3 copy them piece
+// by piece into the same layout.
+//
+// Warps: 0 finds the work and copies, 1 (and 2) issue the products, 2 owns TMEM, 3 helps with plain copies, 4.. exponentials and results.
 #pragma once
 
 #include <type_traits>
@@ -58,13 +61,16 @@ struct TcParams {
     uint32_t idesc_qk, idesc_pv;
     float scale_log2;              // positive: a negative scale negates Q in the product
     int32_t out_vec;               // results can be written 16 bytes at a time
+    int32_t plain;                 // bytes of a plain copy (16, 8, 4 or 2) where tiled copies cannot fetch the rows; 0: tiled copies
 };
 
 template <class S>
 struct Misc {
     uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2];
     uint64_t part_full[kParts], part_empty[kParts], tail_done, turn[2], drain[2];
-    uint32_t stage_mask[S::kStages], slot_mask[2];
+    uint4 stage_keys[S::kStages], slot_keys[2];  // keys that have a page (or lie behind the sequence), a bit each
+    uint32_t slot_missing[2];      // whether some of a slot's keys have none
+    int2 rows[2][2][64];           // plain copies: page and place of a warp's half of the keys of two tiles
     uint32_t tmem;
     int32_t abort;
     AttnPart parts[kParts];
@@ -88,13 +94,25 @@ __device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_
     return true;
 }
 
+// The lowest n bits, n of any size and sign.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// A bit a key from a bit a box of `keys` keys.
+__device__ __forceinline__ uint4 spread_boxes(uint32_t mask, int boxes, int keys) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+        for (int b = 0; b < boxes; ++b)
+            if (mask >> b & 1) w[i] |= low_bits((b + 1) * keys - 32 * i) & ~low_bits(b * keys - 32 * i);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // By a whole warp: all of its lanes go on, or none.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
     return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status));
 }
-
-// The lowest n bits, n of any size and sign.
-__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
@@ -332,7 +350,7 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         const uint32_t st = n % S::kStages, use = n / S::kStages;
         if (use > 0 && !wait(sh.kv_empty + st, (use - 1) & 1)) return false;
         if (elect_one()) {
-            sh.stage_mask[st] = mask >> (i * p.boxes) | ~0u << p.boxes;
+            sh.stage_keys[st] = mask == ~0u ? make_uint4(~0u, ~0u, ~0u, ~0u) : spread_boxes(mask >> (i * p.boxes), p.boxes, p.box_keys);
             mbar_arrive_expect_tx(sh.kv_full + st, S::kKvBytes);
         }
         __syncwarp();
@@ -361,6 +379,7 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         }
         __syncwarp();
         if (!more) break;
+        if (lane == 0 && a.tile0 == a.first && a.tile1 < a.last) attn_note_join(ap, a, blockIdx.x, walk.at.share);
         if (a.first == a.last) continue;
         const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
         if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
@@ -407,6 +426,144 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
     }
 }
 
+// ------------------------------------------------------------------------------------------------ warps 0 and 3: plain copies
+// `bytes` (16, 8, 4 or 2) from global to shared memory, asynchronously from 4 on, or zeros.
+__device__ __forceinline__ void copy_piece(int bytes, uint8_t* dst, const void* src, bool there) {
+    if (bytes == 8)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 8 : 0) : "memory");
+    else if (bytes == 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
+    else if (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
+    else
+        *reinterpret_cast<uint16_t*>(dst) = there ? *static_cast<const uint16_t*>(src) : static_cast<uint16_t>(0);
+}
+
+// What produce does, without tiled copies: warp `id` (0 or 1) brings its half of the rows, 64 threads arrive at a stage.  Copies of
+// kAhead stages are under way at a time; a thread waits for its own, makes them visible to the tensor cores and arrives.
+template <class E, class S, int kStreams>
+__device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, int id, int lane) {
+    constexpr int kAhead = 2;
+    const int bytes = p.plain, elems = bytes / 2;
+    const AttnParams& ap = p.a;
+    const int D = ap.c.head_dim;
+    int32_t* status = ap.b.device_status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    AttnWalk walk;
+    walk.begin(sh.scan.start);
+    AttnPart a{};
+    uint32_t n = 0, told = 0, qn = 0, err = 0;  // stages begun and handed over; units
+    bool ok = true;
+
+    auto tell = [&](uint32_t upto) {  // all but the last stages' copies are there
+        for (; told < upto; ++told) mbar_arrive(sh.kv_full + told % S::kStages);
+    };
+    auto flush = [&]() {
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        tell(n);
+    };
+    // Page and place of this warp's keys of a tile; the bits of those that have one or need none.
+    auto look_up = [&](int32_t tile, uint32_t (&bits)[2]) {
+        __syncwarp();  // the places it overwrites have been read
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t key = static_cast<int64_t>(tile) * S::kKeys + 64 * id + 32 * h + lane;
+            int2 at = make_int2(-1, 0);
+            bool bad = false;
+            if (key < a.keys) {
+                const int32_t i = static_cast<int32_t>(key) / ap.b.page_tokens;
+                at = make_int2(ap.b.table[static_cast<int64_t>(a.table_row) * ap.b.max_pages + i], static_cast<int32_t>(key) - i * ap.b.page_tokens);
+                bad = at.x < 0 || at.x >= ap.b.n_pages;
+                if (bad) at.x = -1;
+            }
+            if (bad) err |= GDN_PAGES_ERR_PAGE;
+            sh.rows[id][tile & 1][32 * h + lane] = at;
+            bits[h] = ~__ballot_sync(~0u, bad);
+        }
+        __syncwarp();
+    };
+    auto load = [&](bool values, int32_t tile, const uint32_t (&bits)[2]) {
+        const E* base = static_cast<const E*>(values ? ap.c.v : ap.c.k) + a.kv_head * (values ? ap.c.v_head_stride : ap.c.k_head_stride);
+        const int64_t page = values ? ap.c.v_page_stride : ap.c.k_page_stride, token = values ? ap.c.v_token_stride : ap.c.k_token_stride;
+        for (int half = 0; half < S::kHalves; ++half) {
+            const uint32_t st = n % S::kStages, use = n / S::kStages;
+            if (use > 0 && !wait(sh.kv_empty + st, (use - 1) & 1)) return false;
+            if (lane == 0) {
+                uint32_t* w = reinterpret_cast<uint32_t*>(sh.stage_keys + st) + 2 * id;
+                w[0] = bits[0];
+                w[1] = bits[1];
+            }
+            const int pieces = (min(D - half * 128, 128) + elems - 1) / elems;
+            for (int r = lane / 8; r < 64; r += 4) {  // eight lanes a row
+                const int2 at = sh.rows[id][tile & 1][r];
+                const E* src = base + max(at.x, 0) * page + at.y * token + half * 128;
+                const int row = 64 * id + r;
+                for (int i = lane % 8; i < pieces; i += 8) {
+                    const int x = i * bytes % 128, c = i * bytes / 128;
+                    copy_piece(bytes, kv_s + st * S::kKvBytes + c * (S::kKeys * 128) + sw128_offset(row, x / 16) + x % 16, src + i * elems, at.x >= 0);
+                }
+            }
+            cp_async_commit();
+            ++n;
+            cp_async_wait<kAhead>();
+            fence_proxy_async_smem();
+            if (n > kAhead) tell(n - kAhead);
+        }
+        return true;
+    };
+
+    for (uint32_t k = 0; ok; ++k) {
+        const bool more = walk.next(ap, a);
+        if (!more) a.tokens = 0;
+        if (id == 0) {
+            if (k >= kParts && !wait(sh.part_empty + k % kParts, (k / kParts - 1) & 1)) break;
+            if (lane == 0) {
+                sh.parts[k % kParts] = a;
+                mbar_arrive(sh.part_full + k % kParts);
+                if (more && a.tile0 == a.first && a.tile1 < a.last) attn_note_join(ap, a, blockIdx.x, walk.at.share);
+            }
+            __syncwarp();
+        }
+        if (!more) break;
+        if (a.first == a.last) continue;
+        flush();  // nobody waits for a stage whose products come before this unit's rows
+        const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
+        if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
+        const int active = a.tokens > p.row_tokens ? kStreams : 1, pieces = (D + elems - 1) / elems;
+        for (int s = 0; s < active; ++s) {
+            for (int r = id * 4 + lane / 8; r < p.row_tokens * ap.group; r += 8) {
+                const int t = r / ap.group, g = r - t * ap.group, token = s * p.row_tokens + t;
+                const bool there = token < a.tokens && g < a.heads;
+                const E* src = static_cast<const E*>(ap.q) + (a.row0 + (there ? token : 0)) * ap.q_stride + static_cast<int64_t>(a.head0 + (there ? g : 0)) * D;
+                for (int i = lane % 8; i < pieces; i += 8) {
+                    const int x = i * bytes % 128, c = i * bytes / 128;
+                    copy_piece(bytes, q_s + (slot + s) * S::kQBytes + c * (kRowTile * 128) + sw128_offset(r, x / 16) + x % 16, src + i * elems, there);
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        mbar_arrive(sh.q_full + slot);
+        ++qn;
+        uint32_t now[2], then[2] = {~0u, ~0u};
+        look_up(a.tile0, now);
+        if (kStreams == 1) ok = load(false, a.tile0, now);
+        for (int32_t tile = a.tile0; ok && tile < a.tile1; ++tile) {
+            const bool next = tile + 1 < a.tile1;
+            if (kStreams == 2) ok = load(false, tile, now);
+            if (next) look_up(tile + 1, then);
+            if (kStreams == 1 && next) ok = load(false, tile + 1, then);
+            ok = ok && load(true, tile, now);
+            now[0] = then[0];
+            now[1] = then[1];
+        }
+    }
+    flush();
+    kv_report(status, err);
+}
+
 // ------------------------------------------------------------------------------------------------ warps 1 and 2: products
 // A warp a stream.  All of it goes through this converged, so that addresses and descriptors stay in uniform registers; one lane issues.
 // What a warp issues completes in order, so that a product may overwrite the S whose P an earlier one reads.  (One warp for both
@@ -442,7 +599,7 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
     };
     // S in slot `slot` (+)= row tile q times the keys of the present stage; with the last half the slot's mask goes along.
     auto scores = [&](int slot, uint32_t q, int half) {
-        const uint32_t mask = sh.stage_mask[st];
+        const uint4 keys = sh.stage_keys[st];
         const uint64_t dq = dq0 + (q * S::kQBytes + half * (S::kChunks * kRowTile * 128)) / 16, dk = dk0 + st * (S::kKvBytes / 16);
         if (full)
             issue_scores<S::kChunks * 4>(tmem + slot * 128, dq, dk, p.idesc_qk, half > 0);
@@ -452,7 +609,9 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
         if (half == S::kHalves - 1) {
             mma_commit_elect(sh.s_full + slot);
             if (lane == 0) {
-                sh.slot_mask[slot] = mask;
+                const uint32_t missing = ~(keys.x & keys.y & keys.z & keys.w);
+                sh.slot_missing[slot] = missing;
+                if (missing) sh.slot_keys[slot] = keys;
                 mbar_arrive(sh.s_full + slot);
             }
             __syncwarp();
@@ -619,7 +778,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
                 tmem_wait_ld();
 #pragma unroll
                 for (int c = 0; c < S::kKeys; c += 32) tmem_regs_ready32(s + c);
-                const uint32_t mask = sh.slot_mask[slot];
+                const uint32_t missing = sh.slot_missing[slot];
                 if (a.tile0 + j < clean0 || a.tile0 + j >= clean1) {
                     const int64_t key0 = static_cast<int64_t>(a.tile0 + j) * S::kKeys;
                     const int from = static_cast<int>(max(lo - key0, int64_t{0}));
@@ -632,10 +791,14 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
                             if (!(bits >> c & 1)) s[w + c] = 0xff800000u;  // -infinity
                     }
                 }
-                if (mask != ~0u) {
+                if (missing) {
 #pragma unroll
-                    for (int c = 0; c < S::kKeys; ++c)
-                        if (!(mask >> (c / p.box_keys) & 1)) s[c] = 0xff800000u;
+                    for (int w = 0; w < S::kKeys; w += 32) {
+                        const uint32_t bits = reinterpret_cast<const uint32_t*>(sh.slot_keys + slot)[w / 32];
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(bits >> c & 1)) s[w + c] = 0xff800000u;
+                    }
                 }
                 float top[4];
 #pragma unroll
@@ -799,11 +962,11 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     griddep_launch_dependents();  // the join's blocks, which wait for this kernel's end
     if (tid == 0) {
         for (int i = 0; i < S::kStages; ++i) {
-            mbar_init(sh.kv_full + i, 1);
+            mbar_init(sh.kv_full + i, p.plain ? 64 : 1);
             mbar_init(sh.kv_empty + i, kStreams);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(sh.q_full + i, 1);
+            mbar_init(sh.q_full + i, p.plain ? 64 : 1);
             mbar_init(sh.q_empty + i, kStreams);
             mbar_init(sh.s_full + i, 2);     // the product, and the slot's mask
             mbar_init(sh.p_half + i, 4);     // a warpgroup's warps
@@ -821,13 +984,19 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
         }
         sh.abort = 0;
         fence_mbar_init();
-        prefetch_tensormap(&map_q);
-        prefetch_tensormap(&map_k);
-        prefetch_tensormap(&map_v);
+        if (!p.plain) {
+            prefetch_tensormap(&map_q);
+            prefetch_tensormap(&map_k);
+            prefetch_tensormap(&map_v);
+        }
     }
     if (warp == 2) {
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
+    }
+    if (p.plain) {  // channels behind the heads' end are never written: zero once and for all
+        for (int i = tid; i < S::kTileBytes / 16; i += S::kThreads) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
     }
     tc_fence_before();
     attn_start<S::kThreads>(p.a, block, gridDim.x, sh.scan);  // and the barriers are there for all
@@ -836,16 +1005,15 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     if (warp < 4) {
         if constexpr (kStreams == 2) regs_dec<80>();
         if (warp == 0) {
-            produce<S, kStreams>(p, &map_q, &map_k, &map_v, sh, q_s, kv_s, lane);
+            if (lane == 0) p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
+            if (p.plain)
+                produce_plain<E, S, kStreams>(p, sh, q_s, kv_s, 0, lane);
+            else
+                produce<S, kStreams>(p, &map_q, &map_k, &map_v, sh, q_s, kv_s, lane);
         } else if (warp <= kStreams) {
             multiply<S, kStreams>(p, sh, q_s, kv_s, tmem, warp - 1, lane);
-        } else if (warp == 3 && lane == 0) {
-            p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
-            AttnWalk walk;
-            walk.begin(sh.scan.start);
-            AttnPart a;
-            while (walk.next(p.a, a))
-                if (a.tile0 == a.first && a.tile1 < a.last) attn_note_join(p.a, a, block, walk.at.share);
+        } else if (warp == 3 && p.plain) {
+            produce_plain<E, S, kStreams>(p, sh, q_s, kv_s, 1, lane);
         }
     } else {
         if constexpr (kStreams == 2) regs_inc<208>();  // 128 x 80 + 256 x 208 of the 384 x 168 registers that the block has
