@@ -451,6 +451,7 @@ void tc_route(Route* r) {
     attn_tc::TcParams& t = r->tc;
     t.row_tokens = rows / p.group;
     p.unit_tokens = r->streams * t.row_tokens;
+    p.unit_cost = r->streams;
     t.plain = tiles_fit(p) ? 0 : widest_piece(p);
     t.box_keys = p.tile;
     while (!t.plain && p.b.page_tokens % t.box_keys) t.box_keys /= 2;
@@ -519,6 +520,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.group = (p.per_kv + p.pieces - 1) / p.pieces;
     p.unit_tokens = kRows / p.group;
     p.tile = kKeys;
+    p.unit_cost = 1;
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
     r.blocks = multiprocessors() * (c.head_dim <= 128 ? 2 : 1);

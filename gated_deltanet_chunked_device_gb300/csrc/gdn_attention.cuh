@@ -50,7 +50,7 @@ __device__ __forceinline__ void kv_report(int32_t* status, uint32_t err) {
 // ---------------------------------------------------------------------------------------------------------------------
 // Attention's work.  A unit is one sequence's `unit_tokens` successive new tokens of one group of query heads that share a
 // key head; its rows are (token, head of the group), token by token.  A unit passes over the tiles of `tile` keys that any
-// of its rows sees: that many steps, and one more for what a unit costs beside them.  All units' steps, in the order
+// of its rows sees: that many steps, and `unit_cost` more for what a unit costs beside them.  All units' steps, in the order
 // (sequence, group, tokens), are one line that is cut into equal pieces, one a block: any mix of long and short sequences
 // fills the GPU evenly, with no list to be written first, and a cut within a unit leaves two partial results to be joined.
 // Where a cut falls follows from the lengths alone, so results do not depend on timing.
@@ -67,6 +67,7 @@ struct AttnParams {
     int32_t unit_tokens, tile;
     int32_t causal, window;
     float scale_log2;              // scale * log2(e): the kernels' exponentials are powers of two
+    int32_t unit_cost;             // steps, about, that a unit's start and end take
     int32_t min_steps;             // a block's least share
     float* part_o;                 // [2 * blocks][unit rows][D], sums of weights times values
     float2* part_ml;               // [2 * blocks][unit rows]: maximum (scaled, log2) and sum of weights
@@ -112,7 +113,7 @@ __device__ __forceinline__ int64_t attn_steps(const AttnParams& p, const KvSpan&
     if (m <= 0) return 0;
     const bool whole = static_cast<int64_t>(m) * p.unit_tokens >= s.n;  // the last unit may be shorter than the others
     const int32_t k = whole ? m - 1 : m;
-    int64_t sum = m;
+    int64_t sum = static_cast<int64_t>(m) * p.unit_cost;
     if (k > 0) {
         const int64_t at = static_cast<int64_t>(s.len) - s.n, keys = s.keys, top = (keys + p.tile - 1) / p.tile;
         sum += p.causal ? attn_sum(at + p.unit_tokens, p.unit_tokens, k, keys, p.tile - 1, p.tile) : k * top;
@@ -244,9 +245,10 @@ struct AttnWalk {
             }
             const int32_t t0 = at.unit * p.unit_tokens, t1 = min(t0 + p.unit_tokens, span.n);
             attn_tiles(p, span, t0, t1, out.first, out.last);
-            const int64_t take = min(at.left, out.last - out.first + 1 - at.skip);
-            out.tile0 = out.first + static_cast<int32_t>(max(at.skip - 1, int64_t{0}));
-            out.tile1 = out.first + static_cast<int32_t>(at.skip + take - 1);
+            const int64_t take = min(at.left, out.last - out.first + p.unit_cost - at.skip);
+            out.tile0 = out.first + static_cast<int32_t>(max(at.skip - p.unit_cost, int64_t{0}));
+            out.tile1 = out.first + static_cast<int32_t>(max(at.skip + take - p.unit_cost, int64_t{0}));
+            const bool starts = at.skip == 0;
             out.row0 = span.start + t0;
             out.tokens = t1 - t0;
             out.pos0 = static_cast<int32_t>(static_cast<int64_t>(span.len) - span.n + t0);
@@ -259,7 +261,7 @@ struct AttnWalk {
             at.left -= take;
             at.skip = 0;
             ++at.unit;
-            if (out.first == out.last || out.tile0 < out.tile1) return true;
+            if (out.first == out.last ? starts : out.tile0 < out.tile1) return true;
         }
         return false;
     }

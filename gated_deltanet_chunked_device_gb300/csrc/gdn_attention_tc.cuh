@@ -162,6 +162,17 @@ __device__ __forceinline__ int32_t stream_end(const TcParams& p, const AttnPart&
     return max(a.tile0, static_cast<int32_t>(min(static_cast<int64_t>(a.tile1), (hi + keys_a_tile - 1) / keys_a_tile)));
 }
 
+// The lane `with` away gets one's second value for its own first: lanes whose bit is set keep their second.
+__device__ __forceinline__ void swap_quads(uint4& a, uint4& b, int bit, int with) {
+    const uint4 give = bit ? a : b;
+    const uint4 got = make_uint4(__shfl_xor_sync(~0u, give.x, with), __shfl_xor_sync(~0u, give.y, with), __shfl_xor_sync(~0u, give.z, with),
+                                 __shfl_xor_sync(~0u, give.w, with));
+    if (bit)
+        a = got;
+    else
+        b = got;
+}
+
 // Where a row's result goes.
 template <class E>
 struct RowOut {
@@ -883,8 +894,13 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
         const RowOut<E> out = row_out<E>(ap, a, block, t, g);
         const float scale = out.o ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
         float finite = 0.f;
+        E* rows4[4]{};             // the rows of this lane's group of four
+#pragma unroll
+        for (int i = 0; i < 4 && kStreams == 2; ++i)
+            rows4[i] = reinterpret_cast<E*>(__shfl_sync(~0u, mine ? reinterpret_cast<unsigned long long>(out.o) : 0ull, (lane & 28) + i));
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
+            __syncwarp();
             uint32_t o[32];
             if (tiles > 0) {
                 tmem_ld32_wait(o_at + c, o);
@@ -892,39 +908,50 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0;
             }
-            if (mine) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (c + i < D) finite = fmaf(__uint_as_float(o[i]), 0.f, finite);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
+            if (out.o && p.out_vec) {
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[i] = make_uint4(pack16<E>(__uint_as_float(o[8 * i]), __uint_as_float(o[8 * i + 1])),
+                                      pack16<E>(__uint_as_float(o[8 * i + 2]), __uint_as_float(o[8 * i + 3])),
+                                      pack16<E>(__uint_as_float(o[8 * i + 4]), __uint_as_float(o[8 * i + 5])),
+                                      pack16<E>(__uint_as_float(o[8 * i + 6]), __uint_as_float(o[8 * i + 7])));
+                if constexpr (kStreams == 1) {  // few rows, most of them nobody's
+                    if (mine)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (c + 8 * i < D) *reinterpret_cast<uint4*>(out.o + c + 8 * i) = x[i];
+                    continue;
+                }
+                // Four lanes swap, so that each writes 16 bytes of the same four rows: 64 bytes of a row at a time (8 prompts: 1494 ->
+                // 1445 us).
+                swap_quads(x[0], x[1], lane & 1, 1);
+                swap_quads(x[2], x[3], lane & 1, 1);
+                swap_quads(x[0], x[2], lane & 2, 2);
+                swap_quads(x[1], x[3], lane & 2, 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (rows4[i] && c + 8 * (lane & 3) < D) *reinterpret_cast<uint4*>(rows4[i] + c + 8 * (lane & 3)) = x[i];
+            } else if (mine && out.o) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
-                    if (c + i < D) finite = fmaf(__uint_as_float(o[i]), 0.f, finite);
+                    if (c + i < D) out.o[c + i] = narrow16<E>(__uint_as_float(o[i]));
+            } else if (mine && D % 4 == 0) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
-                if (out.o) {
-                    if (p.out_vec) {
+                for (int i = 0; i < 32; i += 4)
+                    if (c + i < D) *reinterpret_cast<uint4*>(out.part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            } else if (mine) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            if (c + i < D)
-                                *reinterpret_cast<uint4*>(out.o + c + i) =
-                                    make_uint4(pack16<E>(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                                               pack16<E>(__uint_as_float(o[i + 2]), __uint_as_float(o[i + 3])),
-                                               pack16<E>(__uint_as_float(o[i + 4]), __uint_as_float(o[i + 5])),
-                                               pack16<E>(__uint_as_float(o[i + 6]), __uint_as_float(o[i + 7])));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < D) out.o[c + i] = narrow16<E>(__uint_as_float(o[i]));
-                    }
-                } else if (D % 4 == 0) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-                        if (c + i < D) *reinterpret_cast<uint4*>(out.part + c + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (c + i < D) out.part[c + i] = __uint_as_float(o[i]);
-                }
+                for (int i = 0; i < 32; ++i)
+                    if (c + i < D) out.part[c + i] = __uint_as_float(o[i]);
             }
-            __syncwarp();
         }
+        __syncwarp();
         tc_fence_before();
         if (mine) {
             if (out.lse) *out.lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
