@@ -123,7 +123,7 @@ def _frequencies(f, D, device):
 def _out(name, out, like, T, D, dtype, device):
     """The output tensor (a new one without `out`) and its token stride."""
     if out is None:
-        return torch.empty(like.shape, dtype=dtype, device=like.device), 0
+        return torch.empty_like(like) if like.is_contiguous() else torch.empty(like.shape, dtype=dtype, device=like.device), 0
     return out, _tokens(name, out, like.shape, dtype, device)
 
 
@@ -185,12 +185,13 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     Differentiable in q and k when called without q_out and k_out."""
     if q is None and k is None:
         raise ValueError("q or k must be given")
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k)):
+    if torch.is_grad_enabled() and ((q is not None and q.requires_grad) or (k is not None and k.requires_grad)):
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be differentiated through")
         return _Rotary.apply(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude)
     out = _rotary(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude, q_out, k_out, 0)
-    increment_version([t for t in (q_out, k_out) if t is not None])
+    if q_out is not None or k_out is not None:
+        increment_version([t for t in (q_out, k_out) if t is not None])
     return out
 
 
@@ -213,6 +214,8 @@ def _cache(k_cache, v_cache, D, dtype, device):
             raise ValueError(f"{name} must have contiguous channels")
         strides += t.stride()[:3]
     P, pt, Hk, _ = k_cache.shape
+    if max(P, pt) > 0x7fffffff:
+        raise ValueError("pages and their tokens must fit 32 bits")
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, Hk, D, _QKV_DTYPES[dtype]), P, pt, Hk
 
 
@@ -280,12 +283,12 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     without ``causal``), and with ``window`` only those after p - window.  ``scale`` is 1 / sqrt(D) by default.  ``lse`` [T, heads]
     fp32, when given, receives the logarithm of the sum of the scores' exponentials.  Returns ``output`` [T, heads, D].
 
-    A token that sees nothing gets zeros (lse: minus infinity); what a token does not see has no influence on it, whatever it
+    A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token does not see has no influence on it, whatever it
     holds.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.  Rows past the
     last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable.
 
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and
-    addresses are multiples of 16 bytes."""
+    addresses are multiples of 16 bytes.  fp32 is computed as such, on CUDA cores, at about a hundredth of the rate."""
     T, D, dtype, device = _first("q", q)
     packed, P, pt, Hk = _cache(k_cache, v_cache, D, dtype, device)
     Hq, qs = _heads("q", q, T, D, dtype, device)
@@ -296,6 +299,8 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     batch = _batch(T, table, lengths, seqs, cu_seqlens, tokens_per_seq, P, pt, device_status, device)
     given = output
     output, os_ = _out("output", output, q, T, D, dtype, device)
+    if given is not None and T and given.data_ptr() == q.data_ptr():
+        raise ValueError("output must be apart from q")
     if lse is not None and _tokens("lse", lse, (T, Hq), torch.float32, device):
         raise ValueError("lse must be contiguous")
     args = _pack_attention(q.data_ptr(), output.data_ptr(), _addr(lse), qs, os_, Hq,
@@ -307,5 +312,6 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
         st = L.gdn_attention_run(batch, packed, args, _addr(ws), n, stream)
     if st != 0:
         raise GdnError(st, "gdn_attention_run")
-    increment_version([t for t in (given, lse) if t is not None])
+    if given is not None or lse is not None:
+        increment_version([t for t in (given, lse) if t is not None])
     return output

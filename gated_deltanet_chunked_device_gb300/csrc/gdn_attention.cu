@@ -357,6 +357,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attention_join_kernel(const _
 }
 
 // ------------------------------------------------------------------------------------------------ host side
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool aligned(const void* p, int64_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 
 // Pages, tokens and heads of rows of D elements that do not overlap: from the smallest stride on, each has to pass the span of the
@@ -493,7 +495,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     if (!args) return GDN_ERR_INVALID_ARG;
     gdn_attention_args a = *args;
     const gdn_kv_cache& c = *cache;
-    if (a.heads < 1 || a.heads % c.kv_heads || a.window < 0 || !(a.scale == a.scale) || a.scale - a.scale != 0.f) return GDN_ERR_INVALID_ARG;
+    if (a.heads < 1 || a.heads % c.kv_heads || a.window < 0 || !std::isfinite(a.scale * kLog2e)) return GDN_ERR_INVALID_ARG;
     if (c.head_dim > GDN_ATTENTION_MAX_DIM || static_cast<int64_t>(a.heads) * c.head_dim > (1 << 20)) return GDN_ERR_UNSUPPORTED;
     const int64_t row = static_cast<int64_t>(a.heads) * c.head_dim;
     if (a.q_stride == 0) a.q_stride = row;
@@ -501,6 +503,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     if (batch->total_tokens > 0 && (!a.q || !a.output || !aligned(a.q, dtype_bytes(c.dtype)) || !aligned(a.output, dtype_bytes(c.dtype)) ||
                                     a.q_stride < row || a.output_stride < row))
         return GDN_ERR_INVALID_ARG;
+    if (batch->total_tokens > 0 && a.q == a.output) return GDN_ERR_INVALID_ARG;  // a row may be read again after it is written
     if (!aligned(a.lse, 4)) return GDN_ERR_INVALID_ARG;
     Route r{};
     AttnParams& p = r.p;
@@ -515,7 +518,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.per_kv = a.heads / c.kv_heads;
     p.causal = a.causal != 0;
     p.window = a.window;
-    p.scale_log2 = a.scale * 1.4426950408889634f;
+    p.scale_log2 = a.scale * kLog2e;
     p.pieces = (p.per_kv + kRows - 1) / kRows;
     p.group = (p.per_kv + p.pieces - 1) / p.pieces;
     p.unit_tokens = kRows / p.group;
@@ -539,7 +542,7 @@ gdn_status kv_check(const gdn_kv_batch* batch, const gdn_kv_cache* cache) {
     const gdn_kv_cache& c = *cache;
     if (b.num_seqs < 0 || b.total_tokens < 0 || b.max_seqs < 0 || b.max_pages < 0 || b.n_pages < 0 || b.page_tokens < 1)
         return GDN_ERR_INVALID_ARG;
-    if (b.total_tokens > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (b.total_tokens > GDN_ATTENTION_MAX_TOKENS) return GDN_ERR_UNSUPPORTED;
     if (c.kv_heads < 1 || c.head_dim < 1) return GDN_ERR_INVALID_ARG;
     if (c.dtype != GDN_DTYPE_F32 && c.dtype != GDN_DTYPE_BF16 && c.dtype != GDN_DTYPE_F16) return GDN_ERR_UNSUPPORTED;
     if (!b.cu_seqlens && (b.tokens_per_seq < 1 || static_cast<int64_t>(b.num_seqs) * b.tokens_per_seq != b.total_tokens))

@@ -72,6 +72,7 @@ extern "C" {
 
 #define GDN_ROTARY_MAX_DIM 1024   /* D of rotary calls */
 #define GDN_ATTENTION_MAX_DIM 256 /* D of attention calls */
+#define GDN_ATTENTION_MAX_TOKENS 0x7fff0000LL /* T of append and attention calls */
 
 /* The new tokens of a step, and where they stand in the cache. */
 typedef struct gdn_kv_batch {
@@ -120,7 +121,7 @@ gdn_status gdn_cache_append_run(const gdn_kv_batch *batch, const gdn_kv_cache *c
 
 typedef struct gdn_attention_args {
     const void *q;
-    void *output;
+    void *output; /* apart from q */
     float *lse; /* optional */
     int64_t q_stride, output_stride;
     int32_t heads;

@@ -75,13 +75,13 @@ class Cache:
         self.layout = layout
 
     def placed(self, t):
-        """On the GPU, in one of three layouts: tokens before heads, heads before tokens, or rows wider than needed."""
+        """On the GPU, in one of four layouts: tokens before heads, heads before tokens, or rows wider than needed, by 8 channels or 1."""
         t = t.cuda()
         if self.layout == "head":
             return t.transpose(1, 2).contiguous().transpose(1, 2)
-        if self.layout == "wide":
+        if self.layout in ("wide", "odd"):
             P, pt, H, D = t.shape
-            whole = torch.full((P, 2, pt, H, D + 8), float("nan"), dtype=t.dtype, device="cuda")
+            whole = torch.full((P, 2, pt, H, D + (8 if self.layout == "wide" else 1)), float("nan"), dtype=t.dtype, device="cuda")
             whole[:, 1, :, :, :D] = t
             return whole[:, 1, :, :, :D]
         return t

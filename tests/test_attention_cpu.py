@@ -81,7 +81,8 @@ def test_cache_is_checked(L, kw):
     ({}, {}, dict(q=None), INVALID), ({}, {}, dict(output=None), INVALID), ({}, {}, dict(q=F + 1), INVALID),
     ({}, {}, dict(lse=F + 2), INVALID), ({}, {}, dict(q_stride=255), INVALID), ({}, {}, dict(output_stride=255), INVALID),
     ({}, {}, dict(heads=0), INVALID), ({}, {}, dict(heads=5), INVALID), ({}, {}, dict(window=-1), INVALID),
-    ({}, {}, dict(scale=float("nan")), INVALID), ({}, {}, dict(scale=float("inf")), INVALID),
+    ({}, {}, dict(scale=float("nan")), INVALID), ({}, {}, dict(scale=float("inf")), INVALID), ({}, {}, dict(scale=3e38), INVALID),
+    ({}, {}, dict(output=F + 0x30000), INVALID), (dict(total_tokens=0x7fff0001), {}, {}, UNSUPPORTED),
     ({}, dict(dtype=gdn.DTYPE_F8E4M3), {}, UNSUPPORTED),
     ({}, dict(head_dim=257, k_head_stride=257, k_token_stride=514, k_page_stride=16 * 514, v_head_stride=257, v_token_stride=514,
               v_page_stride=16 * 514), {}, UNSUPPORTED),

@@ -17,7 +17,7 @@ def built():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("D", [1, 8, 33, 64, 80, 100, 128, 192, 256])
+@pytest.mark.parametrize("D", [1, 6, 8, 30, 33, 64, 80, 100, 128, 130, 192, 215, 256])
 def test_ragged_chunks(dtype, D):
     Cache([130, 0, 20, 1, 70], [50, 3, 0, 300, 129], 4, 2, D, 16, dtype, seed=D).check()
 
@@ -35,10 +35,10 @@ def test_sizes_of_pages(dtype, page_tokens):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("layout", ["token", "head", "wide"])
-@pytest.mark.parametrize("D", [64, 128])
-def test_layouts(dtype, layout, D):
-    Cache([60, 9], [10, 200], 8, 2, D, 16, dtype, layout=layout).check(strided=True)
+@pytest.mark.parametrize("layout", ["token", "head", "wide", "odd"])
+@pytest.mark.parametrize("D,page_tokens", [(64, 16), (128, 16), (96, 5)])
+def test_layouts(dtype, layout, D, page_tokens):
+    Cache([60, 9], [10, 200], 8, 2, D, page_tokens, dtype, layout=layout).check(strided=True)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
@@ -95,7 +95,7 @@ def test_rising_scores(dtype):
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("what", ["k", "v"])
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 128, 256, 100])
 def test_what_a_token_does_not_see_has_no_influence(dtype, bad, what, D):
     """A key or value in the middle of the chunk that is not finite: the tokens before it, and those that look back less far, are right."""
     lens, past = [200, 3], [100, 0]
@@ -117,13 +117,35 @@ def test_what_a_token_does_not_see_has_no_influence(dtype, bad, what, D):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-def test_bad_pages_are_left_out_and_reported(dtype):
-    c = Cache([30, 2, 5], [200, 100, 0], 4, 1, 64, 16, dtype)
+@pytest.mark.parametrize("page_tokens", [16, 64, 7])
+@pytest.mark.parametrize("heads", [4, 64])
+def test_bad_pages_are_left_out_and_reported(dtype, page_tokens, heads):
+    c = Cache([30, 2, 5], [200, 100, 0], heads, 1, 64, page_tokens, dtype)
     s = c.seqs.tolist()
-    c.table[s[0], 3] = -1
-    c.table[s[0], 7] = 10 ** 6
+    c.table[s[0], 1] = -1
+    c.table[s[0], 3] = c.k.shape[0]
     c.table[s[1], 0] = -2 ** 31
     c.check(status=DEV["PAGE"])
+
+
+def test_offsets_past_32_bits():
+    """A cache of more than 2^31 elements, pages at both of its ends."""
+    c = Cache([20, 1], [300, 100], 4, 2, 128, 64, "bf16", fill=0.0)
+    g = c.gpu()
+    pages, old = 140000, c.k.shape[0]
+    whole = [torch.empty(pages, *c.k.shape[1:], dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    for t, small in zip(whole, (g["k_cache"], g["v_cache"])):
+        t[pages - old:] = small
+    want = gdn.paged_attention(c.q.cuda(), **g, cu_seqlens=c.cu.cuda())
+    g["table"] = torch.where(g["table"] >= 0, g["table"] + (pages - old), -1)
+    got = gdn.paged_attention(c.q.cuda(), **{**g, "k_cache": whole[0], "v_cache": whole[1]}, cu_seqlens=c.cu.cuda())
+    assert torch.equal(got, want)
+    f = gdn.rotary_frequencies(128)
+    k, v = torch.randn(21, 2, 128, device="cuda").bfloat16(), torch.randn(21, 2, 128, device="cuda").bfloat16()
+    gdn.cache_append(k, v, whole[0], whole[1], g["table"], g["lengths"], seqs=g["seqs"], cu_seqlens=c.cu.cuda(), frequencies=f)
+    small = c.gpu()
+    gdn.cache_append(k, v, small["k_cache"], small["v_cache"], small["table"], g["lengths"], seqs=g["seqs"], cu_seqlens=c.cu.cuda(), frequencies=f)
+    assert torch.equal(whole[0][pages - old:], small["k_cache"]) and torch.equal(whole[1][pages - old:], small["v_cache"])
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -183,16 +205,16 @@ def test_many_sequences():
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
-@pytest.mark.parametrize("D,tokens", [(64, 1), (128, 1), (128, 2), (256, 1)])
-def test_many_units_a_block(dtype, D, tokens):
+@pytest.mark.parametrize("D,tokens,page_tokens", [(64, 1, 16), (128, 1, 16), (128, 2, 64), (256, 1, 32), (128, 1, 12), (99, 1, 64), (250, 1, 10)])
+def test_many_units_a_block(dtype, D, tokens, page_tokens):
     """Each block goes through several sequences with several tiles and a partly filled last one."""
     g = torch.Generator().manual_seed(D + tokens)
     past = torch.randint(0, 1300, (320,), generator=g).tolist()
-    Cache([tokens] * 320, past, 4, 2, D, 16, dtype, seed=D).check(tokens=tokens)
+    Cache([tokens] * 320, past, 4, 2, D, page_tokens, dtype, seed=D).check(tokens=tokens)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("D,page_tokens", [(64, 16), (128, 64), (256, 64)])
+@pytest.mark.parametrize("D,page_tokens", [(64, 16), (128, 64), (256, 64), (128, 10), (100, 64), (47, 7), (200, 20)])
 def test_many_units_of_many_rows_a_block(dtype, D, page_tokens):
     """The same for chunks of tokens: units of several hundred rows, whole ones and cut ones."""
     g = torch.Generator().manual_seed(D)
@@ -265,3 +287,23 @@ def test_on_another_stream():
         got = [gdn.paged_attention(q, **g, cu_seqlens=cu) for _ in range(3)]
     s.synchronize()
     assert all(torch.equal(x, want) for x in got)
+
+
+def test_refusals():
+    c = Cache([4], [10], 4, 2, 64, 16, "bf16")
+    g, q = c.gpu(), c.q.cuda()
+    call = lambda q=q, **kw: gdn.paged_attention(q, **{**g, **kw})  # noqa: E731
+    bad = [dict(cu_seqlens=c.cu.cuda(), tokens_per_seq=1), dict(tokens_per_seq=3), dict(tokens_per_seq=0), dict(seqs=g["seqs"].long()),
+           dict(table=g["table"].long()), dict(lengths=g["lengths"][:1]), dict(lengths=g["lengths"].cpu()), dict(window=-1),
+           dict(k_cache=g["k_cache"].float()), dict(k_cache=g["k_cache"][:, :, :, :32]), dict(v_cache=g["v_cache"][:, :8]),
+           dict(k_cache=g["k_cache"].transpose(2, 3).contiguous().transpose(2, 3)), dict(output=torch.empty(4, 4, 32, device="cuda").bfloat16()),
+           dict(output=q), dict(lse=torch.empty(4, 2, device="cuda")), dict(lse=torch.empty(4, 4, device="cuda").half()),
+           dict(q=q[:, :3]), dict(q=q.double()), dict(q=q[0]), dict(device_status=torch.zeros(1, device="cuda")), dict(cu_seqlens=c.cu.cuda().float()),
+           dict(seqs=None, tokens_per_seq=1, table=g["table"][:2], lengths=g["lengths"][:2])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(gdn.GdnError):
+        call(scale=float("nan"))
+    with pytest.raises(gdn.GdnError):
+        call(k_cache=g["k_cache"][:1].expand(g["k_cache"].shape))  # pages that overlap

@@ -245,3 +245,35 @@ def test_graph_replay_and_other_streams():
     call(again)
     torch.cuda.synchronize()
     assert torch.equal(out, replayed) and torch.equal(again["k_cache"], g["k_cache"])
+
+
+def test_offsets_past_32_bits():
+    """Tokens 20001 elements apart, 120000 of them."""
+    T = 120000
+    whole = torch.zeros(T, 20001, dtype=torch.bfloat16, device="cuda")
+    x = whole[:, :16].view(T, 1, 16)
+    rows = [0, 1, 107000, 107375, T - 1]
+    x[rows] = torch.randn(len(rows), 1, 16, generator=torch.Generator().manual_seed(0)).to(torch.bfloat16).cuda()
+    f = gdn.rotary_frequencies(16)
+    y, _ = gdn.rotary_embedding(x, None, f)
+    compare("q", y[rows], x[rows], rows, f, "bf16")
+
+
+def test_refusals():
+    q, k, v = tensors(6, 2, 1, 16, "bf16")
+    f, p = gdn.rotary_frequencies(16), torch.arange(6, device="cuda")
+    bad = [dict(positions=p, cu_seqlens=p), dict(positions=p[:5]), dict(positions=p.float()), dict(positions=p.cpu()), dict(frequencies=f.float()),
+           dict(frequencies=gdn.rotary_frequencies(18)), dict(frequencies=f.cpu()), dict(frequencies=f[None]), dict(cu_seqlens=p.float()),
+           dict(q_out=q[:3]), dict(k_out=k.float()), dict(q=q.double()), dict(k=k[:, :, :8]), dict(k=k[:5]), dict(q=q[0]), dict(q=None, k=None)]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            gdn.rotary_embedding(**{**dict(q=q, k=k, frequencies=f), **kw})
+    with pytest.raises(ValueError, match="differentiated"):
+        gdn.rotary_embedding(q.requires_grad_(), k, f, k_out=torch.empty_like(k))
+    q.requires_grad_(False)
+    c = Cache([6], [0], 2, 1, 16, 8, "bf16")
+    g = c.gpu()
+    for kw in (dict(output=q), dict(v=v[:5]), dict(k=k[:, :, :8]), dict(q=q.float()), dict(cu_seqlens=c.cu.cuda(), tokens_per_seq=6),
+               dict(k_cache=g["k_cache"].float()), dict(frequencies=gdn.rotary_frequencies(18))):
+        with pytest.raises(ValueError):
+            gdn.cache_append(**{**dict(k=k, v=v), **g, **kw})
