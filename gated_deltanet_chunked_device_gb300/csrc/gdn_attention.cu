@@ -451,7 +451,9 @@ void tc_route(Route* r) {
     r->streams = D <= 128 && p.b.total_tokens * p.per_kv > static_cast<int64_t>(p.b.num_seqs) * rows ? 2 : 1;
     p.tile = 128;
     attn_tc::TcParams& t = r->tc;
-    t.row_tokens = rows / p.group;
+    // Up to 32 rows a sequence, on the average: units of 32 rows, each in every quarter.
+    t.quarters = r->streams == 1 && p.group <= 32 && p.b.total_tokens * p.per_kv <= 32LL * p.b.num_seqs;
+    t.row_tokens = (t.quarters ? 32 : rows) / p.group;
     p.unit_tokens = r->streams * t.row_tokens;
     p.unit_cost = r->streams;
     t.plain = tiles_fit(p) ? 0 : widest_piece(p);

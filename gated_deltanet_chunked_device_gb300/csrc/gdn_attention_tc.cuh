@@ -61,13 +61,14 @@ struct TcParams {
     uint32_t idesc_qk, idesc_pv;
     float scale_log2;              // positive: a negative scale negates Q in the product
     int32_t out_vec;               // results can be written 16 bytes at a time
+    int32_t quarters;              // units of at most 32 rows: each warp of exponentials has a quarter of the keys
     int32_t plain;                 // bytes of a plain copy (16, 8, 4 or 2) where tiled copies cannot fetch the rows; 0: tiled copies
 };
 
 template <class S>
 struct Misc {
     uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2];
-    uint64_t part_full[kParts], part_empty[kParts], tail_done, turn[2], drain[2];
+    uint64_t part_full[kParts], part_empty[kParts], tail_done, mix, turn[2], drain[2];
     uint4 stage_keys[S::kStages], slot_keys[2];  // keys that have a page (or lie behind the sequence), a bit each
     uint32_t slot_missing[2];      // whether some of a slot's keys have none
     int2 rows[2][2][64];           // plain copies: page and place of a warp's half of the keys of two tiles
@@ -397,12 +398,13 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         const int active = a.tokens > p.row_tokens ? kStreams : 1;
         if (elect_one()) {
             constexpr int kAll = S::kHalves * S::kChunks;
-            mbar_arrive_expect_tx(sh.q_full + slot, active * kAll * ap.group * p.row_tokens * 128);
-            for (int s = 0; s < active; ++s)
+            const int times = p.quarters ? 4 : active;  // the same rows in every quarter, or a stream's own
+            mbar_arrive_expect_tx(sh.q_full + slot, times * kAll * ap.group * p.row_tokens * 128);
+            for (int s = 0; s < times; ++s)
 #pragma unroll
                 for (int c = 0; c < kAll; ++c)
-                    tma_load_3d(q_s + (slot + s) * S::kQBytes + c * (kRowTile * 128), map_q, sh.q_full + slot, c * 64, a.head0,
-                                static_cast<int32_t>(a.row0 + s * p.row_tokens));
+                    tma_load_3d(q_s + slot * S::kQBytes + s * (p.quarters ? 32 * 128 : S::kQBytes) + c * (kRowTile * 128), map_q,
+                                sh.q_full + slot, c * 64, a.head0, static_cast<int32_t>(a.row0 + (p.quarters ? 0 : s * p.row_tokens)));
         }
         __syncwarp();
         ++qn;
@@ -541,15 +543,17 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
         flush();  // nobody waits for a stage whose products come before this unit's rows
         const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
         if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
-        const int active = a.tokens > p.row_tokens ? kStreams : 1, pieces = (D + elems - 1) / elems;
+        const int active = a.tokens > p.row_tokens ? kStreams : 1, pieces = D / elems, padded = S::kHalves * p.k_steps * 16 / elems;
         for (int s = 0; s < active; ++s) {
             for (int r = id * 4 + lane / 8; r < p.row_tokens * ap.group; r += 8) {
                 const int t = r / ap.group, g = r - t * ap.group, token = s * p.row_tokens + t;
                 const bool there = token < a.tokens && g < a.heads;
                 const E* src = static_cast<const E*>(ap.q) + (a.row0 + (there ? token : 0)) * ap.q_stride + static_cast<int64_t>(a.head0 + (there ? g : 0)) * D;
-                for (int i = lane % 8; i < pieces; i += 8) {
+                for (int i = lane % 8; i < padded; i += 8) {  // zeros behind the head's end: joined quarters leave anything there
                     const int x = i * bytes % 128, c = i * bytes / 128;
-                    copy_piece(bytes, q_s + (slot + s) * S::kQBytes + c * (kRowTile * 128) + sw128_offset(r, x / 16) + x % 16, src + i * elems, there);
+                    const bool in = there && i < pieces;
+                    uint8_t* to = q_s + (slot + s) * S::kQBytes + c * (kRowTile * 128) + sw128_offset(r, x / 16) + x % 16;
+                    for (int w = 0; w < (p.quarters ? 4 : 1); ++w) copy_piece(bytes, to + w * (32 * 128), in ? src + i * elems : src, in);
                 }
             }
         }
@@ -714,10 +718,10 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
                     return true;
                 };
                 if (!all_scores(g & 1)) return;
-                if (count == 1) mma_commit_elect(sh.q_empty + slot);
+                if (count == 1 && !p.quarters) mma_commit_elect(sh.q_empty + slot);  // quarters: when their results are joined there
                 for (int32_t j = 0; j < count; ++j, ++g) {
                     if (j + 1 < count && !all_scores((g + 1) & 1)) return;
-                    if (j + 2 == count) mma_commit_elect(sh.q_empty + slot);
+                    if (j + 2 == count && !p.quarters) mma_commit_elect(sh.q_empty + slot);
                     for (int half = 0; half < S::kHalves; ++half) {
                         if (!arrived()) return;
                         if (j + 1 == count && held < S::kKeys && !clear_tail(held)) return;
@@ -975,6 +979,229 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
     }
 }
 
+// Few rows: all of a unit's rows lie in every warp's 32 lanes of TMEM, and a warp takes 32 of a tile's 128 keys, with a maximum, a sum
+// and a result of its own; the weights of the other keys are zero.  That is a quarter of the work a tile on the one warp that would
+// have all rows.  At a part's end the four results are joined in the space of the unit's Q.
+template <class E, class S>
+__device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint32_t tmem, int warp, int lane, int32_t block) {
+    constexpr float kOffset = std::is_same<E, __half>::value ? 7.f : 0.f;
+    const AttnParams& ap = p.a;
+    const int D = ap.c.head_dim;
+    int32_t* status = ap.b.device_status;
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, o_at = tmem + lanes + S::kTmemO;
+    uint32_t count = 0, qn = 0, mixes = 0, k = 0;
+    auto meet = [&]() {  // the four warps
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.mix);
+        return wait(&sh.mix, mixes++ & 1);
+    };
+    // Row r of a part: token, head, and its keys.
+    struct Row {
+        int t, g;
+        int32_t lo, hi;
+        bool there;
+    };
+    auto row_of = [&](const AttnPart& a, int r) {
+        Row x;
+        x.t = r / ap.group;
+        x.g = r - x.t * ap.group;
+        x.there = x.t < a.tokens && x.t < p.row_tokens && x.g < a.heads;
+        const int64_t pos = static_cast<int64_t>(a.pos0) + x.t;
+        x.hi = ap.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
+        x.lo = ap.window ? static_cast<int32_t>(max(pos - ap.window + 1, int64_t{0})) : 0;
+        return x;
+    };
+    bool ok = true;
+    for (; ok; ++k) {
+        ok = wait(sh.part_full + k % kParts, k / kParts & 1);
+        if (!ok) break;
+        const AttnPart a = sh.parts[k % kParts];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.part_empty + k % kParts);
+        if (a.tokens == 0) break;
+        const Row mine = row_of(a, lane);
+        if (a.first == a.last) {
+            if (warp == 0 && mine.there) fill_row<E>(ap, a, mine.t, mine.g, 0.f, block);
+            continue;
+        }
+        const int32_t tiles = a.tile1 - a.tile0;
+        float m = -INFINITY, l = 0.f;
+        for (int32_t j = 0; j < tiles; ++j, ++count) {
+            const uint32_t slot = count & 1;
+            ok = wait(sh.s_full + slot, count / 2 & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t s_at = tmem + lanes + slot * 128;
+            uint32_t s[32];
+            tmem_ld32_wait(s_at + 32 * warp, s);
+            const int64_t key0 = static_cast<int64_t>(a.tile0 + j) * S::kKeys + 32 * warp;
+            uint32_t bits = ~0u;
+            if (mine.there)
+                bits = low_bits(static_cast<int>(max(min(mine.hi - key0, int64_t{32}), int64_t{0}))) &
+                       ~low_bits(static_cast<int>(min(max(mine.lo - key0, int64_t{0}), int64_t{32})));
+            if (sh.slot_missing[slot]) bits &= reinterpret_cast<const uint32_t*>(sh.slot_keys + slot)[warp];
+            if (__any_sync(~0u, bits != ~0u))
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    if (!(bits >> c & 1)) s[c] = 0xff800000u;
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) top[c] = __uint_as_float(s[c]);
+#pragma unroll
+            for (int c = 4; c < 32; ++c) top[c % 4] = fmaxf(top[c % 4], __uint_as_float(s[c]));
+            const float x = fmaf(fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), p.scale_log2, -kOffset);
+            const bool raise = mine.there && x > m + kGrowth;
+            if (__any_sync(~0u, raise)) {
+                const float now = raise ? x : m, shrink = raise ? exp2_fast(m - now) : 1.f;
+                m = now;
+                l *= shrink;
+                __syncwarp();
+                if (j > 0) {
+                    ok = wait(sh.pv_done + (count - 1 & 1), (count - 1) / 2 & 1);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld32_wait(o_at + c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * shrink);
+                        tmem_st32(o_at + c, o);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            uint32_t w[16], zero[16];
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < 32; c += 4) {
+                float e[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = exp2_fast(fmaf(__uint_as_float(s[c + i]), p.scale_log2, -base));
+                    sum[i] += e[i];
+                    zero[(c + i) / 2] = 0;
+                }
+                w[c / 2] = pack16<E>(e[0], e[1]);
+                w[c / 2 + 1] = pack16<E>(e[2], e[3]);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+#pragma unroll
+            for (int b = 1; b < 4; ++b) tmem_st16(s_at + (warp + b) % 4 * 16, zero);
+            tmem_st16(s_at + warp * 16, w);
+            if (!ok) break;
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(sh.p_half + slot);
+                mbar_arrive(sh.p_full + slot);
+            }
+        }
+        ok = ok && wait(sh.pv_done + (count - 1 & 1), (count - 1) / 2 & 1);
+        if (!ok) break;
+        tc_fence_after();
+        // The unit's last scores are done, and with them its Q: its space holds the quarters' maxima and sums, then their results, 32
+        // channels at a time.
+        const uint32_t q_slot = qn++ % S::kQSlots;
+        float* mix = reinterpret_cast<float*>(q_s + q_slot * S::kQBytes);
+        reinterpret_cast<float2*>(mix)[warp * 32 + lane] = make_float2(m, l);
+        ok = meet();
+        if (!ok) break;
+        float top = -INFINITY, sum = 0.f;
+        float2 ml[4];
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            ml[w] = reinterpret_cast<const float2*>(mix)[w * 32 + lane];
+            top = fmaxf(top, ml[w].x);
+        }
+        const float base = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum = fmaf(ml[w].y, exp2_fast(ml[w].x - base), sum);
+        const bool whole = a.tile0 == a.first && a.tile1 == a.last;
+        const float by = exp2_fast(m - base) * (whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f);
+        if (warp == 0 && mine.there) {
+            const RowOut<E> out = row_out<E>(ap, a, block, mine.t, mine.g);
+            if (out.lse) *out.lse = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.69314718055994531f;
+            if (out.ml) *out.ml = make_float2(top, sum);
+        }
+        const int r = 8 * warp + lane / 4;  // the row whose result this lane joins, eight channels of 32
+        const Row other = row_of(a, r);
+        const RowOut<E> out = row_out<E>(ap, a, block, other.t, other.g);
+        float finite = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < D && ok; c += 32) {
+            __syncwarp();
+            uint32_t o[32];
+            tmem_ld32_wait(o_at + c, o);
+            ok = meet();  // what was there has been read
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<float4*>(mix + (warp * 32 + lane) * 32 + (i ^ (lane & 7)) * 4) =
+                    make_float4(__uint_as_float(o[4 * i]) * by, __uint_as_float(o[4 * i + 1]) * by, __uint_as_float(o[4 * i + 2]) * by,
+                                __uint_as_float(o[4 * i + 3]) * by);
+            ok = meet();
+            if (!ok) break;
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) y[i] = 0.f;
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 v = *reinterpret_cast<const float4*>(mix + (w * 32 + r) * 32 + ((2 * (lane & 3) + h) ^ (r & 7)) * 4);
+                    y[4 * h] += v.x, y[4 * h + 1] += v.y, y[4 * h + 2] += v.z, y[4 * h + 3] += v.w;
+                }
+            const int d = c + 8 * (lane & 3);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (d + i < D) finite = fmaf(y[i], 0.f, finite);
+            if (!other.there) continue;
+            if (out.o && p.out_vec) {
+                if (d < D) *reinterpret_cast<uint4*>(out.o + d) = make_uint4(pack16<E>(y[0], y[1]), pack16<E>(y[2], y[3]), pack16<E>(y[4], y[5]), pack16<E>(y[6], y[7]));
+            } else if (out.part && D % 4 == 0) {
+                if (d < D) *reinterpret_cast<float4*>(out.part + d) = make_float4(y[0], y[1], y[2], y[3]);
+                if (d + 4 < D) *reinterpret_cast<float4*>(out.part + d + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (d + i < D) {
+                        if (out.o)
+                            out.o[d + i] = narrow16<E>(y[i]);
+                        else
+                            out.part[d + i] = y[i];
+                    }
+            }
+        }
+        if (!ok) break;
+        tc_fence_before();
+        // Q may come again once all have read; the copies that bring it do not see plain accesses by themselves.
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(sh.q_empty + q_slot);
+        for (int d = 1; d < 4; d *= 2) finite += __shfl_xor_sync(~0u, finite, d);
+        const float row_sum = __shfl_sync(~0u, sum, r), row_top = __shfl_sync(~0u, top, r);
+        unsigned spoilt = __ballot_sync(~0u, (lane & 3) == 0 && other.there && finite != 0.f && row_sum - row_sum == 0.f);
+        while (spoilt) {
+            const int from = __ffs(spoilt) - 1;
+            spoilt &= spoilt - 1;
+            __syncwarp();
+            exact_row<E>(ap, a, __shfl_sync(~0u, other.t, from), __shfl_sync(~0u, other.g, from), __shfl_sync(~0u, other.lo, from),
+                         __shfl_sync(~0u, other.hi, from), __shfl_sync(~0u, row_top, from), __shfl_sync(~0u, row_sum, from), block, lane);
+        }
+    }
+    if (!ok && warp == 0) {  // what a wait that ran out has left undone
+        AttnWalk walk;
+        walk.begin(sh.scan.start);
+        AttnPart a;
+        for (uint32_t i = 0; walk.next(ap, a); ++i) {
+            const Row mine = row_of(a, lane);
+            if (i >= k && mine.there) fill_row<E>(ap, a, mine.t, mine.g, __int_as_float(0x7fffffff), block);
+        }
+    }
+}
+
 template <class E, int kDim, int kStreams>
 __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     attention_tc_kernel(const __grid_constant__ TcParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -994,7 +1221,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.q_full + i, p.plain ? 64 : 1);
-            mbar_init(sh.q_empty + i, kStreams);
+            mbar_init(sh.q_empty + i, p.quarters ? 4 : kStreams);
             mbar_init(sh.s_full + i, 2);     // the product, and the slot's mask
             mbar_init(sh.p_half + i, 4);     // a warpgroup's warps
             mbar_init(sh.p_full + i, 4);
@@ -1005,6 +1232,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
             mbar_init(sh.part_empty + i, 5 * kStreams);
         }
         mbar_init(&sh.tail_done, 2);
+        mbar_init(&sh.mix, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.turn + i, 1);
             mbar_init(sh.drain + i, 1);
@@ -1044,7 +1272,14 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
         }
     } else {
         if constexpr (kStreams == 2) regs_inc<208>();  // 128 x 80 + 256 x 208 of the 384 x 168 registers that the block has
-        exponentiate<E, S, kDim, kStreams>(p, sh, tmem, (warp - 4) / 4, warp & 3, lane, block);
+        if constexpr (kStreams == 1) {
+            if (p.quarters)
+                exponentiate_quarters<E, S>(p, sh, q_s, tmem, warp & 3, lane, block);
+            else
+                exponentiate<E, S, kDim, kStreams>(p, sh, tmem, 0, warp & 3, lane, block);
+        } else {
+            exponentiate<E, S, kDim, kStreams>(p, sh, tmem, (warp - 4) / 4, warp & 3, lane, block);
+        }
     }
     __syncwarp();
     tc_fence_before();
