@@ -12,7 +12,8 @@ namespace {
 // ------------------------------------------------------------------------------------------------ CUDA cores
 // Every type, head size and layout: 64 rows of a unit against tiles of 64 keys, all of it fp32, one pass with a running maximum
 // and sum for each row.  256 threads as 16 x 16: a thread has 4 rows by 4 keys of the scores (keys tx + 16 c) and 4 rows by 4 x kCols
-// channels of the result (channels 4 tx + 64 c).
+// channels of the result (channels 4 tx + 64 c).  Large calls in fp32 run at 25 TFLOP/s (2048 tokens over 6144, 16 heads on 2 of 128,
+// 3421 us), half of what a library's fp32 product reaches; small ones are bound by the latency of a block's two or three tiles.
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
 
 __device__ __forceinline__ float wide(float x) { return x; }
@@ -442,6 +443,22 @@ int widest_piece(const AttnParams& p) {
     return static_cast<int>(all & -all);
 }
 
+// Whether the tensor cores take a call.  fp32 would lose its last 13 bits there.  Rows that tiled copies cannot fetch are copied by two
+// warps in such pieces, which bounds the kernel; whether that still pays (us, tensor cores and CUDA cores, 16 heads on 2, bf16):
+//   64 sequences of 4096 tokens, one new: pieces of 16 bytes, heads of 128: 246 and 696; 104: 252 and 728
+//                                                   8 bytes,          100: 389 and 412;  60: 250 and 246
+//                                                   4 bytes,          102: 513 and 811;  62: 342 and 220
+//                                                   2 bytes,          101: 4879 and 809; 63: 2102 and 220
+//   a prompt's 4096 tokens over as many: 16 bytes, 128: 857 and 8649; 8, 100: 1412 and 6120; 4, 102: 1994 and 8989; 2, 101: 9434 and 8983
+// So pieces of 2 bytes, which no asynchronous copy has, are left to the CUDA cores, and few rows of up to 64 channels in pieces of 4 and 8.
+bool tensor_cores(const AttnParams& p) {
+    if (p.c.dtype == GDN_DTYPE_F32 || p.b.n_pages < 1) return false;
+    if (tiles_fit(p)) return true;
+    const int piece = widest_piece(p);
+    const bool many = p.b.total_tokens * p.per_kv > static_cast<int64_t>(p.b.num_seqs) * attn_tc::kRowTile;
+    return piece == 16 || (piece >= 4 && (many || p.c.head_dim > 64));
+}
+
 // The tensor cores' shape.  Two row tiles a unit pay where a sequence has, on the average, rows for more than one.
 void tc_route(Route* r) {
     AttnParams& p = r->p;
@@ -529,7 +546,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
     r.blocks = multiprocessors() * (c.head_dim <= 128 ? 2 : 1);
-    if (c.dtype != GDN_DTYPE_F32 && batch->n_pages > 0) tc_route(&r);  // fp32 would lose its last 13 bits there
+    if (tensor_cores(p)) tc_route(&r);
     *out = r;
     return GDN_OK;
 }

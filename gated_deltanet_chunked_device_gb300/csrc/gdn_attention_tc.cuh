@@ -62,7 +62,7 @@ struct TcParams {
     float scale_log2;              // positive: a negative scale negates Q in the product
     int32_t out_vec;               // results can be written 16 bytes at a time
     int32_t quarters;              // units of at most 32 rows: each warp of exponentials has a quarter of the keys
-    int32_t plain;                 // bytes of a plain copy (16, 8, 4 or 2) where tiled copies cannot fetch the rows; 0: tiled copies
+    int32_t plain;                 // bytes of a plain copy (16, 8 or 4) where tiled copies cannot fetch the rows; 0: tiled copies
 };
 
 template <class S>
@@ -440,16 +440,14 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
 }
 
 // ------------------------------------------------------------------------------------------------ warps 0 and 3: plain copies
-// `bytes` (16, 8, 4 or 2) from global to shared memory, asynchronously from 4 on, or zeros.
+// `bytes` (16, 8 or 4) from global to shared memory, asynchronously, or zeros.
 __device__ __forceinline__ void copy_piece(int bytes, uint8_t* dst, const void* src, bool there) {
     if (bytes == 8)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 8 : 0) : "memory");
     else if (bytes == 4)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 4 : 0) : "memory");
-    else if (bytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
     else
-        *reinterpret_cast<uint16_t*>(dst) = there ? *static_cast<const uint16_t*>(src) : static_cast<uint16_t>(0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
 // What produce does, without tiled copies: warp `id` (0 or 1) brings its half of the rows, 64 threads arrive at a stage.  Copies of
