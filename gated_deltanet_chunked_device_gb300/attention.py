@@ -180,7 +180,7 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     channels (i, i + R / 2) of the first R = 2 * len(frequencies), or (2 i, 2 i + 1) when ``interleaved``; the channels behind
     R stay as they are.  Positions are ``positions`` [T] (int32 or int64, as far as 2^31), or count from 0 in each sequence of
     ``cu_seqlens`` (int32 or int64; rows past its end go on counting), or from 0 over all rows.  Tokens may be strided (slices of a
-    projection's output).  ``q_out`` and ``k_out`` may be q and k themselves.  Returns ``(q_out, k_out)``.
+    projection's output).  ``q_out`` and ``k_out`` may be q and k themselves, or are apart from them.  Returns ``(q_out, k_out)``.
 
     Differentiable in q and k when called without q_out and k_out."""
     if q is None and k is None:
@@ -283,12 +283,14 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     without ``causal``), and with ``window`` only those after p - window.  ``scale`` is 1 / sqrt(D) by default.  ``lse`` [T, heads]
     fp32, when given, receives the logarithm of the sum of the scores' exponentials.  Returns ``output`` [T, heads, D].
 
-    A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token does not see has no influence on it, whatever it
-    holds.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.  Rows past the
-    last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable.
+    A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token
+    does not see has no influence on it, whatever it holds.  ``output``, when given, has its rows apart from q's (slices of one
+    tensor are allowed).  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.
+    Rows past the last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable.
 
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and
-    addresses are multiples of 16 bytes.  fp32 is computed as such, on CUDA cores, at about a hundredth of the rate."""
+    addresses are multiples of 16 bytes.  Heads of an odd number of channels, and fp32, are computed on CUDA cores, at about a
+    fiftieth of the rate."""
     T, D, dtype, device = _first("q", q)
     packed, P, pt, Hk = _cache(k_cache, v_cache, D, dtype, device)
     Hq, qs = _heads("q", q, T, D, dtype, device)

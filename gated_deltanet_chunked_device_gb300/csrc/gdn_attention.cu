@@ -1,5 +1,6 @@
 // gdn_attention.cu -- attention over a paged cache (include/gdn_attention.h):
 // host side, the kernel on CUDA cores, and the join of units that were cut.
+#include <algorithm>
 #include <cmath>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -384,6 +385,17 @@ bool apart(int64_t pages, int64_t page_stride, int64_t tokens, int64_t token_str
     return true;
 }
 
+// Whether T rows of `row` bytes each at x and y, so many bytes from row to row, have no byte in common.  Rows of one stride may lie
+// between each other (slices of one tensor); of others only the spans are compared.
+bool rows_apart(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t T, int64_t row) {
+    using wide_t = __int128;
+    const wide_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    if (b >= a + static_cast<wide_t>(T - 1) * x_stride + row || a >= b + static_cast<wide_t>(T - 1) * y_stride + row) return true;
+    if (T == 1 || x_stride != y_stride) return false;
+    const wide_t off = (a > b ? a - b : b - a) % x_stride;
+    return off >= row && x_stride - off >= row;
+}
+
 struct Route {
     AttnParams p;
     attn_tc::TcParams tc;          // streams > 0
@@ -522,7 +534,10 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     if (batch->total_tokens > 0 && (!a.q || !a.output || !aligned(a.q, dtype_bytes(c.dtype)) || !aligned(a.output, dtype_bytes(c.dtype)) ||
                                     a.q_stride < row || a.output_stride < row))
         return GDN_ERR_INVALID_ARG;
-    if (batch->total_tokens > 0 && a.q == a.output) return GDN_ERR_INVALID_ARG;  // a row may be read again after it is written
+    const int64_t bytes = dtype_bytes(c.dtype);
+    if (std::max(a.q_stride, a.output_stride) > (1LL << 56)) return GDN_ERR_INVALID_ARG;
+    if (batch->total_tokens > 0 && !rows_apart(a.q, a.q_stride * bytes, a.output, a.output_stride * bytes, batch->total_tokens, row * bytes))
+        return GDN_ERR_INVALID_ARG;  // a row may be read again after it is written
     if (!aligned(a.lse, 4)) return GDN_ERR_INVALID_ARG;
     Route r{};
     AttnParams& p = r.p;

@@ -92,6 +92,28 @@ def test_attention_is_checked(L, b, c, a, expect):
     assert run_attention(L, batch(**b), cache(**c), attention(**a)) == expect
 
 
+# Rows of q: 10 of 4 x 64 bf16, 512 bytes each.
+@pytest.mark.parametrize("kw,expect", [
+    (dict(output=F + 0x30000 + 2), INVALID), (dict(output=F + 0x30000 - 2), INVALID), (dict(output=F + 0x30000 + 9 * 512), INVALID),
+    (dict(output=F + 0x30000 - 10 * 512 + 2), INVALID),
+    (dict(q_stride=512, output_stride=512, output=F + 0x30000 + 510), INVALID),
+    (dict(q_stride=512, output_stride=512, output=F + 0x30000 + 514), INVALID),
+    (dict(q_stride=512, output_stride=768, output=F + 0x30000 + 512), INVALID),
+    (dict(q_stride=1 << 62, output_stride=1 << 62, output=F + 0x30000 + 2), INVALID)])
+def test_output_is_apart_from_q(L, kw, expect):
+    assert run_attention(L, batch(), cache(), attention(**kw)) == expect
+    assert L.gdn_attention_workspace(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(attention(**kw))) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(output=F + 0x30000 + 10 * 512), dict(output=F + 0x30000 - 10 * 512), dict(q_stride=512, output_stride=512, output=F + 0x30000 + 512),
+    dict(q_stride=512, output_stride=512, output=F + 0x30000 - 512), dict(q_stride=512, output_stride=512, output=F + 0x30000 + 1024 * 3 + 512)])
+def test_output_beside_q_is_taken(L, kw):
+    b, c, a = batch(), cache(), attention(**kw)  # a workspace too small is refused after the rest
+    assert run_attention(L, b, c, a, ws=16) == INVALID
+    assert L.gdn_attention_workspace(ctypes.byref(b), ctypes.byref(c), ctypes.byref(a)) > 0
+
+
 def test_attention_needs_its_workspace(L):
     b, c, a = batch(), cache(), attention()
     assert run_attention(L, b, c, a, ws=16) == INVALID

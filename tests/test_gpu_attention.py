@@ -289,6 +289,25 @@ def test_on_another_stream():
     assert all(torch.equal(x, want) for x in got)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page_tokens", [(60, 64), (62, 64), (63, 64), (64, 46), (100, 64), (101, 64), (102, 64), (104, 46), (250, 16), (252, 16)])
+def test_rows_that_tiled_copies_cannot_fetch(dtype, D, page_tokens):
+    """Few rows and many, in pieces of 16, 8, 4 and 2 bytes."""
+    Cache([1] * 5, [0, 45, 130, 700, 1000], 16, 2, D, page_tokens, dtype, seed=D).check(tokens=1)
+    Cache([300, 1], [100, 700], 16, 2, D, page_tokens, dtype, seed=D + 1).check()
+
+
+def test_output_and_queries_as_slices_of_one_tensor():
+    c = Cache([130, 20], [50, 300], 4, 2, 64, 16, "bf16")
+    g, cu, q = c.gpu(), c.cu.cuda(), c.q.cuda()
+    want = gdn.paged_attention(q, **g, cu_seqlens=cu)
+    both = torch.cat([q, torch.zeros_like(q)], 1)
+    gdn.paged_attention(both[:, :4], **g, cu_seqlens=cu, output=both[:, 4:])
+    assert torch.equal(both[:, :4], q) and torch.equal(both[:, 4:], want)
+    with pytest.raises(gdn.GdnError):
+        gdn.paged_attention(both[:, :4], **g, cu_seqlens=cu, output=both[:, 1:5])
+
+
 def test_refusals():
     c = Cache([4], [10], 4, 2, 64, 16, "bf16")
     g, q = c.gpu(), c.q.cuda()
