@@ -301,6 +301,7 @@ cudaError_t launch_simple_typed(const AttnParams& p, int32_t blocks, cudaStream_
 
 // ------------------------------------------------------------------------------------------------ the join
 // A warp a row: the parts' results, each with its own maximum, weighted to the largest one, in the parts' order.
+// Bound by latency: its blocks are launched ahead and wait, and those without a cut unit leave at once.
 constexpr int kJoinWarps = 8;
 
 template <class E>
