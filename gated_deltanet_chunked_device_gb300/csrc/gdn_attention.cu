@@ -485,7 +485,10 @@ void tc_route(Route* r) {
     t.quarters = r->streams == 1 && p.group <= 32 && p.b.total_tokens * p.per_kv <= 32LL * p.b.num_seqs;
     t.row_tokens = (t.quarters ? 32 : rows) / p.group;
     p.unit_tokens = r->streams * t.row_tokens;
-    p.unit_cost = r->streams;
+    // What a unit's start and end take, in tiles.  One row tile (us with 1, 2, 3, 4 and 6): 300 sequences of 0 to 2093 tokens, one new, 16
+    // heads on 2, heads of 256: 222, 175, 149, 142, 142; 128: 111, 90, 83, 84, 83; 64: 88, 75, 72, 73, 71.  1000 tokens over 2500 beside 63
+    // single ones, heads of 256: 140, 132, 129, 128, 134.  Against it: 4 tokens of 64 sequences under a window of 1024: 69, 70, 72, 72, 73.
+    p.unit_cost = r->streams == 2 ? 2 : 3;
     t.plain = tiles_fit(p) ? 0 : widest_piece(p);
     t.box_keys = p.tile;
     while (!t.plain && p.b.page_tokens % t.box_keys) t.box_keys /= 2;

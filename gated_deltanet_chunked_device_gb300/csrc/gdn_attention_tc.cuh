@@ -20,8 +20,8 @@
 // Bounds and figures (GB300).  Many rows: the chain scores - exponentials - weights - products of two streams; the tensor pipe works
 // 59 % of the time (2048 tokens over 30720, 32 heads on 16 of 128, fp16: 0.9 ms, 1.17 PFLOP/s; 8 prompts of 33720 tokens, 32 heads on
 // 8, bf16: 1.45 ms, 1.15 PFLOP/s).  Single tokens over long contexts: HBM (512 sequences of up to 8192, bf16: 331 us, 0.97 of a
-// measured copy).  Four tokens under a window of 1024, heads of 64, pages of 16: a tile's steps and a copy a page of 2 KB (67 us, floor
-// 20; 80 before four warps shared a tile's keys).  Heads of 256 with many rows: the chain of a single row tile (tensor pipe 33 %).
+// measured copy).  Four tokens under a window of 1024, heads of 64, pages of 16: a tile's steps and a copy a page of 2 KB (71 us, floor
+// 20; four warps that share a tile's keys brought 80 to 67, a division that suits short sequences cost 4).  Heads of 256 with many rows: the chain of a single row tile (tensor pipe 33 %).
 //
 // Where tiled copies cannot fetch the rows (pages of sizes that are no multiple of 8, heads of 100 channels) warps 0 and 3 copy them
 // piece by piece into the same layout; that bounds the kernel then (a chunk of 4096 tokens over as many, 16 heads on 2: 208 us with
