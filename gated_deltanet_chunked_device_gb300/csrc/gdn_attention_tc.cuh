@@ -545,7 +545,6 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
         }
         if (!more) break;
         if (a.first == a.last) continue;
-        flush();  // nobody waits for a stage whose products come before this unit's rows
         const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
         if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
         const int active = a.tokens > p.row_tokens ? kStreams : 1, pieces = D / elems, padded = S::kHalves * p.k_steps * 16 / elems;
@@ -579,8 +578,9 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
             now[0] = then[0];
             now[1] = then[1];
         }
+        flush();  // before any wait for this part's end: it ends with these stages
     }
-    flush();
+    flush();  // after a wait that ran out: no copy may be under way when the block ends
     kv_report(status, err);
 }
 
