@@ -501,6 +501,7 @@ void tc_route(Route* r) {
     // Scores of keys that are not seen are -infinity, which has to survive the scaling: zero becomes a scale that any finite score vanishes in.
     t.scale_log2 = fmaxf(fabsf(p.scale_log2), 1e-30f);
     t.out_vec = D % 8 == 0 && p.o_stride % 8 == 0 && aligned(p.o, 16);
+    t.wait_cycles = attn_tc::kWaitCycles;
     r->blocks = multiprocessors();
     r->rows = p.unit_tokens * p.group;
     t.a = p;

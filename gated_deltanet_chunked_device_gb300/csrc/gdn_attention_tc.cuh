@@ -70,6 +70,7 @@ struct TcParams {
     int32_t out_vec;               // results can be written 16 bytes at a time
     int32_t quarters;              // units of at most 32 rows: each warp of exponentials has a quarter of the keys
     int32_t plain;                 // bytes of a plain copy (16, 8 or 4) where tiled copies cannot fetch the rows; 0: tiled copies
+    long long wait_cycles;         // limit of a wait
 };
 
 template <class S>
@@ -88,12 +89,14 @@ struct Misc {
 template <class S>
 constexpr size_t smem_bytes() { return S::kTileBytes + sizeof(Misc<S>); }
 
-// Waits with a limit of about a second; the first that runs out makes all others give up.
-__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
+constexpr long long kWaitCycles = 2000000000LL;  // about a second
+
+// Waits up to a limit; the first wait that runs out makes all others give up.
+__device__ __forceinline__ bool wait_long(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status, long long limit) {
     const long long t0 = clock64();
     while (!mbar_try_wait_sleep(bar, parity, 1000)) {
         if (*static_cast<volatile int32_t*>(abort)) return false;
-        if (clock64() - t0 > 2000000000LL) {
+        if (clock64() - t0 > limit) {
             *static_cast<volatile int32_t*>(abort) = 1;
             kv_report(status, GDN_DEVICE_ERR_TIMEOUT);
             return false;
@@ -118,8 +121,8 @@ __device__ __forceinline__ uint4 spread_boxes(uint32_t mask, int boxes, int keys
 }
 
 // By a whole warp: all of its lanes go on, or none.
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status) {
-    return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status));
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int32_t* abort, int32_t* status, long long limit) {
+    return __all_sync(~0u, mbar_try_wait(bar, parity) || wait_long(bar, parity, abort, status, limit));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -333,7 +336,7 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
     const AttnParams& ap = p.a;
     const int32_t pt = ap.b.page_tokens;
     int32_t* status = ap.b.device_status;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
     AttnWalk walk;
     walk.begin(sh.scan.start);
     AttnPart a{};
@@ -440,10 +443,14 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         }
     }
     kv_report(status, err);
-    if (*static_cast<volatile int32_t*>(&sh.abort)) {  // no copy may be under way when the block ends
-        for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) mbar_wait(sh.kv_full + i % S::kStages, i / S::kStages & 1);
-        for (uint32_t i = qn > S::kQSlots ? qn - S::kQSlots : 0; i < qn; ++i) mbar_wait(sh.q_full + i % S::kQSlots, i / S::kQSlots & 1);
-    }
+    // No copy may be under way when the block ends: another warp's wait may run out after this one has gone through.
+    const long long t0 = clock64();
+    auto settled = [&](uint64_t* bar, uint32_t parity) {
+        while (!mbar_try_wait(bar, parity) && clock64() - t0 < kWaitCycles / 4) {
+        }
+    };
+    for (uint32_t i = n > S::kStages ? n - S::kStages : 0; i < n; ++i) settled(sh.kv_full + i % S::kStages, i / S::kStages & 1);
+    for (uint32_t i = qn > S::kQSlots ? qn - S::kQSlots : 0; i < qn; ++i) settled(sh.q_full + i % S::kQSlots, i / S::kQSlots & 1);
 }
 
 // ------------------------------------------------------------------------------------------------ warps 0 and 3: plain copies
@@ -466,7 +473,7 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
     const AttnParams& ap = p.a;
     const int D = ap.c.head_dim;
     int32_t* status = ap.b.device_status;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
     AttnWalk walk;
     walk.begin(sh.scan.start);
     AttnPart a{};
@@ -591,7 +598,7 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
 template <class S, int kStreams>
 __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, uint32_t tmem, int stream, int lane) {
     int32_t* status = p.a.b.device_status;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
     const uint64_t dq0 = desc_kmajor_sw128(smem_u32(q_s) + stream * S::kQBytes), dk0 = desc_kmajor_sw128(smem_u32(kv_s));
     const uint64_t dv0 = desc_mnmajor_sw128(smem_u32(kv_s), S::kKeys * 128);
     const bool full = p.k_steps == S::kChunks * 4;
@@ -756,7 +763,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
     const AttnParams& ap = p.a;
     const int D = ap.c.head_dim;
     int32_t* status = ap.b.device_status;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
     const int row = warp * 32 + lane, tile_t = row / ap.group, g = row - tile_t * ap.group, t = stream * p.row_tokens + tile_t;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_at = tmem + lanes + S::kTmemO + stream * 128;
@@ -993,7 +1000,7 @@ __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q
     const AttnParams& ap = p.a;
     const int D = ap.c.head_dim;
     int32_t* status = ap.b.device_status;
-    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status); };
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16, o_at = tmem + lanes + S::kTmemO;
     uint32_t count = 0, qn = 0, mixes = 0, k = 0;
     auto meet = [&]() {  // the four warps
