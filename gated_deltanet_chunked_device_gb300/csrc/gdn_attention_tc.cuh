@@ -251,6 +251,11 @@ __device__ __forceinline__ void exact_row(const AttnParams& p, const AttnPart& a
     }
 }
 
+// Notes a unit that later blocks go on with, so that the join comes to its rows.
+__device__ __forceinline__ void note_cut(const AttnParams& p, const AttnPart& a, int32_t block, const AttnWalk& walk) {
+    if (a.tile0 == a.first && a.tile1 < a.last) attn_note_join(p, a, block, walk.at.share);
+}
+
 // A row's result without keys (zero), or after a wait that ran out (NaN).
 template <class E>
 __device__ __forceinline__ void fill_row(const AttnParams& p, const AttnPart& a, int t, int g, float value, int32_t block) {
@@ -401,7 +406,7 @@ __device__ void produce(const TcParams& p, const CUtensorMap* map_q, const CUten
         }
         __syncwarp();
         if (!more) break;
-        if (lane == 0 && a.tile0 == a.first && a.tile1 < a.last) attn_note_join(ap, a, blockIdx.x, walk.at.share);
+        if (lane == 0) note_cut(ap, a, blockIdx.x, walk);
         if (a.first == a.last) continue;
         const uint32_t slot = qn % S::kQSlots, use = qn / S::kQSlots;
         if (use > 0 && !wait(sh.q_empty + slot, (use - 1) & 1)) break;
@@ -546,7 +551,7 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
             if (lane == 0) {
                 sh.parts[k % kParts] = a;
                 mbar_arrive(sh.part_full + k % kParts);
-                if (more && a.tile0 == a.first && a.tile1 < a.last) attn_note_join(ap, a, blockIdx.x, walk.at.share);
+                if (more) note_cut(ap, a, blockIdx.x, walk);
             }
             __syncwarp();
         }
@@ -986,8 +991,11 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
         AttnWalk walk;
         walk.begin(sh.scan.start);
         AttnPart a;
-        for (uint32_t i = 0; walk.next(ap, a); ++i)
-            if (i >= k && tile_t < p.row_tokens && t < a.tokens && g < a.heads) fill_row<E>(ap, a, t, g, __int_as_float(0x7fffffff), block);
+        for (uint32_t i = 0; walk.next(ap, a); ++i) {
+            if (i < k) continue;
+            if (tile_t < p.row_tokens && t < a.tokens && g < a.heads) fill_row<E>(ap, a, t, g, __int_as_float(0x7fffffff), block);
+            if (stream == 0 && row == 0) note_cut(ap, a, block, walk);
+        }
     }
 }
 
@@ -1203,13 +1211,15 @@ __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q
                          __shfl_sync(~0u, other.hi, from), __shfl_sync(~0u, row_top, from), __shfl_sync(~0u, row_sum, from), block, lane);
         }
     }
-    if (!ok && warp == 0) {  // what a wait that ran out has left undone
+    if (!ok) {  // what a wait that ran out has left undone: the rows whose results this warp joins
         AttnWalk walk;
         walk.begin(sh.scan.start);
         AttnPart a;
         for (uint32_t i = 0; walk.next(ap, a); ++i) {
-            const Row mine = row_of(a, lane);
-            if (i >= k && mine.there) fill_row<E>(ap, a, mine.t, mine.g, __int_as_float(0x7fffffff), block);
+            if (i < k) continue;
+            const Row mine = row_of(a, 8 * warp + lane / 4);
+            if ((lane & 3) == 0 && mine.there) fill_row<E>(ap, a, mine.t, mine.g, __int_as_float(0x7fffffff), block);
+            if (warp == 0 && lane == 0) note_cut(ap, a, block, walk);
         }
     }
 }
@@ -1227,6 +1237,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     const int32_t block = blockIdx.x;
     griddep_launch_dependents();  // the join's blocks, which wait for this kernel's end
     if (tid == 0) {
+        p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
         for (int i = 0; i < S::kStages; ++i) {
             mbar_init(sh.kv_full + i, p.plain ? 64 : 1);
             mbar_init(sh.kv_empty + i, kStreams);
@@ -1272,7 +1283,6 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
     if (warp < 4) {
         if constexpr (kStreams == 2) regs_dec<80>();
         if (warp == 0) {
-            if (lane == 0) p.a.joins[2 * block] = make_int4(0, 0, 0, 0);
             if (p.plain)
                 produce_plain<E, S, kStreams>(p, sh, q_s, kv_s, 0, lane);
             else

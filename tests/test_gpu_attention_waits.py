@@ -1,4 +1,5 @@
-"""What attention over a paged cache does when a wait inside its kernel runs out: it ends, reports it, and leaves the GPU in order.
+"""What attention over a paged cache does when a wait inside its kernel runs out: it ends, reports it, and leaves the GPU in order; every
+row is NaN or right, those of units that several blocks share too.
 
 The kernel runs with half of each tile of keys and values never fetched, so that its waits for them run out (attention_waits.cu), or
 with a limit of nothing at all, so that a wait gives up as soon as it would have to go on."""
@@ -68,3 +69,25 @@ def test_the_kernel_ends_and_the_next_one_is_right(waits, dtype, D, heads, kv_he
     if missing:
         assert not bool((torch.isfinite(out) & (out != 7.0)).any())  # nothing passes for a result
     c.check()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,heads,kv_heads,lens", SHAPES)
+@pytest.mark.parametrize("page_tokens,missing", [(64, 1), (64, 0), (20, 0)])
+def test_rows_are_nan_or_right(waits, dtype, D, heads, kv_heads, lens, page_tokens, missing):
+    """Contexts long enough that most units are cut; a sequence without keys among them, whose rows are zero."""
+    past = [3000 + 7 * i for i in range(len(lens))]
+    past[1] = -lens[1]
+    c = Cache(lens, past, heads, kv_heads, D, page_tokens, dtype, seed=D)
+    want_lse = torch.empty(c.q.shape[:2], device="cuda")
+    want = gdn.paged_attention(c.q.cuda(), **c.gpu(), cu_seqlens=c.cu.cuda(), lse=want_lse)
+    for _ in range(1 if missing else 5):
+        out, lse, status = run(waits, c, CYCLES if missing else -1, missing)
+        assert bool((torch.isnan(out) | (out == want)).all()) and bool((torch.isnan(lse) | (lse == want_lse)).all())
+        gone = torch.isnan(out).any(-1)
+        if missing:
+            keys = torch.ones(len(lens), dtype=torch.bool)
+            keys[1] = False
+            rows = keys.repeat_interleave(torch.tensor(lens)).cuda()
+            assert bool(torch.isnan(out[rows]).all()) and bool(torch.isnan(lse[rows]).all())
+        assert bool(gone.any()) == (status != 0)
