@@ -76,7 +76,7 @@ struct TcParams {
 template <class S>
 struct Misc {
     uint64_t kv_full[S::kStages], kv_empty[S::kStages], q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], pv_done[2];
-    uint64_t part_full[kParts], part_empty[kParts], tail_done, mix, turn[2], drain[2];
+    uint64_t part_full[kParts], part_empty[kParts], both, mix, turn[2], drain[2];
     uint4 stage_keys[S::kStages], slot_keys[2];  // keys that have a page (or lie behind the sequence), a bit each
     uint32_t slot_missing[2];      // whether some of a slot's keys have none
     int2 rows[2][2][64];           // plain copies: page and place of a warp's half of the keys of two tiles
@@ -84,6 +84,9 @@ struct Misc {
     int32_t abort;
     AttnPart parts[kParts];
     AttnScan<S::kThreads> scan;
+    // Tiles [x, y) of a stream's part that had values set apart, for every second part: in the place of the scan's sums, which have done
+    // their work when the walk starts.
+    __device__ __forceinline__ int2& unfinite(int stream, uint32_t part) { return reinterpret_cast<int2*>(scan.sums)[2 * stream + (part & 1)]; }
 };
 
 template <class S>
@@ -208,46 +211,126 @@ __device__ __forceinline__ RowOut<E> row_out(const AttnParams& p, const AttnPart
     return r;
 }
 
-// One row from the keys that it sees, by a warp: where a hidden value that is not finite (taken times zero by the product) has
-// spoilt the row.  m is the row's maximum as used, l its sum.
+// Values that are not finite, two at a time (16 bits each): marked by their sign bits; and left out.
 template <class E>
-__device__ __forceinline__ void exact_row(const AttnParams& p, const AttnPart& a, int t, int g, int32_t lo, int32_t hi, float m, float l,
-                                       int32_t block, int lane) {
+__device__ __forceinline__ uint32_t unfinite_signs(uint32_t x) {
+    if constexpr (std::is_same<E, __half>::value) return ((x & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
+    return ((x & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+template <class E>
+__device__ __forceinline__ uint32_t finite_only(uint32_t x) {
+    return x & ~((unfinite_signs<E>(x) >> 15) * 0xffffu);
+}
+// x * 0 + sum: NaN from the first x on that is not finite.
+template <class E>
+__device__ __forceinline__ uint32_t taint(uint32_t x, uint32_t sum) {
+    uint32_t r;
+    if constexpr (std::is_same<E, __half>::value)
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    else
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0u), "r"(sum));
+    return r;
+}
+
+// Keys [every0, every1): those of the sequence that all rows of a part see (every1 may be the smaller one).
+__device__ __forceinline__ void keys_of_all(const AttnParams& p, const AttnPart& a, int32_t& every0, int32_t& every1) {
+    const int64_t pos = a.pos0;
+    every0 = p.window ? static_cast<int32_t>(max(pos + a.tokens - p.window, int64_t{0})) : 0;
+    every1 = p.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
+}
+// Whether all rows see what the sequence has of keys [key, key + n).
+__device__ __forceinline__ bool seen_by_all(const AttnPart& a, int64_t key, int n, int32_t every0, int32_t every1) {
+    return key >= a.keys || (key >= every0 && (every1 == a.keys || key + n <= every1));
+}
+// How many of the tile's 128 keys the sequence has.
+__device__ __forceinline__ int held_of(const AttnPart& a, int32_t tile) {
+    return static_cast<int>(min(a.keys - static_cast<int64_t>(tile) * 128, int64_t{128}));
+}
+// The tile's blocks of 32 keys that some row does not see whole, a bit each.
+__device__ __forceinline__ uint32_t cut_blocks(const AttnPart& a, int32_t tile, int32_t every0, int32_t every1) {
+    uint32_t cut = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+        if (!seen_by_all(a, static_cast<int64_t>(tile) * 128 + 32 * b, 32, every0, every1)) cut |= 1u << b;
+    return cut;
+}
+
+// What rows get of the values that are not finite among those that they see, from the cache itself: by a warp, its lanes' rows (row:
+// there is one, with keys) against `tiles`.  It is added to a row's result, in blocks of keys that some row does not see whole (in
+// others the products have taken it), or takes its place (kInstead: the rows of lanes 0, 4, 8 ..).  A seen value counts however small
+// its weight is.
+template <class E, bool kInstead>
+__device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart& a, bool row, int t, int g, int32_t lo, int32_t hi, int2 tiles,
+                                             int32_t block, int lane) {
     const int D = p.c.head_dim;
-    const E* q = static_cast<const E*>(p.q) + (a.row0 + t) * p.q_stride + static_cast<int64_t>(a.head0 + g) * D;
-    float x[8], acc[8];
+    uint64_t placed = 0;           // kInstead: channels whose results have been replaced, 8 bits a row
+    auto value = [&](int64_t at, int d) { return at >= 0 && d < D ? wide16(static_cast<const E*>(p.c.v)[at + d]) : 0.f; };
+    int32_t every0, every1;
+    keys_of_all(p, a, every0, every1);
+    __syncwarp();  // the rows' other results are there for all lanes
+    for (int64_t key0 = static_cast<int64_t>(tiles.x) * 128; key0 < static_cast<int64_t>(tiles.y) * 128; key0 += 32) {
+        if (!kInstead && seen_by_all(a, key0, 32, every0, every1)) continue;
+        const int64_t key = key0 + lane;
+        const int first = static_cast<int>(min(max(lo - key0, int64_t{0}), int64_t{32})), end = static_cast<int>(min(max(hi - key0, int64_t{0}), int64_t{32}));
+        uint32_t seen = row ? low_bits(end) & ~low_bits(first) : 0u;
+        const uint32_t some = __reduce_or_sync(~0u, seen);
+        int64_t at = -1;  // where the key's values are
+        if (some >> lane & 1 && key < a.keys) {
+            const int32_t i = static_cast<int32_t>(key) / p.b.page_tokens, slot = static_cast<int32_t>(key) - i * p.b.page_tokens;
+            const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + i];
+            if (page >= 0 && page < p.b.n_pages) at = page * p.c.v_page_stride + slot * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
+        }
+        // Which of the keys have such values: two channels a lane and load (rows are multiples of 4 bytes here), 16 loads at a time.
+        uint32_t bad = 0;
+#pragma unroll 1
+        for (int d = 2 * lane; d - 2 * lane < D; d += 64)
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 16) {
+                if (!(some >> i0 & 0xffffu)) continue;
+                uint32_t x[16];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        x[c] = lane + 32 * c < D ? wide16(q[lane + 32 * c]) : 0.f;
-        acc[c] = 0.f;
-    }
-    const int64_t from = max(static_cast<int64_t>(a.tile0) * p.tile, static_cast<int64_t>(lo));
-    const int64_t upto = min(static_cast<int64_t>(a.tile1) * p.tile, static_cast<int64_t>(hi));
-    for (int64_t key = from; key < upto; ++key) {
-        const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + key / p.b.page_tokens];
-        if (page < 0 || page >= p.b.n_pages) continue;
-        const int64_t in = key % p.b.page_tokens;
-        const E* k = static_cast<const E*>(p.c.k) + page * p.c.k_page_stride + in * p.c.k_token_stride + a.kv_head * p.c.k_head_stride;
-        const E* v = static_cast<const E*>(p.c.v) + page * p.c.v_page_stride + in * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
-        float s = 0.f;
+                for (int i = 0; i < 16; ++i) {
+                    const int64_t from = __shfl_sync(~0u, at, i0 + i);
+                    x[i] = 0;
+                    if (from >= 0 && d < D) x[i] = *reinterpret_cast<const uint32_t*>(static_cast<const E*>(p.c.v) + from + d);
+                }
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (lane + 32 * c < D) s = fmaf(x[c], wide16(k[lane + 32 * c]), s);
-        for (int d = 16; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
-        const float w = exp2f(fmaf(s, p.scale_log2, -m));
+                for (int i = 0; i < 16; ++i)
+                    if (unfinite_signs<E>(x[i])) bad |= 1u << (i0 + i);
+            }
+        seen &= __reduce_or_sync(~0u, bad);
+        for (unsigned rows = __ballot_sync(~0u, seen != 0); rows; rows &= rows - 1) {
+            const int r = __ffs(rows) - 1;
+            const RowOut<E> out = row_out<E>(p, a, block, __shfl_sync(~0u, t, r), __shfl_sync(~0u, g, r));
+            float sum[8]{};
+            for (uint32_t k = __shfl_sync(~0u, seen, r); k; k &= k - 1) {
+                const int64_t from = __shfl_sync(~0u, at, __ffs(k) - 1);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-            if (lane + 32 * c < D) acc[c] = fmaf(w, wide16(v[lane + 32 * c]), acc[c]);
-    }
-    const RowOut<E> out = row_out<E>(p, a, block, t, g);
+                for (int c = 0; c < 8; ++c) {
+                    const float v = value(from, lane + 32 * c);
+                    if (v - v != 0.f) sum[c] += v;
+                }
+            }
+            bool over = true;  // all of the row is NaN, and nothing changes that
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-        const int d = lane + 32 * c;
-        if (d >= D) break;
-        if (out.o)
-            out.o[d] = narrow16<E>(l == 0.f ? 0.f : acc[c] / l);
-        else
-            out.part[d] = acc[c];
+            for (int c = 0; c < 8; ++c) {
+                const int d = lane + 32 * c;
+                if (d >= D) break;
+                float now = out.o ? wide16(out.o[d]) : out.part[d];
+                const uint64_t bit = 1ull << (2 * (r & 28) + c);
+                if (sum[c] != 0.f) {
+                    now = kInstead && !(placed & bit) ? sum[c] : now + sum[c];
+                    placed |= bit;
+                    if (out.o)
+                        out.o[d] = narrow16<E>(now);
+                    else
+                        out.part[d] = now;
+                }
+                over &= now != now && (!kInstead || (placed & bit));
+            }
+            if (__all_sync(~0u, over) && lane == r) row = false;
+        }
+        if (!__any_sync(~0u, row)) return;
     }
 }
 
@@ -596,11 +679,59 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
     kv_report(status, err);
 }
 
+// A weight of zero makes nothing of a value only if that is finite.  So the products must not see what the page of a sequence's last
+// tile holds behind the sequence (rows from `held` on: anything), nor, in blocks of 32 keys of which some row does not see all,
+// values that are not finite: these become zero in shared memory, and reach the rows that see them by add_unfinite.  By a whole warp,
+// eight lanes a row of a chunk, four rows at a time.  It runs once or twice a unit, between code that fills the instruction cache: short
+// loops, which a warp fetches once, take a twentieth of the time of unrolled ones (8 prompts, heads of 256: 1581 and 1886 us).
+template <class S>
+__device__ __forceinline__ uint4* stage_rows(uint8_t* stage, int chunk, int row, int lane) {
+    return reinterpret_cast<uint4*>(stage + chunk * (S::kKeys * 128) + row * 128 + lane * 16);
+}
+// Clears the rows behind the end; returns whether the blocks hold values that are not finite.
+template <class E, class S>
+__device__ __forceinline__ bool settle_values(uint8_t* stage, int held, uint32_t blocks, int lane) {
+    uint32_t sum[4]{};
+#pragma unroll 1
+    for (int c = 0; c < S::kChunks; ++c) {
+        if (held < S::kKeys) {
+            uint4 *at = stage_rows<S>(stage, c, held & ~3, lane), *end = stage_rows<S>(stage, c, S::kKeys, 0);
+            if (lane / 8 >= (held & 3)) *at = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+            for (at += 32; at < end; at += 32) *at = make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll 1
+        for (int i0 = blocks ? 0 : S::kKeys; i0 < S::kKeys; i0 += 16) {
+            if (!(blocks >> (i0 / 32) & 1)) continue;
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = *stage_rows<S>(stage, c, i0 + 4 * i, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum[0] = taint<E>(x[i].x, sum[0]), sum[1] = taint<E>(x[i].y, sum[1]), sum[2] = taint<E>(x[i].z, sum[2]), sum[3] = taint<E>(x[i].w, sum[3]);
+        }
+    }
+    return __any_sync(~0u, (unfinite_signs<E>(sum[0]) | unfinite_signs<E>(sum[1]) | unfinite_signs<E>(sum[2]) | unfinite_signs<E>(sum[3])) != 0);
+}
+// Makes them zero, in every `of`-th group of four rows.
+template <class E, class S>
+__device__ __forceinline__ void set_apart(uint8_t* stage, int first, int of, uint32_t blocks, int lane) {
+#pragma unroll 1
+    for (int c = 0; c < S::kChunks; ++c)
+#pragma unroll 1
+        for (int i = 4 * first; i < S::kKeys; i += 4 * of) {
+            if (!(blocks >> (i / 32) & 1)) continue;
+            uint4* at = stage_rows<S>(stage, c, i, lane);
+            const uint4 x = *at;
+            *at = make_uint4(finite_only<E>(x.x), finite_only<E>(x.y), finite_only<E>(x.z), finite_only<E>(x.w));
+        }
+}
+
 // ------------------------------------------------------------------------------------------------ warps 1 and 2: products
 // A warp a stream.  All of it goes through this converged, so that addresses and descriptors stay in uniform registers; one lane issues.
 // What a warp issues completes in order, so that a product may overwrite the S whose P an earlier one reads.  (One warp for both
 // streams was what bound the kernel: waits, barriers and bookkeeping between two rows of products cost it more than the products.)
-template <class S, int kStreams>
+template <class E, class S, int kStreams>
 __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* kv_s, uint32_t tmem, int stream, int lane) {
     int32_t* status = p.a.b.device_status;
     auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_warp(bar, parity, &sh.abort, status, p.wait_cycles); };
@@ -608,7 +739,8 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
     const uint64_t dv0 = desc_mnmajor_sw128(smem_u32(kv_s), S::kKeys * 128);
     const bool full = p.k_steps == S::kChunks * 4;
     const uint32_t o_at = tmem + S::kTmemO + stream * 128;
-    uint32_t st = 0, ph = 0, qn = 0, g = 0, seen = 0, tails = 0, turns = 0;  // stage and its phase; units; tiles
+    uint32_t st = 0, ph = 0, qn = 0, g = 0, seen = 0, turns = 0;  // stage and its phase; units; tiles
+    uint32_t met = 0;  // meetings of the two warps
 
     auto arrived = [&]() { return wait(sh.kv_full + st, ph); };
     auto arrived_next = [&]() { return st + 1 == S::kStages ? wait(sh.kv_full, ph ^ 1) : wait(sh.kv_full + st + 1, ph); };
@@ -658,17 +790,25 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
         if (lane == 0) mbar_arrive(sh.kv_empty + st);
         __syncwarp();
     };
-    // The sequence's last tile: what its page holds behind the sequence may be anything, and a weight of zero does not make nothing of
-    // it.  The warps take turns row by row.  The exponentials of this tile are under way meanwhile.
-    auto clear_tail = [&](int held) {
-        for (int i = held + stream; i < S::kKeys; i += kStreams)
-            for (int c = lane; c < S::kChunks * 8; c += 32)
-                *reinterpret_cast<uint4*>(kv_s + st * S::kKvBytes + c / 8 * (S::kKeys * 128) + i * 128 + c % 8 * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+    auto meet = [&]() {  // the two warps
         __syncwarp();
         if (kStreams == 1) return true;
-        if (lane == 0) mbar_arrive(&sh.tail_done);
-        return wait(&sh.tail_done, tails++ & 1);
+        if (lane == 0) mbar_arrive(&sh.both);
+        return wait(&sh.both, met++ & 1);
+    };
+    // The values of a stage become as a product may have them, while the tile's exponentials are under way.  Each warp looks through
+    // the blocks on its own; only where they hold what has to be set apart the two meet, before one of them changes what the other
+    // may still have to read.
+    auto settle = [&](int held, uint32_t blocks, bool& found) {
+        uint8_t* tile = kv_s + st * S::kKvBytes;
+        found = settle_values<E, S>(tile, held, blocks, lane);
+        if (found) {
+            if (!meet()) return false;
+            set_apart<E, S>(tile, stream, kStreams, blocks, lane);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        return !found || meet();
     };
     auto run = [&]() {
         for (uint32_t k = 0;; ++k) {
@@ -683,7 +823,28 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
             if (!wait(sh.q_full + slot, qn / S::kQSlots & 1)) return;
             ++qn;
             const int32_t count = a.tile1 - a.tile0;
-            const int held = static_cast<int>(min(a.keys - static_cast<int64_t>(a.tile1 - 1) * S::kKeys, int64_t{S::kKeys}));  // of the last tile
+            int32_t every0, every1;
+            keys_of_all(p.a, a, every0, every1);
+            // tiles that need nothing: all rows see all of their keys, and the sequence has them all
+            const int32_t whole0 = static_cast<int32_t>((static_cast<int64_t>(every0) + S::kKeys - 1) / S::kKeys) - a.tile0, whole1 = every1 / S::kKeys - a.tile0;
+            int2 unfinite = make_int2(0x7fffffff, 0);
+            auto settle_tile = [&](int32_t j) {
+                if (j >= whole0 && j < whole1) return true;
+                const int32_t tile = a.tile0 + j;
+                bool found = false;
+                if (!settle(held_of(a, tile), cut_blocks(a, tile, every0, every1), found)) return false;
+                if (found) unfinite = make_int2(min(unfinite.x, tile), tile + 1);
+                return true;
+            };
+            // The part's last product is out (kStreams == 1: one product more): told with the tiles that had values set apart.
+            auto tell_done = [&](int slot, bool last) {
+                if (lane == 0) {
+                    if (last) sh.unfinite(stream, qn) = unfinite;
+                    mbar_arrive(sh.pv_done + slot);
+                }
+                __syncwarp();
+                mma_commit_elect(sh.pv_done + slot);
+            };
             if constexpr (kStreams == 2) {
                 const int32_t end = stream_end(p, a, stream, S::kKeys) - a.tile0;
                 if (!arrived() || !turn()) return;
@@ -698,7 +859,7 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
                 for (int32_t j = 0; j < count; ++j) {
                     const bool next = j + 1 < count;
                     if (!arrived()) return;
-                    if (!next && held < S::kKeys && !clear_tail(held)) return;
+                    if (!settle_tile(j)) return;
                     if (next && !arrived_next()) return;
                     if (j < end && !wait(sh.p_half + stream, seen & 1)) return;
                     if (!turn()) return;
@@ -708,7 +869,7 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
                         if (!wait(sh.p_full + stream, seen++ & 1)) return;
                         tc_fence_after();
                         values(stream, 0, 1, true);
-                        if (j + 1 == end) mma_commit_elect(sh.pv_done + stream);
+                        if (j + 1 == end) tell_done(stream, true);
                         mma_commit_elect(sh.kv_empty + st);
                     } else {
                         skip();
@@ -741,13 +902,13 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
                     if (j + 2 == count && !p.quarters) mma_commit_elect(sh.q_empty + slot);
                     for (int half = 0; half < S::kHalves; ++half) {
                         if (!arrived()) return;
-                        if (j + 1 == count && held < S::kKeys && !clear_tail(held)) return;
+                        if (!settle_tile(j)) return;
                         for (int h = 0; h < 2; ++h) {
                             if (half == 0 && !wait((h ? sh.p_full : sh.p_half) + (g & 1), g / 2 & 1)) return;
                             tc_fence_after();
                             values(g & 1, half, h, h > 0 || j > 0);
                         }
-                        if (half == S::kHalves - 1) mma_commit_elect(sh.pv_done + (g & 1));
+                        if (half == S::kHalves - 1) tell_done(g & 1, j + 1 == count);
                         mma_commit_elect(sh.kv_empty + st);
                         advance();
                     }
@@ -772,7 +933,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
     const int row = warp * 32 + lane, tile_t = row / ap.group, g = row - tile_t * ap.group, t = stream * p.row_tokens + tile_t;
     const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
     const uint32_t o_at = tmem + lanes + S::kTmemO + stream * 128;
-    uint32_t count = 0, done = 0;  // tiles, and parts with tiles, of this stream so far
+    uint32_t count = 0, done = 0, units = 0;  // tiles, and parts with tiles, of this stream so far; parts with tiles of either
     uint32_t k = 0;
     bool ok = true;
     for (; ok; ++k) {
@@ -787,6 +948,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
             if (mine) fill_row<E>(ap, a, t, g, 0.f, block);
             continue;
         }
+        ++units;
         const int64_t pos = static_cast<int64_t>(a.pos0) + t;
         const int32_t hi = ap.causal ? static_cast<int32_t>(min(max(pos + 1, int64_t{0}), static_cast<int64_t>(a.keys))) : a.keys;
         const int32_t lo = ap.window ? static_cast<int32_t>(max(pos - ap.window + 1, int64_t{0})) : 0;
@@ -914,7 +1076,6 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
         if (!live) continue;
         const RowOut<E> out = row_out<E>(ap, a, block, t, g);
         const float scale = out.o ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
-        float finite = 0.f;
         E* rows4[4]{};             // the rows of this lane's group of four
 #pragma unroll
         for (int i = 0; i < 4 && kStreams == 2; ++i)
@@ -929,9 +1090,6 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] = 0;
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (c + i < D) finite = fmaf(__uint_as_float(o[i]), 0.f, finite);
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * scale);
             if (out.o && p.out_vec) {
@@ -978,14 +1136,8 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
             if (out.lse) *out.lse = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
             if (out.ml) *out.ml = make_float2(m, l);
         }
-        unsigned spoilt = __ballot_sync(~0u, mine && finite != 0.f && l - l == 0.f);
-        while (spoilt) {
-            const int from = __ffs(spoilt) - 1;
-            spoilt &= spoilt - 1;
-            __syncwarp();
-            exact_row<E>(ap, a, __shfl_sync(~0u, t, from), __shfl_sync(~0u, g, from), __shfl_sync(~0u, lo, from), __shfl_sync(~0u, hi, from),
-                         __shfl_sync(~0u, m, from), __shfl_sync(~0u, l, from), block, lane);
-        }
+        const int2 unfinite = tiles > 0 ? sh.unfinite(stream, units) : make_int2(0, 0);
+        if (unfinite.x < unfinite.y) add_unfinite<E, false>(ap, a, mine && l > 0.f, t, g, lo, hi, unfinite, block, lane);
     }
     if (!ok) {  // what a wait that ran out has left undone
         AttnWalk walk;
@@ -1148,7 +1300,7 @@ __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q
         const int r = 8 * warp + lane / 4;  // the row whose result this lane joins, eight channels of 32
         const Row other = row_of(a, r);
         const RowOut<E> out = row_out<E>(ap, a, block, other.t, other.g);
-        float finite = 0.f;
+        bool spoilt = false;
 #pragma unroll 1
         for (int c = 0; c < D && ok; c += 32) {
             __syncwarp();
@@ -1174,9 +1326,28 @@ __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q
                     y[4 * h] += v.x, y[4 * h + 1] += v.y, y[4 * h + 2] += v.z, y[4 * h + 3] += v.w;
                 }
             const int d = c + 8 * (lane & 3);
+            float sum0 = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                if (d + i < D) finite = fmaf(y[i], 0.f, finite);
+                if (d + i < D) sum0 = fmaf(y[i], 0.f, sum0);
+            // A warp takes the others' keys times zero, so that a value that is not finite makes NaN in the other three.  A single
+            // infinite result beside them is the row's: it would be NaN, too, if there were such values among the others' keys.
+            if (sum0 != 0.f && other.there) {
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    float kept = 0.f;
+                    int infinite = 0;
+                    for (int w = 0; w < 4; ++w) {
+                        const float v = mix[(w * 32 + r) * 32 + ((2 * (lane & 3) + i / 4) ^ (r & 7)) * 4 + i % 4];
+                        if (v == v && v - v != 0.f) kept = v, ++infinite;
+                    }
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        if (u == i && infinite == 1 && y[u] != y[u]) y[u] = kept;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) spoilt |= d + i < D && y[i] != y[i];
+            }
             if (!other.there) continue;
             if (out.o && p.out_vec) {
                 if (d < D) *reinterpret_cast<uint4*>(out.o + d) = make_uint4(pack16<E>(y[0], y[1]), pack16<E>(y[2], y[3]), pack16<E>(y[4], y[5]), pack16<E>(y[6], y[7]));
@@ -1200,16 +1371,13 @@ __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(sh.q_empty + q_slot);
-        for (int d = 1; d < 4; d *= 2) finite += __shfl_xor_sync(~0u, finite, d);
-        const float row_sum = __shfl_sync(~0u, sum, r), row_top = __shfl_sync(~0u, top, r);
-        unsigned spoilt = __ballot_sync(~0u, (lane & 3) == 0 && other.there && finite != 0.f && row_sum - row_sum == 0.f);
-        while (spoilt) {
-            const int from = __ffs(spoilt) - 1;
-            spoilt &= spoilt - 1;
-            __syncwarp();
-            exact_row<E>(ap, a, __shfl_sync(~0u, other.t, from), __shfl_sync(~0u, other.g, from), __shfl_sync(~0u, other.lo, from),
-                         __shfl_sync(~0u, other.hi, from), __shfl_sync(~0u, row_top, from), __shfl_sync(~0u, row_sum, from), block, lane);
-        }
+        const float weights = __shfl_sync(~0u, sum, r);
+        const bool row = (lane & 3) == 0 && other.there && weights > 0.f;
+        const int2 unfinite = sh.unfinite(0, qn);
+        if (__any_sync(~0u, spoilt && weights > 0.f))  // the sum of such values that a row sees takes its place
+            add_unfinite<E, true>(ap, a, row, other.t, other.g, other.lo, other.hi, make_int2(a.tile0, a.tile1), block, lane);
+        else if (unfinite.x < unfinite.y)
+            add_unfinite<E, false>(ap, a, row, other.t, other.g, other.lo, other.hi, unfinite, block, lane);
     }
     if (!ok) {  // what a wait that ran out has left undone: the rows whose results this warp joins
         AttnWalk walk;
@@ -1248,13 +1416,13 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
             mbar_init(sh.s_full + i, 2);     // the product, and the slot's mask
             mbar_init(sh.p_half + i, 4);     // a warpgroup's warps
             mbar_init(sh.p_full + i, 4);
-            mbar_init(sh.pv_done + i, 1);
+            mbar_init(sh.pv_done + i, 2);     // the product, and what was set apart in its values
         }
         for (int i = 0; i < kParts; ++i) {
             mbar_init(sh.part_full + i, 1);
             mbar_init(sh.part_empty + i, 5 * kStreams);
         }
-        mbar_init(&sh.tail_done, 2);
+        mbar_init(&sh.both, 2);
         mbar_init(&sh.mix, 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(sh.turn + i, 1);
@@ -1288,7 +1456,7 @@ __global__ void __launch_bounds__(128 + 128 * kStreams, 1)
             else
                 produce<S, kStreams>(p, &map_q, &map_k, &map_v, sh, q_s, kv_s, lane);
         } else if (warp <= kStreams) {
-            multiply<S, kStreams>(p, sh, q_s, kv_s, tmem, warp - 1, lane);
+            multiply<E, S, kStreams>(p, sh, q_s, kv_s, tmem, warp - 1, lane);
         } else if (warp == 3 && p.plain) {
             produce_plain<E, S, kStreams>(p, sh, q_s, kv_s, 1, lane);
         }
