@@ -180,7 +180,7 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     channels (i, i + R / 2) of the first R = 2 * len(frequencies), or (2 i, 2 i + 1) when ``interleaved``; the channels behind
     R stay as they are.  Positions are ``positions`` [T] (int32 or int64, as far as 2^31), or count from 0 in each sequence of
     ``cu_seqlens`` (int32 or int64; rows past its end go on counting), or from 0 over all rows.  Tokens may be strided (slices of a
-    projection's output).  ``q_out`` and ``k_out`` may be q and k themselves, or are apart from them.  Returns ``(q_out, k_out)``.
+    projection's output).  ``q_out`` and ``k_out`` may be q and k themselves, or are apart from them and from each other.  Returns ``(q_out, k_out)``.
 
     Differentiable in q and k when called without q_out and k_out."""
     if q is None and k is None:
@@ -248,7 +248,7 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     channels).  The batch is packed by ``cu_seqlens`` [N + 1], or has ``tokens_per_seq`` tokens a sequence (decode), or is one
     sequence; sequence i is row ``seqs[i]`` (None: i) of ``table`` and ``lengths``, and ``lengths`` counts the new tokens already: new
     token j of n has position lengths - n + j.  ``q`` [T, heads, D], when given, is turned as well, to ``output`` (a new tensor
-    without it; q itself is allowed) in the same launch.  Returns that, or None.
+    without it; q itself is allowed, else apart from q, k and v) in the same launch.  Returns that, or None.
 
     No two entries of ``seqs`` may name one row.  Tokens without a page are not written (``device_status``, an int32 tensor, receives
     the bits of DEVICE_ERR and PAGES_ERR).  Rows past the last sequence are padding and stay as they are.  A step of serving: not

@@ -386,17 +386,6 @@ bool apart(int64_t pages, int64_t page_stride, int64_t tokens, int64_t token_str
     return true;
 }
 
-// Whether T rows of `row` bytes each at x and y, so many bytes from row to row, have no byte in common.  Rows of one stride may lie
-// between each other (slices of one tensor); of others only the spans are compared.
-bool rows_apart(const void* x, int64_t x_stride, const void* y, int64_t y_stride, int64_t T, int64_t row) {
-    using wide_t = __int128;
-    const wide_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
-    if (b >= a + static_cast<wide_t>(T - 1) * x_stride + row || a >= b + static_cast<wide_t>(T - 1) * y_stride + row) return true;
-    if (T == 1 || x_stride != y_stride) return false;
-    const wide_t off = (a > b ? a - b : b - a) % x_stride;
-    return off >= row && x_stride - off >= row;
-}
-
 struct Route {
     AttnParams p;
     attn_tc::TcParams tc;          // streams > 0
@@ -541,7 +530,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
         return GDN_ERR_INVALID_ARG;
     const int64_t bytes = dtype_bytes(c.dtype);
     if (std::max(a.q_stride, a.output_stride) > (1LL << 56)) return GDN_ERR_INVALID_ARG;
-    if (batch->total_tokens > 0 && !rows_apart(a.q, a.q_stride * bytes, a.output, a.output_stride * bytes, batch->total_tokens, row * bytes))
+    if (batch->total_tokens > 0 && !rows_apart(a.q, a.q_stride * bytes, row * bytes, a.output, a.output_stride * bytes, row * bytes, batch->total_tokens))
         return GDN_ERR_INVALID_ARG;  // a row may be read again after it is written
     if (!aligned(a.lse, 4)) return GDN_ERR_INVALID_ARG;
     Route r{};

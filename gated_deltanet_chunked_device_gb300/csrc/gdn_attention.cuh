@@ -277,6 +277,17 @@ __device__ __forceinline__ void attn_note_join(const AttnParams& p, const AttnPa
     p.joins[2 * block + 1] = make_int4(static_cast<int32_t>(a.row0), static_cast<int32_t>(a.row0 >> 32), 0, 0);
 }
 
+// Whether T rows each at x and y, of so many bytes and so many bytes apart, have no byte in common.  Rows of one stride may lie
+// between each other (slices of one tensor); of others only the spans are compared.
+inline bool rows_apart(const void* x, int64_t x_stride, int64_t x_row, const void* y, int64_t y_stride, int64_t y_row, int64_t T) {
+    using wide_t = __int128;
+    const wide_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    if (b >= a + static_cast<wide_t>(T - 1) * x_stride + x_row || a >= b + static_cast<wide_t>(T - 1) * y_stride + y_row) return true;
+    if (T == 1 || x_stride != y_stride) return false;
+    const wide_t off = ((b - a) % x_stride + x_stride) % x_stride;  // from a row of x to the next of y
+    return off >= x_row && x_stride - off >= y_row;
+}
+
 // What the host can see of a batch and a cache.
 gdn_status kv_check(const gdn_kv_batch* batch, const gdn_kv_cache* cache);
 

@@ -372,6 +372,18 @@ bool tensor_ok(const void* p, gdn_dtype t, int64_t& stride, int64_t row) {
     return stride >= row;
 }
 
+// Whether rows that are written are apart from others of the call's T tokens (`same`: or are these, in place).
+struct Rows {
+    const void* at;
+    int64_t stride, row;           // elements
+};
+bool apart(const Rows& out, const Rows& other, bool same, int64_t T, int64_t size) {
+    if (T == 0 || out.row == 0 || other.row == 0) return true;
+    if (same && out.at == other.at && out.stride == other.stride) return true;
+    if (out.stride > (1LL << 56) || other.stride > (1LL << 56)) return false;
+    return rows_apart(out.at, out.stride * size, out.row * size, other.at, other.stride * size, other.row * size, T);
+}
+
 // What both calls check; fills the tensors and the turn.
 gdn_status make_params(const gdn_rotary_args* args, int64_t T, bool append, RotaryParams* out) {
     if (!args) return GDN_ERR_INVALID_ARG;
@@ -392,8 +404,14 @@ gdn_status make_params(const gdn_rotary_args* args, int64_t T, bool append, Rota
     if (T > 0 && a.kv_heads &&
         (!tensor_ok(a.k, a.dtype, p.k_stride, k_row) || (!append && !tensor_ok(a.k_out, a.dtype, p.k_out_stride, k_row))))
         return GDN_ERR_INVALID_ARG;
-    if (a.heads && p.q == p.q_out && p.q_stride != p.q_out_stride) return GDN_ERR_INVALID_ARG;
-    if (a.kv_heads && !append && p.k == p.k_out && p.k_stride != p.k_out_stride) return GDN_ERR_INVALID_ARG;
+    // Warps read and write their tokens, and parts of one token, in any order.
+    const int64_t size = dtype_bytes(a.dtype);
+    const Rows q{p.q, p.q_stride, q_row}, k{p.k, p.k_stride, k_row}, q_out{p.q_out, p.q_out_stride, q_row};
+    if (!apart(q_out, q, true, T, size) || !apart(q_out, k, false, T, size)) return GDN_ERR_INVALID_ARG;
+    if (!append) {
+        const Rows k_out{p.k_out, p.k_out_stride, k_row};
+        if (!apart(k_out, k, true, T, size) || !apart(k_out, q, false, T, size) || !apart(k_out, q_out, false, T, size)) return GDN_ERR_INVALID_ARG;
+    }
     p.q_same = p.q == p.q_out;
     p.k_same = !append && p.k == p.k_out;
     p.frequencies = a.frequencies;
@@ -437,6 +455,9 @@ gdn_status gdn_cache_append_run(const gdn_kv_batch* batch, const gdn_kv_cache* c
     if (args->kv_heads != cache->kv_heads || args->head_dim != cache->head_dim || args->dtype != cache->dtype) return GDN_ERR_INVALID_ARG;
     if (batch->total_tokens == 0 || batch->num_seqs == 0) return GDN_OK;
     if (!gdn::tensor_ok(v, args->dtype, v_stride, static_cast<int64_t>(args->kv_heads) * args->head_dim)) return GDN_ERR_INVALID_ARG;
+    const int64_t q_row = static_cast<int64_t>(args->heads) * args->head_dim, v_row = static_cast<int64_t>(args->kv_heads) * args->head_dim;
+    if (!gdn::apart(gdn::Rows{p.q_out, p.q_out_stride, q_row}, gdn::Rows{v, v_stride, v_row}, false, batch->total_tokens, gdn::dtype_bytes(args->dtype)))
+        return GDN_ERR_INVALID_ARG;
     p.v = v;
     p.v_stride = v_stride;
     p.b = *batch;

@@ -99,7 +99,7 @@ typedef struct gdn_kv_cache {
 /* What is turned, and how.  q or k may be NULL (heads or kv_heads 0). */
 typedef struct gdn_rotary_args {
     const void *q, *k;
-    void *q_out, *k_out; /* may be q and k themselves (same stride) */
+    void *q_out, *k_out; /* q and k themselves (same stride), or apart from q, k, v and each other */
     int64_t q_stride, k_stride, q_out_stride, k_out_stride;
     const double *frequencies;
     int32_t heads, kv_heads, head_dim, rotary_dim; /* rotary_dim even, 0 <= R <= D */
@@ -115,7 +115,8 @@ gdn_status gdn_rotary_run(const gdn_rotary_args *args, const void *positions, in
 
 /* k, turned, and v, as it is, into the cache; q, turned, to q_out (both NULL:
  * keys and values alone).  args' k_out is not used; rotary_dim = 0 turns
- * nothing.  v [T, kv_heads, D] has v_stride elements from token to token. */
+ * nothing.  v [T, kv_heads, D] has v_stride elements from token to token.  All
+ * of them are apart from the caches, which is not checked. */
 gdn_status gdn_cache_append_run(const gdn_kv_batch *batch, const gdn_kv_cache *cache, const gdn_rotary_args *args, const void *v,
                                 int64_t v_stride, void *stream);
 

@@ -225,3 +225,31 @@ def test_definition_attends_by_hand():
     table[1, 0] = -1
     out, *_ = ref.attend(q, k, v, table, [0, 3], [1], [2], 1.0)
     assert out[0, 0, 0] == 0 and out[1, 0, 0] == 0.0
+
+
+# 10 rows of q (4 x 64 bf16, 512 bytes), and of k and v (256 bytes).  Slices of one tensor: 1024 bytes from token to token.
+FUSED = dict(q=F, k=F + 512, q_stride=512, k_stride=512)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=F + 0x30000 + 2), dict(q_out=F + 0x30000 + 128), dict(q_out=F + 0x30000 - 128), dict(q_out=F + 0x30000 + 9 * 512),
+    dict(q_out=F + 0x40000), dict(q_out=F + 0x40000 - 128), dict(q_out=F + 0x40000 + 9 * 256), dict(q_out=F + 0x40000, q_out_stride=1024),
+    {**FUSED, "q_out": F + 128, "q_out_stride": 512}, {**FUSED, "q_out": F + 256, "q_out_stride": 512},
+    {**FUSED, "q_out": F + 640, "q_out_stride": 512}, {**FUSED, "q_out": F, "q_out_stride": 0},
+    {**FUSED, "q": F + 128, "q_out": F + 128, "q_out_stride": 512}, dict(q_out=F + 0x30000 + 2, q_out_stride=1 << 62)])
+def test_turned_queries_are_apart_or_in_place(L, kw):
+    assert L.gdn_rotary_run(ctypes.byref(rotary(**kw)), None, 0, None, 0, 0, 10, None) == INVALID
+    assert L.gdn_cache_append_run(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(rotary(**kw)), F + 0x80000, 0, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(k_out=F + 0x40000 + 128), dict(k_out=F + 0x30000), dict(k_out=F + 0x30000 + 9 * 512), dict(k_out=F + 0x50000),
+    dict(k_out=F + 0x50000 + 4096), {**FUSED, "q_out": F, "q_out_stride": 512, "k_out": F + 256, "k_out_stride": 512},
+    dict(q_out=F + 0x50000, q_out_stride=512, k_out=F + 0x50000 + 256, k_out_stride=512), dict(heads=0, q=None, q_out=None, k_out=F + 0x40000 + 2)])
+def test_turned_keys_are_apart_or_in_place(L, kw):
+    assert L.gdn_rotary_run(ctypes.byref(rotary(**kw)), None, 0, None, 0, 0, 10, None) == INVALID
+
+
+@pytest.mark.parametrize("v,stride", [(F + 0x50000, 0), (F + 0x50000 + 9 * 512 + 510, 0), (F + 0x50000 - 9 * 256, 0), (F + 0x50000 - 4096, 512)])
+def test_turned_queries_are_apart_from_the_values(L, v, stride):
+    assert L.gdn_cache_append_run(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(rotary()), v, stride, None) == INVALID
