@@ -185,6 +185,8 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     Differentiable in q and k when called without q_out and k_out."""
     if q is None and k is None:
         raise ValueError("q or k must be given")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("q_out needs q, and k_out needs k")
     if torch.is_grad_enabled() and ((q is not None and q.requires_grad) or (k is not None and k.requires_grad)):
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be differentiated through")

@@ -253,3 +253,10 @@ def test_turned_keys_are_apart_or_in_place(L, kw):
 @pytest.mark.parametrize("v,stride", [(F + 0x50000, 0), (F + 0x50000 + 9 * 512 + 510, 0), (F + 0x50000 - 9 * 256, 0), (F + 0x50000 - 4096, 512)])
 def test_turned_queries_are_apart_from_the_values(L, v, stride):
     assert L.gdn_cache_append_run(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(rotary()), v, stride, None) == INVALID
+
+
+def test_an_output_needs_its_input():
+    x, f = torch.zeros(2, 1, 8), gdn.rotary_frequencies(8, device="cpu")
+    for kw in (dict(q=None, k=x, q_out=x), dict(q=x, k=None, k_out=x)):
+        with pytest.raises(ValueError, match="needs"):
+            gdn.rotary_embedding(frequencies=f, **kw)
