@@ -287,7 +287,7 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
 
     A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token
     does not see has no influence on it, whatever it holds.  ``output``, when given, has its rows apart from q's (slices of one
-    tensor are allowed).  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.
+    tensor are allowed), and ``lse`` lies apart from both.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.
     Rows past the last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable.
 
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and

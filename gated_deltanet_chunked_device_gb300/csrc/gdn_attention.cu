@@ -533,6 +533,12 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     if (batch->total_tokens > 0 && !rows_apart(a.q, a.q_stride * bytes, row * bytes, a.output, a.output_stride * bytes, row * bytes, batch->total_tokens))
         return GDN_ERR_INVALID_ARG;  // a row may be read again after it is written
     if (!aligned(a.lse, 4)) return GDN_ERR_INVALID_ARG;
+    if (a.lse && batch->total_tokens > 0) {
+        const int64_t T = batch->total_tokens, lse_row = a.heads * int64_t{4};
+        if (!rows_apart(a.lse, lse_row, lse_row, a.q, a.q_stride * bytes, row * bytes, T) ||
+            !rows_apart(a.lse, lse_row, lse_row, a.output, a.output_stride * bytes, row * bytes, T))
+            return GDN_ERR_INVALID_ARG;
+    }
     Route r{};
     AttnParams& p = r.p;
     p.b = *batch;

@@ -123,7 +123,7 @@ gdn_status gdn_cache_append_run(const gdn_kv_batch *batch, const gdn_kv_cache *c
 typedef struct gdn_attention_args {
     const void *q;
     void *output; /* its rows apart from q's */
-    float *lse; /* optional */
+    float *lse; /* optional; apart from q and output */
     int64_t q_stride, output_stride;
     int32_t heads;
     float scale;

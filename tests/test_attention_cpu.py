@@ -260,3 +260,11 @@ def test_an_output_needs_its_input():
     for kw in (dict(q=None, k=x, q_out=x), dict(q=x, k=None, k_out=x)):
         with pytest.raises(ValueError, match="needs"):
             gdn.rotary_embedding(frequencies=f, **kw)
+
+
+@pytest.mark.parametrize("lse", [F + 0x30000, F + 0x30000 + 9 * 512 + 508, F + 0x30000 - 9 * 16, F + 0x40000 + 512, F + 0x40000 - 4])
+def test_logarithms_are_apart(L, lse):
+    assert run_attention(L, batch(), cache(), attention(lse=lse)) == INVALID
+    assert L.gdn_attention_workspace(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(attention(lse=lse))) == 0
+    for beside in (F + 0x30000 - 160, F + 0x30000 + 10 * 512, F + 0x50000):
+        assert L.gdn_attention_workspace(ctypes.byref(batch()), ctypes.byref(cache()), ctypes.byref(attention(lse=beside))) > 0
