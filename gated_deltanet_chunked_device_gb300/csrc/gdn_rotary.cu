@@ -193,19 +193,34 @@ __device__ __forceinline__ void copy_heads(const E* src, int32_t src_head, E* ds
     }
 }
 
+// The fraction of a turn, in units of 2^-64, that `radians` make: the mantissa times 1 / (2 pi) to 128 bits, of which the exponent picks
+// 64.  Off by less than a unit for |radians| < 2^63: 2^-33 of a turn at a position of 2^31.  (In doubles, a rounded 1 / (2 pi) was off
+// by 2^-55 of the angle, and a second double for what it lacks took 1.5 us more for 4096 tokens: there are few units for doubles.)
+__device__ __forceinline__ uint64_t turns_of(double radians) {
+    constexpr uint64_t kHigh = 0x28be60db9391054aull, kLow = 0x7f09d5f47d4d3770ull;  // floor(2^128 / (2 pi))
+    const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(radians));
+    const int field = static_cast<int>(bits >> 52 & 0x7ff);
+    const uint64_t m = (bits & ((1ull << 52) - 1)) | (field ? 1ull << 52 : 0ull);
+    const int shift = 64 - ((field ? field : 1) - 1075);  // of the product, whose low 128 bits are a fraction: its bits from `shift` on
+    const uint64_t p0 = m * kLow, p1 = __umul64hi(m, kLow) + m * kHigh, p2 = __umul64hi(m, kHigh) + (p1 < m * kHigh);
+    uint64_t turn = 0;
+    if (shift >= 128)
+        turn = shift < 192 ? p2 >> (shift - 128) : 0;
+    else if (shift > 64)
+        turn = p1 >> (shift - 64) | p2 << (128 - shift);
+    else if (shift > 0)
+        turn = shift == 64 ? p1 : p0 >> shift | p1 << (64 - shift);
+    return bits >> 63 ? 0 - turn : turn;
+}
+
 template <class E, int V, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, kResident) rotary_kernel(const __grid_constant__ RotaryParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, half = p.R / 2;
-    // Frequencies as turns a token in units of 2^-64 of a turn: a position times that, modulo 2^64, is the angle's fraction of
-    // a turn, exact but for the frequency's own rounding (2^-55 of a turn a token).
+    // Frequencies as turns a token in units of 2^-64 of a turn: a position times that, modulo 2^64, is the angle's fraction of a turn.
     int64_t* turns = reinterpret_cast<int64_t*>(smem);
     float2* cs = reinterpret_cast<float2*>(turns + half) + warp * half;
-    for (int i = tid; i < half; i += kThreads) {
-        double r = p.frequencies[i] * 0.15915494309189533577;  // 1 / (2 pi)
-        r -= rint(r);
-        turns[i] = static_cast<int64_t>(static_cast<uint64_t>(__double2ll_rn(r * 4611686018427387904.0)) << 2);  // 2^62
-    }
+    for (int i = tid; i < half; i += kThreads) turns[i] = static_cast<int64_t>(turns_of(p.frequencies[i]));
     __syncthreads();
     uint32_t err = 0;
     if (p.b.cu_seqlens && p.b.device_status && blockIdx.x == 0) {

@@ -11,9 +11,9 @@
  *
  * with (a, b) = (x[i], x[i + R / 2]), or (x[2 i], x[2 i + 1]) when interleaved;
  * channels R .. D - 1 stay as they are.  The angle's fraction of a turn is
- * formed exactly (64-bit integers), so positions may be as far as 2^31; sines,
- * products and sums are fp32, the result is rounded once.  The backward pass is
- * the same call with inverse != 0: the turn the other way.
+ * formed in integers, right to 2^-33 of a turn at positions as far as 2^31;
+ * sines, products and sums are fp32, the result is rounded once.  The backward
+ * pass is the same call with inverse != 0: the turn the other way.
  *
  * The cache.  A page is one row of k and of v, [n_pages, page_tokens, kv_heads,
  * D] with any strides over contiguous channels; table, lengths and n_pages are
