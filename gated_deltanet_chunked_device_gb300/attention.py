@@ -156,6 +156,24 @@ def _rotary(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude, q_
     return q_out, k_out
 
 
+def _wants_grad(*tensors):
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
+class _Serving(torch.autograd.Function):
+    """A step of serving: what `run` returns, with a history that says that there is no gradient."""
+
+    @staticmethod
+    def forward(ctx, name, run, *inputs):
+        ctx.name = name
+        return run()
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError(f"{ctx.name} is a step of serving and has no gradient; a loss through it needs the attention in other "
+                           "operations, serving torch.no_grad()")
+
+
 class _Rotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, frequencies, positions, cu_seqlens, interleaved, magnitude):
@@ -167,6 +185,8 @@ class _Rotary(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dq, dk):
+        if ctx.needs_input_grad[2]:
+            raise RuntimeError("rotary_embedding has no gradient with respect to its frequencies")
         frequencies, positions, cu_seqlens = ctx.saved_tensors
         dq, dk = (d.contiguous() if d is not None and n else None for d, n in zip((dq, dk), ctx.needs_input_grad))
         if dq is not None or dk is not None:
@@ -182,7 +202,8 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     ``cu_seqlens`` (int32 or int64; rows past its end go on counting), or from 0 over all rows.  Tokens may be strided (slices of a
     projection's output).  ``q_out`` and ``k_out`` may be q and k themselves, or are apart from them and from each other.  Returns ``(q_out, k_out)``.
 
-    Differentiable in q and k when called without q_out and k_out."""
+    Differentiable in q and k when called without q_out and k_out; not in the frequencies (a backward pass that would need their
+    gradients raises an error)."""
     if q is None and k is None:
         raise ValueError("q or k must be given")
     if (q is None and q_out is not None) or (k is None and k_out is not None):
@@ -190,6 +211,8 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
     if torch.is_grad_enabled() and ((q is not None and q.requires_grad) or (k is not None and k.requires_grad)):
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be differentiated through")
+        return _Rotary.apply(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude)
+    if q_out is None and k_out is None and _wants_grad(frequencies):
         return _Rotary.apply(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude)
     out = _rotary(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude, q_out, k_out, 0)
     if q_out is not None or k_out is not None:
@@ -254,7 +277,15 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
 
     No two entries of ``seqs`` may name one row.  Tokens without a page are not written (``device_status``, an int32 tensor, receives
     the bits of DEVICE_ERR and PAGES_ERR).  Rows past the last sequence are padding and stay as they are.  A step of serving: not
-    differentiable."""
+    differentiable (a backward pass through a new output raises an error; one through ``output`` or the caches ends there)."""
+    if output is None and q is not None and _wants_grad(q, frequencies):
+        return _Serving.apply("cache_append", lambda: _append(k, v, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, q, frequencies,
+                                                              interleaved, magnitude, None, device_status), q, frequencies)
+    return _append(k, v, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, q, frequencies, interleaved, magnitude, output,
+                   device_status)
+
+
+def _append(k, v, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, q, frequencies, interleaved, magnitude, output, device_status):
     T, D, dtype, device = _first("k", k)
     packed, P, pt, Hk = _cache(k_cache, v_cache, D, dtype, device)
     batch = _batch(T, table, lengths, seqs, cu_seqlens, tokens_per_seq, P, pt, device_status, device)
@@ -288,11 +319,19 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token
     does not see has no influence on it, whatever it holds.  ``output``, when given, has its rows apart from q's (slices of one
     tensor are allowed), and ``lse`` lies apart from both.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.
-    Rows past the last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable.
+    Rows past the last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable (a backward
+    pass through a new output raises an error; one through ``output`` or ``lse`` ends there).
 
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and
     addresses are multiples of 16 bytes.  Heads of an odd number of channels, and fp32, are computed on CUDA cores, at about a
     fiftieth of the rate."""
+    if output is None and _wants_grad(q, k_cache, v_cache):
+        return _Serving.apply("paged_attention", lambda: _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal,
+                                                                 window, None, lse, device_status), q, k_cache, v_cache)
+    return _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal, window, output, lse, device_status)
+
+
+def _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal, window, output, lse, device_status):
     T, D, dtype, device = _first("q", q)
     packed, P, pt, Hk = _cache(k_cache, v_cache, D, dtype, device)
     Hq, qs = _heads("q", q, T, D, dtype, device)
