@@ -9,8 +9,7 @@
 //     O += P V                P from TMEM, O fp32 in TMEM
 //
 // m is the row's running maximum, raised (and O and the sum l scaled down) only when it has grown by more than 2^8: P stays
-// below 2^8 (fp16: 2^15, from an offset of 2^7 that lifts small weights out of fp16's subnormals), and any m gives the same
-// quotient.  P is rounded to 16 bits for the product, relative to itself; l sums the unrounded weights in fp32.
+// below 1 (fp16: 2^15), and any m gives the same quotient.  P is rounded to 16 bits for the product, relative to itself; l sums the unrounded weights in fp32.
 //
 // Two shapes.  kStreams = 2, for many rows: two row tiles against the same keys, each with a warpgroup of its own for the
 // exponentials, so that the tensor cores work on one while the other's are computed.  kStreams = 1, for few rows, or heads of
@@ -40,6 +39,11 @@ namespace attn_tc {
 
 constexpr int kRowTile = 128;
 constexpr float kGrowth = 8.f;      // log2 of how far a row's maximum may fall behind
+// log2 of a row's largest weight as P holds it, when its maximum has just been taken.  fp16: weights are lifted out of its subnormals, and
+// stay below 2^15.  bf16 has the range of fp32: weights stay below 1, so that sums of them times large values overflow no sooner than
+// a softmax's does.
+template <class E>
+constexpr float weight_offset() { return std::is_same<E, __half>::value ? 7.f : -kGrowth; }
 constexpr int kParts = 4;           // parts handed from the producer to the others ahead
 
 template <int kDim, int kStreams>
@@ -925,7 +929,7 @@ __device__ void multiply(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint8_t* 
 // ------------------------------------------------------------------------------------------------ warps 4..: exponentials, results
 template <class E, class S, int kDim, int kStreams>
 __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int stream, int warp, int lane, int32_t block) {
-    constexpr float kOffset = std::is_same<E, __half>::value ? 7.f : 0.f;
+    constexpr float kOffset = weight_offset<E>();
     const AttnParams& ap = p.a;
     const int D = ap.c.head_dim;
     int32_t* status = ap.b.device_status;
@@ -1156,7 +1160,7 @@ __device__ void exponentiate(const TcParams& p, Misc<S>& sh, uint32_t tmem, int 
 // have all rows.  At a part's end the four results are joined in the space of the unit's Q.
 template <class E, class S>
 __device__ void exponentiate_quarters(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint32_t tmem, int warp, int lane, int32_t block) {
-    constexpr float kOffset = std::is_same<E, __half>::value ? 7.f : 0.f;
+    constexpr float kOffset = weight_offset<E>();
     const AttnParams& ap = p.a;
     const int D = ap.c.head_dim;
     int32_t* status = ap.b.device_status;
