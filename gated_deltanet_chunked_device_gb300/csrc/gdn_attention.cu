@@ -487,8 +487,9 @@ void tc_route(Route* r) {
     const bool f16 = p.c.dtype == GDN_DTYPE_F16;
     t.idesc_qk = idesc_16bit_f32(rows, p.tile, false, false, p.scale_log2 < 0.f, f16);
     t.idesc_pv = idesc_16bit_f32(rows, 16 * t.k_steps, false, true, false, f16);
-    // Scores of keys that are not seen are -infinity, which has to survive the scaling: zero becomes a scale that any finite score vanishes in.
-    t.scale_log2 = fmaxf(fabsf(p.scale_log2), 1e-30f);
+    // Scores of keys that are not seen are -infinity, which has to survive the scaling: zero becomes fp32's smallest number, in which the
+    // largest finite score, 2^128, becomes 2^-21.
+    t.scale_log2 = fmaxf(fabsf(p.scale_log2), 0x1p-149f);
     t.out_vec = D % 8 == 0 && p.o_stride % 8 == 0 && aligned(p.o, 16);
     t.wait_cycles = attn_tc::kWaitCycles;
     r->blocks = multiprocessors();

@@ -29,3 +29,14 @@ def test_large_values(dtype, value, heads, tokens):
     for s in c.seqs.tolist():
         c.k[c.table[s, 2:4].long(), :, :, 0] = 5.5
     c.check(scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, 1e-40, -1e-38, 1e-37])
+@pytest.mark.parametrize("tokens", [1, 150])
+def test_small_scales_of_large_scores(dtype, scale, tokens):
+    """Scores of up to 64e36 under scales that leave nothing of them, or some units: with a scale of zero every key counts the same."""
+    c = Cache([tokens] * 3, [300 - tokens, 40, 500], 4, 2, 64, 16, dtype, seed=3)
+    c.q = torch.full_like(c.q, 1e18)
+    c.k = (c.k.float().sign() * 1e18).to(c.dtype)
+    c.check(scale=scale)
