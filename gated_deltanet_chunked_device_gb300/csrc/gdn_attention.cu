@@ -13,8 +13,10 @@ namespace {
 // ------------------------------------------------------------------------------------------------ CUDA cores
 // Every type, head size and layout: 64 rows of a unit against tiles of 64 keys, all of it fp32, one pass with a running maximum
 // and sum for each row.  256 threads as 16 x 16: a thread has 4 rows by 4 keys of the scores (keys tx + 16 c) and 4 rows by 4 x kCols
-// channels of the result (channels 4 tx + 64 c).  Large calls in fp32 run at 25 TFLOP/s (2048 tokens over 6144, 16 heads on 2 of 128,
-// 3421 us), half of what a library's fp32 product reaches; small ones are bound by the latency of a block's two or three tiles.
+// channels of the result (channels 4 tx + 64 c).  Large calls in fp32 run at 26 TFLOP/s (2048 tokens over 6144, 16 heads on 2 of 128,
+// 3250 us; of 112, two blocks an SM: 2445 us), half of what a library's fp32 product reaches; small ones are bound by the latency of a
+// block's two or three tiles, single tokens by one warp of eight that works while nothing is fetched (64 sequences of 4096, 16 heads on 2
+// of 128: 515 us, of which HBM needs 81).
 constexpr int kRows = 64, kKeys = 64, kThreads = 256;
 
 __device__ __forceinline__ float wide(float x) { return x; }
@@ -32,14 +34,18 @@ struct alignas(sizeof(E) * V) Vec {
 // The lowest n bits, n of any size and sign.
 __device__ __forceinline__ uint64_t low_bits64(int64_t n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// Floats from row to row in shared memory: a multiple of 4 that is 4 more than one of 32, so that 16-byte accesses of successive
-// rows fall into different banks.
-__host__ __device__ inline int row_floats(int D) { return (D + 3) / 4 * 4 % 32 == 4 ? (D + 3) / 4 * 4 : (D + 31) / 32 * 32 + 4; }
+// Floats from row to row in shared memory: an odd multiple of 4, so that 16-byte accesses of eight successive rows fall into different
+// banks.
+__host__ __device__ inline int row_floats(int D) { return 4 * ((D + 3) / 4 | 1); }
 
 size_t simple_smem(int D) { return sizeof(float) * (3 * kRows * row_floats(D) + kRows * (kKeys + 4)) + kKeys * 2 * sizeof(int64_t); }
 
-template <class E, int kVec, int kCols>
-__global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1) attention_simple_kernel(const __grid_constant__ AttnParams p) {
+// Blocks an SM: two where the shared memory of both (and some 1.5 KB each beside it) fits, which is for heads of up to 124 channels.  A
+// kernel is compiled for the number that it runs with.
+int simple_resident(int D) { return 2 * (simple_smem(D) + 1536) <= 228 * 1024 ? 2 : 1; }
+
+template <class E, int kVec, int kCols, int kBlocks>
+__global__ void __launch_bounds__(kThreads, kBlocks) attention_simple_kernel(const __grid_constant__ AttnParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ AttnScan<kThreads> scan;
     __shared__ uint32_t there_s[2];        // the keys of a tile that have a page, a bit a key
@@ -277,10 +283,10 @@ __global__ void __launch_bounds__(kThreads, kCols <= 2 ? 2 : 1) attention_simple
     kv_report(p.b.device_status, err);
 }
 
-template <class E, int kVec, int kCols>
+template <class E, int kVec, int kCols, int kBlocks>
 cudaError_t launch_simple(const AttnParams& p, int32_t blocks, cudaStream_t stream) {
     const size_t smem = simple_smem(p.c.head_dim);
-    auto kernel = attention_simple_kernel<E, kVec, kCols>;
+    auto kernel = attention_simple_kernel<E, kVec, kCols, kBlocks>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kThreads, smem, stream>>>(p);
@@ -294,9 +300,10 @@ cudaError_t launch_simple_typed(const AttnParams& p, int32_t blocks, cudaStream_
     bool vec = reinterpret_cast<uintptr_t>(p.c.k) % (4 * sizeof(E)) == 0 && reinterpret_cast<uintptr_t>(p.c.v) % (4 * sizeof(E)) == 0;
     for (int64_t s : strides) vec = vec && s % 4 == 0;
     const int D = p.c.head_dim;
-    if (D <= 64) return vec ? launch_simple<E, 4, 1>(p, blocks, stream) : launch_simple<E, 1, 1>(p, blocks, stream);
-    if (D <= 128) return vec ? launch_simple<E, 4, 2>(p, blocks, stream) : launch_simple<E, 1, 2>(p, blocks, stream);
-    return vec ? launch_simple<E, 4, 4>(p, blocks, stream) : launch_simple<E, 1, 4>(p, blocks, stream);
+    if (D <= 64) return vec ? launch_simple<E, 4, 1, 2>(p, blocks, stream) : launch_simple<E, 1, 1, 2>(p, blocks, stream);
+    if (simple_resident(D) == 2) return vec ? launch_simple<E, 4, 2, 2>(p, blocks, stream) : launch_simple<E, 1, 2, 2>(p, blocks, stream);
+    if (D <= 128) return vec ? launch_simple<E, 4, 2, 1>(p, blocks, stream) : launch_simple<E, 1, 2, 1>(p, blocks, stream);
+    return vec ? launch_simple<E, 4, 4, 1>(p, blocks, stream) : launch_simple<E, 1, 4, 1>(p, blocks, stream);
 }
 
 // ------------------------------------------------------------------------------------------------ the join
@@ -561,7 +568,7 @@ gdn_status make_route(const gdn_kv_batch* batch, const gdn_kv_cache* cache, cons
     p.unit_cost = 1;
     p.min_steps = 2;
     r.rows = p.unit_tokens * p.group;
-    r.blocks = multiprocessors() * (c.head_dim <= 128 ? 2 : 1);
+    r.blocks = multiprocessors() * simple_resident(c.head_dim);
     if (tensor_cores(p)) tc_route(&r);
     *out = r;
     return GDN_OK;
