@@ -156,10 +156,6 @@ def _rotary(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude, q_
     return q_out, k_out
 
 
-def _wants_grad(*tensors):
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
-
-
 class _Serving(torch.autograd.Function):
     """A step of serving: what `run` returns, with a history that says that there is no gradient."""
 
@@ -212,7 +208,7 @@ def rotary_embedding(q, k, frequencies, positions=None, cu_seqlens=None, interle
         if q_out is not None or k_out is not None:
             raise ValueError("q_out and k_out cannot be differentiated through")
         return _Rotary.apply(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude)
-    if q_out is None and k_out is None and _wants_grad(frequencies):
+    if frequencies is not None and frequencies.requires_grad and torch.is_grad_enabled() and q_out is None and k_out is None:
         return _Rotary.apply(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude)
     out = _rotary(q, k, frequencies, positions, cu_seqlens, interleaved, magnitude, q_out, k_out, 0)
     if q_out is not None or k_out is not None:
@@ -278,7 +274,7 @@ def cache_append(k, v, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     No two entries of ``seqs`` may name one row.  Tokens without a page are not written (``device_status``, an int32 tensor, receives
     the bits of DEVICE_ERR and PAGES_ERR).  Rows past the last sequence are padding and stay as they are.  A step of serving: not
     differentiable (a backward pass through a new output raises an error; one through ``output`` or the caches ends there)."""
-    if output is None and q is not None and _wants_grad(q, frequencies):
+    if output is None and q is not None and torch.is_grad_enabled() and (q.requires_grad or (frequencies is not None and frequencies.requires_grad)):
         return _Serving.apply("cache_append", lambda: _append(k, v, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, q, frequencies,
                                                               interleaved, magnitude, None, device_status), q, frequencies)
     return _append(k, v, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, q, frequencies, interleaved, magnitude, output,
@@ -325,7 +321,7 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and
     addresses are multiples of 16 bytes.  Heads of an odd number of channels, and fp32, are computed on CUDA cores, at about a
     fiftieth of the rate."""
-    if output is None and _wants_grad(q, k_cache, v_cache):
+    if output is None and torch.is_grad_enabled() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad):
         return _Serving.apply("paged_attention", lambda: _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal,
                                                                  window, None, lse, device_status), q, k_cache, v_cache)
     return _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal, window, output, lse, device_status)
