@@ -262,80 +262,110 @@ __device__ __forceinline__ uint32_t cut_blocks(const AttnPart& a, int32_t tile, 
 // What rows get of the values that are not finite among those that they see, from the cache itself: by a warp, its lanes' rows (row:
 // there is one, with keys) against `tiles`.  It is added to a row's result, in blocks of keys that some row does not see whole (in
 // others the products have taken it), or takes its place (kInstead: the rows of lanes 0, 4, 8 ..).  A seen value counts however small
-// its weight is.
+// its weight is.  A lane has two neighbouring channels of each 64; of 32 keys it notes, a bit a key, where they are infinite of either
+// sign (NaN: both), which answers for all rows: a block takes some thousand cycles whatever it holds.
 template <class E, bool kInstead>
 __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart& a, bool row, int t, int g, int32_t lo, int32_t hi, int2 tiles,
                                              int32_t block, int lane) {
+    constexpr uint32_t kMantissa = std::is_same<E, __half>::value ? 0x03ffu : 0x007fu;
     const int D = p.c.head_dim;
     uint64_t placed = 0;           // kInstead: channels whose results have been replaced, 8 bits a row
-    auto value = [&](int64_t at, int d) { return at >= 0 && d < D ? wide16(static_cast<const E*>(p.c.v)[at + d]) : 0.f; };
+    uint32_t all_pos = 0, all_neg = 0;  // kInstead: channels that keys of all rows make infinite
+    // Row r (a lane's) gets infinities in the channels that the bits name.
+    auto give = [&](int r, uint32_t up, uint32_t down) {
+        if (!__any_sync(~0u, (up | down) != 0)) return;
+        const RowOut<E> out = row_out<E>(p, a, block, __shfl_sync(~0u, t, r), __shfl_sync(~0u, g, r));
+        bool over = true;          // all of the row is NaN, and nothing changes that
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const int d = 2 * lane + 64 * (c / 2) + c % 2;
+            if (d >= D) break;
+            const bool plus = up >> c & 1, minus = down >> c & 1;
+            const uint64_t bit = 1ull << (2 * (r & 28) + c);
+            float now = out.o ? wide16(out.o[d]) : out.part[d];
+            if (plus || minus) {
+                const float x = plus && minus ? __int_as_float(0x7fffffff) : plus ? INFINITY : -INFINITY;
+                now = kInstead && !(placed & bit) ? x : now + x;
+                placed |= bit;
+                if (out.o)
+                    out.o[d] = narrow16<E>(now);
+                else
+                    out.part[d] = now;
+            }
+            over &= now != now && (!kInstead || (placed & bit));
+        }
+        if (__all_sync(~0u, over) && lane == r) row = false;
+    };
     int32_t every0, every1;
     keys_of_all(p, a, every0, every1);
     __syncwarp();  // the rows' other results are there for all lanes
     for (int64_t key0 = static_cast<int64_t>(tiles.x) * 128; key0 < static_cast<int64_t>(tiles.y) * 128; key0 += 32) {
-        if (!kInstead && seen_by_all(a, key0, 32, every0, every1)) continue;
+        const bool whole = seen_by_all(a, key0, 32, every0, every1);
+        if (!kInstead && whole) continue;
         const int64_t key = key0 + lane;
         const int first = static_cast<int>(min(max(lo - key0, int64_t{0}), int64_t{32})), end = static_cast<int>(min(max(hi - key0, int64_t{0}), int64_t{32}));
-        uint32_t seen = row ? low_bits(end) & ~low_bits(first) : 0u;
-        const uint32_t some = __reduce_or_sync(~0u, seen);
+        const uint32_t seen = row ? low_bits(end) & ~low_bits(first) : 0u, some = __reduce_or_sync(~0u, seen);
         int64_t at = -1;  // where the key's values are
         if (some >> lane & 1 && key < a.keys) {
             const int32_t i = static_cast<int32_t>(key) / p.b.page_tokens, slot = static_cast<int32_t>(key) - i * p.b.page_tokens;
             const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + i];
             if (page >= 0 && page < p.b.n_pages) at = page * p.c.v_page_stride + slot * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
         }
-        // Which of the keys have such values: two channels a lane and load (rows are multiples of 4 bytes here), 16 loads at a time.
-        uint32_t bad = 0;
-#pragma unroll 1
-        for (int d = 2 * lane; d - 2 * lane < D; d += 64)
-#pragma unroll 1
-            for (int i0 = 0; i0 < 32; i0 += 16) {
-                if (!(some >> i0 & 0xffffu)) continue;
-                uint32_t x[16];
+        uint32_t pos[8]{}, neg[8]{};
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+        for (int c = 0; c < 4; ++c) {
+            const int d = 2 * lane + 64 * c;  // rows are multiples of 4 bytes here
+            if (64 * c >= D) break;
+#pragma unroll 1
+            for (int i0 = 0; i0 < 32; i0 += 8) {
+                if (!(some >> i0 & 0xffu)) continue;
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
                     const int64_t from = __shfl_sync(~0u, at, i0 + i);
                     x[i] = 0;
                     if (from >= 0 && d < D) x[i] = *reinterpret_cast<const uint32_t*>(static_cast<const E*>(p.c.v) + from + d);
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (unfinite_signs<E>(x[i])) bad |= 1u << (i0 + i);
-            }
-        seen &= __reduce_or_sync(~0u, bad);
-        for (unsigned rows = __ballot_sync(~0u, seen != 0); rows; rows &= rows - 1) {
-            const int r = __ffs(rows) - 1;
-            const RowOut<E> out = row_out<E>(p, a, block, __shfl_sync(~0u, t, r), __shfl_sync(~0u, g, r));
-            float sum[8]{};
-            for (uint32_t k = __shfl_sync(~0u, seen, r); k; k &= k - 1) {
-                const int64_t from = __shfl_sync(~0u, at, __ffs(k) - 1);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t bad = unfinite_signs<E>(x[i]);
+                    if (!bad) continue;
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    const float v = value(from, lane + 32 * c);
-                    if (v - v != 0.f) sum[c] += v;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t v = x[i] >> (16 * h) & 0xffffu, bit = bad >> (15 + 16 * h) & 1u;
+                        const bool nan = v & kMantissa;
+                        if (nan || !(v & 0x8000u)) pos[2 * c + h] |= bit << (i0 + i);
+                        if (nan || (v & 0x8000u)) neg[2 * c + h] |= bit << (i0 + i);
+                    }
                 }
             }
-            bool over = true;  // all of the row is NaN, and nothing changes that
+        }
+        if (kInstead && whole) {
+            bool nan = true;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const int d = lane + 32 * c;
-                if (d >= D) break;
-                float now = out.o ? wide16(out.o[d]) : out.part[d];
-                const uint64_t bit = 1ull << (2 * (r & 28) + c);
-                if (sum[c] != 0.f) {
-                    now = kInstead && !(placed & bit) ? sum[c] : now + sum[c];
-                    placed |= bit;
-                    if (out.o)
-                        out.o[d] = narrow16<E>(now);
-                    else
-                        out.part[d] = now;
-                }
-                over &= now != now && (!kInstead || (placed & bit));
+                if (pos[c]) all_pos |= 1u << c;
+                if (neg[c]) all_neg |= 1u << c;
+                if (2 * lane + 64 * (c / 2) + c % 2 < D) nan &= (all_pos & all_neg) >> c & 1;
             }
-            if (__all_sync(~0u, over) && lane == r) row = false;
+            if (__all_sync(~0u, nan)) break;
+            continue;
+        }
+        for (unsigned rows = __ballot_sync(~0u, seen != 0); rows; rows &= rows - 1) {
+            const int r = __ffs(rows) - 1;
+            const uint32_t keys = __shfl_sync(~0u, seen, r);
+            uint32_t up = 0, down = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (pos[c] & keys) up |= 1u << c;
+                if (neg[c] & keys) down |= 1u << c;
+            }
+            give(r, up, down);
         }
         if (!__any_sync(~0u, row)) return;
     }
+    if (kInstead)
+        for (unsigned rows = __ballot_sync(~0u, row); rows; rows &= rows - 1) give(__ffs(rows) - 1, all_pos, all_neg);
 }
 
 // Notes a unit that later blocks go on with, so that the join comes to its rows.

@@ -115,3 +115,31 @@ def test_a_long_context(dtype, heads, kv_heads, D, page_tokens):
             sees[first:n, :heads // kv_heads, 5] = True
             assert torch.equal(got[~sees], want[~sees]) and not bool(torch.isfinite(got[sees]).any()), (n, pos)
     assert int(word) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D,page_tokens", [(64, 64), (128, 64), (256, 64), (128, 20)])
+@pytest.mark.parametrize("tokens", [1, 4, 500])
+def test_a_channel_that_is_infinite_throughout(dtype, D, page_tokens, tokens):
+    """As where a projection overflows: over 131072 tokens one channel of one head is infinite, another one of both signs, a third NaN."""
+    past, heads, kv_heads = 131072 - tokens, 4, 2
+    g = torch.Generator("cuda").manual_seed(1)
+    pages = -(-(past + tokens) // page_tokens)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float16)  # noqa: E731
+    q, k, v = r(tokens, heads, D), r(pages, page_tokens, kv_heads, D), r(pages, page_tokens, kv_heads, D)
+    table = torch.randperm(pages, generator=g, device="cuda").int()[None]
+    lengths = torch.tensor([past + tokens], dtype=torch.int32, device="cuda")
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    call = lambda: gdn.paged_attention(q, k, v, table, lengths, device_status=word)  # noqa: E731
+    want = call()
+    v[:, :, 1, 3] = -INF
+    v[:, :, 1, 10] = INF
+    v[0, :, 1, 10] = -INF
+    v[:, :, 1, 63] = NAN
+    got = call()
+    same = torch.ones_like(want, dtype=torch.bool)
+    same[:, 2:, [3, 10, 63]] = False
+    assert int(word) == 0 and torch.equal(got[same], want[same])
+    if tokens < 500 or dtype == "bf16":  # fp16 weights below 2^-32 of the largest make NaN of an infinity in the products
+        assert bool((got[:, 2:, 3] == -INF).all())
+    assert not bool(torch.isfinite(got[:, 2:, 3]).any()) and bool(torch.isnan(got[:, 2:, [10, 63]]).all())
