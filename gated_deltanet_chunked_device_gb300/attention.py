@@ -75,7 +75,8 @@ def rotary_frequencies(rotary_dim, base=10000.0, factor=1.0, original_length=Non
 
     ``factor`` divides all of them; with ``original_length`` (the context that a model was trained on) only those that turn
     at most ``slow_turns`` times over that length are divided, those that turn ``fast_turns`` times or more stay, and in
-    between the two are mixed in proportion to the number of turns."""
+    between the two are mixed in proportion to the number of turns.  (Models whose released code mixes in proportion to the channel's
+    index between those two numbers of turns need frequencies of their own: any float64 vector will do.)"""
     if rotary_dim < 0 or rotary_dim % 2:
         raise ValueError("rotary_dim must be even")
     if not (base > 0 and factor > 0):
@@ -313,14 +314,18 @@ def paged_attention(q, k_cache, v_cache, table, lengths, seqs=None, cu_seqlens=N
     fp32, when given, receives the logarithm of the sum of the scores' exponentials.  Returns ``output`` [T, heads, D].
 
     A token that sees nothing gets zeros (lse: minus infinity; so does one that sees only scores of minus infinity); what a token
-    does not see has no influence on it, whatever it holds.  ``output``, when given, has its rows apart from q's (slices of one
-    tensor are allowed), and ``lse`` lies apart from both.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR; what has no page is not seen.
-    Rows past the last sequence are padding and stay as they are.  D is at most 256.  A step of serving: not differentiable (a backward
-    pass through a new output raises an error; one through ``output`` or ``lse`` ends there).
+    does not see has no influence on it, whatever it holds.  A channel in which it sees an infinite value is infinite (NaN, where it
+    sees both signs or NaN, or where the weight, rounded to q's type, vanishes).  Sums of weights times values are fp32: values past
+    the largest fp32 divided by the number of keys may overflow.  ``output``, when given, has its rows apart from q's (slices of one
+    tensor are allowed), and ``lse`` lies apart from both.  ``device_status`` (int32) receives the bits of DEVICE_ERR and PAGES_ERR;
+    what has no page is not seen.  After "TIMEOUT", a wait inside the kernel that ran out, what depends on it is NaN.  Rows past the last sequence are padding and stay as they
+    are.  D is at most 256.  A step of serving: not differentiable (a backward pass through a new output raises an error; one through
+    ``output`` or ``lse`` ends there).
 
     Fastest in bf16 and fp16 where D is a multiple of 8, pages have a multiple of 8 tokens, and q's and the caches' strides and
-    addresses are multiples of 16 bytes.  Heads of an odd number of channels, and fp32, are computed on CUDA cores, at about a
-    fiftieth of the rate."""
+    addresses are multiples of 16 bytes.  Other pages, strides and addresses take two to ten times as long.  On CUDA cores, at about a
+    fortieth of the rate, are computed: fp32; rows (heads, strides or addresses of q and the caches) that are no multiples of 4 bytes;
+    and few tokens of up to 124 channels (64, where rows are multiples of 8 bytes) in rows that are no multiples of 16 bytes."""
     if output is None and torch.is_grad_enabled() and (q.requires_grad or k_cache.requires_grad or v_cache.requires_grad):
         return _Serving.apply("paged_attention", lambda: _attend(q, k_cache, v_cache, table, lengths, seqs, cu_seqlens, tokens_per_seq, scale, causal,
                                                                  window, None, lse, device_status), q, k_cache, v_cache)

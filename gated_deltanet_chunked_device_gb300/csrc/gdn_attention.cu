@@ -454,18 +454,21 @@ int widest_piece(const AttnParams& p) {
 
 // Whether the tensor cores take a call.  fp32 would lose its last 13 bits there.  Rows that tiled copies cannot fetch are copied by two
 // warps in such pieces, which bounds the kernel; whether that still pays (us, tensor cores and CUDA cores, 16 heads on 2, bf16):
-//   64 sequences of 4096 tokens, one new: pieces of 16 bytes, heads of 128: 246 and 696; 104: 252 and 728
-//                                                   8 bytes,          100: 389 and 412;  60: 250 and 246
-//                                                   4 bytes,          102: 513 and 811;  62: 342 and 220
-//                                                   2 bytes,          101: 4879 and 809; 63: 2102 and 220
-//   a prompt's 4096 tokens over as many: 16 bytes, 128: 857 and 8649; 8, 100: 1412 and 6120; 4, 102: 1994 and 8989; 2, 101: 9434 and 8983
-// So pieces of 2 bytes, which no asynchronous copy has, are left to the CUDA cores, and few rows of up to 64 channels in pieces of 4 and 8.
+//   64 sequences of 4096 tokens, one new: pieces of 16 bytes, heads of 128: 240 and 710; 104: 248 and 410
+//                                                   8 bytes,          100: 377 and 401; 92: 314 and 390; 84: 314 and 383;  60: 248 and 237
+//                                                   4 bytes,          202: 955 and 1264; 126: 555 and 742; 122: 554 and 458; 102: 505 and
+//                                                                     440; 70: 397 and 368;  62: 342 and 209
+//                                                   2 bytes,          101: 4879 and 436; 63: 2102 and 209
+//   a prompt's 4096 tokens over as many: 16 bytes, 128: 847 and 8668; 8, 100: 1403 and 6148; 4, 102: 1986 and 6275; 2, 101: 9434 and 6272
+// So pieces of 2 bytes, which no asynchronous copy has, are left to the CUDA cores; and of few rows those in pieces of 8 bytes up to 64
+// channels, and those in pieces of 4 where two blocks fit an SM.
 bool tensor_cores(const AttnParams& p) {
     if (p.c.dtype == GDN_DTYPE_F32 || p.b.n_pages < 1) return false;
     if (tiles_fit(p)) return true;
     const int piece = widest_piece(p);
     const bool many = p.b.total_tokens * p.per_kv > static_cast<int64_t>(p.b.num_seqs) * attn_tc::kRowTile;
-    return piece == 16 || (piece >= 4 && (many || p.c.head_dim > 64));
+    const bool small = piece == 8 ? p.c.head_dim <= 64 : simple_resident(p.c.head_dim) == 2;
+    return piece == 16 || (piece >= 4 && (many || !small));
 }
 
 // The tensor cores' shape.  Two row tiles a unit pay where a sequence has, on the average, rows for more than one.

@@ -9,7 +9,8 @@
 //     O += P V                P from TMEM, O fp32 in TMEM
 //
 // m is the row's running maximum, raised (and O and the sum l scaled down) only when it has grown by more than 2^8: P stays
-// below 1 (fp16: 2^15), and any m gives the same quotient.  P is rounded to 16 bits for the product, relative to itself; l sums the unrounded weights in fp32.
+// below 1 (fp16: 2^15), and any m gives the same quotient.  P is rounded to 16 bits for the product, relative to itself; l sums the
+// unrounded weights in fp32.
 //
 // Two shapes.  kStreams = 2, for many rows: two row tiles against the same keys, each with a warpgroup of its own for the
 // exponentials, so that the tensor cores work on one while the other's are computed.  kStreams = 1, for few rows, or heads of
@@ -18,13 +19,14 @@
 //
 // Bounds and figures (GB300).  Many rows: the chain scores - exponentials - weights - products of two streams; the tensor pipe works
 // 59 % of the time (2048 tokens over 30720, 32 heads on 16 of 128, fp16: 0.9 ms, 1.17 PFLOP/s; 8 prompts of 33720 tokens, 32 heads on
-// 8, bf16: 1.45 ms, 1.15 PFLOP/s).  Single tokens over long contexts: HBM (512 sequences of up to 8192, bf16: 331 us, 0.97 of a
-// measured copy).  Four tokens under a window of 1024, heads of 64, pages of 16: a tile's steps and a copy a page of 2 KB (71 us, floor
-// 20; four warps that share a tile's keys brought 80 to 67, a division that suits short sequences cost 4).  Heads of 256 with many rows: the chain of a single row tile (tensor pipe 33 %).
+// 8, bf16: 1.42 ms, 1.18 PFLOP/s).  Single tokens over long contexts: HBM (512 sequences of up to 8192, bf16: 331 us, 0.97 of a
+// measured copy).  Four tokens under a window of 1024, heads of 64, pages of 16: a tile's steps and a copy a page of 2 KB (72 us, floor
+// 20; four warps that share a tile's keys brought 80 to 67, a division that suits short sequences cost 4, looking through the values of
+// cut tiles 2).  Heads of 256 with many rows: the chain of a single row tile (tensor pipe 35 %).
 //
 // Where tiled copies cannot fetch the rows (pages of sizes that are no multiple of 8, heads of 100 channels) warps 0 and 3 copy them
-// piece by piece into the same layout; that bounds the kernel then (a chunk of 4096 tokens over as many, 16 heads on 2: 208 us with
-// tiled copies, 857 in pieces of 16 bytes).
+// piece by piece into the same layout; that bounds the kernel then (a chunk of 4096 tokens over as many, 16 heads on 2: 197 us with
+// tiled copies, 850 in pieces of 16 bytes).
 //
 // Warps: 0 finds the work and copies, 1 (and 2) issue the products, 2 owns TMEM, 3 helps with plain copies, 4.. exponentials and results.
 #pragma once

@@ -31,7 +31,9 @@
  * types the tensor cores take w relative to the row's running maximum rounded
  * to that type; o is rounded once.  lse = log sum_s exp(scale q . k_s).  A row
  * that sees nothing has o = 0 and lse = -infinity.  A key that a row does not
- * see has no influence on it, whatever it holds.
+ * see has no influence on it, whatever it holds.  A channel in which a row sees
+ * an infinite value is infinite; NaN, where it sees both signs or NaN, or where
+ * that value's weight vanishes in its type.
  *
  * Shapes (device memory):
  *   q, q_out, output    [T, heads, D], k, v and k_out [T, kv_heads, D]: a

@@ -39,3 +39,11 @@ def test_as_many_blocks_as_fit_at_once(D):
     up = lambda n: -(-n // 256) * 256  # noqa: E731
     want = up(2 * blocks * 16) + up(2 * blocks * 64 * 8) + up(2 * blocks * 64 * D * 4)
     assert gdn.lib().gdn_attention_workspace(ctypes.byref(batch), ctypes.byref(kv), ctypes.byref(args)) == want
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("D", [60, 62, 70, 84, 102, 122, 126, 130])
+def test_few_rows_in_narrow_pieces(dtype, D):
+    """Rows that are multiples of 4 or 8 bytes, on either side of what goes to the CUDA cores."""
+    Cache([1] * 5, [0, 45, 130, 700, 1000], 16, 2, D, 64, dtype, seed=D).check(tokens=1)
+    Cache([3] * 4, [0, 45, 130, 700], 4, 2, D, 20, dtype, seed=D).check(tokens=3, window=90)
