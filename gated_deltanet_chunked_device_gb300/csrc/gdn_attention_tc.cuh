@@ -718,8 +718,8 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
 // A weight of zero makes nothing of a value only if that is finite.  So the products must not see what the page of a sequence's last
 // tile holds behind the sequence (rows from `held` on: anything), nor, in blocks of 32 keys of which some row does not see all,
 // values that are not finite: these become zero in shared memory, and reach the rows that see them by add_unfinite.  By a whole warp,
-// eight lanes a row of a chunk, four rows at a time.  It runs once or twice a unit, between code that fills the instruction cache: short
-// loops, which a warp fetches once, take a twentieth of the time of unrolled ones (8 prompts, heads of 256: 1581 and 1886 us).
+// eight lanes a row of a chunk, four rows at a time.  It runs once or twice a unit, between code that fills the instruction cache, so
+// that its own has to come first: short loops, not unrolled ones (8 prompts, heads of 256: 1581 us, 1886 with loops unrolled by 8).
 template <class S>
 __device__ __forceinline__ uint4* stage_rows(uint8_t* stage, int chunk, int row, int lane) {
     return reinterpret_cast<uint4*>(stage + chunk * (S::kKeys * 128) + row * 128 + lane * 16);
