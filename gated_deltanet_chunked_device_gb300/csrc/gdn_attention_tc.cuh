@@ -272,7 +272,7 @@ __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart
     constexpr uint32_t kMantissa = std::is_same<E, __half>::value ? 0x03ffu : 0x007fu;
     const int D = p.c.head_dim;
     uint64_t placed = 0;           // kInstead: channels whose results have been replaced, 8 bits a row
-    uint32_t all_pos = 0, all_neg = 0;  // kInstead: channels that keys of all rows make infinite
+    uint32_t all_pos[4]{}, all_neg[4]{};  // kInstead: channels that keys of all rows make infinite, by the signs of a lane's pairs
     // Row r (a lane's) gets infinities in the channels that the bits name.
     auto give = [&](int r, uint32_t up, uint32_t down) {
         if (!__any_sync(~0u, (up | down) != 0)) return;
@@ -298,6 +298,7 @@ __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart
         }
         if (__all_sync(~0u, over) && lane == r) row = false;
     };
+    if (!__any_sync(~0u, row)) return;
     int32_t every0, every1;
     keys_of_all(p, a, every0, every1);
     __syncwarp();  // the rows' other results are there for all lanes
@@ -313,21 +314,49 @@ __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart
             const int32_t page = p.b.table[static_cast<int64_t>(a.table_row) * p.b.max_pages + i];
             if (page >= 0 && page < p.b.n_pages) at = page * p.c.v_page_stride + slot * p.c.v_token_stride + a.kv_head * p.c.v_head_stride;
         }
+        // Of keys i0 .., the pair of channels from d on; rows are multiples of 4 bytes here.  All loads go out at once: what is not there
+        // reads the cache's first pair, and is dropped.
+        const uint32_t there = __ballot_sync(~0u, at >= 0);
+        at = max(at, int64_t{0});
+        auto load = [&](auto& x, int i0, int d) {
+            constexpr int kLoads = static_cast<int>(sizeof(x) / 4);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                x[i] = *reinterpret_cast<const volatile uint32_t*>(static_cast<const E*>(p.c.v) + __shfl_sync(~0u, at, i0 + i) + (d < D ? d : 0));
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                if (d >= D || !(there >> (i0 + i) & 1)) x[i] = 0;
+        };
+        if (kInstead && whole) {
+            bool nan = true;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (64 * c >= D) break;
+#pragma unroll 1
+                for (int i0 = 0; i0 < 32; i0 += 16) {
+                    uint32_t x[16];
+                    load(x, i0, 2 * lane + 64 * c);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t bad = unfinite_signs<E>(x[i]), is_nan = (x[i] & (kMantissa | kMantissa << 16)) + 0x7fff7fffu;
+                        all_pos[c] |= bad & (~x[i] | is_nan);
+                        all_neg[c] |= bad & (x[i] | is_nan);
+                    }
+                }
+                if (2 * lane + 64 * c < D) nan &= (all_pos[c] & all_neg[c]) == 0x80008000u;
+            }
+            if (__all_sync(~0u, nan)) break;
+            continue;
+        }
         uint32_t pos[8]{}, neg[8]{};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const int d = 2 * lane + 64 * c;  // rows are multiples of 4 bytes here
             if (64 * c >= D) break;
 #pragma unroll 1
             for (int i0 = 0; i0 < 32; i0 += 8) {
                 if (!(some >> i0 & 0xffu)) continue;
                 uint32_t x[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int64_t from = __shfl_sync(~0u, at, i0 + i);
-                    x[i] = 0;
-                    if (from >= 0 && d < D) x[i] = *reinterpret_cast<const uint32_t*>(static_cast<const E*>(p.c.v) + from + d);
-                }
+                load(x, i0, 2 * lane + 64 * c);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const uint32_t bad = unfinite_signs<E>(x[i]);
@@ -342,17 +371,6 @@ __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart
                 }
             }
         }
-        if (kInstead && whole) {
-            bool nan = true;
-#pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                if (pos[c]) all_pos |= 1u << c;
-                if (neg[c]) all_neg |= 1u << c;
-                if (2 * lane + 64 * (c / 2) + c % 2 < D) nan &= (all_pos & all_neg) >> c & 1;
-            }
-            if (__all_sync(~0u, nan)) break;
-            continue;
-        }
         for (unsigned rows = __ballot_sync(~0u, seen != 0); rows; rows &= rows - 1) {
             const int r = __ffs(rows) - 1;
             const uint32_t keys = __shfl_sync(~0u, seen, r);
@@ -366,8 +384,15 @@ __device__ __forceinline__ void add_unfinite(const AttnParams& p, const AttnPart
         }
         if (!__any_sync(~0u, row)) return;
     }
-    if (kInstead)
-        for (unsigned rows = __ballot_sync(~0u, row); rows; rows &= rows - 1) give(__ffs(rows) - 1, all_pos, all_neg);
+    if (kInstead) {
+        uint32_t up = 0, down = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            up |= (all_pos[c / 2] >> (15 + 16 * (c % 2)) & 1u) << c;
+            down |= (all_neg[c / 2] >> (15 + 16 * (c % 2)) & 1u) << c;
+        }
+        for (unsigned rows = __ballot_sync(~0u, row); rows; rows &= rows - 1) give(__ffs(rows) - 1, up, down);
+    }
 }
 
 // Notes a unit that later blocks go on with, so that the join comes to its rows.
@@ -718,8 +743,8 @@ __device__ void produce_plain(const TcParams& p, Misc<S>& sh, uint8_t* q_s, uint
 // A weight of zero makes nothing of a value only if that is finite.  So the products must not see what the page of a sequence's last
 // tile holds behind the sequence (rows from `held` on: anything), nor, in blocks of 32 keys of which some row does not see all,
 // values that are not finite: these become zero in shared memory, and reach the rows that see them by add_unfinite.  By a whole warp,
-// eight lanes a row of a chunk, four rows at a time.  It runs once or twice a unit, between code that fills the instruction cache, so
-// that its own has to come first: short loops, not unrolled ones (8 prompts, heads of 256: 1581 us, 1886 with loops unrolled by 8).
+// eight lanes a row of a chunk, four rows at a time.  It runs once or twice a unit, between code that fills the instruction cache: short
+// loops, with four loads at a time (8 prompts, heads of 256: 1581 us; unrolled over 32 rows 1611, with a test before each load 1886).
 template <class S>
 __device__ __forceinline__ uint4* stage_rows(uint8_t* stage, int chunk, int row, int lane) {
     return reinterpret_cast<uint4*>(stage + chunk * (S::kKeys * 128) + row * 128 + lane * 16);
